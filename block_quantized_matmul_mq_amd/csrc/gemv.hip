@@ -24,6 +24,7 @@
 #include <cstdlib>
 
 #include "mq_device.h"
+#include "mq_epilogue.h"
 #include "mq_internal.h"
 #include "weight_units.h"
 
@@ -228,12 +229,12 @@ __device__ __forceinline__ uint32_t digits(float x, int k) {
 
 // LDS layout (dynamic): three digit planes of plane_bytes(K) | block exponents
 // int | sums f32 | partials f32 [tile_units]  (see lds_layout below)
-template <int QT, int kThreads, int kSlots>
+template <int QT, int kThreads, int kSlots, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restrict__ W,
                                                         const float* __restrict__ x,
                                                         float* __restrict__ y, int N, int K,
                                                         int64_t row_bytes, int tile_units, int blk_stride,
-                                                        int blk_off) {
+                                                        int blk_off, EP ep) {
     using Unit = typename UnitOf<QT>::T;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int U = K / Unit::kValues;
@@ -408,7 +409,7 @@ __global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restric
                 for (int j = lane_in; j < U; j += width) s += pr[j];
             }
             s = group_sum(s, width);
-            if (r < rows && lane_in == 0) y[t0 + r] = s;
+            if (r < rows && lane_in == 0) y[t0 + r] = ep(s, t0 + r, t0 + r);
         }
         __syncthreads();
     }
@@ -419,20 +420,21 @@ constexpr int kGemvThreads = 1024;
 constexpr int kGemvSlots = 2;
 
 template <int QT>
-const void* kernel_ptr() {
-    return reinterpret_cast<const void*>(gemv_kernel<QT, kGemvThreads, kGemvSlots>);
+const void* kernel_ptr(bool ep) {
+    return ep ? reinterpret_cast<const void*>(gemv_kernel<QT, kGemvThreads, kGemvSlots, Epilogue>)
+              : reinterpret_cast<const void*>(gemv_kernel<QT, kGemvThreads, kGemvSlots, NoEpilogue>);
 }
 
-const void* kernel_for(int type) {
+const void* kernel_for(int type, bool ep) {
     switch (type) {
-        case kQ4_K: return kernel_ptr<kQ4_K>();
-        case kQ5_K: return kernel_ptr<kQ5_K>();
-        case kQ6_K: return kernel_ptr<kQ6_K>();
-        case kQ8_0: return kernel_ptr<kQ8_0>();
-        case kQ4_0: return kernel_ptr<kQ4_0>();
-        case kQ4_1: return kernel_ptr<kQ4_1>();
-        case kQ5_0: return kernel_ptr<kQ5_0>();
-        case kQ5_1: return kernel_ptr<kQ5_1>();
+        case kQ4_K: return kernel_ptr<kQ4_K>(ep);
+        case kQ5_K: return kernel_ptr<kQ5_K>(ep);
+        case kQ6_K: return kernel_ptr<kQ6_K>(ep);
+        case kQ8_0: return kernel_ptr<kQ8_0>(ep);
+        case kQ4_0: return kernel_ptr<kQ4_0>(ep);
+        case kQ4_1: return kernel_ptr<kQ4_1>(ep);
+        case kQ5_0: return kernel_ptr<kQ5_0>(ep);
+        case kQ5_1: return kernel_ptr<kQ5_1>(ep);
         default: return nullptr;
     }
 }
@@ -463,24 +465,25 @@ int gemv_tile_units(int type, int64_t K, size_t lds_limit) {
 }
 
 hipError_t gemv_set_attributes(size_t lds_limit) {
-    for (int type : {kQ4_K, kQ5_K, kQ6_K, kQ8_0, kQ4_0, kQ4_1, kQ5_0, kQ5_1}) {
-        hipError_t e = hipFuncSetAttribute(kernel_for(type), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                           int(lds_limit));
-        if (e != hipSuccess) return e;
-    }
+    for (int type : {kQ4_K, kQ5_K, kQ6_K, kQ8_0, kQ4_0, kQ4_1, kQ5_0, kQ5_1})
+        for (bool ep : {false, true}) {
+            hipError_t e = hipFuncSetAttribute(kernel_for(type, ep), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(lds_limit));
+            if (e != hipSuccess) return e;
+        }
     return hipSuccess;
 }
 
 hipError_t launch_gemv(int type, BlockLayout layout, const uint8_t* W, const float* x, float* y, int64_t N,
-                       int64_t K, hipStream_t s, const char** name) {
+                       int64_t K, const Epilogue* ep, hipStream_t s, const char** name) {
     const DeviceInfo* info = device_info();
     if (!info) return hipErrorInvalidDevice;
     if (type == kQ4_K && gemv_mfma_applies(type, N, K, info->cu_count))
-        return launch_gemv_mfma(W, x, y, N, K, info->cu_count, s, name);
+        return launch_gemv_mfma(W, x, y, N, K, info->cu_count, ep, s, name);
     if (gemv_tiled_applies(type, layout, W, N, K, info->cu_count))
-        return launch_gemv_tiled(type, W, x, y, N, K, info->cu_count, s, name);
+        return launch_gemv_tiled(type, W, x, y, N, K, info->cu_count, ep, s, name);
     if (gemv_wide_applies(type, layout, W, N, K, info->cu_count))
-        return launch_gemv_wide(type, W, x, y, N, K, info->cu_count, s, name);
+        return launch_gemv_wide(type, W, x, y, N, K, info->cu_count, ep, s, name);
     int tile = gemv_tile_units(type, K, info->lds_per_block);
     if (tile <= 0) return hipErrorInvalidValue;
     const int vals = unit_values(type);
@@ -493,7 +496,7 @@ hipError_t launch_gemv(int type, BlockLayout layout, const uint8_t* W, const flo
     const int64_t rows_tile = (rows_wg + ntiles - 1) / ntiles;
     tile = int(rows_tile * U);
     const size_t shmem = fixed_lds_bytes(type, K) + size_t(tile) * 4;
-    const void* kern = kernel_for(type);
+    const void* kern = kernel_for(type, ep != nullptr);
     const bool repacked = layout.off != 0 || (type == kQ6_K && layout.stride != 210);
     switch (type) {
         case kQ8_0: *name = repacked ? "gemv<q8_0 repacked>" : "gemv<q8_0>"; break;
@@ -508,7 +511,7 @@ hipError_t launch_gemv(int type, BlockLayout layout, const uint8_t* W, const flo
     }
     int64_t row_bytes = (K / block_values_of(type)) * layout.stride;
     int n = int(N), k = int(K), stride = layout.stride, off = layout.off;
-    void* args[] = {&W, &x, &y, &n, &k, &row_bytes, &tile, &stride, &off};
+    void* args[] = {&W, &x, &y, &n, &k, &row_bytes, &tile, &stride, &off, epilogue_arg(ep)};
     return hipLaunchKernel(kern, dim3(grid), dim3(kGemvThreads), args, shmem, s);
 }
 

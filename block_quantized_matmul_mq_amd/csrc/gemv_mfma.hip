@@ -38,6 +38,7 @@
 #include <utility>
 
 #include "mq_device.h"
+#include "mq_epilogue.h"
 #include "mq_internal.h"
 
 namespace mq {
@@ -120,11 +121,11 @@ __device__ __forceinline__ float sum_lane_groups(float v) {
 }
 
 // NB: LDS ring slots per wave (items in flight + the one being computed).
-template <int NB>
+template <int NB, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_mfma_q4k_kernel(const uint8_t* __restrict__ W,
                                                                  const float* __restrict__ x,
                                                                  float* __restrict__ y, int N, int K,
-                                                                 int row_bytes) {
+                                                                 int row_bytes, EP ep) {
     // One static array per ring slot: with compile-time slot numbers the compiler knows
     // which slot a read touches and waits for that slot's loads only.
     __shared__ __attribute__((aligned(16))) uint8_t ring0[kWaves * kItemBytes];
@@ -292,7 +293,7 @@ __global__ __launch_bounds__(kThreads) void gemv_mfma_q4k_kernel(const uint8_t* 
     s = lanes8_sum<2>(s);
     if (j == 0 && r < tiles * kTileRows) {
         const int row = (w0 + (r / kTileRows) * G) * kTileRows + r % kTileRows;
-        if (row < N) y[row] = s;
+        if (row < N) y[row] = ep(s, row, row);
     }
 }
 
@@ -321,11 +322,11 @@ constexpr uint32_t kPastEnd = 0x7FFF0000u;   // a buffer offset past the end of 
 // On Q4_K's row-tiled layout (TILED) the tile is a group of that layout, TR its rows, and an
 // item is one contiguous run of TR x 144 bytes; the kernel is otherwise the same, and so are
 // its results, bit for bit.
-template <int NB, bool TILED>
+template <int NB, bool TILED, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_mfma_q4k_long_kernel(const uint8_t* __restrict__ W,
                                                                        const float* __restrict__ x,
                                                                        float* __restrict__ y, int N, int K,
-                                                                       int row_bytes, int TR, int nbytes) {
+                                                                       int row_bytes, int TR, int nbytes, EP ep) {
     __shared__ __attribute__((aligned(16))) uint8_t ring0[kWaves * kItemBytes];
     __shared__ __attribute__((aligned(16))) uint8_t ring1[kWaves * kItemBytes];
     __shared__ __attribute__((aligned(16))) uint8_t ring2[NB > 2 ? kWaves * kItemBytes : 16];
@@ -464,7 +465,7 @@ __global__ __launch_bounds__(kThreads) void gemv_mfma_q4k_long_kernel(const uint
         sum = (v.x + v.y) + (v.z + v.w);
     }
     sum = lanes8_sum<2>(sum);
-    if (j == 0 && rr < rows) y[r0 + rr] = sum;
+    if (j == 0 && rr < rows) y[r0 + rr] = ep(sum, r0 + rr, r0 + rr);
 }
 
 
@@ -641,11 +642,11 @@ constexpr int tiled_slot_bytes() { return kTileRows * kMaxSB * TiledItem<QT>::kS
 // D: tiles in flight (register ring; two measured faster than three or four); CPL: 16-byte
 // chunks per lane and tile.  The loop is unrolled over lcm(D, 2) tiles so that every ring
 // and slot index is a compile-time constant.
-template <int QT, int D, int CPL>
+template <int QT, int D, int CPL, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_tiled_kernel(const uint8_t* __restrict__ W,
                                                               const float* __restrict__ x,
                                                               float* __restrict__ y, int N, int K,
-                                                              int row_bytes) {
+                                                              int row_bytes, EP ep) {
     using Item = TiledItem<QT>;
     constexpr int kSlot = tiled_slot_bytes<QT>();
     // (16 bytes past a full slot: the aligned dwords read around a row's last block may
@@ -752,7 +753,7 @@ __global__ __launch_bounds__(kThreads) void gemv_tiled_kernel(const uint8_t* __r
                   ((4 * j + 2 < SB ? v.z : 0.f) + (4 * j + 3 < SB ? v.w : 0.f));
         s = lanes8_sum<2>(s);
         const int row = (w0 + k * G) * kTileRows + r;
-        if (j == 0 && row < N) y[row] = s;
+        if (j == 0 && row < N) y[row] = ep(s, row, row);
     };
 
     // Tile 0 into slot 0; then per tile k: compute it, sum the rows of tile k - 1, move
@@ -799,12 +800,12 @@ __global__ __launch_bounds__(kThreads) void gemv_tiled_kernel(const uint8_t* __r
 // Tiles ahead in registers: one, as for the f32 kernel above (two measured 5% slower on the
 // vocab head at M = 8).
 constexpr int kQ8TiledDepth = 1;
-template <int MR, bool DUMP, int CPL>
+template <int MR, bool DUMP, int CPL, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_q8_q6k_kernel(const uint8_t* __restrict__ W,
                                                                const int8_t* __restrict__ codes,
                                                                const float* __restrict__ xscale,
                                                                float* __restrict__ Y, int32_t* __restrict__ dots,
-                                                               int M, int N, int K, int row_bytes) {
+                                                               int M, int N, int K, int row_bytes, EP ep) {
     constexpr int kSlot = tiled_slot_bytes<kQ6_K>();
     constexpr int H = MR / 4;   // MFMAs per quarter
     constexpr int kStage = MR * 256 * kMaxSB;
@@ -972,7 +973,10 @@ __global__ __launch_bounds__(kThreads) void gemv_q8_q6k_kernel(const uint8_t* __
                         ((4 * j + 2 < SB ? v.z : 0.f) + (4 * j + 3 < SB ? v.w : 0.f));
             }
             const int row = (w0 + k * G) * kTileRows + r;
-            if (m < M && row < N) Y[int64_t(m) * N + row] = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            if (m < M && row < N) {
+                const int64_t at = int64_t(m) * N + row;
+                Y[at] = ep((s4[0] + s4[1]) + (s4[2] + s4[3]), at, row);
+            }
         }
     };
 
@@ -1028,11 +1032,11 @@ struct WideItem {
     static_assert(kSCB % 16 == 0 && kChunks % 16 == 0, "whole chunks");
 };
 
-template <int QT, int NB>
+template <int QT, int NB, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_wide_kernel(const uint8_t* __restrict__ W,
                                                              const float* __restrict__ x,
                                                              float* __restrict__ y, int N, int K,
-                                                             int row_bytes) {
+                                                             int row_bytes, EP ep) {
     using WI = WideItem<QT>;
     constexpr int kIB = WI::kBytes;
     // (16 bytes past each ring: a field read as the aligned dwords around it may reach 4
@@ -1171,7 +1175,7 @@ __global__ __launch_bounds__(kThreads) void gemv_wide_kernel(const uint8_t* __re
     s = lanes8_sum<2>(s);
     if (j == 0 && r < tiles * kTileRows) {
         const int row = (w0 + (r / kTileRows) * G) * kTileRows + r % kTileRows;
-        if (row < N) y[row] = s;
+        if (row < N) y[row] = ep(s, row, row);
     }
 }
 
@@ -1185,16 +1189,17 @@ constexpr int wide_ring() {
 }
 
 template <int QT>
-const void* wide_instance() {
+const void* wide_instance(bool ep) {
     constexpr int nb = wide_ring<QT>();
-    return reinterpret_cast<const void*>(gemv_wide_kernel<QT, nb>);
+    return ep ? reinterpret_cast<const void*>(gemv_wide_kernel<QT, nb, Epilogue>)
+              : reinterpret_cast<const void*>(gemv_wide_kernel<QT, nb, NoEpilogue>);
 }
 
-const void* wide_kernel(int type) {
+const void* wide_kernel(int type, bool ep) {
     switch (type) {
-        case kQ8_0: return wide_instance<kQ8_0>();
-        case kQ4_0: return wide_instance<kQ4_0>();
-        case kQ5_0: return wide_instance<kQ5_0>();
+        case kQ8_0: return wide_instance<kQ8_0>(ep);
+        case kQ4_0: return wide_instance<kQ4_0>(ep);
+        case kQ5_0: return wide_instance<kQ5_0>(ep);
         default: return nullptr;
     }
 }
@@ -1246,31 +1251,33 @@ int tiled_sb_bytes(int type) { return type == kQ6_K ? TiledItem<kQ6_K>::kSBBytes
 
 // Instances for the chunks per lane that rows of kMinSB .. kMaxSB super-chunks need.
 template <int QT, int CPL>
-const void* tiled_instance() {
+const void* tiled_instance(bool ep) {
     constexpr int lo = (kMinSB * TiledItem<QT>::kSBBytes + kThreads - 1) / kThreads;
     constexpr int hi = (kMaxSB * TiledItem<QT>::kSBBytes + kThreads - 1) / kThreads;
-    if constexpr (CPL >= lo && CPL <= hi) return reinterpret_cast<const void*>(gemv_tiled_kernel<QT, kTiledDepth, CPL>);
+    if constexpr (CPL >= lo && CPL <= hi)
+        return ep ? reinterpret_cast<const void*>(gemv_tiled_kernel<QT, kTiledDepth, CPL, Epilogue>)
+                  : reinterpret_cast<const void*>(gemv_tiled_kernel<QT, kTiledDepth, CPL, NoEpilogue>);
     return nullptr;
 }
 
 template <int QT>
-const void* tiled_kernel(int cpl) {
+const void* tiled_kernel(int cpl, bool ep) {
     switch (cpl) {
-        case 2: return tiled_instance<QT, 2>();
-        case 3: return tiled_instance<QT, 3>();
-        case 4: return tiled_instance<QT, 4>();
-        case 5: return tiled_instance<QT, 5>();
+        case 2: return tiled_instance<QT, 2>(ep);
+        case 3: return tiled_instance<QT, 3>(ep);
+        case 4: return tiled_instance<QT, 4>(ep);
+        case 5: return tiled_instance<QT, 5>(ep);
         default: return nullptr;
     }
 }
 
-const void* tiled_kernel_for(int type, int cpl) { return type == kQ6_K ? tiled_kernel<kQ6_K>(cpl) : nullptr; }
+const void* tiled_kernel_for(int type, int cpl, bool ep) { return type == kQ6_K ? tiled_kernel<kQ6_K>(cpl, ep) : nullptr; }
 
-template <int MR, bool DUMP>
+template <int MR, bool DUMP, class EP>
 const void* q8_q6k_kernel(int cpl) {
     switch (cpl) {
-        case 3: return reinterpret_cast<const void*>(gemv_q8_q6k_kernel<MR, DUMP, 3>);
-        case 4: return reinterpret_cast<const void*>(gemv_q8_q6k_kernel<MR, DUMP, 4>);
+        case 3: return reinterpret_cast<const void*>(gemv_q8_q6k_kernel<MR, DUMP, 3, EP>);
+        case 4: return reinterpret_cast<const void*>(gemv_q8_q6k_kernel<MR, DUMP, 4, EP>);
         default: return nullptr;
     }
 }
@@ -1291,14 +1298,14 @@ bool gemv_tiled_applies(int type, BlockLayout layout, const uint8_t* W, int64_t 
 }
 
 hipError_t launch_gemv_tiled(int type, const uint8_t* W, const float* x, float* y, int64_t N, int64_t K,
-                             int cu_count, hipStream_t s, const char** name) {
+                             int cu_count, const Epilogue* ep, hipStream_t s, const char** name) {
     const int64_t T = (N + kTileRows - 1) / kTileRows;
     const int grid = int(T < cu_count ? T : cu_count);
     int n = int(N), k = int(K), row_bytes = int((K / 256) * tiled_sb_bytes(type));
-    const void* f = tiled_kernel_for(type, (row_bytes + kThreads - 1) / kThreads);   // chunks per lane
+    const void* f = tiled_kernel_for(type, (row_bytes + kThreads - 1) / kThreads, ep != nullptr);   // chunks per lane
     if (!f) return hipErrorInvalidValue;
     *name = "gemv_mfma<q6_K>";
-    void* args[] = {&W, &x, &y, &n, &k, &row_bytes};
+    void* args[] = {&W, &x, &y, &n, &k, &row_bytes, epilogue_arg(ep)};
     return hipLaunchKernel(f, dim3(grid), dim3(kThreads), args, 0, s);
 }
 
@@ -1309,19 +1316,23 @@ bool gemv_q8_tiled_applies(int type, BlockLayout layout, const uint8_t* W, const
 }
 
 hipError_t launch_gemv_q8_tiled(int type, const uint8_t* W, const int8_t* codes, const float* xs, float* Y,
-                                int32_t* dots, int64_t M, int64_t N, int64_t K, int cu_count, hipStream_t s,
-                                const char** name) {
+                                int32_t* dots, int64_t M, int64_t N, int64_t K, int cu_count, const Epilogue* ep,
+                                hipStream_t s, const char** name) {
     if (type != kQ6_K) return hipErrorInvalidValue;
     const int64_t T = (N + kTileRows - 1) / kTileRows;
     const int grid = int(T < cu_count ? T : cu_count);
     int m = int(M), n = int(N), k = int(K), row_bytes = int((K / 256) * TiledItem<kQ6_K>::kSBBytes);
     const int cpl = (row_bytes + kThreads - 1) / kThreads;
     const bool dump = dots != nullptr;
-    const void* f = M <= 4 ? (dump ? q8_q6k_kernel<4, true>(cpl) : q8_q6k_kernel<4, false>(cpl))
-                           : (dump ? q8_q6k_kernel<8, true>(cpl) : q8_q6k_kernel<8, false>(cpl));
+    const void* f = M <= 4 ? (dump ? q8_q6k_kernel<4, true, NoEpilogue>(cpl)
+                              : ep ? q8_q6k_kernel<4, false, Epilogue>(cpl)
+                                   : q8_q6k_kernel<4, false, NoEpilogue>(cpl))
+                           : (dump ? q8_q6k_kernel<8, true, NoEpilogue>(cpl)
+                              : ep ? q8_q6k_kernel<8, false, Epilogue>(cpl)
+                                   : q8_q6k_kernel<8, false, NoEpilogue>(cpl));
     if (!f) return hipErrorInvalidValue;
     *name = "gemv_q8_mfma<q6_K>";
-    void* args[] = {&W, &codes, &xs, &Y, &dots, &m, &n, &k, &row_bytes};
+    void* args[] = {&W, &codes, &xs, &Y, &dots, &m, &n, &k, &row_bytes, epilogue_arg(ep)};
     return hipLaunchKernel(f, dim3(grid), dim3(kThreads), args, 0, s);
 }
 
@@ -1356,23 +1367,23 @@ bool gemv_wide_applies(int type, BlockLayout layout, const uint8_t* W, int64_t N
 }
 
 hipError_t launch_gemv_wide(int type, const uint8_t* W, const float* x, float* y, int64_t N, int64_t K,
-                            int cu_count, hipStream_t s, const char** name) {
+                            int cu_count, const Epilogue* ep, hipStream_t s, const char** name) {
     const int64_t T = (N + kTileRows - 1) / kTileRows;
     const int grid = int(T < cu_count ? T : cu_count);
     int n = int(N), k = int(K), row_bytes = int((K / 256) * wide_scb(type));
-    const void* f = wide_kernel(type);
+    const void* f = wide_kernel(type, ep != nullptr);
     switch (type) {
         case kQ8_0: *name = "gemv_mfma<q8_0>"; break;
         case kQ4_0: *name = "gemv_mfma<q4_0>"; break;
         case kQ5_0: *name = "gemv_mfma<q5_0>"; break;
         default: return hipErrorInvalidValue;
     }
-    void* args[] = {&W, &x, &y, &n, &k, &row_bytes};
+    void* args[] = {&W, &x, &y, &n, &k, &row_bytes, epilogue_arg(ep)};
     return hipLaunchKernel(f, dim3(grid), dim3(kThreads), args, 0, s);
 }
 
-hipError_t launch_gemv_row_tiled(const uint8_t* W, const float* x, float* y, int64_t N, int64_t K, hipStream_t s,
-                                 const char** name) {
+hipError_t launch_gemv_row_tiled(const uint8_t* W, const float* x, float* y, int64_t N, int64_t K,
+                                 const Epilogue* ep, hipStream_t s, const char** name) {
     // (the callers check row_tiled_k(K) and K <= MQ_MAX_K: a row-tiled matrix of N <= 2^24
     // rows then ends below kPastEnd only while N * row bytes does, which is checked here)
     const size_t nbytes = row_tiled_bytes(N, K);
@@ -1380,9 +1391,10 @@ hipError_t launch_gemv_row_tiled(const uint8_t* W, const float* x, float* y, int
     *name = "gemv_mfma_long<q4_K row-tiled>";
     const int tr = row_tile_rows(N);
     int n = int(N), k = int(K), row_bytes = int((K / 256) * 144), t = tr, nb = int(nbytes);
-    void* args[] = {&W, &x, &y, &n, &k, &row_bytes, &t, &nb};
-    return hipLaunchKernel(reinterpret_cast<const void*>(gemv_mfma_q4k_long_kernel<kLongRing, true>),
-                           dim3(unsigned((N + tr - 1) / tr)), dim3(kThreads), args, 0, s);
+    void* args[] = {&W, &x, &y, &n, &k, &row_bytes, &t, &nb, epilogue_arg(ep)};
+    const void* f = ep ? reinterpret_cast<const void*>(gemv_mfma_q4k_long_kernel<kLongRing, true, Epilogue>)
+                       : reinterpret_cast<const void*>(gemv_mfma_q4k_long_kernel<kLongRing, true, NoEpilogue>);
+    return hipLaunchKernel(f, dim3(unsigned((N + tr - 1) / tr)), dim3(kThreads), args, 0, s);
 }
 
 bool gemv_mfma_applies(int type, int64_t N, int64_t K, int cu_count) {
@@ -1393,23 +1405,26 @@ bool gemv_mfma_applies(int type, int64_t N, int64_t K, int cu_count) {
 }
 
 hipError_t launch_gemv_mfma(const uint8_t* W, const float* x, float* y, int64_t N, int64_t K, int cu_count,
-                            hipStream_t s, const char** name) {
+                            const Epilogue* ep, hipStream_t s, const char** name) {
     if (const int tr = long_tile_rows(N, K, cu_count)) {
         *name = "gemv_mfma_long<q4_K>";
         int n = int(N), k = int(K), row_bytes = int((K / 256) * 144), t = tr, nbytes = int(N * row_bytes);
-        void* args[] = {&W, &x, &y, &n, &k, &row_bytes, &t, &nbytes};
-        return hipLaunchKernel(reinterpret_cast<const void*>(gemv_mfma_q4k_long_kernel<kLongRing, false>),
-                               dim3(unsigned((N + tr - 1) / tr)), dim3(kThreads), args, 0, s);
+        void* args[] = {&W, &x, &y, &n, &k, &row_bytes, &t, &nbytes, epilogue_arg(ep)};
+        const void* f = ep ? reinterpret_cast<const void*>(gemv_mfma_q4k_long_kernel<kLongRing, false, Epilogue>)
+                           : reinterpret_cast<const void*>(gemv_mfma_q4k_long_kernel<kLongRing, false, NoEpilogue>);
+        return hipLaunchKernel(f, dim3(unsigned((N + tr - 1) / tr)), dim3(kThreads), args, 0, s);
     }
     const Plan p = plan(N, K, cu_count);
     if (p.grid <= 0) return hipErrorInvalidValue;
     *name = "gemv_mfma<q4_K>";
     int n = int(N), k = int(K), row_bytes = int((K / 256) * 144);
-    void* args[] = {&W, &x, &y, &n, &k, &row_bytes};
+    void* args[] = {&W, &x, &y, &n, &k, &row_bytes, epilogue_arg(ep)};
     const int64_t tiles = (N + kTileRows - 1) / kTileRows;
-    const void* kern = tiles >= int64_t(kRingDeepTiles) * p.grid
-                           ? reinterpret_cast<const void*>(gemv_mfma_q4k_kernel<kRingDeep>)
-                           : reinterpret_cast<const void*>(gemv_mfma_q4k_kernel<kRing>);
+    const bool deep = tiles >= int64_t(kRingDeepTiles) * p.grid;
+    const void* kern = ep ? (deep ? reinterpret_cast<const void*>(gemv_mfma_q4k_kernel<kRingDeep, Epilogue>)
+                                  : reinterpret_cast<const void*>(gemv_mfma_q4k_kernel<kRing, Epilogue>))
+                          : (deep ? reinterpret_cast<const void*>(gemv_mfma_q4k_kernel<kRingDeep, NoEpilogue>)
+                                  : reinterpret_cast<const void*>(gemv_mfma_q4k_kernel<kRing, NoEpilogue>));
     return hipLaunchKernel(kern, dim3(p.grid),
                            dim3(kThreads), args, 0, s);
 }

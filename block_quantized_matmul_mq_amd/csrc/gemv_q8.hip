@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "mq_device.h"
+#include "mq_epilogue.h"
 #include "mq_internal.h"
 #include "weight_units.h"
 
@@ -99,14 +100,14 @@ __host__ __device__ constexpr size_t factor_bytes(int U) {
     return size_t(MR) * U * factor_unit_bytes(QT);
 }
 
-template <int QT, int MR, bool DUMP>
+template <int QT, int MR, bool DUMP, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_q8_kernel(const uint8_t* __restrict__ W,
                                                            const int8_t* __restrict__ codes,
                                                            const float* __restrict__ xscale,
                                                            const int32_t* __restrict__ xsum, float* __restrict__ Y,
                                                            int32_t* __restrict__ dots, int M, int N, int K,
                                                            int64_t row_bytes, int tile_units, int blk_stride,
-                                                           int blk_off) {
+                                                           int blk_off, EP ep) {
     using Sh = Shape<QT>;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     const int U = K / Sh::kValues;
@@ -350,7 +351,8 @@ __global__ __launch_bounds__(kThreads) void gemv_q8_kernel(const uint8_t* __rest
                 const float* pr = part + int64_t(row) * U * MR + m;
                 float s = 0.f;
                 for (int j = 0; j < U; ++j) s += pr[j * MR];
-                Y[int64_t(m) * N + t0 + row] = s;
+                const int64_t at = int64_t(m) * N + t0 + row;
+                Y[at] = ep(s, at, t0 + row);
             }
         }
         __syncthreads();
@@ -366,32 +368,36 @@ size_t fixed_bytes(int type, int MR, int64_t K) {
 
 int rows_for(int64_t M) { return M <= 1 ? 1 : (M <= 2 ? 2 : (M <= 4 ? 4 : 8)); }
 
+// The product, the block-dot export, the product with an epilogue.
+enum Variant { kProduct, kDump, kEpilogue };
+
 template <int QT, int MR>
-const void* kernel_ptr(bool dump) {
-    return dump ? reinterpret_cast<const void*>(gemv_q8_kernel<QT, MR, true>)
-                : reinterpret_cast<const void*>(gemv_q8_kernel<QT, MR, false>);
+const void* kernel_ptr(Variant v) {
+    return v == kDump       ? reinterpret_cast<const void*>(gemv_q8_kernel<QT, MR, true, NoEpilogue>)
+           : v == kEpilogue ? reinterpret_cast<const void*>(gemv_q8_kernel<QT, MR, false, Epilogue>)
+                            : reinterpret_cast<const void*>(gemv_q8_kernel<QT, MR, false, NoEpilogue>);
 }
 
 template <int QT>
-const void* kernel_for_type(int mr, bool dump) {
+const void* kernel_for_type(int mr, Variant v) {
     switch (mr) {
-        case 1: return kernel_ptr<QT, 1>(dump);
-        case 2: return kernel_ptr<QT, 2>(dump);
-        case 4: return kernel_ptr<QT, 4>(dump);
-        default: return kernel_ptr<QT, 8>(dump);
+        case 1: return kernel_ptr<QT, 1>(v);
+        case 2: return kernel_ptr<QT, 2>(v);
+        case 4: return kernel_ptr<QT, 4>(v);
+        default: return kernel_ptr<QT, 8>(v);
     }
 }
 
-const void* kernel_for(int type, int mr, bool dump) {
+const void* kernel_for(int type, int mr, Variant v) {
     switch (type) {
-        case kQ4_K: return kernel_for_type<kQ4_K>(mr, dump);
-        case kQ5_K: return kernel_for_type<kQ5_K>(mr, dump);
-        case kQ6_K: return kernel_for_type<kQ6_K>(mr, dump);
-        case kQ8_0: return kernel_for_type<kQ8_0>(mr, dump);
-        case kQ4_0: return kernel_for_type<kQ4_0>(mr, dump);
-        case kQ4_1: return kernel_for_type<kQ4_1>(mr, dump);
-        case kQ5_0: return kernel_for_type<kQ5_0>(mr, dump);
-        case kQ5_1: return kernel_for_type<kQ5_1>(mr, dump);
+        case kQ4_K: return kernel_for_type<kQ4_K>(mr, v);
+        case kQ5_K: return kernel_for_type<kQ5_K>(mr, v);
+        case kQ6_K: return kernel_for_type<kQ6_K>(mr, v);
+        case kQ8_0: return kernel_for_type<kQ8_0>(mr, v);
+        case kQ4_0: return kernel_for_type<kQ4_0>(mr, v);
+        case kQ4_1: return kernel_for_type<kQ4_1>(mr, v);
+        case kQ5_0: return kernel_for_type<kQ5_0>(mr, v);
+        case kQ5_1: return kernel_for_type<kQ5_1>(mr, v);
         default: return nullptr;
     }
 }
@@ -402,7 +408,7 @@ bool gemv_q8_applies(int type, int64_t M, int64_t K) {
     // a function of the shape alone (the code planes, the factor arrays and the partials of
     // one row must fit the 160 KB of LDS a gfx950 workgroup may use), so that the scratch
     // sizing of mq_gemm does not depend on the device
-    if (M < 1 || M > kGemvQ8MaxRows || !kernel_for(type, 1, false)) return false;
+    if (M < 1 || M > kGemvQ8MaxRows || !kernel_for(type, 1, kProduct)) return false;
     const int mr = rows_for(M);
     return fixed_bytes(type, mr, K) + size_t(K / unit_values(type)) * mr * 4 <= kGfx950LdsBytes;
 }
@@ -410,8 +416,8 @@ bool gemv_q8_applies(int type, int64_t M, int64_t K) {
 hipError_t gemv_q8_set_attributes(size_t lds_limit) {
     for (int type : {kQ4_K, kQ5_K, kQ6_K, kQ8_0, kQ4_0, kQ4_1, kQ5_0, kQ5_1})
         for (int mr : {1, 2, 4, 8})
-            for (bool dump : {false, true}) {
-                hipError_t e = hipFuncSetAttribute(kernel_for(type, mr, dump),
+            for (Variant v : {kProduct, kDump, kEpilogue}) {
+                hipError_t e = hipFuncSetAttribute(kernel_for(type, mr, v),
                                                    hipFuncAttributeMaxDynamicSharedMemorySize, int(lds_limit));
                 if (e != hipSuccess) return e;
             }
@@ -420,11 +426,11 @@ hipError_t gemv_q8_set_attributes(size_t lds_limit) {
 
 hipError_t launch_gemv_q8(int type, BlockLayout lay, const uint8_t* W, const int8_t* codes, const float* xs,
                           const int32_t* xsum, float* Y, int32_t* dots, int64_t M, int64_t N, int64_t K,
-                          hipStream_t s, const char** name) {
+                          const Epilogue* ep, hipStream_t s, const char** name) {
     const DeviceInfo* info = device_info();
     if (!info) return hipErrorInvalidDevice;
     if (gemv_q8_tiled_applies(type, lay, W, codes, M, N, K, info->cu_count))
-        return launch_gemv_q8_tiled(type, W, codes, xs, Y, dots, M, N, K, info->cu_count, s, name);
+        return launch_gemv_q8_tiled(type, W, codes, xs, Y, dots, M, N, K, info->cu_count, ep, s, name);
     const int mr = rows_for(M);
     const int vals = unit_values(type);
     const int U = int(K / vals);
@@ -455,8 +461,9 @@ hipError_t launch_gemv_q8(int type, BlockLayout lay, const uint8_t* W, const int
     }
     int64_t row_bytes = (K / block_values_of(type)) * lay.stride;
     int m = int(M), n = int(N), k = int(K), stride = lay.stride, off = lay.off;
-    void* args[] = {&W, &codes, &xs, &xsum, &Y, &dots, &m, &n, &k, &row_bytes, &tile_units, &stride, &off};
-    return hipLaunchKernel(kernel_for(type, mr, dots != nullptr), dim3(grid), dim3(kThreads), args, shmem, s);
+    void* args[] = {&W, &codes, &xs, &xsum, &Y, &dots, &m, &n, &k, &row_bytes, &tile_units, &stride, &off,
+                    epilogue_arg(ep)};
+    return hipLaunchKernel(kernel_for(type, mr, dots ? kDump : ep ? kEpilogue : kProduct), dim3(grid), dim3(kThreads), args, shmem, s);
 }
 
 }  // namespace mq

@@ -48,6 +48,7 @@
 
 #include "mmq_splitk.h"
 #include "mq_device.h"
+#include "mq_epilogue.h"
 #include "mq_internal.h"
 #include "weight_units.h"
 
@@ -377,7 +378,7 @@ template <> struct WeightRegs<kQ6_K> {
 // exist); for Q4_K it also loads the matching code sums into registers, and after its
 // loads have landed forms the min-term factor dx * sum of those slots itself (its own
 // loads are complete after its own wait, before any barrier).
-template <int QT, int BM>
+template <int QT, int BM, bool PRECISE>
 struct ActDirect {
     static constexpr int kCodeIns = BM / 32;           // 1 KB code instructions per wave
     static constexpr int kScaleIns = NB * BM / 64;     // 64-dword scale instructions in all
@@ -433,15 +434,30 @@ struct ActDirect {
             for (int j = 0; j < 2; ++j) {
                 if (2 * wave + j < kScaleIns) {
                     const int slot = 64 * (2 * wave + j) + lane;
-                    (&sm.tx[buf][0][0])[slot] = bf16_hilo((&sm.dx[buf][0][0])[slot] * float(sums[j]));
+                    const float tx = (&sm.dx[buf][0][0])[slot] * float(sums[j]);
+                    (&sm.tx[buf][0][0])[slot] = PRECISE ? __float_as_uint(tx) : bf16_hilo(tx);
                 }
             }
         }
     }
 };
 
+// The min term of the products with an epilogue, to f32 precision: tx (f32 bits) cut into three
+// bf16 pieces (24 bits: exact), mw in two (exact as well: f16 times 6 bits, 17 bits), six
+// slots of K = 8 per block in two MFMAs instead of three in one.  The products without an
+// epilogue keep their 2^-16 term (and their bits).
+__device__ __forceinline__ void min_term_f32(uint32_t t0, uint32_t t1, uint32_t w0, uint32_t w1, v16f& acc) {
+    const Bf16x3 x0 = bf16_split3(t0), x1 = bf16_split3(t1);
+    const v4i a = {int(x0.hh), int(x0.mm), int(x1.hh), int(x1.mm)}, b = {int(w0), int(w0), int(w1), int(w1)};
+    const v4i c = {int(x0.ll), 0, int(x1.ll), 0};
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, c), __builtin_bit_cast(v8bf, b), acc, 0, 0,
+                                                  0);
+    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b), acc, 0, 0,
+                                                  0);
+}
+
 // ------------------------------------------------------------------ kernel
-template <int QT, int BM, bool DUMP>
+template <int QT, int BM, bool DUMP, class EP>
 __global__ __launch_bounds__(256, 2) void mmq_kernel(const uint8_t* __restrict__ W,
                                                      const int8_t* __restrict__ codes,
                                                      const float* __restrict__ xscale,
@@ -450,7 +466,7 @@ __global__ __launch_bounds__(256, 2) void mmq_kernel(const uint8_t* __restrict__
                                                      float* __restrict__ partial, unsigned* __restrict__ counters,
                                                      int M, int N, int K, int64_t row_bytes, int blk_stride,
                                                      int blk_off, int tiles_m, int full, int split_tiles, int splits,
-                                                     int total_steps) {
+                                                     int total_steps, EP ep) {
     using T = TileShape<BM>;
     constexpr int TI = T::TI, TJ = T::TJ;
     __shared__ __attribute__((aligned(16))) Smem<QT, BM> sm;
@@ -492,7 +508,7 @@ __global__ __launch_bounds__(256, 2) void mmq_kernel(const uint8_t* __restrict__
 #pragma unroll
             for (int v = 0; v < 16; ++v) acc[i][j][v] = 0.f;
 
-    ActDirect<QT, BM> act;
+    ActDirect<QT, BM, EP::kIs> act;
     act.init(codes, xscale, xsum, m0, M, K);
     WeightRegs<QT> wr;
 
@@ -594,6 +610,10 @@ __global__ __launch_bounds__(256, 2) void mmq_kernel(const uint8_t* __restrict__
                 const int ar = arow0 + 32 * i, br = brow0 + 32 * j;
                 const uint32_t t0 = sm.tx[buf][2 * g][ar], t1 = sm.tx[buf][2 * g + 1][ar];
                 const uint32_t w0 = sm.mw[buf][2 * g][br], w1 = sm.mw[buf][2 * g + 1][br];
+                if constexpr (EP::kIs) {
+                    min_term_f32(t0, t1, w0, w1, acc[i][j]);
+                    return;
+                }
                 const v4i a = {int((t0 & 0xFFFFu) | (t0 << 16)), int(t0 >> 16), int((t1 & 0xFFFFu) | (t1 << 16)),
                                int(t1 >> 16)};
                 const v4i b = {int(w0), int(w0 & 0xFFFFu), int(w1), int(w1 & 0xFFFFu)};
@@ -654,7 +674,10 @@ __global__ __launch_bounds__(256, 2) void mmq_kernel(const uint8_t* __restrict__
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
             const int m = m0 + 32 * TI * wm + 32 * i + acc_row(v, g);
-            if (m < M && n < N) Y[int64_t(m) * N + n] = y[v];
+            if (m < M && n < N) {
+                const int64_t at = int64_t(m) * N + n;
+                Y[at] = ep(y[v], at, n);
+            }
         }
     };
     if (whole) {
@@ -695,76 +718,96 @@ __global__ __launch_bounds__(256, 2) void mmq_kernel(const uint8_t* __restrict__
 
 // Explicit instantiations: the host-side launch stubs of these kernels are otherwise not
 // emitted by this compiler when they are only named inside launch_shaped below.
-#define MQ_MMQ_INSTANCE(QT, BM, DUMP)                                                                        \
-    template __global__ void mmq_kernel<QT, BM, DUMP>(const uint8_t* __restrict__, const int8_t* __restrict__, \
+#define MQ_MMQ_INSTANCE(QT, BM, DUMP, EP)                                                                    \
+    template __global__ void mmq_kernel<QT, BM, DUMP, EP>(const uint8_t* __restrict__, const int8_t* __restrict__, \
                                                       const float* __restrict__, const int32_t* __restrict__,  \
                                                       float* __restrict__, int32_t* __restrict__,              \
                                                       float* __restrict__, unsigned* __restrict__, int, int, int, \
-                                                      int64_t, int, int, int, int, int, int, int);
-MQ_MMQ_INSTANCE(kQ5_K, 32, false)
-MQ_MMQ_INSTANCE(kQ5_K, 128, false)
-MQ_MMQ_INSTANCE(kQ5_K, 32, true)
-MQ_MMQ_INSTANCE(kQ5_K, 128, true)
-MQ_MMQ_INSTANCE(kQ4_0, 32, false)
-MQ_MMQ_INSTANCE(kQ4_0, 128, false)
-MQ_MMQ_INSTANCE(kQ4_0, 32, true)
-MQ_MMQ_INSTANCE(kQ4_0, 128, true)
-MQ_MMQ_INSTANCE(kQ4_1, 32, false)
-MQ_MMQ_INSTANCE(kQ4_1, 128, false)
-MQ_MMQ_INSTANCE(kQ4_1, 32, true)
-MQ_MMQ_INSTANCE(kQ4_1, 128, true)
-MQ_MMQ_INSTANCE(kQ5_0, 32, false)
-MQ_MMQ_INSTANCE(kQ5_0, 128, false)
-MQ_MMQ_INSTANCE(kQ5_0, 32, true)
-MQ_MMQ_INSTANCE(kQ5_0, 128, true)
-MQ_MMQ_INSTANCE(kQ5_1, 32, false)
-MQ_MMQ_INSTANCE(kQ5_1, 128, false)
-MQ_MMQ_INSTANCE(kQ5_1, 32, true)
-MQ_MMQ_INSTANCE(kQ5_1, 128, true)
-MQ_MMQ_INSTANCE(kQ8_0, 32, false)
-MQ_MMQ_INSTANCE(kQ8_0, 128, false)
-MQ_MMQ_INSTANCE(kQ4_K, 32, false)
-MQ_MMQ_INSTANCE(kQ4_K, 128, false)
-MQ_MMQ_INSTANCE(kQ6_K, 32, false)
-MQ_MMQ_INSTANCE(kQ6_K, 128, false)
-MQ_MMQ_INSTANCE(kQ8_0, 32, true)
-MQ_MMQ_INSTANCE(kQ8_0, 128, true)
-MQ_MMQ_INSTANCE(kQ4_K, 32, true)
-MQ_MMQ_INSTANCE(kQ4_K, 128, true)
-MQ_MMQ_INSTANCE(kQ6_K, 32, true)
-MQ_MMQ_INSTANCE(kQ6_K, 128, true)
+                                                      int64_t, int, int, int, int, int, int, int, EP);
+MQ_MMQ_INSTANCE(kQ5_K, 32, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_K, 32, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ5_K, 128, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_K, 128, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ5_K, 32, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_K, 128, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_0, 32, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_0, 32, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ4_0, 128, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_0, 128, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ4_0, 32, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_0, 128, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_1, 32, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_1, 32, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ4_1, 128, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_1, 128, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ4_1, 32, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_1, 128, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_0, 32, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_0, 32, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ5_0, 128, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_0, 128, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ5_0, 32, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_0, 128, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_1, 32, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_1, 32, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ5_1, 128, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_1, 128, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ5_1, 32, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ5_1, 128, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ8_0, 32, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ8_0, 32, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ8_0, 128, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ8_0, 128, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ4_K, 32, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_K, 32, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ4_K, 128, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_K, 128, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ6_K, 32, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ6_K, 32, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ6_K, 128, false, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ6_K, 128, false, Epilogue)
+MQ_MMQ_INSTANCE(kQ8_0, 32, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ8_0, 128, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_K, 32, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ4_K, 128, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ6_K, 32, true, NoEpilogue)
+MQ_MMQ_INSTANCE(kQ6_K, 128, true, NoEpilogue)
 #undef MQ_MMQ_INSTANCE
 
 template <int QT, int BM>
 hipError_t launch_shaped(const uint8_t* W, const int8_t* codes, const float* xs, const int32_t* xsum, float* Y,
                          int32_t* dots, float* partial, unsigned* counters, int64_t M, int64_t N, int64_t K,
-                         BlockLayout lay, const MmqPlan& plan, hipStream_t s) {
+                         BlockLayout lay, const MmqPlan& plan, const Epilogue* ep, hipStream_t s) {
     const int tiles_m = int((M + BM - 1) / BM);
     const int total = plan.full + plan.split_tiles * plan.splits;
     const int64_t row_bytes = (K / block_values_of(QT)) * lay.stride;
     if (dots)
-        hipLaunchKernelGGL((mmq_kernel<QT, BM, true>), dim3(total), dim3(256), 0, s, W, codes, xs, xsum, Y, dots,
-                           partial, counters, int(M), int(N), int(K), row_bytes, lay.stride, lay.off, tiles_m,
-                           plan.full, plan.split_tiles, plan.splits, plan.steps);
+        hipLaunchKernelGGL((mmq_kernel<QT, BM, true, NoEpilogue>), dim3(total), dim3(256), 0, s, W, codes, xs, xsum, Y,
+                           dots, partial, counters, int(M), int(N), int(K), row_bytes, lay.stride, lay.off, tiles_m,
+                           plan.full, plan.split_tiles, plan.splits, plan.steps, NoEpilogue{});
+    else if (ep)
+        hipLaunchKernelGGL((mmq_kernel<QT, BM, false, Epilogue>), dim3(total), dim3(256), 0, s, W, codes, xs, xsum, Y,
+                           dots, partial, counters, int(M), int(N), int(K), row_bytes, lay.stride, lay.off, tiles_m,
+                           plan.full, plan.split_tiles, plan.splits, plan.steps, *ep);
     else
-        hipLaunchKernelGGL((mmq_kernel<QT, BM, false>), dim3(total), dim3(256), 0, s, W, codes, xs, xsum, Y, dots,
-                           partial, counters, int(M), int(N), int(K), row_bytes, lay.stride, lay.off, tiles_m,
-                           plan.full, plan.split_tiles, plan.splits, plan.steps);
+        hipLaunchKernelGGL((mmq_kernel<QT, BM, false, NoEpilogue>), dim3(total), dim3(256), 0, s, W, codes, xs, xsum,
+                           Y, dots, partial, counters, int(M), int(N), int(K), row_bytes, lay.stride, lay.off, tiles_m,
+                           plan.full, plan.split_tiles, plan.splits, plan.steps, NoEpilogue{});
     return hipGetLastError();
 }
 
 template <int QT>
 hipError_t launch_typed(const uint8_t* W, const int8_t* codes, const float* xs, const int32_t* xsum,
                         float* Y, int32_t* dots, float* partial, unsigned* counters, int64_t M, int64_t N,
-                        int64_t K, BlockLayout lay, hipStream_t s) {
+                        int64_t K, BlockLayout lay, const Epilogue* ep, hipStream_t s) {
     const MmqPlan plan = mmq_plan(QT, M, N, K);
     if (!counters && partial) {   // the caller's scratch: counters, then the partial tiles
         counters = reinterpret_cast<unsigned*>(partial);
         partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(partial) + kSplitkCounterBytes);
     }
     if (plan.bm == 32)
-        return launch_shaped<QT, 32>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, plan, s);
-    return launch_shaped<QT, 128>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, plan, s);
+        return launch_shaped<QT, 32>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, plan, ep, s);
+    return launch_shaped<QT, 128>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, plan, ep, s);
 }
 
 }  // namespace
@@ -832,36 +875,36 @@ size_t mmq_partial_bytes(int type, int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_mmq(int type, BlockLayout lay, const uint8_t* W, const int8_t* codes, const float* xs,
                       const int32_t* xsum, float* Y, int32_t* dots, void* scratch, unsigned* counters, int64_t M,
-                      int64_t N, int64_t K, hipStream_t s, const char** name) {
-    if (gemv_q8_applies(type, M, K)) return launch_gemv_q8(type, lay, W, codes, xs, xsum, Y, dots, M, N, K, s, name);
-    if (mmq_kw_applies(type, lay, M, N, K)) return launch_mmq_kw(W, codes, xs, xsum, Y, dots, M, N, K, s, name);
+                      int64_t N, int64_t K, const Epilogue* ep, hipStream_t s, const char** name) {
+    if (gemv_q8_applies(type, M, K)) return launch_gemv_q8(type, lay, W, codes, xs, xsum, Y, dots, M, N, K, ep, s, name);
+    if (mmq_kw_applies(type, lay, M, N, K)) return launch_mmq_kw(W, codes, xs, xsum, Y, dots, M, N, K, ep, s, name);
     float* partial = static_cast<float*>(scratch);
     const bool repacked = lay.off != 0 || (type == kQ6_K && lay.stride != 210);
     switch (type) {
         case kQ8_0:
             *name = repacked ? "mmq<q8_0 repacked>" : "mmq<q8_0>";
-            return launch_typed<kQ8_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, s);
+            return launch_typed<kQ8_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
         case kQ4_K:
             *name = "mmq<q4_K>";
-            return launch_typed<kQ4_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, s);
+            return launch_typed<kQ4_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
         case kQ6_K:
             *name = repacked ? "mmq<q6_K repacked>" : "mmq<q6_K>";
-            return launch_typed<kQ6_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, s);
+            return launch_typed<kQ6_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
         case kQ5_K:
             *name = "mmq<q5_K>";
-            return launch_typed<kQ5_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, s);
+            return launch_typed<kQ5_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
         case kQ4_0:
             *name = "mmq<q4_0>";
-            return launch_typed<kQ4_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, s);
+            return launch_typed<kQ4_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
         case kQ4_1:
             *name = "mmq<q4_1>";
-            return launch_typed<kQ4_1>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, s);
+            return launch_typed<kQ4_1>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
         case kQ5_0:
             *name = "mmq<q5_0>";
-            return launch_typed<kQ5_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, s);
+            return launch_typed<kQ5_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
         case kQ5_1:
             *name = "mmq<q5_1>";
-            return launch_typed<kQ5_1>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, s);
+            return launch_typed<kQ5_1>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
         default: return hipErrorInvalidValue;
     }
 }

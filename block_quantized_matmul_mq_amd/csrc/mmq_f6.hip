@@ -47,6 +47,7 @@
 #include "mmq_common.h"
 #include "mmq_splitk.h"
 #include "mq_device.h"
+#include "mq_epilogue.h"
 #include "mq_internal.h"
 
 namespace mq {
@@ -120,14 +121,14 @@ __device__ __forceinline__ uint32_t weight_piece(int j, int R, int n0) {
 }
 
 // ------------------------------------------------------------------ kernel
-template <bool DUMP>
+template <bool DUMP, class EP>
 __global__ __launch_bounds__(kThreads, 2) void mmq_f6_q4k_kernel(const uint8_t* __restrict__ Wp,
                                                                  const uint8_t* __restrict__ Ap,
                                                                  float* __restrict__ Y, int32_t* __restrict__ dots,
                                                                  float* __restrict__ partial,
                                                                  unsigned* __restrict__ counters, int M, int N, int K,
                                                                  int Mp, int Np, int tiles_m, int full,
-                                                                 int split_tiles, int splits, int total_steps) {
+                                                                 int split_tiles, int splits, int total_steps, EP ep) {
     constexpr int TI = 2, TJ = 2;
 
     // Work split: workgroups [0, full) own whole tiles 0..full-1; the remaining split_tiles
@@ -365,7 +366,10 @@ __global__ __launch_bounds__(kThreads, 2) void mmq_f6_q4k_kernel(const uint8_t* 
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int m = m0 + 64 * wm + 32 * i + mfma32_acc_row(v, g);
-                    if (m < M && n < N) Y[int64_t(m) * N + n] = acc[i][j][v];
+                    if (m < M && n < N) {
+                        const int64_t at = int64_t(m) * N + n;
+                        Y[at] = ep(acc[i][j][v], at, n);
+                    }
                 }
             }
         return;
@@ -392,20 +396,24 @@ __global__ __launch_bounds__(kThreads, 2) void mmq_f6_q4k_kernel(const uint8_t* 
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
                 const int m = m0 + 64 * wm + 32 * i + mfma32_acc_row(v, g);
-                if (m < M && n < N) Y[int64_t(m) * N + n] = y[j * 16 + v];
+                if (m < M && n < N) {
+                    const int64_t at = int64_t(m) * N + n;
+                    Y[at] = ep(y[j * 16 + v], at, n);
+                }
             }
         }
     }
 }
 
-template __global__ void mmq_f6_q4k_kernel<false>(const uint8_t* __restrict__, const uint8_t* __restrict__,
-                                                  float* __restrict__, int32_t* __restrict__, float* __restrict__,
-                                                  unsigned* __restrict__, int, int, int, int, int, int, int, int, int,
-                                                  int);
-template __global__ void mmq_f6_q4k_kernel<true>(const uint8_t* __restrict__, const uint8_t* __restrict__,
-                                                 float* __restrict__, int32_t* __restrict__, float* __restrict__,
-                                                 unsigned* __restrict__, int, int, int, int, int, int, int, int, int,
-                                                 int);
+#define MQ_F6_INSTANCE(DUMP, EP)                                                                                  \
+    template __global__ void mmq_f6_q4k_kernel<DUMP, EP>(const uint8_t* __restrict__, const uint8_t* __restrict__, \
+                                                         float* __restrict__, int32_t* __restrict__,               \
+                                                         float* __restrict__, unsigned* __restrict__, int, int,    \
+                                                         int, int, int, int, int, int, int, int, EP);
+MQ_F6_INSTANCE(false, NoEpilogue)
+MQ_F6_INSTANCE(false, Epilogue)
+MQ_F6_INSTANCE(true, NoEpilogue)
+#undef MQ_F6_INSTANCE
 
 }  // namespace
 
@@ -448,7 +456,8 @@ size_t mmq_f6_partial_bytes(int64_t M, int64_t N, int64_t K) {
 }
 
 hipError_t launch_mmq_f6(const uint8_t* Wp, const uint8_t* Ap, float* Y, int32_t* dots, void* scratch,
-                         unsigned* counters, int64_t M, int64_t N, int64_t K, hipStream_t s, const char** name) {
+                         unsigned* counters, int64_t M, int64_t N, int64_t K, const Epilogue* ep, hipStream_t s,
+                         const char** name) {
     *name = "mmq_f6<q4_K plane>";
     const MmqPlan plan = mmq_f6_plan(M, N, K);
     const int tiles_m = int((M + BM - 1) / BM);
@@ -460,13 +469,17 @@ hipError_t launch_mmq_f6(const uint8_t* Wp, const uint8_t* Ap, float* Y, int32_t
     }
     const int Mp = int(f6_act_rows(M)), Np = int(f6_weight_rows(N));
     if (dots)
-        hipLaunchKernelGGL(mmq_f6_q4k_kernel<true>, dim3(total), dim3(kThreads), 0, s, Wp, Ap, Y, dots, partial,
-                           counters, int(M), int(N), int(K), Mp, Np, tiles_m, plan.full, plan.split_tiles,
-                           plan.splits, plan.steps);
+        hipLaunchKernelGGL((mmq_f6_q4k_kernel<true, NoEpilogue>), dim3(total), dim3(kThreads), 0, s, Wp, Ap, Y, dots,
+                           partial, counters, int(M), int(N), int(K), Mp, Np, tiles_m, plan.full, plan.split_tiles,
+                           plan.splits, plan.steps, NoEpilogue{});
+    else if (ep)
+        hipLaunchKernelGGL((mmq_f6_q4k_kernel<false, Epilogue>), dim3(total), dim3(kThreads), 0, s, Wp, Ap, Y, dots,
+                           partial, counters, int(M), int(N), int(K), Mp, Np, tiles_m, plan.full, plan.split_tiles,
+                           plan.splits, plan.steps, *ep);
     else
-        hipLaunchKernelGGL(mmq_f6_q4k_kernel<false>, dim3(total), dim3(kThreads), 0, s, Wp, Ap, Y, dots, partial,
-                           counters, int(M), int(N), int(K), Mp, Np, tiles_m, plan.full, plan.split_tiles,
-                           plan.splits, plan.steps);
+        hipLaunchKernelGGL((mmq_f6_q4k_kernel<false, NoEpilogue>), dim3(total), dim3(kThreads), 0, s, Wp, Ap, Y, dots,
+                           partial, counters, int(M), int(N), int(K), Mp, Np, tiles_m, plan.full, plan.split_tiles,
+                           plan.splits, plan.steps, NoEpilogue{});
     return hipGetLastError();
 }
 

@@ -36,6 +36,7 @@
 
 #include "mmq_common.h"
 #include "mq_device.h"
+#include "mq_epilogue.h"
 #include "mq_internal.h"
 
 namespace mq {
@@ -107,7 +108,9 @@ __device__ __forceinline__ void scale_min(uint32_t s0, uint32_t s1, uint32_t s2,
     mn = half ? mn_hi : mn_lo;
 }
 
-template <bool DUMP>
+// PRECISE (the products with an epilogue): the min term to f32 precision, tx in three bf16
+// pieces (exact) against mw in two (exact: f16 times 6 bits), in two MFMAs instead of one.
+template <bool DUMP, bool PRECISE>
 struct Step {
     int h;
     int32_t* dots;
@@ -183,10 +186,21 @@ struct Step {
             const int b = 2 * h + i;
             const float dxb = __builtin_bit_cast(float, h ? R.dx[2 + i] : R.dx[i]);
             const int32_t sb = h ? R.sum[2 + i] : R.sum[i];
-            t[i] = bf16_hilo_bits(dxb * float(sb));
+            const float tx = dxb * float(sb);
+            t[i] = PRECISE ? __float_as_uint(tx) : bf16_hilo_bits(tx);
             uint32_t sc, mn;
             scale_min(s0, s1, s2, half, b, sc, mn);
             w[i] = bf16_hilo_bits(-(dmin * float(mn)));
+        }
+        if constexpr (PRECISE) {
+            const Bf16x3 x0 = bf16_split3(t[0]), x1 = bf16_split3(t[1]);
+            const v4i a = {int(x0.hh), int(x0.mm), int(x1.hh), int(x1.mm)}, c = {int(x0.ll), 0, int(x1.ll), 0};
+            const v4i b = {int(w[0]), int(w[0]), int(w[1]), int(w[1])};
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, c), __builtin_bit_cast(v8bf, b),
+                                                          acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b),
+                                                          acc, 0, 0, 0);
+            return;
         }
         const v4i am = {int((t[0] & 0xFFFFu) | (t[0] << 16)), int(t[0] >> 16), int((t[1] & 0xFFFFu) | (t[1] << 16)),
                         int(t[1] >> 16)};
@@ -199,7 +213,7 @@ struct Step {
 // One workgroup of kWaves waves per 32 x 32 output tile; wave w takes K-steps
 // [w S / kWaves, (w + 1) S / kWaves) of the S = K / 128 steps.  Two workgroups fit on a
 // CU (at most 256 registers a lane); the block-dot export keeps more registers instead.
-template <bool DUMP>
+template <bool DUMP, class EP>
 __global__ __launch_bounds__(64 * kWaves, DUMP ? 1 : 2) void mmq_kw_q4k_kernel(const uint8_t* __restrict__ W,
                                                                            const int8_t* __restrict__ codes,
                                                                            const float* __restrict__ xscale,
@@ -207,7 +221,7 @@ __global__ __launch_bounds__(64 * kWaves, DUMP ? 1 : 2) void mmq_kw_q4k_kernel(c
                                                                            float* __restrict__ Y,
                                                                            int32_t* __restrict__ dots, int M, int N,
                                                                            int K, int64_t row_bytes, int tiles_n,
-                                                                           int tiles) {
+                                                                           int tiles, EP ep) {
     __shared__ Partials<DUMP> red;
     // workgroups dealt to one XCD take consecutive tiles: the tiles of one row of tiles
     // share its activation rows
@@ -233,7 +247,7 @@ __global__ __launch_bounds__(64 * kWaves, DUMP ? 1 : 2) void mmq_kw_q4k_kernel(c
     op.vw = uint32_t(min(r, cols - 1) * row_bytes);
     op.vq = op.vw + 16 + 16 * h;
 
-    Step<DUMP> st;
+    Step<DUMP, EP::kIs> st;
     st.h = h;
     st.dots = dots;
     st.N = N;
@@ -289,19 +303,23 @@ __global__ __launch_bounds__(64 * kWaves, DUMP ? 1 : 2) void mmq_kw_q4k_kernel(c
 #pragma unroll
         for (int w = 1; w < kWaves; ++w) y += red[w][v][l];
         const int mr = mfma32_acc_row(v, l >> 5), nc = l & 31;
-        if (mr < rows && nc < cols) Y[int64_t(m0 + mr) * N + n0 + nc] = y;
+        if (mr < rows && nc < cols) {
+            const int64_t at = int64_t(m0 + mr) * N + n0 + nc;
+            Y[at] = ep(y, at, n0 + nc);
+        }
     }
 }
 
 // Explicit instantiations (the launch stubs are otherwise not emitted when the kernels are
 // only named inside the launcher).
-#define MQ_KW_INSTANCE(DUMP)                                                                                  \
-    template __global__ void mmq_kw_q4k_kernel<DUMP>(const uint8_t* __restrict__, const int8_t* __restrict__,  \
+#define MQ_KW_INSTANCE(DUMP, EP)                                                                              \
+    template __global__ void mmq_kw_q4k_kernel<DUMP, EP>(const uint8_t* __restrict__, const int8_t* __restrict__,  \
                                                      const float* __restrict__, const int32_t* __restrict__,   \
                                                      float* __restrict__, int32_t* __restrict__, int, int, int, \
-                                                     int64_t, int, int);
-MQ_KW_INSTANCE(false)
-MQ_KW_INSTANCE(true)
+                                                     int64_t, int, int, EP);
+MQ_KW_INSTANCE(false, NoEpilogue)
+MQ_KW_INSTANCE(false, Epilogue)
+MQ_KW_INSTANCE(true, NoEpilogue)
 #undef MQ_KW_INSTANCE
 
 }  // namespace
@@ -329,17 +347,20 @@ bool mmq_kw_applies(int type, BlockLayout lay, int64_t M, int64_t N, int64_t K) 
 }
 
 hipError_t launch_mmq_kw(const uint8_t* W, const int8_t* codes, const float* xs, const int32_t* xsum, float* Y,
-                         int32_t* dots, int64_t M, int64_t N, int64_t K, hipStream_t s, const char** name) {
+                         int32_t* dots, int64_t M, int64_t N, int64_t K, const Epilogue* ep, hipStream_t s, const char** name) {
     const int tiles_m = int((M + kTile - 1) / kTile), tiles_n = int((N + kTile - 1) / kTile);
     const int tiles = tiles_m * tiles_n;
     const int64_t row_bytes = (K / 256) * 144;
     *name = "mmq_kw<q4_K>";
     if (dots)
-        hipLaunchKernelGGL((mmq_kw_q4k_kernel<true>), dim3(tiles), dim3(64 * kWaves), 0, s, W, codes, xs, xsum, Y,
-                           dots, int(M), int(N), int(K), row_bytes, tiles_n, tiles);
+        hipLaunchKernelGGL((mmq_kw_q4k_kernel<true, NoEpilogue>), dim3(tiles), dim3(64 * kWaves), 0, s, W, codes, xs,
+                           xsum, Y, dots, int(M), int(N), int(K), row_bytes, tiles_n, tiles, NoEpilogue{});
+    else if (ep)
+        hipLaunchKernelGGL((mmq_kw_q4k_kernel<false, Epilogue>), dim3(tiles), dim3(64 * kWaves), 0, s, W, codes, xs,
+                           xsum, Y, dots, int(M), int(N), int(K), row_bytes, tiles_n, tiles, *ep);
     else
-        hipLaunchKernelGGL((mmq_kw_q4k_kernel<false>), dim3(tiles), dim3(64 * kWaves), 0, s, W, codes, xs, xsum, Y,
-                           dots, int(M), int(N), int(K), row_bytes, tiles_n, tiles);
+        hipLaunchKernelGGL((mmq_kw_q4k_kernel<false, NoEpilogue>), dim3(tiles), dim3(64 * kWaves), 0, s, W, codes, xs,
+                           xsum, Y, dots, int(M), int(N), int(K), row_bytes, tiles_n, tiles, NoEpilogue{});
     return hipGetLastError();
 }
 

@@ -13,6 +13,7 @@
 #include <string>
 
 #include "../../include/mq.h"
+#include "mq_epilogue.h"
 #include "mq_internal.h"
 
 namespace mq {
@@ -151,6 +152,11 @@ const DeviceInfo* device_info() {
 
 }  // namespace mq
 
+static_assert(MQ_MOE_MAX_EXPERTS == mq::kMoeMaxExperts && MQ_MOE_MAX_PAIRS == mq::kMoeMaxPairs &&
+              MQ_MOE_MAX_TOPK == mq::kMoeMaxTopk, "mixture-of-experts limits");
+static_assert(MQ_ACT_NONE == mq::kActNone && MQ_ACT_SILU == mq::kActSilu && MQ_ACT_GELU_TANH == mq::kActGeluTanh &&
+              MQ_ACT_GELU_ERF == mq::kActGeluErf && MQ_ACT_RELU == mq::kActRelu, "activation ids");
+
 using namespace mq;
 
 extern "C" {
@@ -199,8 +205,9 @@ int mq_init(int device) {
     // Kernel attributes are set here, once, so that no call ever sets one inside a stream capture.
     e = gemv_set_attributes(lds);
     if (e == hipSuccess) e = gemv_q8_set_attributes(lds);
+    if (e == hipSuccess) e = moe_set_attributes(lds);
     if (e != hipSuccess)
-        return fail(MQ_ERR_DEVICE, "mq_init: setting the GEMV LDS limit to %zu bytes failed: %s", lds,
+        return fail(MQ_ERR_DEVICE, "mq_init: setting the kernels' LDS limit to %zu bytes failed: %s", lds,
                     hipGetErrorName(e));
     if (!info.noalloc_scratch) {
         // This device's copy of the array: its device address, read with the device current
@@ -289,8 +296,8 @@ int mq_quantize_act(const float* X, void* Xq, int64_t M, int64_t K, void* stream
     return launch_status(fn, e, "quantize_act");
 }
 
-int mq_gemv(const void* W, int type, const float* x, float* y, int64_t N, int64_t K, void* stream) {
-    const char* fn = "mq_gemv";
+static int gemv_common(const char* fn, const void* W, int type, const float* x, float* y, int64_t N, int64_t K,
+                       const Epilogue* ep, void* stream) {
     if (!W || !x || !y) return fail(MQ_ERR_ARG, "%s: null pointer (W=%p x=%p y=%p)", fn, W, (const void*)x, (void*)y);
     BlockLayout lay;
     const int base = parse_type(type, lay);
@@ -312,7 +319,7 @@ int mq_gemv(const void* W, int type, const float* x, float* y, int64_t N, int64_
     if (lay.row_tiled) {
         const char* kernel = "gemv_mfma_long<q4_K row-tiled>";
         if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, kernel);
-        hipError_t e = launch_gemv_row_tiled(static_cast<const uint8_t*>(W), x, y, N, K,
+        hipError_t e = launch_gemv_row_tiled(static_cast<const uint8_t*>(W), x, y, N, K, ep,
                                              static_cast<hipStream_t>(stream), &kernel);
         return launch_status(fn, e, kernel);
     }
@@ -321,13 +328,36 @@ int mq_gemv(const void* W, int type, const float* x, float* y, int64_t N, int64_
                     device_info()->lds_per_block);
     const char* kernel = "gemv";
     if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, "gemv");
-    hipError_t e = launch_gemv(type, lay, static_cast<const uint8_t*>(W), x, y, N, K,
+    hipError_t e = launch_gemv(type, lay, static_cast<const uint8_t*>(W), x, y, N, K, ep,
                                static_cast<hipStream_t>(stream), &kernel);
     return launch_status(fn, e, kernel);
 }
 
+// The terms of an epilogue: act in range, each given pointer aligned for f32.
+static int check_epilogue(const char* fn, const float* bias, int act, const float* mul, const float* residual) {
+    if (act < 0 || act >= kActs) return fail(MQ_ERR_ARG, "%s: unknown activation %d", fn, act);
+    if (!aligned(bias, 4) || !aligned(mul, 4) || !aligned(residual, 4))
+        return fail(MQ_ERR_ALIGN, "%s: bias, mul and residual must be 4-byte aligned (bias=%p mul=%p residual=%p)", fn,
+                    (const void*)bias, (const void*)mul, (const void*)residual);
+    return MQ_OK;
+}
+
+int mq_gemv(const void* W, int type, const float* x, float* y, int64_t N, int64_t K, void* stream) {
+    return gemv_common("mq_gemv", W, type, x, y, N, K, nullptr, stream);
+}
+
+int mq_gemv_ep(const void* W, int type, const float* x, float* y, int64_t N, int64_t K, const float* bias, int act,
+               const float* mul, const float* residual, void* stream) {
+    const char* fn = "mq_gemv_ep";
+    const int rc = check_epilogue(fn, bias, act, mul, residual);
+    if (rc) return rc;
+    const Epilogue ep = {bias, mul, residual, act};
+    return gemv_common(fn, W, type, x, y, N, K, &ep, stream);
+}
+
 static int gemm_common(const char* fn, const void* W, int type, const void* Xq, float* Y, int32_t* D,
-                       void* scratch, unsigned* counters, int64_t M, int64_t N, int64_t K, void* stream) {
+                       void* scratch, unsigned* counters, int64_t M, int64_t N, int64_t K, const Epilogue* ep,
+                       void* stream) {
     if (!W || !Xq || (!Y && !D))
         return fail(MQ_ERR_ARG, "%s: null pointer (W=%p Xq=%p out=%p)", fn, W, Xq, Y ? (void*)Y : (void*)D);
     BlockLayout lay;
@@ -355,27 +385,40 @@ static int gemm_common(const char* fn, const void* W, int type, const void* Xq, 
     if (is_plane(lay)) {
         if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, "mmq_f6<q4_K plane>");
         hipError_t e = launch_mmq_f6(static_cast<const uint8_t*>(W), xq + act_f6_offset(M, K), Y, D, scratch, counters,
-                                     M, N, K, static_cast<hipStream_t>(stream), &kernel);
+                                     M, N, K, ep, static_cast<hipStream_t>(stream), &kernel);
         return launch_status(fn, e, kernel);
     }
     if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, "mmq");
     hipError_t e = launch_mmq(type, lay, static_cast<const uint8_t*>(W), reinterpret_cast<const int8_t*>(xq),
                               reinterpret_cast<const float*>(xq + act_scale_offset(M, K)),
                               reinterpret_cast<const int32_t*>(xq + act_sum_offset(M, K)), Yout, D, scratch,
-                              counters, M, N, K, static_cast<hipStream_t>(stream), &kernel);
+                              counters, M, N, K, ep, static_cast<hipStream_t>(stream), &kernel);
     return launch_status(fn, e, kernel);
 }
 
-int mq_gemm(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N, int64_t K, void* scratch,
-            size_t scratch_bytes, void* stream) {
-    const char* fn = "mq_gemm";
+static int gemm_with_scratch(const char* fn, const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N,
+                             int64_t K, const Epilogue* ep, void* scratch, size_t scratch_bytes, void* stream) {
     if (!Y) return fail(MQ_ERR_ARG, "%s: null Y", fn);
     const size_t need = mq_gemm_scratch_bytes(type, M, N, K);
     if (scratch_bytes < need || (need && !scratch))
         return fail(MQ_ERR_SIZE, "%s: scratch of %zu bytes at %p, %zu required", fn, scratch_bytes, scratch, need);
     if (need && !aligned(scratch, 16))
         return fail(MQ_ERR_ALIGN, "%s: scratch must be 16-byte aligned (%p)", fn, scratch);
-    return gemm_common(fn, W, type, Xq, Y, nullptr, need ? scratch : nullptr, nullptr, M, N, K, stream);
+    return gemm_common(fn, W, type, Xq, Y, nullptr, need ? scratch : nullptr, nullptr, M, N, K, ep, stream);
+}
+
+int mq_gemm(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N, int64_t K, void* scratch,
+            size_t scratch_bytes, void* stream) {
+    return gemm_with_scratch("mq_gemm", W, type, Xq, Y, M, N, K, nullptr, scratch, scratch_bytes, stream);
+}
+
+int mq_gemm_ep(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N, int64_t K, const float* bias,
+               int act, const float* mul, const float* residual, void* scratch, size_t scratch_bytes, void* stream) {
+    const char* fn = "mq_gemm_ep";
+    const int rc = check_epilogue(fn, bias, act, mul, residual);
+    if (rc) return rc;
+    const Epilogue ep = {bias, mul, residual, act};
+    return gemm_with_scratch(fn, W, type, Xq, Y, M, N, K, &ep, scratch, scratch_bytes, stream);
 }
 
 int mq_gemm_noalloc(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N, int64_t K,
@@ -394,7 +437,7 @@ int mq_gemm_noalloc(const void* W, int type, const void* Xq, float* Y, int64_t M
     if (rc) return rc;
     uint8_t* base = device_info()->noalloc_scratch;
     return gemm_common(fn, W, type, Xq, Y, nullptr, base + kNoAllocCounterBytes, reinterpret_cast<unsigned*>(base),
-                       M, N, K, stream);
+                       M, N, K, nullptr, stream);
 }
 
 size_t mq_debug_lds_bytes(int what, int type, int64_t K) {
@@ -420,7 +463,112 @@ int mq_debug_gemm_blockdots(const void* W, int type, const void* Xq, int32_t* D,
                             void* stream) {
     const char* fn = "mq_debug_gemm_blockdots";
     if (!D) return fail(MQ_ERR_ARG, "%s: null D", fn);
-    return gemm_common(fn, W, type, Xq, nullptr, D, nullptr, nullptr, M, N, K, stream);
+    return gemm_common(fn, W, type, Xq, nullptr, D, nullptr, nullptr, M, N, K, nullptr, stream);
+}
+
+size_t mq_moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K) {
+    if (M <= 0 || topk <= 0 || F <= 0 || K <= 0 || F > MQ_MAX_K || K > MQ_MAX_K || M > MQ_MOE_MAX_PAIRS ||
+        topk > MQ_MOE_MAX_PAIRS || M * topk > MQ_MOE_MAX_PAIRS)
+        return 0;
+    return moe_scratch_bytes(M * topk, F, K);
+}
+
+int mq_moe_ffn(const void* Wg, const void* Wu, int gu_type, const void* Wd, int d_type, const float* X,
+               const int32_t* ids, const float* wts, const float* residual, float* Y, int64_t M, int64_t topk,
+               int64_t E, int64_t F, int64_t K, int act, void* scratch, size_t scratch_bytes, void* stream) {
+    const char* fn = "mq_moe_ffn";
+    if (!Wg || !Wu || !Wd || !X || !ids || !wts || !Y || !scratch)
+        return fail(MQ_ERR_ARG, "%s: null pointer (Wg=%p Wu=%p Wd=%p X=%p ids=%p wts=%p Y=%p scratch=%p)", fn, Wg, Wu, Wd,
+                    (const void*)X, (const void*)ids, (const void*)wts, (void*)Y, scratch);
+    if (act < 0 || act >= kActs) return fail(MQ_ERR_ARG, "%s: unknown activation %d", fn, act);
+    MoeLayer l = {};
+    l.gu_type = parse_type(gu_type, l.gu_layout);
+    l.d_type = parse_type(d_type, l.d_layout);
+    if (l.gu_type == 0 || is_plane(l.gu_layout) || l.gu_layout.row_tiled)
+        return fail(MQ_ERR_TYPE, "%s: unsupported gate / up weight type %d", fn, gu_type);
+    if (l.d_type == 0 || is_plane(l.d_layout) || l.d_layout.row_tiled)
+        return fail(MQ_ERR_TYPE, "%s: unsupported down weight type %d", fn, d_type);
+    int rc = check_weight_shape(fn, l.gu_type, F, K);
+    if (rc == MQ_OK) rc = check_weight_shape(fn, l.d_type, K, F);
+    if (rc) return rc;
+    if (F > MQ_MAX_K || K > MQ_MAX_K)
+        return fail(MQ_ERR_SHAPE, "%s: F=%lld K=%lld exceeds %d", fn, (long long)F, (long long)K, MQ_MAX_K);
+    if (M <= 0 || topk <= 0 || E <= 0)
+        return fail(MQ_ERR_ARG, "%s: M=%lld topk=%lld E=%lld must be positive", fn, (long long)M, (long long)topk,
+                    (long long)E);
+    if (E > MQ_MOE_MAX_EXPERTS)
+        return fail(MQ_ERR_SHAPE, "%s: E=%lld exceeds %d", fn, (long long)E, MQ_MOE_MAX_EXPERTS);
+    if (M > MQ_MOE_MAX_PAIRS || topk > MQ_MOE_MAX_PAIRS || M * topk > MQ_MOE_MAX_PAIRS)
+        return fail(MQ_ERR_SHAPE, "%s: M=%lld topk=%lld are more than %d (token, choice) pairs", fn, (long long)M,
+                    (long long)topk, MQ_MOE_MAX_PAIRS);
+    const size_t need = moe_scratch_bytes(M * topk, F, K);
+    if (scratch_bytes < need)
+        return fail(MQ_ERR_SIZE, "%s: scratch of %zu bytes, %zu required", fn, scratch_bytes, need);
+    if (!aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(Wd, 16) || !aligned(X, 16) || !aligned(Y, 16) ||
+        !aligned(residual, 16) || !aligned(scratch, 16) || !aligned(ids, 4) || !aligned(wts, 4))
+        return fail(MQ_ERR_ALIGN, "%s: weights, X, residual, Y and scratch must be 16-byte, ids and wts 4-byte aligned",
+                    fn);
+    rc = check_ready(fn);
+    if (rc) return rc;
+    l.Wg = static_cast<const uint8_t*>(Wg);
+    l.Wu = static_cast<const uint8_t*>(Wu);
+    l.Wd = static_cast<const uint8_t*>(Wd);
+    l.X = X;
+    l.ids = ids;
+    l.wts = wts;
+    l.residual = residual;
+    l.Y = Y;
+    l.scratch = scratch;
+    l.M = M;
+    l.topk = topk;
+    l.E = E;
+    l.F = F;
+    l.K = K;
+    l.act = act;
+    l.cu_count = device_info()->cu_count;
+    const char* kernel = "moe_ffn";
+    if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, kernel);
+    hipError_t e = launch_moe_ffn(l, static_cast<hipStream_t>(stream), &kernel);
+    return launch_status(fn, e, kernel);
+}
+
+size_t mq_moe_route_scratch_bytes(int64_t M, int64_t K, int64_t E) {
+    if (M <= 0 || K <= 0 || E <= 0 || K % 32 != 0 || M > MQ_MAX_M || K > MQ_MAX_K || E > MQ_MOE_MAX_EXPERTS) return 0;
+    return moe_route_scratch_bytes(M, K, E);
+}
+
+int mq_moe_route(const float* X, const float* Wr, const float* bias, int32_t* ids, float* wts, int64_t M, int64_t K,
+                 int64_t E, int64_t topk, int score, int norm, float scale, void* scratch, size_t scratch_bytes,
+                 void* stream) {
+    const char* fn = "mq_moe_route";
+    if (!X || !Wr || !ids || !wts || !scratch)
+        return fail(MQ_ERR_ARG, "%s: null pointer (X=%p Wr=%p ids=%p wts=%p scratch=%p)", fn, (const void*)X,
+                    (const void*)Wr, (void*)ids, (void*)wts, scratch);
+    if (M <= 0 || K <= 0 || E <= 0 || topk <= 0)
+        return fail(MQ_ERR_ARG, "%s: M=%lld K=%lld E=%lld topk=%lld must be positive", fn, (long long)M, (long long)K,
+                    (long long)E, (long long)topk);
+    if (score != MQ_SCORE_SOFTMAX && score != MQ_SCORE_SIGMOID)
+        return fail(MQ_ERR_ARG, "%s: unknown score %d", fn, score);
+    if (K % 32 != 0) return fail(MQ_ERR_SHAPE, "%s: K=%lld is not a multiple of 32", fn, (long long)K);
+    if (M > MQ_MAX_M || K > MQ_MAX_K || E > MQ_MOE_MAX_EXPERTS)
+        return fail(MQ_ERR_SHAPE, "%s: M=%lld K=%lld E=%lld exceeds M<=%d K<=%d E<=%d", fn, (long long)M, (long long)K,
+                    (long long)E, MQ_MAX_M, MQ_MAX_K, MQ_MOE_MAX_EXPERTS);
+    if (topk > E || topk > MQ_MOE_MAX_TOPK)
+        return fail(MQ_ERR_SHAPE, "%s: topk=%lld exceeds E=%lld or %d", fn, (long long)topk, (long long)E,
+                    MQ_MOE_MAX_TOPK);
+    const size_t need = moe_route_scratch_bytes(M, K, E);
+    if (scratch_bytes < need)
+        return fail(MQ_ERR_SIZE, "%s: scratch of %zu bytes, %zu required", fn, scratch_bytes, need);
+    if (!aligned(X, 16) || !aligned(Wr, 16) || !aligned(scratch, 16) || !aligned(bias, 4) || !aligned(ids, 4) ||
+        !aligned(wts, 4))
+        return fail(MQ_ERR_ALIGN, "%s: X, Wr and scratch must be 16-byte, bias, ids and wts 4-byte aligned", fn);
+    int rc = check_ready(fn);
+    if (rc) return rc;
+    const MoeRoute r = {X, Wr, bias, ids, wts, scratch, M, K, E, topk, score, norm != 0, scale};
+    const char* kernel = "moe_route";
+    if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, kernel);
+    hipError_t e = launch_moe_route(r, static_cast<hipStream_t>(stream), &kernel);
+    return launch_status(fn, e, kernel);
 }
 
 int mq_repack(const void* W, int type, int64_t N, int64_t K, size_t nbytes, void* Wr, size_t wr_bytes,

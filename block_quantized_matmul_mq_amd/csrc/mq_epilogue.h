@@ -1,0 +1,72 @@
+// Activations, and the epilogue that mq_gemv_ep and mq_gemm_ep apply where a kernel stores its
+// result:  y[m][n] = act(acc + bias[n]) * mul[m][n] + residual[m][n]   (absent terms are left out).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mq {
+
+constexpr int kActNone = 0;
+constexpr int kActSilu = 1;
+constexpr int kActGeluTanh = 2;
+constexpr int kActGeluErf = 3;
+constexpr int kActRelu = 4;
+constexpr int kActs = 5;
+
+// (act is uniform: one branch.  Both gelus in the forms that lose nothing to cancellation for
+// negative v: 1 + tanh(u) = 2 / (1 + e^-2u), 1 + erf(t) = erfc(-t).)
+__device__ __forceinline__ float activate(float v, int act) {
+    switch (act) {
+        case kActSilu: return v / (1.0f + expf(-v));
+        case kActGeluTanh: return v / (1.0f + expf(-1.5957691216057308f * fmaf(0.044715f * v, v * v, v)));
+        case kActGeluErf: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+        case kActRelu: return fmaxf(v, 0.0f);
+        default: return v;
+    }
+}
+
+// The products without an epilogue.
+struct NoEpilogue {
+    static constexpr bool kIs = false;
+    __device__ __forceinline__ float operator()(float acc, int64_t, int) const { return acc; }
+};
+
+// at: m N + n.  mul and residual may be the output itself: an element is read by the thread
+// that then writes it.
+struct Epilogue {
+    static constexpr bool kIs = true;
+    const float* bias;
+    const float* mul;
+    const float* residual;
+    int act;
+    __device__ __forceinline__ float operator()(float acc, int64_t at, int n) const {
+        float v = bias ? acc + bias[n] : acc;
+        v = activate(v, act);
+        if (mul) v *= mul[at];
+        if (residual) v += residual[at];
+        return v;
+    }
+};
+
+// The epilogue argument of a kernel launched through an argument array (ep null: NoEpilogue's,
+// one byte that nothing reads).
+inline void* epilogue_arg(const Epilogue* ep) {
+    static NoEpilogue none;
+    return ep ? const_cast<void*>(static_cast<const void*>(ep)) : static_cast<void*>(&none);
+}
+
+// An f32 (its bits) as three bf16 pieces of 8 bits each, high + mid + low exactly; each piece
+// twice in a dword (an MFMA operand meets it with both halves of a hi | lo pair).
+struct Bf16x3 {
+    uint32_t hh, mm, ll;
+};
+__device__ __forceinline__ Bf16x3 bf16_split3(uint32_t bits) {
+    const uint32_t h = bits & 0xFFFF0000u;
+    const float r = __uint_as_float(bits) - __uint_as_float(h);
+    const uint32_t m = __float_as_uint(r) & 0xFFFF0000u;
+    const uint32_t l = __float_as_uint(r - __uint_as_float(m));
+    return Bf16x3{h | (h >> 16), m | (m >> 16), (l & 0xFFFF0000u) | (l >> 16)};
+}
+
+}  // namespace mq

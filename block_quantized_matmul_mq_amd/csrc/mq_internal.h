@@ -61,6 +61,9 @@ struct DeviceInfo {
 };
 const DeviceInfo* device_info();  // null if mq_init has not succeeded on the current device
 
+// The epilogue of the products (mq_epilogue.h); a null pointer to a launcher: none.
+struct Epilogue;
+
 // How weight blocks are stored: bytes per block slot and the offset of the GGUF block in
 // its slot.  The GGUF payload itself is {34, 0} (Q8_0), {144, 0} (Q4_K), {210, 0} (Q6_K);
 // mq_repack writes Q8_0 as {36, 2} and Q6_K as {224, 0}.
@@ -83,8 +86,8 @@ inline size_t row_tiled_bytes(int64_t N, int64_t K) {
 }
 hipError_t launch_repack_q4k_row_tiled(const uint8_t* W, uint8_t* Wr, int64_t N, int64_t K, hipStream_t s);
 // The long-row Q4_K GEMV on the row-tiled layout (gemv_mfma.hip): one group per workgroup.
-hipError_t launch_gemv_row_tiled(const uint8_t* W, const float* x, float* y, int64_t N, int64_t K, hipStream_t s,
-                                 const char** kernel_name);
+hipError_t launch_gemv_row_tiled(const uint8_t* W, const float* x, float* y, int64_t N, int64_t K,
+                                 const Epilogue* ep, hipStream_t s, const char** kernel_name);
 
 // Kernel launchers: they enqueue on `s` and return the launch status (hipGetLastError read
 // right after the launch).  Arguments are validated by the callers in mq_api.hip.
@@ -97,28 +100,28 @@ size_t fixed_lds_bytes(int type, int64_t K);
 size_t mmq_smem_bytes(int type, int bm);
 hipError_t gemv_set_attributes(size_t lds_limit);
 hipError_t launch_gemv(int type, BlockLayout layout, const uint8_t* W, const float* x, float* y, int64_t N,
-                       int64_t K, hipStream_t s, const char** kernel_name);
+                       int64_t K, const Epilogue* ep, hipStream_t s, const char** kernel_name);
 // Q4_K GEMV with the dot products on int8 matrix cores and the weights streamed through
 // LDS, for wide matrices (gemv_mfma.hip).
 bool gemv_mfma_applies(int type, int64_t N, int64_t K, int cu_count);
 hipError_t launch_gemv_mfma(const uint8_t* W, const float* x, float* y, int64_t N, int64_t K, int cu_count,
-                            hipStream_t s, const char** kernel_name);
+                            const Epilogue* ep, hipStream_t s, const char** kernel_name);
 // GEMV on int8 matrix cores with whole 16-row tiles streamed through LDS, for wide
 // matrices of the other block types in the GGUF layout (gemv_mfma.hip).
 bool gemv_tiled_applies(int type, BlockLayout layout, const uint8_t* W, int64_t N, int64_t K, int cu_count);
 hipError_t launch_gemv_tiled(int type, const uint8_t* W, const float* x, float* y, int64_t N, int64_t K,
-                             int cu_count, hipStream_t s, const char** kernel_name);
+                             int cu_count, const Epilogue* ep, hipStream_t s, const char** kernel_name);
 // GEMV on int8 matrix cores with per-wave items, for wide Q8_0 and Q4_0 matrices in the
 // GGUF layout (gemv_mfma.hip).
 bool gemv_wide_applies(int type, BlockLayout layout, const uint8_t* W, int64_t N, int64_t K, int cu_count);
 hipError_t launch_gemv_wide(int type, const uint8_t* W, const float* x, float* y, int64_t N, int64_t K,
-                            int cu_count, hipStream_t s, const char** kernel_name);
+                            int cu_count, const Epilogue* ep, hipStream_t s, const char** kernel_name);
 // mq_gemm for M <= 8 q8 rows on the same whole-tile stream (Q6_K, wide, GGUF layout).
 bool gemv_q8_tiled_applies(int type, BlockLayout layout, const uint8_t* W, const int8_t* codes, int64_t M,
                            int64_t N, int64_t K, int cu_count);
 hipError_t launch_gemv_q8_tiled(int type, const uint8_t* W, const int8_t* codes, const float* xs, float* Y,
-                                int32_t* dots, int64_t M, int64_t N, int64_t K, int cu_count, hipStream_t s,
-                                const char** kernel_name);
+                                int32_t* dots, int64_t M, int64_t N, int64_t K, int cu_count, const Epilogue* ep,
+                                hipStream_t s, const char** kernel_name);
 // MMQ work split over bm x 128 (int8) or 128 x 128 (fp6) output tiles: the first `full`
 // tiles are computed whole; each of the remaining `split_tiles` is cut into `splits` ranges
 // of whole K-steps, whose f32 partial tiles go to scratch and are summed in the same launch
@@ -141,14 +144,15 @@ size_t mmq_partial_bytes(int type, int64_t M, int64_t N, int64_t K);
 // partial tiles, or null when scratch holds both (mmq_splitk.h's layout).
 hipError_t launch_mmq(int type, BlockLayout layout, const uint8_t* W, const int8_t* codes, const float* scales,
                       const int32_t* sums, float* Y, int32_t* dots, void* scratch, unsigned* counters, int64_t M,
-                      int64_t N, int64_t K, hipStream_t s, const char** kernel_name);
+                      int64_t N, int64_t K, const Epilogue* ep, hipStream_t s, const char** kernel_name);
 // Q4_K (GGUF layout) with few output tiles: one 32 x 32 tile per workgroup, its K range
 // split over the workgroup's waves (mmq_kw.hip); taken by launch_mmq whenever
 // mmq_kw_applies.  It needs no scratch.
 bool mmq_kw_applies(int type, BlockLayout layout, int64_t M, int64_t N, int64_t K);
 size_t mmq_kw_lds_bytes();
 hipError_t launch_mmq_kw(const uint8_t* W, const int8_t* codes, const float* scales, const int32_t* sums, float* Y,
-                         int32_t* dots, int64_t M, int64_t N, int64_t K, hipStream_t s, const char** kernel_name);
+                         int32_t* dots, int64_t M, int64_t N, int64_t K, const Epilogue* ep, hipStream_t s,
+                         const char** kernel_name);
 // Q4_K in the MMQ plane (mq_repack's layout): block dots on the fp6 matrix units from the
 // activation plane's fp6 section (mmq_f6.hip).  Any M.
 MmqPlan mmq_f6_plan(int64_t M, int64_t N, int64_t K);
@@ -156,7 +160,8 @@ size_t mmq_f6_scratch_bytes(int64_t M, int64_t N, int64_t K);
 size_t mmq_f6_partial_bytes(int64_t M, int64_t N, int64_t K);
 size_t mmq_f6_lds_bytes();
 hipError_t launch_mmq_f6(const uint8_t* Wp, const uint8_t* Ap, float* Y, int32_t* dots, void* scratch,
-                         unsigned* counters, int64_t M, int64_t N, int64_t K, hipStream_t s, const char** name);
+                         unsigned* counters, int64_t M, int64_t N, int64_t K, const Epilogue* ep, hipStream_t s,
+                         const char** name);
 // mq_repack of Q4_K: the GGUF payload -> the MMQ plane (repack.hip).
 hipError_t launch_repack_q4k_plane(const uint8_t* W, uint8_t* Wp, int64_t N, int64_t K, hipStream_t s);
 // mq_gemm for M <= kGemvQ8MaxRows: a multi-row GEMV over the quantized activation plane
@@ -167,7 +172,44 @@ bool gemv_q8_applies(int type, int64_t M, int64_t K);
 hipError_t gemv_q8_set_attributes(size_t lds_limit);
 hipError_t launch_gemv_q8(int type, BlockLayout lay, const uint8_t* W, const int8_t* codes, const float* scales,
                           const int32_t* sums, float* Y, int32_t* dots, int64_t M, int64_t N, int64_t K,
-                          hipStream_t s, const char** kernel_name);
+                          const Epilogue* ep, hipStream_t s, const char** kernel_name);
+// mq_moe_ffn (moe.hip): at most kMoeMaxPairs (token, choice) pairs and kMoeMaxExperts experts;
+// up to kMoeFewPairs pairs take the kernels that exchange nothing between workgroups.
+constexpr int kMoeMaxExperts = 512;
+constexpr int kMoeMaxPairs = 4096;
+constexpr int kMoeFewPairs = 32;
+constexpr int kMoeMaxTopk = 64;   // choices per token of mq_moe_route (a lane each)
+struct MoeLayer {
+    const uint8_t *Wg, *Wu, *Wd;
+    int gu_type, d_type;
+    BlockLayout gu_layout, d_layout;
+    const float* X;
+    const int32_t* ids;
+    const float* wts;
+    const float* residual;
+    float* Y;
+    void* scratch;
+    int64_t M, topk, E, F, K;
+    int act;
+    int cu_count;
+};
+bool moe_few_pairs(int64_t pairs);
+size_t moe_scratch_bytes(int64_t pairs, int64_t F, int64_t K);
+hipError_t moe_set_attributes(size_t lds_limit);
+hipError_t launch_moe_ffn(const MoeLayer& layer, hipStream_t s, const char** kernel_name);
+// mq_moe_route (moe_route.hip)
+struct MoeRoute {
+    const float *X, *Wr, *bias;
+    int32_t* ids;
+    float* wts;
+    void* scratch;
+    int64_t M, K, E, topk;
+    int score;
+    bool norm;
+    float scale;
+};
+size_t moe_route_scratch_bytes(int64_t M, int64_t K, int64_t E);
+hipError_t launch_moe_route(const MoeRoute& r, hipStream_t s, const char** kernel_name);
 // mq_repack: every `in_bytes`-byte block of W into a `slot_bytes`-byte slot of Wr at offset
 // `off`, the rest of the slot zero (repack.hip).
 hipError_t launch_repack(const uint8_t* W, uint8_t* Wr, int64_t blocks, int in_bytes, int slot_bytes, int off,

@@ -21,6 +21,10 @@ Q6_K = 14
 REPACKED = 0x100   # OR-ed into Q8_0 / Q6_K / Q4_K: weights in the layout mq_repack writes
 ROW_TILED = 0x200  # OR-ed into Q4_K: its row-tiled layout (long-row GEMV), from repack(.., Q4_K | ROW_TILED, ..)
 
+# Activations of gemv_ep / gemm_ep / moe_ffn and router scores of moe_route (include/mq.h)
+ACT_NONE, ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF, ACT_RELU = range(5)
+SCORE_SOFTMAX, SCORE_SIGMOID = range(2)
+
 MQ_OK = 0
 ERRORS = {
     -1: "MQ_ERR_ARG", -2: "MQ_ERR_SHAPE", -3: "MQ_ERR_TYPE", -4: "MQ_ERR_SIZE",
@@ -45,6 +49,22 @@ _SIGNATURES = {
     "mq_gemm": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                ctypes.c_size_t, ctypes.c_void_p]),
+    "mq_gemv_ep": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                  ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p]),
+    "mq_gemm_ep": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                  ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mq_moe_route_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
+    "mq_moe_route": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                    ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                    ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t,
+                                    ctypes.c_void_p]),
+    "mq_moe_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
+    "mq_moe_ffn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_int,
+                                  ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                  ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "mq_debug_lds_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int64]),
     "mq_gemm_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]),
@@ -317,3 +337,151 @@ def gemm_blockdots(W, qtype, Xq, M, N, K, D=None, stream=None):
     _check(load().mq_debug_gemm_blockdots(ctypes.c_void_p(W.data_ptr()), qtype, ctypes.c_void_p(Xq.data_ptr()),
                                           ctypes.c_void_p(D.data_ptr()), M, N, K, _stream(stream)))
     return D
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _terms(fn, M, N, bias, mul, residual):
+    """The epilogue's tensors that are given, checked."""
+    given = []
+    for t, numel, name in ((bias, N, "bias"), (mul, M * N, "mul"), (residual, M * N, "residual")):
+        if t is not None:
+            _f32(t, numel, fn, name)
+            given.append(t)
+    return given
+
+
+def gemv_ep(W, qtype, x, N, K, bias=None, act=ACT_NONE, mul=None, residual=None, y=None, stream=None):
+    """y[N] = act(deq(W) @ x + bias) * mul + residual, one launch (bias, mul, residual: f32 [N] or None;
+    y may be mul or residual)."""
+    import torch
+    _weights(W, qtype, N, K, "gemv_ep")
+    _f32(x, K, "gemv_ep", "x")
+    given = _terms("gemv_ep", 1, N, bias, mul, residual)
+    if y is None:
+        y = torch.empty(N, dtype=torch.float32, device=x.device)
+    else:
+        _f32(y, N, "gemv_ep", "y")
+    _same_device("gemv_ep", W, x, y, *given)
+    _check(load().mq_gemv_ep(W.data_ptr(), qtype, x.data_ptr(), y.data_ptr(), N, K, _ptr(bias), act, _ptr(mul),
+                             _ptr(residual), _stream(stream)))
+    return y
+
+
+def gemm_ep(W, qtype, Xq, M, N, K, bias=None, act=ACT_NONE, mul=None, residual=None, Y=None, scratch=None,
+            stream=None):
+    """Y[M, N] = act(product + bias) * mul + residual, the product of gemm (bias: f32 [N]; mul, residual:
+    f32 [M, N]; each may be None; Y may be mul or residual)."""
+    import torch
+    _weights(W, qtype, N, K, "gemm_ep")
+    _act_plane(Xq, M, K, "gemm_ep")
+    given = _terms("gemm_ep", M, N, bias, mul, residual)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=torch.float32, device=Xq.device)
+    else:
+        _f32(Y, M * N, "gemm_ep", "Y")
+    need = gemm_scratch_bytes(qtype, M, N, K)
+    if scratch is None and need:
+        scratch = torch.zeros(need, dtype=torch.uint8, device=Xq.device)
+    if scratch is not None:
+        _buffer(scratch, need, "gemm_ep", "scratch")
+        given.append(scratch)
+    _same_device("gemm_ep", W, Xq, Y, *given)
+    _check(load().mq_gemm_ep(W.data_ptr(), qtype, Xq.data_ptr(), Y.data_ptr(), M, N, K, _ptr(bias), act, _ptr(mul),
+                             _ptr(residual), _ptr(scratch), 0 if scratch is None else _nbytes(scratch),
+                             _stream(stream)))
+    return Y
+
+
+def _i32(t, numel, fn, name):
+    import torch
+    if t.dtype != torch.int32:
+        _refuse(-1, fn, f"{name} must be int32, not {t.dtype}")
+    _contiguous(t, fn, name)
+    if t.numel() != numel:
+        _refuse(-4, fn, f"{name} has {t.numel()} elements, {numel} expected")
+
+
+def _rows(X, fn):
+    if X.dim() != 2:
+        _refuse(-1, fn, f"X must be 2-D [M, K], not {tuple(X.shape)}")
+    return X.shape
+
+
+def moe_route_scratch_bytes(M, K, E):
+    return load().mq_moe_route_scratch_bytes(M, K, E)
+
+
+def moe_route(X, Wr, topk, bias=None, score=SCORE_SOFTMAX, norm=True, scale=1.0, ids=None, wts=None, scratch=None,
+              stream=None):
+    """(ids int32 [M, topk], wts f32 [M, topk]) of tokens X (f32 [M, K]) by router weights Wr (f32 [E, K]);
+    bias: f32 [E], added to the scores for the choice only.  scratch: moe_route_scratch_bytes(M, K, E) bytes,
+    zero before its first use."""
+    import torch
+    M, K = _rows(X, "moe_route")
+    E = Wr.shape[0]
+    _f32(X, M * K, "moe_route", "X")
+    _f32(Wr, E * K, "moe_route", "Wr")
+    need = moe_route_scratch_bytes(M, K, E)
+    if scratch is None:
+        scratch = torch.zeros(max(need, 16), dtype=torch.uint8, device=X.device)
+    else:
+        _buffer(scratch, need, "moe_route", "scratch")
+    tensors = [X, Wr, scratch]
+    if bias is not None:
+        _f32(bias, E, "moe_route", "bias")
+        tensors.append(bias)
+    if ids is None:
+        ids = torch.empty((M, topk), dtype=torch.int32, device=X.device)
+    else:
+        _i32(ids, M * topk, "moe_route", "ids")
+    if wts is None:
+        wts = torch.empty((M, topk), dtype=torch.float32, device=X.device)
+    else:
+        _f32(wts, M * topk, "moe_route", "wts")
+    _same_device("moe_route", ids, wts, *tensors)
+    _check(load().mq_moe_route(X.data_ptr(), Wr.data_ptr(), _ptr(bias), ids.data_ptr(), wts.data_ptr(), M, K, E, topk,
+                               score, int(norm), scale, scratch.data_ptr(), _nbytes(scratch), _stream(stream)))
+    return ids, wts
+
+
+def moe_scratch_bytes(M, topk, F, K):
+    return load().mq_moe_scratch_bytes(M, topk, F, K)
+
+
+def moe_ffn(Wg, Wu, gu_type, Wd, d_type, X, ids, wts, E, F, act=ACT_SILU, residual=None, Y=None, scratch=None,
+            stream=None):
+    """Y[M, K] = residual + sum_j wts[:, j] * down_e(act(gate_e(X)) * up_e(X)), e = ids[:, j]: a
+    mixture-of-experts feed-forward layer for a few tokens.  Wg, Wu: E matrices of F x K weights, Wd: E of
+    K x F (uint8 payloads); ids int32 and wts f32 [M, topk].  scratch: moe_scratch_bytes(M, topk, F, K) bytes."""
+    import torch
+    M, K = _rows(X, "moe_ffn")
+    _f32(X, M * K, "moe_ffn", "X")
+    _weights(Wg, gu_type, E * F, K, "moe_ffn")
+    _weights(Wu, gu_type, E * F, K, "moe_ffn")
+    _weights(Wd, d_type, E * K, F, "moe_ffn")
+    if ids.dim() != 2 or ids.shape[0] != M:
+        _refuse(-1, "moe_ffn", f"ids must be [M, topk] with M={M}, not {tuple(ids.shape)}")
+    topk = ids.shape[1]
+    _i32(ids, M * topk, "moe_ffn", "ids")
+    _f32(wts, M * topk, "moe_ffn", "wts")
+    tensors = [Wg, Wu, Wd, X, ids, wts]
+    if residual is not None:
+        _f32(residual, M * K, "moe_ffn", "residual")
+        tensors.append(residual)
+    if Y is None:
+        Y = torch.empty((M, K), dtype=torch.float32, device=X.device)
+    else:
+        _f32(Y, M * K, "moe_ffn", "Y")
+    need = moe_scratch_bytes(M, topk, F, K)
+    if scratch is None:
+        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
+    else:
+        _buffer(scratch, need, "moe_ffn", "scratch")
+    _same_device("moe_ffn", Y, scratch, *tensors)
+    _check(load().mq_moe_ffn(Wg.data_ptr(), Wu.data_ptr(), gu_type, Wd.data_ptr(), d_type, X.data_ptr(), ids.data_ptr(),
+                             wts.data_ptr(), _ptr(residual), Y.data_ptr(), M, topk, E, F, K, act, scratch.data_ptr(),
+                             _nbytes(scratch), _stream(stream)))
+    return Y

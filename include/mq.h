@@ -114,10 +114,24 @@ extern "C" {
 #define MQ_ERR_LAUNCH (-7) /* a kernel launch was refused                     */
 #define MQ_ERR_NOINIT (-8) /* mq_init has not succeeded on the current device */
 
+/* Activations of the epilogues and of mq_moe_ffn. */
+#define MQ_ACT_NONE 0      /* v                                                          */
+#define MQ_ACT_SILU 1      /* v / (1 + e^-v)                                             */
+#define MQ_ACT_GELU_TANH 2 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2          */
+#define MQ_ACT_GELU_ERF 3  /* v (1 + erf(v / sqrt 2)) / 2                                */
+#define MQ_ACT_RELU 4      /* max(v, 0)                                                  */
+
+/* Router scores of mq_moe_route. */
+#define MQ_SCORE_SOFTMAX 0
+#define MQ_SCORE_SIGMOID 1
+
 /* Upper bounds accepted by the calls (sizes beyond them are MQ_ERR_SHAPE). */
 #define MQ_MAX_K 32768          /* inputs per row                 */
 #define MQ_MAX_N (1 << 24)      /* output rows                    */
 #define MQ_MAX_M (1 << 20)      /* activation rows for mq_gemm    */
+#define MQ_MOE_MAX_EXPERTS 512  /* experts of a layer             */
+#define MQ_MOE_MAX_PAIRS 4096   /* M * topk of mq_moe_ffn         */
+#define MQ_MOE_MAX_TOPK 64      /* choices per token of mq_moe_route */
 
 /*
  * mq_init -- select `device`, check that it is gfx950, record its compute-unit
@@ -251,6 +265,73 @@ size_t mq_gemm_scratch_bytes(int type, int64_t M, int64_t N, int64_t K);
 int mq_gemm(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N, int64_t K,
             void* scratch, size_t scratch_bytes, void* stream);
 
+/*
+ * mq_gemv_ep / mq_gemm_ep -- the products with an epilogue in the launch that computes them:
+ *   y[m][n] = act(acc[m][n] + bias[n]) * mul[m][n] + residual[m][n]
+ * with acc the product of mq_gemv (M = 1) or mq_gemm and act an MQ_ACT_* id.  bias (N f32),
+ * mul and residual (M x N f32, row-major, as Y) are device memory or NULL; a NULL term is left
+ * out.  Everything else -- types and layouts, shapes, limits, the accuracy of acc, the
+ * quantized plane Xq, scratch (mq_gemm_scratch_bytes), errors -- is as for mq_gemv and mq_gemm.
+ * mul and residual may be the output itself (the residual stream updated in place), or the
+ * same buffer; no input may overlap the output otherwise.  MQ_ERR_ARG for an unknown act.
+ * So a gated feed-forward layer takes three products and no other launch:
+ *   u = mq_gemv(Wup), h = mq_gemv_ep(Wgate, act = MQ_ACT_SILU, mul = u),
+ *   y = mq_gemv_ep(Wdown, h, residual = y).
+ * The min term of Q4_K, Q5_K, Q4_1 and Q5_1 on the int8 kernels is formed to f32 precision
+ * here (mq_gemm forms it to 2^-16), so an mq_gemm_ep without terms agrees with mq_gemm to
+ * mq_gemm's accuracy, for those types not bit for bit; the other types' acc are the same bits.
+ */
+int mq_gemv_ep(const void* W, int type, const float* x, float* y, int64_t N, int64_t K, const float* bias, int act,
+               const float* mul, const float* residual, void* stream);
+int mq_gemm_ep(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N, int64_t K, const float* bias,
+               int act, const float* mul, const float* residual, void* scratch, size_t scratch_bytes, void* stream);
+
+/*
+ * mq_moe_route -- the router of a mixture of experts, for M tokens X (f32 [M][K]) and router
+ * weights Wr (f32 [E][K]):
+ *   z[m][e] = sum_k X[m][k] Wr[e][k]           (summed in f64)
+ *   p = softmax of z[m] over the E experts (MQ_SCORE_SOFTMAX), or 1 / (1 + e^-z) (MQ_SCORE_SIGMOID)
+ *   ids[m][0..topk-1] = the topk experts of largest z, or of largest p + bias when bias (f32 [E],
+ *     a selection bias that does not enter the weights) is not NULL, in falling order; of equal
+ *     ones the lower index first, a NaN after every number
+ *   wts[m][j] = scale * p[ids[m][j]], divided by the sum of the topk chosen p when norm != 0.
+ * ids int32 and wts f32, [M][topk], as mq_moe_ffn reads them.  K % 32 == 0; 1 <= topk <= E and
+ * <= MQ_MOE_MAX_TOPK.  Every id is in [0, E) and a token's ids differ, whatever X holds.
+ * scratch: mq_moe_route_scratch_bytes(M, K, E) bytes (0 for a shape the call refuses), 16-byte
+ * aligned; its first 256 KiB are counters that must be zero before the first call and that every
+ * call leaves at zero; calls that share one buffer, of any shapes, must be ordered on one stream.
+ * Deterministic.  MQ_ERR_SIZE for a scratch that is too small.
+ */
+size_t mq_moe_route_scratch_bytes(int64_t M, int64_t K, int64_t E);
+int mq_moe_route(const float* X, const float* Wr, const float* bias, int32_t* ids, float* wts, int64_t M, int64_t K,
+                 int64_t E, int64_t topk, int score, int norm, float scale, void* scratch, size_t scratch_bytes,
+                 void* stream);
+
+/*
+ * mq_moe_ffn -- a mixture-of-experts feed-forward layer for a few tokens (decode):
+ *   Y[m] = residual[m] + sum_{j < topk} wts[m][j] * Wd[e] ( act(Wg[e] X[m]) * (Wu[e] X[m]) ),  e = ids[m][j]
+ * Wg, Wu: E matrices of F x K weights of gu_type one after another; Wd: E matrices of K x F
+ * weights of d_type (each 16-byte aligned, mq_weight_bytes(gu_type, E F, K) and
+ * mq_weight_bytes(d_type, E K, F) bytes); every GGUF type, and MQ_REPACKED Q8_0 and Q6_K.
+ * X, residual (or NULL: 0), Y: f32 [M][K]; ids int32, wts f32: [M][topk].  An id outside
+ * [0, E) (a choice that another device serves, or padding) adds nothing, and no weight is
+ * read for it; a token whose ids are all outside gets its residual.  The same expert may stand
+ * twice in a token's ids.  K a multiple of gu_type's block, F of d_type's; K, F <= MQ_MAX_K;
+ * E <= MQ_MOE_MAX_EXPERTS; M * topk <= MQ_MOE_MAX_PAIRS (a larger batch belongs to mq_gemm,
+ * expert by expert).  Y may be X or residual.
+ * f32 accuracy: activations keep 22 bits relative to the largest of their 32-value block, block dots
+ * are exact integers, all sums f32.  A token with an infinity or a NaN gets NaN outputs.
+ * Deterministic: a token's bits depend on its own row, ids and weights and on which kernels run
+ * (M * topk <= 32 or more), not on the other tokens.
+ * scratch: mq_moe_scratch_bytes(M, topk, F, K) bytes (0 for sizes the call refuses), 16-byte
+ * aligned, no initial value; calls that share one buffer must be ordered on one stream.
+ * Runs two launches, or three for more than 32 pairs.
+ */
+size_t mq_moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K);
+int mq_moe_ffn(const void* Wg, const void* Wu, int gu_type, const void* Wd, int d_type, const float* X,
+               const int32_t* ids, const float* wts, const float* residual, float* Y, int64_t M, int64_t topk,
+               int64_t E, int64_t F, int64_t K, int act, void* scratch, size_t scratch_bytes, void* stream);
+
 /* Partial-tile bytes of mq_gemm_noalloc's per-device scratch array. */
 #define MQ_NOALLOC_PARTIAL_BYTES (32u << 20)
 
@@ -342,7 +423,9 @@ int mq_device_lds_bytes(void);
  *   mq_gemm: "mmq_f6<q4_K plane>" (MQ_Q4_K | MQ_REPACKED, any M),
  *     "gemv_q8_mfma<q6_K>" (M <= 8, Q6_K, as gemv_mfma<q6_K>),
  *     "gemv_q8<type>" (other M <= 8 shapes that fit LDS), "mmq_kw<q4_K>" (Q4_K,
- *     GGUF payload, few output tiles: see mq_gemm_scratch_bytes), else "mmq<type>". */
+ *     GGUF payload, few output tiles: see mq_gemm_scratch_bytes), else "mmq<type>";
+ *   mq_gemv_ep, mq_gemm_ep: the name of the product's kernel; mq_moe_route: "moe_route";
+ *   mq_moe_ffn: "moe_pairs" (M * topk <= 32) or "moe_grouped". */
 const char* mq_last_kernel(void);
 
 /* Library version string. */

@@ -15,7 +15,8 @@ What is here:
                        ``q4_k_plane`` / ``act_f6_section`` the fp6 planes of the
                        Q4_K prefill product (weights and activations);
                        ``q4_k_row_tiled`` Q4_K's row-tiled layout for the
-                       long-row GEMV.
+                       long-row GEMV; ``epilogue``, ``moe_route`` and ``moe_ffn``
+                       the feed-forward operators around the products.
 * ``bitwise_decode`` -- a second, independently written per-block decoder that
                        assembles every field bit by bit; it exists only to
                        cross-check ``mq_oracle``'s vectorised decoders.
@@ -38,4 +39,5 @@ from .mq_oracle import (  # noqa: F401
     REPACK_SLOT, repack, unpack_repacked,
     PLANE_ROWS, ACT_PLANE_ROWS, e2m3_value, e2m3_code_of_half, fp6_records, bf16_hilo, q4_k_plane,
     act_f6_section, row_tile_rows, q4_k_row_tiled, unpack_q4_k_row_tiled,
+    activation, epilogue, moe_route, moe_ffn, magnitude,
 )

@@ -651,3 +651,97 @@ def mmq_from_block_dots(raw, qtype, q, d, S, N, K):
         main = np.einsum("mb,nb,mnb->mn", dx, dw, D)
         return main + np.einsum("mb,nb,mb->mn", dx, mw, S)
     raise ValueError(f"unsupported type {qtype}")
+
+
+# ------------------------------------------------------------------ feed-forward operators
+
+def activation(v, act):
+    """MQ_ACT_* of v in f64: 0 none, 1 silu, 2 gelu (tanh form), 3 gelu (erf), 4 relu."""
+    v = np.asarray(v, dtype=np.float64)
+    if act == 1:
+        return v * _logistic(v)
+    if act == 2:
+        return v * _logistic(2.0 * np.sqrt(2.0 / np.pi) * (v + 0.044715 * v ** 3))
+    if act == 3:
+        from scipy.special import ndtr   # the normal distribution function (1 + erf(v / sqrt 2)) / 2
+        return v * ndtr(v)
+    return np.maximum(v, 0.0) if act == 4 else v
+
+
+def _logistic(v):
+    return 0.5 * (1.0 + np.tanh(0.5 * v))
+
+
+def epilogue(acc, bias, act, mul, residual):
+    """act(acc + bias) * mul + residual in f64; None terms are left out.  acc [M, N]."""
+    v = np.asarray(acc, dtype=np.float64)
+    v = v if bias is None else v + np.asarray(bias, dtype=np.float64)
+    v = activation(v, act)
+    v = v if mul is None else v * np.asarray(mul, dtype=np.float64)
+    return v if residual is None else v + np.asarray(residual, dtype=np.float64)
+
+
+def moe_route(X, Wr, topk, bias=None, score=0, norm=True, scale=1.0):
+    """(ids [M, topk], wts f64 [M, topk]) of the router: logits X Wr^T, softmax (score 0) or sigmoid
+    (1), the topk largest logits (of score + bias with a bias), ties to the lower index."""
+    z = np.asarray(X, dtype=np.float64) @ np.asarray(Wr, dtype=np.float64).T
+    if score == 0:
+        p = np.exp(z - z.max(axis=1, keepdims=True))
+        p = p / p.sum(axis=1, keepdims=True)
+    else:
+        p = _logistic(z)
+    key = z if bias is None else p + np.asarray(bias, dtype=np.float64)
+    key = np.where(np.isnan(key), -np.inf, key)
+    ids = np.argsort(-key, axis=1, kind="stable")[:, :topk]
+    w = np.take_along_axis(p, ids, axis=1)
+    if norm:
+        w = w / w.sum(axis=1, keepdims=True)
+    return ids, w * scale
+
+
+def moe_ffn(raw_g, raw_u, gu_type, raw_d, d_type, X, ids, wts, E, F, act=1, residual=None):
+    """(Y f64 [M, K], bound [M, K]) of the expert layer.  `bound` is an error bound of a computation that
+    keeps 22 bits of x and h relative to the largest value of their 32-value block and rounds every f32 step:
+    a product of magnitude S = sum |w| |x| (the min term apart) with n terms is off by at most
+    2^-22 sum |w| max_block |x| + (32 + K / 256) 2^-24 S.  Very small values: the 22-bit integers' scale is
+    at least 2^-120, so every staged value may be off by half of that, 2^-121, whatever its block (this also
+    covers an h below f32's least number 2^-149, which rounds to nothing)."""
+    X = np.asarray(X, dtype=np.float64)
+    M, K = X.shape
+    Y = np.zeros((M, K)) if residual is None else np.asarray(residual, dtype=np.float64).copy()
+    bound = np.abs(Y) * 2.0 ** -24
+
+    def product(raw, qtype, rows, cols, x, dx):
+        w = decode(raw, qtype, rows, cols)
+        mag = magnitude(raw, qtype, rows, cols)
+        top = np.repeat(np.abs(x).reshape(-1, 32).max(axis=1), 32)
+        return w @ x, mag @ (2.0 ** -22 * top + (32 + cols / 256) * 2.0 ** -24 * np.abs(x) + dx + 2.0 ** -121)
+
+    for m in range(M):
+        for j, e in enumerate(ids[m]):
+            if e < 0 or e >= E:
+                continue
+            g, dg = product(raw_g.reshape(E, -1)[e], gu_type, F, K, X[m], 0.0)
+            u, du = product(raw_u.reshape(E, -1)[e], gu_type, F, K, X[m], 0.0)
+            a = activation(g, act)
+            h = a * u
+            # (every activation's slope is below 1.13)
+            dh = 1.13 * dg * (np.abs(u) + du) + np.abs(a) * du + 16 * 2.0 ** -24 * np.abs(h)
+            d, dd = product(raw_d.reshape(E, -1)[e], d_type, K, F, h, dh)
+            w = float(wts[m, j])
+            Y[m] += w * d
+            bound[m] += abs(w) * (dd + (4 + len(ids[m])) * 2.0 ** -24 * np.abs(d))
+    return Y, bound + 2.0 ** -22 * np.abs(Y)
+
+
+def magnitude(raw, qtype, N, K):
+    """|d code| + |min| of every weight [N, K]: what the products sum before they cancel."""
+    w = decode(raw, qtype, N, K)
+    if qtype in (Q4_K, Q5_K):
+        dmin, mn = (q4_k_fields if qtype == Q4_K else q5_k_fields)(raw, N, K)[1:4:2]
+        low = np.repeat(-dmin[..., None] * mn, 32, axis=-1).reshape(N, K)
+    elif qtype in (Q4_1, Q5_1):
+        low = np.repeat(legacy_fields(raw, qtype, N, K)[1], 32, axis=-1).reshape(N, K)
+    else:
+        return np.abs(w)
+    return np.abs(w - low) + np.abs(low)
