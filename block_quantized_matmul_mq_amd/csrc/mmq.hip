@@ -669,15 +669,20 @@ __global__ __launch_bounds__(256, 2) void mmq_kernel(const uint8_t* __restrict__
     // Y store: for a fixed accumulator element the 32 lanes of a group write 32 consecutive n.
     // The block-dot export variant stores only the dots.
     if constexpr (DUMP) return;
-    auto store = [&](int i, int j, const float* y) {
+    auto store = [&](int i, int j, const float* acc16) {
         const int n = n0 + 32 * TJ * wn + 32 * j + r32;
+        const int mrow = m0 + 32 * TI * wm + 32 * i;
+        float y[16];
+#pragma unroll
+        for (int v = 0; v < 16; ++v) y[v] = acc16[v];
+        if constexpr (EP::kIs) {
+            const int nc = min(n, N - 1);
+            ep.column(y, nc, [&](int v) { return int64_t(min(mrow + acc_row(v, g), M - 1)) * N + nc; });
+        }
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
-            const int m = m0 + 32 * TI * wm + 32 * i + acc_row(v, g);
-            if (m < M && n < N) {
-                const int64_t at = int64_t(m) * N + n;
-                Y[at] = ep(y[v], at, n);
-            }
+            const int m = mrow + acc_row(v, g);
+            if (m < M && n < N) Y[int64_t(m) * N + n] = y[v];
         }
     };
     if (whole) {

@@ -357,21 +357,27 @@ __global__ __launch_bounds__(kThreads, 2) void mmq_f6_q4k_kernel(const uint8_t* 
     if constexpr (DUMP) return;
     // A split tile puts its partial into its piece's slot, and the piece that counts in
     // last sums all pieces' slots in piece order into Y.
+    auto store = [&](int i, int j, auto&& value) {
+        const int n = n0 + 64 * wn + 32 * j + r32;
+        const int mrow = m0 + 64 * wm + 32 * i;
+        float y[16];
+#pragma unroll
+        for (int v = 0; v < 16; ++v) y[v] = value(v);
+        if constexpr (EP::kIs) {
+            const int nc = min(n, N - 1);
+            ep.column(y, nc, [&](int v) { return int64_t(min(mrow + mfma32_acc_row(v, g), M - 1)) * N + nc; });
+        }
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const int m = mrow + mfma32_acc_row(v, g);
+            if (m < M && n < N) Y[int64_t(m) * N + n] = y[v];
+        }
+    };
     if (whole) {
 #pragma unroll
         for (int i = 0; i < TI; ++i)
 #pragma unroll
-            for (int j = 0; j < TJ; ++j) {
-                const int n = n0 + 64 * wn + 32 * j + r32;
-#pragma unroll
-                for (int v = 0; v < 16; ++v) {
-                    const int m = m0 + 64 * wm + 32 * i + mfma32_acc_row(v, g);
-                    if (m < M && n < N) {
-                        const int64_t at = int64_t(m) * N + n;
-                        Y[at] = ep(acc[i][j][v], at, n);
-                    }
-                }
-            }
+            for (int j = 0; j < TJ; ++j) store(i, j, [&](int v) { return acc[i][j][v]; });
         return;
     }
     constexpr uint32_t kSlotBytes = BM * BN * sizeof(float);
@@ -391,17 +397,7 @@ __global__ __launch_bounds__(kThreads, 2) void mmq_f6_q4k_kernel(const uint8_t* 
         float y[TJ * 16];
         splitk_sum<TJ * 16, kThreads>(slots, kSlotBytes, pieces, i * TJ * 4, y);
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-            const int n = n0 + 64 * wn + 32 * j + r32;
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int m = m0 + 64 * wm + 32 * i + mfma32_acc_row(v, g);
-                if (m < M && n < N) {
-                    const int64_t at = int64_t(m) * N + n;
-                    Y[at] = ep(y[j * 16 + v], at, n);
-                }
-            }
-        }
+        for (int j = 0; j < TJ; ++j) store(i, j, [&](int v) { return y[j * 16 + v]; });
     }
 }
 

@@ -47,6 +47,33 @@ struct Epilogue {
         if (residual) v += residual[at];
         return v;
     }
+    // The same for C elements of one column n, at(v) the (valid) place of element v: each term's
+    // loads are issued together and before the activations, instead of one round trip per element
+    // (512 x 18944 x 3584 Q4_K with silu and mul: 195 -> 178 us).
+    template <int C, class At>
+    __device__ __forceinline__ void column(float (&y)[C], int n, const At& at) const {
+        float f[C], r[C];
+        float b = 0.f;
+        if (bias) b = bias[n];
+        if (mul)
+#pragma unroll
+            for (int v = 0; v < C; ++v) f[v] = mul[at(v)];
+        if (residual)
+#pragma unroll
+            for (int v = 0; v < C; ++v) r[v] = residual[at(v)];
+        if (bias)
+#pragma unroll
+            for (int v = 0; v < C; ++v) y[v] += b;
+        if (act != kActNone)
+#pragma unroll
+            for (int v = 0; v < C; ++v) y[v] = activate(y[v], act);
+        if (mul)
+#pragma unroll
+            for (int v = 0; v < C; ++v) y[v] *= f[v];
+        if (residual)
+#pragma unroll
+            for (int v = 0; v < C; ++v) y[v] += r[v];
+    }
 };
 
 // The epilogue argument of a kernel launched through an argument array (ep null: NoEpilogue's,
