@@ -7,31 +7,34 @@
 // keep weight loads in flight and to spend few instructions per weight.
 //
 // Split.  Two launches, because every output of the down product needs every h of its token:
-//   up    one workgroup per (expert, 16 TW rows of F): both the gate and the up rows, so that
-//         act(g) * u is formed where both sums meet; h goes to scratch, f32 [pair][F].
-//   down  few pairs: one workgroup per 16 rows of Y for all pairs, which sums the pairs itself
-//         (nothing is exchanged between workgroups); many pairs: one per (expert, 16 TW rows),
-//         weighted partial rows to scratch [pair][K], and a third launch adds each token's k
-//         rows in choice order.
-// With many pairs the workgroups of `up` and `down` collect the pairs of their expert, so that
-// an expert's weights are read once for all its tokens (in chunks of at most 8).
+//   up    one workgroup per (chosen expert, a few 16-row tiles of F), for all the expert's
+//         pairs: both the gate and the up rows, so that act(g) * u is formed where both sums
+//         meet; h goes to scratch, f32 [pair][F].
+//   down  up to kMoeFewTokens tokens: one workgroup per 16 rows of Y for every expert, which adds a
+//         token's choices itself (nothing is exchanged between workgroups); more tokens: one per
+//         (chosen expert, tiles), weighted partial rows to scratch [pair][K], and a third launch
+//         adds each token's rows in choice order.
+// An expert's weights are read once for all its tokens (eight at a time).
 //
 // Arithmetic.  The exact-integer scheme of the GEMV kernels: per 32-value block of the
 // activations x = 2^-s v with v an integer of at most 22 bits (relative to the block's largest
 // value the staged x is off by at most 2^-22), v = 65536 d2 + 256 d1 + d0 in signed bytes.
-// v_mfma_i32_16x16x64_i8 per 16-value chunk of four units at a time:
-//   B (64 x 16): column n = weight row n of the tile, lane group q (lanes 16q .. 16q + 15)
-//                holds 16 codes of unit q (64 of the 256 values of a group);
-//   A (16 x 64): row 4q + p (p < 3) = digit plane p of the same 16 values in lane group q,
-//                zero elsewhere,
-// so lane (n, q) receives exactly its own unit's three plane sums (all exact) and applies its own
-// block scales in f32.  The four units of a row are summed by lane swaps; each (group, tile,
-// token) leaves one partial per row in LDS, and the partials of a row are summed in a fixed
-// order: the result does not depend on timing.
+// One v_mfma_i32_16x16x32_i8 per 32-value block multiplies four tokens:
+//   A (16 x 32): row 4 t + p (p < 3) = digit plane p of token t (row 4 t + 3 repeats plane 2),
+//   B (32 x 16): column n = the block's 32 codes of weight row n; lane (n, q) holds eight of them,
+// so lane (n, q) receives the three plane sums of token q and row n (all exact), combines them and
+// applies the block's scale in f32.  A wave walks the 256-value groups of its 16 rows with one f32
+// accumulator per four tokens; nothing crosses lanes.  (Q6_K's scales change every 16 values: a
+// second product over A's first 16 values gives the first half, the difference the second.)
+// The same work for one token wastes three quarters of the matrix rows, which have the room: one
+// token's vector work is about 100 instructions per 2304 weight bytes, 40% of the time those bytes take
+// from HBM.
 //
-// A lane's 64 values of a weight row are loaded straight into registers (16-byte loads, also
-// where the block starts on a 2-byte boundary), several items ahead.  Items are ordered group
-// first, so a wave keeps the tokens' A operands in registers while it walks the tiles.
+// Weights: a wave reads one group of its 16 rows at a time as whole 16-byte chunks, consecutive lanes on
+// consecutive chunks, into registers, kDepth groups ahead, and passes each through LDS of its own,
+// where every lane picks the bytes its operands need.  (Loading those 8-byte pieces straight from
+// memory, 16 rows apart, kept the address path busy for most of the time the bytes take from HBM:
+// 48 tokens, 4096 x 1536 Q4_K gate and up, 348 us.)
 #include <algorithm>
 #include <type_traits>
 
@@ -42,222 +45,245 @@
 
 namespace mq {
 
+// Few tokens: at most kMoeFewTokens of at most kMoeFewPairs pairs.
+bool moe_few(int64_t M, int64_t topk) { return M <= kMoeFewTokens && M * topk <= kMoeFewPairs; }
+
 namespace {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kFracBits = 22;
-constexpr int kTokens = 8;                  // tokens of one expert computed together
-constexpr int kUnitBytes = 768 + 32 + 64;   // staged 256 values: digit planes, block scales, sums
-constexpr int kStageBudget = 72 * 1024;     // LDS of staged activations and partials: two workgroups per CU
+constexpr int kTokens = 8;                   // tokens of one expert computed together
+constexpr int kPlane = 288;                  // bytes of a staged digit plane: 256 and 32 (bank spread)
+constexpr int kPlanes = 3 * kPlane;
+constexpr int kStageBudget = 64 * 1024;      // LDS of staged activations
+constexpr int kDepth = 2;                    // weight groups in flight per wave
 
-__device__ __forceinline__ uint4 load16(const uint8_t* p) {
-    uint4 v;
-    __builtin_memcpy(&v, p, 16);   // (unaligned: one 16-byte load)
-    return v;
-}
-__device__ __forceinline__ uint32_t load4(const uint8_t* p) {
-    uint32_t v;
-    __builtin_memcpy(&v, p, 4);
-    return v;
+// A wave-uniform pointer to device memory held in scalar registers: a load from it plus a 32-bit lane
+// offset then takes one vector register for its address (the compiler otherwise keeps a 64-bit pointer
+// per lane for every load of the loop, and runs out of registers).  It stays a global pointer: a flat
+// load would be waited for with every LDS read.
+typedef const __attribute__((address_space(1))) uint8_t* global_bytes;
+__device__ __forceinline__ global_bytes scalar(const uint8_t* p) {
+    global_bytes g = (global_bytes)p;
+    asm("" : "+s"(g));
+    return g;
 }
 
-// LDS writes of every wave visible, without waiting for loads in flight
+// LDS writes of every wave visible, without waiting for global loads in flight
 // (__syncthreads waits for those too).
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-__device__ __forceinline__ v4i as_v4i(const uint4 v) { return v4i{int(v.x), int(v.y), int(v.z), int(v.w)}; }
-
 // ------------------------------------------------------------------ weights
-// Scales per lane unit (64 values): one per 32-value block, or per 16-value run (Q6_K).
-template <int QT> constexpr int scales_per_unit() { return QT == kQ6_K ? 4 : 2; }
-// A code is unsigned with an offset taken off through the integer sum of v (Q6_K, Q4_0, Q5_0)
+// A code is unsigned with an offset, taken off through the integer sum of v
 template <int QT> constexpr int code_offset() { return QT == kQ6_K ? 32 : QT == kQ4_0 ? 8 : QT == kQ5_0 ? 16 : 0; }
-// Whether |sum code v| can pass 2^31 (the plane sums are then combined in f32): 5-bit codes
+// Whether |sum code v| over a block can pass 2^31 (the plane sums are then combined in f32): 5-bit codes
 // without an offset and 8-bit codes.  (The others: 32 * 15 * 2^22 < 2^31; with the offset taken
 // off, modulo 2^32, 16 * 32 * (2^22 - 1) and 32 * 16 * (2^22 - 1) < 2^31.)
 template <int QT> constexpr bool wide_sums() { return QT == kQ8_0 || QT == kQ5_K || QT == kQ5_1; }
 
-// One item for one lane: unit q (64 values) of 256-value group g of one weight row, decoded
-// to four chunks of 16 codes (MFMA B operands), the scales of its blocks and their minima
-// (value = ds * code - dm).
+// Lane (n, q)'s part of one 256-value group of weight row n: of each of the eight 32-value blocks
+// eight codes as MFMA B bytes, which the blocks' layouts order differently:
+//   K-quants and Q8_0: values 8 q .. 8 q + 7 of the block;
+//   Q4_0, Q4_1, Q5_0, Q5_1: values 4 q .. 4 q + 3 and 16 + 4 q .. 16 + 4 q + 3 (a nibble pair per byte)
+// (the staged activations are in the same order), and each block's scale and minimum:
+//   weight = d * sc[b] * code - dm * mn[b]   (Q6_K: sc[2 b + half of the block]).
 template <int QT>
-struct Decoded {
-    v4i chunk[4];
-    float ds[scales_per_unit<QT>()];
-    float dm[2];
+struct Group {
+    static constexpr int kScales = QT == kQ6_K ? 16 : 8;
+    uint64_t codes[8];
+    float sc[kScales];
+    float mn[8];
+    float d, dm;
 };
 
+// Bytes of a group of a row, and the 16-byte chunks that cover it from any even start (K-quants of
+// 16-byte blocks: from a 16-byte boundary), in the GGUF payload or in the slots mq_repack writes.
+template <int QT> constexpr bool whole_chunks() { return QT == kQ4_K || QT == kQ5_K; }
+template <int QT> constexpr int group_bytes() { return 8 * Legacy<QT>::kBytes; }
+template <> constexpr int group_bytes<kQ4_K>() { return 144; }
+template <> constexpr int group_bytes<kQ5_K>() { return 176; }
+template <> constexpr int group_bytes<kQ6_K>() { return 224; }   // 210 from any even start, or a 224-byte slot
+template <> constexpr int group_bytes<kQ8_0>() { return 288; }   // 272 bytes, or eight 36-byte slots
 template <int QT>
-struct Bytes;
+constexpr int row_chunks() {
+    constexpr bool covered = whole_chunks<QT>() || QT == kQ6_K;
+    return (group_bytes<QT>() + (covered ? 0 : 14) + 15) / 16;
+}
 
-template <>
-struct Bytes<kQ4_K> {
-    uint4 hd, c0, c1;
-    __device__ void load(const uint8_t* row, int g, int q, int, int, int) {
-        const uint8_t* b = row + 144 * g;
-        hd = load16(b);
-        c0 = load16(b + 16 + 32 * q);
-        c1 = load16(b + 32 + 32 * q);
-    }
-    __device__ void decode(Decoded<kQ4_K>& o, int q) const {
-        const v4i a = as_v4i(c0), b = as_v4i(c1);
-        o.chunk[0] = a & 0x0F0F0F0F;
-        o.chunk[1] = b & 0x0F0F0F0F;
-        o.chunk[2] = (a >> 4) & 0x0F0F0F0F;
-        o.chunk[3] = (b >> 4) & 0x0F0F0F0F;
-        RawQ4K r;
-        r.hd = hd;
-        uint32_t sc, mn;
-        r.scale_min(q, sc, mn);
-        const float d = r.d(), dmin = r.dmin();   // (f16 times 6 bits: exact products)
-        o.ds[0] = d * ubyte_f<0>(sc);
-        o.ds[1] = d * ubyte_f<1>(sc);
-        o.dm[0] = dmin * ubyte_f<0>(mn);
-        o.dm[1] = dmin * ubyte_f<1>(mn);
-    }
-};
-
-template <>
-struct Bytes<kQ5_K> {
-    uint4 hd, h0, h1, c0, c1;
-    __device__ void load(const uint8_t* row, int g, int q, int, int, int) {
-        const uint8_t* b = row + 176 * g;
-        hd = load16(b);
-        h0 = load16(b + 16);
-        h1 = load16(b + 32);
-        c0 = load16(b + 48 + 32 * q);
-        c1 = load16(b + 64 + 32 * q);
-    }
-    __device__ void decode(Decoded<kQ5_K>& o, int q) const {
-        const v4i a = as_v4i(c0), b = as_v4i(c1);
-        const v4i ha = as_v4i(h0) >> (2 * q), hb = as_v4i(h1) >> (2 * q);
-        o.chunk[0] = (a & 0x0F0F0F0F) | ((ha & 0x01010101) << 4);
-        o.chunk[1] = (b & 0x0F0F0F0F) | ((hb & 0x01010101) << 4);
-        o.chunk[2] = ((a >> 4) & 0x0F0F0F0F) | (((ha >> 1) & 0x01010101) << 4);
-        o.chunk[3] = ((b >> 4) & 0x0F0F0F0F) | (((hb >> 1) & 0x01010101) << 4);
-        RawQ5K r;
-        r.hd = hd;
-        uint32_t sc, mn;
-        r.scale_min(q, sc, mn);
-        const float d = r.d(), dmin = r.dmin();
-        o.ds[0] = d * ubyte_f<0>(sc);
-        o.ds[1] = d * ubyte_f<1>(sc);
-        o.dm[0] = dmin * ubyte_f<0>(mn);
-        o.dm[1] = dmin * ubyte_f<1>(mn);
-    }
-};
-
-// Unit q of Q6_K: super-block half h = q / 2, lanes l0 = 16 (q % 2) .. + 15 of each of the four
-// 32-value runs of that half; chunk c = run c (one sub-scale each).
-template <>
-struct Bytes<kQ6_K> {
-    uint4 a, b, hq;
-    uint32_t s0, s1, dbits;
-    __device__ void load(const uint8_t* row, int g, int q, int, int stride, int off) {
-        const uint8_t* blk = row + stride * g + off;
-        const int h = q >> 1, l0 = 16 * (q & 1);
-        a = load16(blk + 64 * h + l0);
-        b = load16(blk + 64 * h + 32 + l0);
-        hq = load16(blk + 128 + 32 * h + l0);
-        s0 = load4(blk + 192 + 8 * h);
-        s1 = load4(blk + 196 + 8 * h);
-        dbits = load_u16(blk + 208);
-    }
-    __device__ void decode(Decoded<kQ6_K>& o, int q) const {
-        const v4i A = as_v4i(a), B = as_v4i(b), H = as_v4i(hq);
-        const float d = half_bits_to_float(dbits);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const v4i src = (c & 1) ? B : A;
-            o.chunk[c] = ((c < 2 ? src : (src >> 4)) & 0x0F0F0F0F) | (((H >> (2 * c)) & 0x03030303) << 4);
-            o.ds[c] = d * RawQ6K::subscale(c, q, s0, s1);   // (f16 times 8 bits: exact)
-        }
-        o.dm[0] = o.dm[1] = 0.f;
-    }
-};
-
-// The 32-value types: unit q = blocks 2q and 2q + 1 of the group's eight.  In a last group of
-// fewer than eight blocks the lanes past the row's end read its last block again (their staged
-// activations are zero).
-template <>
-struct Bytes<kQ8_0> {
-    uint4 c[4];
-    uint32_t db[2];
-    __device__ void load(const uint8_t* row, int g, int q, int blocks, int stride, int off) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint8_t* b = row + stride * min(8 * g + 2 * q + i, blocks - 1) + off;
-            db[i] = load_u16(b);
-            c[2 * i] = load16(b + 2);
-            c[2 * i + 1] = load16(b + 18);
-        }
-    }
-    __device__ void decode(Decoded<kQ8_0>& o, int) const {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o.chunk[k] = as_v4i(c[k]);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            o.ds[i] = half_bits_to_float(db[i]);
-            o.dm[i] = 0.f;
-        }
-    }
-};
-
+// One group of a wave's 16 rows: chunk c (row c / row_chunks, 16 bytes c % row_chunks of the row's
+// group) in register c / 64 of lane c % 64, then at byte 16 c of the wave's LDS slot.
 template <int QT>
-struct LegacyBytes {
-    using L = Legacy<QT>;
-    uint4 c[2];
-    uint32_t db[2], hb[2];
-    __device__ void load(const uint8_t* row, int g, int q, int blocks, int, int) {
+struct Tile {
+    static constexpr int kRow = row_chunks<QT>() * 16;      // LDS bytes of a row
+    static constexpr int kSlot = 16 * kRow;
+    static constexpr int kChunks = 16 * row_chunks<QT>();
+    static constexpr int kLoads = (kChunks + 63) / 64;
+    v4u r[kLoads];
+
+    // lane constants: byte offsets of its chunks' rows in the tile, and of the chunks in the row
+    struct Lane {
+        uint32_t row[kLoads], col[kLoads];
+        __device__ Lane(int lane, uint32_t row_bytes) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint8_t* b = row + L::kBytes * min(8 * g + 2 * q + i, blocks - 1);
-            constexpr int at = L::kMin ? 4 : 2;
-            db[i] = L::kMin ? load4(b) : load_u16(b);
-            hb[i] = L::kHigh ? load4(b + at) : 0u;
-            c[i] = load16(b + at + (L::kHigh ? 4 : 0));
-        }
-    }
-    __device__ void decode(Decoded<QT>& o, int) const {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const v4i v = as_v4i(c[i]);
-            v4i lo = v & 0x0F0F0F0F, hi = (v >> 4) & 0x0F0F0F0F;
-            if constexpr (L::kHigh) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    lo[k] |= int(spread4((hb[i] >> (4 * k)) & 15u) << 4);
-                    hi[k] |= int(spread4((hb[i] >> (16 + 4 * k)) & 15u) << 4);
-                }
+            for (int i = 0; i < kLoads; ++i) {
+                const int c = min(lane + 64 * i, kChunks - 1);
+                row[i] = uint32_t(c / row_chunks<QT>()) * row_bytes;
+                col[i] = uint32_t(c % row_chunks<QT>()) * 16;
             }
-            o.chunk[2 * i] = lo;
-            o.chunk[2 * i + 1] = hi;
-            o.ds[i] = half_bits_to_float(db[i] & 0xFFFFu);
-            o.dm[i] = L::kMin ? -half_bits_to_float(db[i] >> 16) : 0.f;
+        }
+    };
+    // `tile`: the tile's first byte (16-byte aligned, 16 row_bytes long); `at`: the group's byte in a row.
+    // Chunks past the tile (they hold none of the rows' bytes) read its last one.
+    __device__ void load(const uint8_t* tile, const Lane& l, uint32_t at, uint32_t tile_bytes) {
+        const global_bytes b = scalar(tile);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            uint32_t o = l.row[i] + at;
+            if constexpr (!whole_chunks<QT>()) o = min(o & ~15u, tile_bytes - 16 - l.col[i]);
+            r[i] = *(const __attribute__((address_space(1))) v4u*)(b + (o + l.col[i]));
         }
     }
+    __device__ void store(uint8_t* slot, int lane) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            if (64 * (i + 1) <= kChunks || lane + 64 * i < kChunks)
+                *reinterpret_cast<v4u*>(slot + 16 * (lane + 64 * i)) = r[i];
+    }
 };
-template <> struct Bytes<kQ4_0> : LegacyBytes<kQ4_0> {};
-template <> struct Bytes<kQ4_1> : LegacyBytes<kQ4_1> {};
-template <> struct Bytes<kQ5_0> : LegacyBytes<kQ5_0> {};
-template <> struct Bytes<kQ5_1> : LegacyBytes<kQ5_1> {};
+
+// LDS reads of 4 and 8 bytes at even byte `at` of a row (which starts on a dword), as the dwords that
+// hold them.
+__device__ __forceinline__ uint32_t even4(const uint8_t* row, uint32_t at) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + (at >> 2);
+    return align_byte(w[1], w[0], at & 3u);
+}
+__device__ __forceinline__ uint64_t even8(const uint8_t* row, uint32_t at) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + (at >> 2);
+    return (uint64_t(align_byte(w[2], w[1], at & 3u)) << 32) | align_byte(w[1], w[0], at & 3u);
+}
+__device__ __forceinline__ uint32_t even2(const uint8_t* row, uint32_t at) {
+    return *reinterpret_cast<const uint16_t*>(row + at);
+}
+
+// decode(o, b, s, q, g, blocks, stride): lane (n, q)'s operands of a group whose bytes start at byte s
+// (even, below 16) of its row's chunks b in LDS.
+
+// The eight 6-bit (scale, min) pairs of a Q4_K / Q5_K header, and d, dmin.
+template <class G>
+__device__ __forceinline__ void header(G& o, const uint4 hd) {
+    const uint32_t sc0 = hd.y & 0x3F3F3F3Fu, mn0 = hd.z & 0x3F3F3F3Fu;
+    const uint32_t sc1 = (hd.w & 0x0F0F0F0Fu) | ((hd.y >> 2) & 0x30303030u);
+    const uint32_t mn1 = ((hd.w >> 4) & 0x0F0F0F0Fu) | ((hd.z >> 2) & 0x30303030u);
+    o.sc[0] = ubyte_f<0>(sc0); o.sc[1] = ubyte_f<1>(sc0); o.sc[2] = ubyte_f<2>(sc0); o.sc[3] = ubyte_f<3>(sc0);
+    o.sc[4] = ubyte_f<0>(sc1); o.sc[5] = ubyte_f<1>(sc1); o.sc[6] = ubyte_f<2>(sc1); o.sc[7] = ubyte_f<3>(sc1);
+    o.mn[0] = ubyte_f<0>(mn0); o.mn[1] = ubyte_f<1>(mn0); o.mn[2] = ubyte_f<2>(mn0); o.mn[3] = ubyte_f<3>(mn0);
+    o.mn[4] = ubyte_f<0>(mn1); o.mn[5] = ubyte_f<1>(mn1); o.mn[6] = ubyte_f<2>(mn1); o.mn[7] = ubyte_f<3>(mn1);
+    o.d = half_bits_to_float(hd.x & 0xFFFFu);
+    o.dm = half_bits_to_float(hd.x >> 16);
+}
+
+__device__ __forceinline__ void decode(Group<kQ4_K>& o, const uint8_t* b, uint32_t s, int q, int, int, int) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint64_t c = *reinterpret_cast<const uint64_t*>(b + 16 + 32 * i + 8 * q);
+        o.codes[2 * i] = c & 0x0F0F0F0F0F0F0F0Full;
+        o.codes[2 * i + 1] = (c >> 4) & 0x0F0F0F0F0F0F0F0Full;
+    }
+    header(o, *reinterpret_cast<const uint4*>(b));
+}
+
+__device__ __forceinline__ void decode(Group<kQ5_K>& o, const uint8_t* b, uint32_t s, int q, int, int, int) {
+    const uint64_t h = *reinterpret_cast<const uint64_t*>(b + 16 + 8 * q);   // bit i of byte l: bit 4 of value l of block i
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint64_t c = *reinterpret_cast<const uint64_t*>(b + 48 + 32 * (i / 2) + 8 * q);
+        const uint64_t low = (i & 1) ? c >> 4 : c;
+        const uint64_t high = i < 4 ? h << (4 - i) : h >> (i - 4);
+        o.codes[i] = (low & 0x0F0F0F0F0F0F0F0Full) | (high & 0x1010101010101010ull);
+    }
+    header(o, *reinterpret_cast<const uint4*>(b));
+}
+
+// Block 4 h + r of Q6_K: half h, run r; low bits in ql[64 h + 32 (r % 2) ..], nibble r / 2, high bits
+// at bit 2 r of qh[32 h ..]; the sub-scales of its two 16-value halves are scales[8 h + 2 r ..].
+__device__ __forceinline__ void decode(Group<kQ6_K>& o, const uint8_t* b, uint32_t s, int q, int, int, int) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint64_t qh = even8(b, s + 128 + 32 * h + 8 * q);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint64_t ql = even8(b, s + 64 * h + 32 * k + 8 * q);
+            // runs k (low nibbles) and k + 2 (high nibbles)
+            const uint64_t h0 = k == 0 ? qh << 4 : qh << 2, h1 = k == 0 ? qh : qh >> 2;
+            o.codes[4 * h + k] = (ql & 0x0F0F0F0F0F0F0F0Full) | (h0 & 0x3030303030303030ull);
+            o.codes[4 * h + k + 2] = ((ql >> 4) & 0x0F0F0F0F0F0F0F0Full) | (h1 & 0x3030303030303030ull);
+        }
+        const uint64_t sub = even8(b, s + 192 + 8 * h);
+        const uint32_t sw[2] = {uint32_t(sub), uint32_t(sub >> 32)};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.sc[8 * h + i] = float(int32_t(sw[i >> 2] << (24 - 8 * (i & 3))) >> 24);
+    }
+    o.d = half_bits_to_float(even2(b, s + 208));
+    o.dm = 0.f;
+}
+
+// The 32-value types: block 8 g + i of the row.  In a last group of fewer than eight blocks those past
+// the row's end are its last block again (their staged activations are zero).
+__device__ __forceinline__ void decode(Group<kQ8_0>& o, const uint8_t* b, uint32_t s, int q, int g, int blocks,
+                                       int stride) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t p = s + stride * min(i, blocks - 1 - 8 * g);
+        o.codes[i] = even8(b, p + 2 + 8 * q);
+        o.sc[i] = half_bits_to_float(even2(b, p));
+    }
+    o.d = 1.f;
+    o.dm = 0.f;
+}
+
+template <int QT>
+__device__ __forceinline__ void decode(Group<QT>& o, const uint8_t* b, uint32_t s, int q, int g, int blocks, int) {
+    using L = Legacy<QT>;
+    constexpr int at = L::kMin ? 4 : 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t p = s + L::kBytes * min(i, blocks - 1 - 8 * g);
+        const uint32_t c = even4(b, p + at + (L::kHigh ? 4 : 0) + 4 * q);
+        uint32_t lo = c & 0x0F0F0F0Fu, hi = (c >> 4) & 0x0F0F0F0Fu;
+        if constexpr (L::kHigh) {
+            const uint32_t h = even4(b, p + at) >> (4 * q);   // bits 0..3 and 16..19: this lane's values
+            lo |= spread4(h & 15u) << 4;
+            hi |= spread4((h >> 16) & 15u) << 4;
+        }
+        o.codes[i] = (uint64_t(hi) << 32) | lo;
+        o.sc[i] = half_bits_to_float(even2(b, p));
+        o.mn[i] = L::kMin ? half_bits_to_float(even2(b, p + 2)) : 0.f;
+    }
+    o.d = 1.f;
+    o.dm = -1.f;
+}
 
 // ------------------------------------------------------------------ staged activations
-// One unit of staged LDS: 256 values of one token (kUnitBytes): digit planes int8 [3][256],
-// f32 scale 2^-s of each 32-value block, and what the type needs of the integer sums of v:
-//   types with a minimum: f32 2^-s sum(v) per block; Q4_0, Q5_0: int32 sum(v) per block;
-//   Q6_K: int32 sum(v) per 16-value run, run 2c + i of half h at 8 h + 4 i + c.
+// `count` tokens' 256 values of one group in LDS, count * unit_bytes: the digit planes of every token
+// (kPlanes each, plane p at kPlane p), then the f32 scales 2^-s of every token's eight blocks (32
+// bytes each), then what the type needs of the integer sums of v (32 or, Q6_K, 64 bytes each):
+//   types with a minimum: f32 2^-s sum(v) per block; Q4_0, Q5_0: int32 offset * sum(v) per block;
+//   Q6_K: int32 32 sum(v) per 16-value half, half i of block b at 2 b + i.
 // All of them come from the same rounded v that the digits hold, so a code's offset or a
 // minimum multiplies exactly the x that the codes meet.  A block that holds an infinity or a
 // NaN has a NaN scale: every output of that token becomes NaN.
+template <int QT> constexpr int sum_bytes() { return QT == kQ6_K ? 64 : 32; }
+template <int QT> constexpr int unit_bytes() { return kPlanes + 32 + sum_bytes<QT>(); }
+
 __device__ __forceinline__ uint32_t digits3(int v) { return (uint32_t(v) + 0x00808080u) ^ 0x00808080u; }
 
-// Stage 256 values: lane l holds values 4l .. 4l + 3 (zeros past the row's end).
+// Stage token t's 256 values: lane l holds values 4l .. 4l + 3 (zeros past the row's end).
 template <int QT>
-__device__ __forceinline__ void stage_unit(uint8_t* unit, const float4 x, int lane) {
+__device__ __forceinline__ void stage_token(uint8_t* group, int t, int count, const float4 x, int lane) {
     float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
     a = lanes8_max(a);
     // v in (-2^22, 2^22): amax = m 2^E, m in [0.5, 1), s = 22 - E (at most 120: blocks below
@@ -269,198 +295,97 @@ __device__ __forceinline__ void stage_unit(uint8_t* unit, const float4 x, int la
     const uint32_t r0 = digits3(v0), r1 = digits3(v1), r2 = digits3(v2), r3 = digits3(v3);
     const uint32_t t01 = __builtin_amdgcn_perm(r1, r0, 0x05010400u), t23 = __builtin_amdgcn_perm(r3, r2, 0x05010400u);
     const uint32_t u01 = __builtin_amdgcn_perm(r1, r0, 0x00000602u), u23 = __builtin_amdgcn_perm(r3, r2, 0x00000602u);
-    uint32_t* planes = reinterpret_cast<uint32_t*>(unit);
-    planes[lane] = __builtin_amdgcn_perm(t23, t01, 0x05040100u);
-    planes[64 + lane] = __builtin_amdgcn_perm(t23, t01, 0x07060302u);
-    planes[128 + lane] = __builtin_amdgcn_perm(u23, u01, 0x05040100u);
-    float* scl = reinterpret_cast<float*>(unit + 768);
+    // the lane's dword of its block, in the order of the B bytes
+    const int b = lane >> 3, k = lane & 7;
+    const int pos = 8 * b + (Legacy<QT>::kIs ? (k < 4 ? 2 * k : 2 * k - 7) : k);
+    uint32_t* planes = reinterpret_cast<uint32_t*>(group + t * kPlanes) + pos;
+    planes[0] = __builtin_amdgcn_perm(t23, t01, 0x05040100u);
+    planes[kPlane / 4] = __builtin_amdgcn_perm(t23, t01, 0x07060302u);
+    planes[kPlane / 2] = __builtin_amdgcn_perm(u23, u01, 0x05040100u);
+    float* scl = reinterpret_cast<float*>(group + count * kPlanes + t * 32);
     // (0 * x is NaN for an infinity or a NaN and 0 otherwise; a sum keeps the NaN)
     float bad = 0.f * x.x + 0.f * x.y + (0.f * x.z + 0.f * x.w);
     bad = lanes8_sum(bad);
     const float scale = ldexpf(1.0f, -s) + bad;
-    const int b = lane >> 3;
-    if ((lane & 7) == 0) scl[b] = scale;
+    if (k == 0) scl[b] = scale;
+    uint8_t* sums = group + count * (kPlanes + 32) + t * sum_bytes<QT>();
     int sum = (v0 + v1) + (v2 + v3);
     if constexpr (QT == kQ6_K) {
-        sum = lanes8_sum<2>(sum);   // 16-value runs: run 2 b + i, b = 4 h + c
-        if ((lane & 3) == 0)
-            reinterpret_cast<int*>(unit + 800)[8 * (b >> 2) + 4 * ((lane >> 2) & 1) + (b & 3)] = sum;
+        sum = lanes8_sum<2>(sum);
+        if ((k & 3) == 0) reinterpret_cast<int*>(sums)[2 * b + (k >> 2)] = code_offset<QT>() * sum;
     } else if constexpr (code_offset<QT>() != 0) {
         sum = lanes8_sum(sum);
-        if ((lane & 7) == 0) reinterpret_cast<int*>(unit + 800)[b] = sum;
+        if (k == 0) reinterpret_cast<int*>(sums)[b] = code_offset<QT>() * sum;
     } else if constexpr (has_min_term<QT>()) {
         sum = lanes8_sum(sum);
-        if ((lane & 7) == 0) reinterpret_cast<float*>(unit + 800)[b] = float(sum) * scale;
+        if (k == 0) reinterpret_cast<float*>(sums)[b] = float(sum) * scale;
     }
 }
 
 // ------------------------------------------------------------------ products
-// Sum over the lanes l, l ^ 16, l ^ 32, l ^ 48.
-__device__ __forceinline__ float sum_units(float v) {
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    const float s = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
-// The A operands of T tokens' staged units (consecutive in LDS) for this lane.
-template <int QT, int T>
-struct Operands {
-    v4i a[T][4];
-    __device__ void load(const uint8_t* lds, int lane_off, int unit0, bool live, const uint8_t* zero) {
-        constexpr int step = QT == kQ6_K ? 32 : 16;   // bytes between a lane's chunks
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const uint8_t* p = live ? lds + (unit0 + t) * kUnitBytes + lane_off : zero;
-#pragma unroll
-            for (int c = 0; c < 4; ++c) a[t][c] = *reinterpret_cast<const v4i*>(p + step * c);
-        }
-    }
-};
-
-// This lane's unit of one item against one token: its share of the row's dot product.
+// What a lane reads of a staged group of `count` tokens for tokens 4 S .. 4 S + 3: its A row's digits of
+// each block, and the scales and sums of token 4 S + q.  (Tokens past the last are the last again;
+// their results are not used.)
 template <int QT>
-__device__ __forceinline__ float unit_dot(const Decoded<QT>& w, const v4i (&a)[4], const uint8_t* unit, int q) {
-    constexpr int NS = scales_per_unit<QT>();
+struct LaneTokens {
+    int a;       // byte offset of the A row's digits of block 0 (+ 32 b)
+    int scale;   // of the token's block scales
+    int sums;
+    __device__ LaneTokens(int lane, int set, int count) {
+        const int row = lane & 15, q = lane >> 4;
+        const int ta = min(4 * set + (row >> 2), count - 1), tq = min(4 * set + q, count - 1);
+        a = ta * kPlanes + min(row & 3, 2) * kPlane + 8 * q;
+        scale = count * kPlanes + tq * 32;
+        sums = count * (kPlanes + 32) + tq * sum_bytes<QT>();
+    }
+};
+
+// acc += the group's share of the dot product of weight row n with token 4 S + q
+template <int QT>
+__device__ __forceinline__ float group_dot(const Group<QT>& w, const uint8_t* staged, const LaneTokens<QT>& l, float acc) {
     const v4i z = {0, 0, 0, 0};
-    float r = 0.f;
-    float sc[NS];
-    int si[NS];
-    float sx[2];
-    if constexpr (NS == 4) {
-        const float4 f = *reinterpret_cast<const float4*>(unit + 768 + 16 * (q >> 1));
-        sc[0] = f.x; sc[1] = f.y; sc[2] = f.z; sc[3] = f.w;
-        const int4 i = *reinterpret_cast<const int4*>(unit + 800 + 32 * (q >> 1) + 16 * (q & 1));
-        si[0] = i.x; si[1] = i.y; si[2] = i.z; si[3] = i.w;
-    } else {
-        const float2 f = *reinterpret_cast<const float2*>(unit + 768 + 8 * q);
-        sc[0] = f.x; sc[1] = f.y;
-        if constexpr (code_offset<QT>() != 0) {
-            const int2 i = *reinterpret_cast<const int2*>(unit + 800 + 8 * q);
-            si[0] = i.x; si[1] = i.y;
-        }
-        if constexpr (has_min_term<QT>()) {
-            const float2 m = *reinterpret_cast<const float2*>(unit + 800 + 8 * q);
-            sx[0] = m.x; sx[1] = m.y;
-        }
+    float s[8];
+    *reinterpret_cast<float4*>(s) = *reinterpret_cast<const float4*>(staged + l.scale);
+    *reinterpret_cast<float4*>(s + 4) = *reinterpret_cast<const float4*>(staged + l.scale + 16);
+    constexpr int kSums = QT == kQ6_K ? 16 : 8;
+    union {
+        int i[kSums];
+        float f[kSums];
+    } sum;
+    if constexpr (code_offset<QT>() != 0 || has_min_term<QT>()) {
+#pragma unroll
+        for (int i = 0; i < kSums; i += 4)
+            *reinterpret_cast<int4*>(sum.i + i) = *reinterpret_cast<const int4*>(staged + l.sums + 4 * i);
     }
+    auto joined = [](const v4i& c) { return (((uint32_t(c[2]) << 8) + uint32_t(c[1])) << 8) + uint32_t(c[0]); };
+    float codes = 0.f, mins = 0.f;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-        v4i c = z;
-#pragma unroll
-        for (int k = 0; k < 4 / NS; ++k)
-            c = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[s * (4 / NS) + k], w.chunk[s * (4 / NS) + k], c, 0, 0, 0);
-        float f;
-        if constexpr (wide_sums<QT>()) {
-            f = fmaf(float(c[2]), 65536.0f, fmaf(float(c[1]), 256.0f, float(c[0])));
+    for (int b = 0; b < 8; ++b) {
+        const long a = *reinterpret_cast<const long*>(staged + l.a + 32 * b);
+        const v4i c = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, long(w.codes[b]), z, 0, 0, 0);
+        if constexpr (QT == kQ6_K) {
+            // lane groups 0 and 1 hold the block's first 16 values
+            const long first = (threadIdx.x & 32) ? 0l : a;
+            const v4i c1 = __builtin_amdgcn_mfma_i32_16x16x32_i8(first, long(w.codes[b]), z, 0, 0, 0);
+            const uint32_t all = joined(c), one = joined(c1);
+            const float f1 = float(int(one - uint32_t(sum.i[2 * b])));
+            const float f2 = float(int(all - one - uint32_t(sum.i[2 * b + 1])));
+            codes = fmaf(fmaf(w.sc[2 * b], f1, w.sc[2 * b + 1] * f2), s[b], codes);
         } else {
-            int i = int((((uint32_t(c[2]) << 8) + uint32_t(c[1])) << 8) + uint32_t(c[0]));
-            if constexpr (code_offset<QT>() != 0) i = int(uint32_t(i) - uint32_t(code_offset<QT>()) * uint32_t(si[s]));
-            f = float(i);
-        }
-        r = fmaf(w.ds[s] * sc[s], f, r);
-    }
-    if constexpr (has_min_term<QT>()) r = fmaf(-w.dm[0], sx[0], fmaf(-w.dm[1], sx[1], r));
-    return r;
-}
-
-// Where an item of a wave is: where(i).  Its partials go to part[i T + t][16].
-struct ItemAt {
-    const uint8_t* row;   // the lane's weight row (block 0)
-    int group;            // 256-value group of the row
-    int unit;             // first of the T staged units
-};
-
-template <int QT, int T, int DEPTH, class Where>
-__device__ __forceinline__ void prime_items(Bytes<QT> (&buf)[DEPTH], const Where& where, int i0, int i1, int q,
-                                            int blocks, int stride, int off) {
-#pragma unroll
-    for (int j = 0; j < DEPTH; ++j)
-        if (i0 + j < i1) {
-            const ItemAt at = where(i0 + j);
-            buf[j].load(at.row, at.group, q, blocks, stride, off);
-        }
-}
-
-template <int QT, int T, int DEPTH, class Where>
-__device__ __forceinline__ void run_items(Bytes<QT> (&buf)[DEPTH], const Where& where, int i0, int i1, int lane,
-                                          const uint8_t* staged, const uint8_t* zero, float* part, int blocks,
-                                          int stride, int off) {
-    const int n = lane & 15, q = lane >> 4;
-    const bool live = (n >> 2) == q && (n & 3) < 3;
-    const int lane_off = 256 * (n & 3) + (QT == kQ6_K ? 128 * (q >> 1) + 16 * (q & 1) : 64 * q);
-    Operands<QT, T> op;
-    int have = -1;
-    auto compute = [&](const Bytes<QT>& b, int i) {
-        const ItemAt at = where(i);
-        if (at.unit != have) {   // uniform
-            op.load(staged, lane_off, at.unit, live, zero);
-            have = at.unit;
-        }
-        Decoded<QT> w;
-        b.decode(w, q);
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-            const float r = sum_units(unit_dot<QT>(w, op.a[t], staged + (at.unit + t) * kUnitBytes, q));
-            if (q == 0) part[(i * T + t) * 16 + n] = r;
-        }
-    };
-    auto load = [&](Bytes<QT>& b, int i) {
-        const ItemAt at = where(i);
-        b.load(at.row, at.group, q, blocks, stride, off);
-    };
-    int i = i0;
-    // steady part: one load per computed item, no conditions (the compiler then waits for
-    // exactly the item it needs); the drain issues no loads past the end
-    for (; i + 2 * DEPTH <= i1; i += DEPTH) {
-#pragma unroll
-        for (int j = 0; j < DEPTH; ++j) {
-            compute(buf[j], i + j);
-            load(buf[j], i + j + DEPTH);
+            float f;
+            if constexpr (wide_sums<QT>()) {
+                f = fmaf(float((c[2] << 8) + c[1]), 256.0f, float(c[0]));   // (|256 c2 + c1| < 2^28)
+            } else if constexpr (code_offset<QT>() != 0) {
+                f = float(int(joined(c) - uint32_t(sum.i[b])));
+            } else {
+                f = float(int(joined(c)));
+            }
+            codes = fmaf(f * s[b], w.sc[b], codes);
+            if constexpr (has_min_term<QT>()) mins = fmaf(sum.f[b], w.mn[b], mins);
         }
     }
-#pragma unroll
-    for (int j = 0; j < 2 * DEPTH; ++j) {
-        if (i + j < i1) {
-            compute(buf[j % DEPTH], i + j);
-            if (j < DEPTH && i + j + DEPTH < i1) load(buf[j % DEPTH], i + j + DEPTH);
-        }
-    }
-}
-
-// The x of a wave's share of the units to stage, requested before the weights (a wave's loads
-// return in order), staged after.  Units wave, wave + kWaves, ... of `units`.
-constexpr int kEarly = 4;
-struct EarlyX {
-    float4 v[kEarly];
-};
-template <class Source>
-__device__ __forceinline__ float4 unit_x(const Source& src, int u, int lane) {
-    const float* p;
-    int left;   // values from the unit's first to the row's end
-    src(u, p, left);
-    float4 v = {0.f, 0.f, 0.f, 0.f};
-    if (4 * lane < left) v = reinterpret_cast<const float4*>(p)[lane];
-    return v;
-}
-template <class Source>
-__device__ __forceinline__ void early_x(EarlyX& e, const Source& src, int units, int wave, int lane) {
-#pragma unroll
-    for (int j = 0; j < kEarly; ++j) {
-        const int u = wave + kWaves * j;
-        if (u < units) e.v[j] = unit_x(src, u, lane);
-    }
-}
-template <int QT, class Source>
-__device__ __forceinline__ void stage_units(const EarlyX& e, const Source& src, uint8_t* staged, int units, int wave,
-                                            int lane) {
-#pragma unroll
-    for (int j = 0; j < kEarly; ++j) {
-        const int u = wave + kWaves * j;
-        if (u < units) stage_unit<QT>(staged + u * kUnitBytes, e.v[j], lane);
-    }
-    for (int u = wave + kWaves * kEarly; u < units; u += kWaves)
-        stage_unit<QT>(staged + u * kUnitBytes, unit_x(src, u, lane), lane);
+    if constexpr (has_min_term<QT>()) acc = fmaf(-w.dm, mins, acc);
+    return fmaf(w.d, codes, acc);
 }
 
 struct MoeArgs {
@@ -469,280 +394,542 @@ struct MoeArgs {
     const float* x;        // up: X [M][in]; down: h [pair][in]
     const int32_t* ids;    // [pairs]
     const float* wts;      // [pairs] (down)
-    const float* residual; // [M][rows] or null (down, few pairs)
+    const float* residual; // [M][rows] or null (down, few tokens)
     float* out;            // up: h [pair][rows]; down: Y [M][rows], or weighted rows [pair][rows]
     int pairs, topk, experts;
     int in, rows;          // values per weight row, weight rows per expert
     int groups;            // 256-value groups per row
-    int phase;             // groups staged at a time (few pairs' down: units)
-    int tiles;             // 16-row tiles per workgroup
+    int splits;            // waves that share a tile's groups (wave ks takes groups ks, ks + splits, ..)
+    int set;               // many tokens: tokens staged together
     int act;
     int stride, off;       // weight block layout
     int64_t row_bytes;
 };
 
-// The sum of one output's partials over its units u (groups of a row, or groups of a token's
-// pairs): four running sums, of the u that leave 0, 1, 2, 3 modulo 4, kept over all phases and
-// added as (0 + 1) + (2 + 3) at the end.  So the order is the same whether four threads hold one
-// of them each (few outputs) or one thread all four, and wherever a phase ends: a token's bits do
-// not depend on what else the workgroup computes.
-struct RowSums {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    // `read(u)` is unit u's partial of this thread's output, u0 <= u < u1
-    template <class Read>
-    __device__ void add(bool split, int j, int u0, int u1, const Read& read) {
-        if (split) {
-            for (int u = u0 + ((j - u0) & 3); u < u1; u += 4) s[0] += read(u);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                for (int u = u0 + ((k - u0) & 3); u < u1; u += 4) s[k] += read(u);
-        }
-    }
-    // the total, in the output's first thread; red[4][outputs] (LDS) is free before and after
-    __device__ float total(bool split, int outputs, float* red) const {
-        if (!split) return (s[0] + s[1]) + (s[2] + s[3]);
-        const int tid = threadIdx.x;
-        if (tid < 4 * outputs) red[tid] = s[0];
-        lds_barrier();
-        float v = 0.f;
-        if (tid < outputs) v = (red[tid] + red[outputs + tid]) + (red[2 * outputs + tid] + red[3 * outputs + tid]);
-        lds_barrier();
-        return v;
-    }
-};
+template <int QT>
+__device__ __forceinline__ int row_blocks(int in) {
+    return QT == kQ4_K || QT == kQ5_K || QT == kQ6_K ? in >> 8 : in >> 5;
+}
 
-// ------------------------------------------------------------------ up, and down with many pairs
-// blockIdx.x: 16 TW rows of the expert; blockIdx.y: slot.  PAIRS: the slot is a pair; else it is
-// the slot-th chosen expert, and the workgroup takes all its pairs, kTokens at a time.
-// LDS: pair list | staged units | partials | sums.
-template <int QT, bool UP>
-struct GroupShape {
-    static constexpr int kMats = UP ? 2 : 1;
-};
+// Block slots of a 256-value group.
+template <int QT>
+constexpr int row_blocks_per_group() {
+    return QT == kQ4_K || QT == kQ5_K || QT == kQ6_K ? 1 : 8;
+}
 
-template <int QT, bool UP, int T, int DEPTH>
-__device__ __forceinline__ void group_chunk(const MoeArgs& a, int expert, int tile0, int tiles, const int* list,
-                                            int count, uint8_t* staged, const uint8_t* zero, float* part, float* red) {
-    constexpr int kMats = GroupShape<QT, UP>::kMats;
+// The chosen experts as bits in LDS (`bits`, kMoeMaxExperts of them); ends with a barrier.
+__device__ __forceinline__ void chosen_experts(const MoeArgs& a, unsigned* bits) {
+    const int tid = threadIdx.x;
+    if (tid < kMoeMaxExperts / 32) bits[tid] = 0u;
+    lds_barrier();
+    for (int p = tid; p < a.pairs; p += kThreads) {
+        const int e = a.ids[p];
+        if (unsigned(e) < unsigned(a.experts)) atomicOr(&bits[e >> 5], 1u << (e & 31));
+    }
+    lds_barrier();
+}
+
+// ------------------------------------------------------------------ up, and down with many tokens
+// blockIdx.x: kWaves / splits 16-row tiles of the expert; blockIdx.y: the slot-th chosen expert, or
+// (ONE token) the token's choice.  Wave w: tile w / splits of the workgroup, part w % splits of its groups.
+// SETS: four tokens each.
+template <int QT, bool UP, int SETS>
+__device__ __forceinline__ void expert_tiles(const MoeArgs& a, int expert, const int* list, int count, uint8_t* staged,
+                                             uint8_t* slots, float* red) {
+    constexpr int kMats = UP ? 2 : 1;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, q = lane >> 4;
-    const int nt = tiles * kMats;
-    const int blocks = QT == kQ4_K || QT == kQ5_K || QT == kQ6_K ? a.in >> 8 : a.in >> 5;
-    const int64_t row0 = (int64_t(expert) * a.rows + 16 * tile0 + n) * a.row_bytes;
-    // outputs o = (tile, token, row), of thread o, or of threads o, outputs + o, ... (RowSums)
-    const int outputs = tiles * 16 * T;
-    const bool split = 4 * outputs <= kThreads;
-    const int j = split ? tid / outputs : 0, o = tid - j * outputs;
-    const int o_tile = o / (16 * T), o_t = (o >> 4) & (T - 1), o_r = o & 15;
-    const bool has_output = split ? j < 4 : tid < outputs;
-    RowSums sums[kMats];
-    for (int g0 = 0; g0 < a.groups; g0 += a.phase) {
-        const int ng = min(a.phase, a.groups - g0);
-        const int items = ng * nt;
-        const int i0 = wave * items / kWaves, i1 = (wave + 1) * items / kWaves;
-        auto where = [&](int i) {   // group-major: tiles (and both matrices) of one group in turn
-            const int g = i / nt, m = i - g * nt;
-            const int tile = UP ? m >> 1 : m;
-            const uint8_t* w = UP && (m & 1) ? a.w1 : a.w0;
-            return ItemAt{w + row0 + int64_t(16 * tile) * a.row_bytes, g0 + g, g * T};
-        };
-        auto source = [&](int u, const float*& p, int& left) {   // unit u = (group, token)
-            const int g = u / T, t = u - g * T;
-            const int pair = list[min(t, count - 1)];
-            const int r = UP ? pair / a.topk : pair;
-            p = a.x + int64_t(r) * a.in + 256 * (g0 + g);
-            left = a.in - 256 * (g0 + g);
-        };
-        EarlyX ex;
-        early_x(ex, source, ng * T, wave, lane);
-        Bytes<QT> buf[DEPTH];
-        prime_items<QT, T, DEPTH>(buf, where, i0, i1, q, blocks, a.stride, a.off);
-        stage_units<QT>(ex, source, staged, ng * T, wave, lane);
-        lds_barrier();
-        run_items<QT, T, DEPTH>(buf, where, i0, i1, lane, staged, zero, part, blocks, a.stride, a.off);
-        lds_barrier();
-        if (has_output) {
+    const int tiles_wg = kWaves / a.splits;
+    const int wtile = wave / a.splits, ks = wave - wtile * a.splits;
+    const int tile = blockIdx.x * tiles_wg + wtile;
+    const bool active = 16 * tile < a.rows;
+    const int blocks = row_blocks<QT>(a.in);
+    const int64_t at = (int64_t(expert) * a.rows + 16 * (active ? tile : 0)) * a.row_bytes;
+    const uint8_t* const w[2] = {a.w0 + at, UP ? a.w1 + at : nullptr};
+    const uint32_t row_bytes = uint32_t(a.row_bytes), tile_bytes = 16 * row_bytes;
+    const uint32_t group_step = uint32_t(row_blocks_per_group<QT>() * a.stride);
+    const typename Tile<QT>::Lane lanes(lane, row_bytes);
+    uint8_t* slot = slots + wave * Tile<QT>::kSlot;
+    // this wave's groups ks, ks + splits, ...: item j
+    const int items = active && ks < a.groups ? (a.groups - ks + a.splits - 1) / a.splits : 0;
+    Tile<QT> buf[kDepth][kMats];
+    // (past the last item: its first again)
+    auto load = [&](auto slot_c, int j) __attribute__((always_inline)) {
+        const uint32_t at_byte = uint32_t(ks + a.splits * (j < items ? j : 0)) * group_step;
 #pragma unroll
-            for (int mat = 0; mat < kMats; ++mat)
-                sums[mat].add(split, j, g0, g0 + ng, [&](int g) {
-                    return part[(((g - g0) * nt + o_tile * kMats + mat) * T + o_t) * 16 + o_r];
-                });
+        for (int m = 0; m < kMats; ++m)
+            buf[decltype(slot_c)::value][m].load(w[m], lanes, at_byte, tile_bytes);
+    };
+    float acc[kMats][SETS];
+#pragma unroll
+    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int s = 0; s < SETS; ++s) acc[m][s] = 0.f;
+    const LaneTokens<QT> at0(lane, 0, count), at1(lane, SETS - 1, count);
+    const int unit = count * unit_bytes<QT>();
+    auto compute = [&](auto slot_c, int j, int g0) __attribute__((always_inline)) {
+        const int g = ks + a.splits * j;
+        const uint8_t* group = staged + (g - g0) * unit;
+        const uint8_t* mine = slot + n * Tile<QT>::kRow;
+        const uint32_t start =
+            whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(g) * group_step) & 15u);
+#pragma unroll
+        for (int m = 0; m < kMats; ++m) {
+            // (one wave's LDS operations complete in order: the reads see these writes, and the next
+            // writes come after the reads)
+            buf[decltype(slot_c)::value][m].store(slot, lane);
+            __builtin_amdgcn_wave_barrier();
+            Group<QT> d;
+            decode(d, mine, start, q, g, blocks, a.stride);
+            acc[m][0] = group_dot<QT>(d, group, at0, acc[m][0]);
+            if constexpr (SETS == 2) acc[m][1] = group_dot<QT>(d, group, at1, acc[m][1]);
+            __builtin_amdgcn_sched_barrier(0);   // one matrix at a time: registers
         }
-        lds_barrier();   // the partials and staged units are free
-    }
-    float v[kMats];
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    static_assert(kDepth == 2, "the loops below name the slots");
+    // Groups staged at a time: what fits the budget, whole turns of two groups per wave.
+    const int turn = kDepth * a.splits;
+    const int phase = min(a.groups, kStageBudget / unit / turn * turn);
+    int j = 0;
+    for (int g0 = 0; g0 < a.groups; g0 += phase) {
+        const int ng = min(phase, a.groups - g0);
+        // Units u = (group, token) of this phase, dealt to the waves; x is requested before the
+        // weights (a wave's loads return in order).
+        const int units = ng * count;
+        auto unit_x = [&](int u) {
+            const int g = u / count, t = u - g * count;
+            const int pair = list[t];
+            const int r = UP ? pair / a.topk : pair;
+            const int k0 = 256 * (g0 + g) + 4 * lane;
+            float4 v = {0.f, 0.f, 0.f, 0.f};
+            if (k0 < a.in) v = *reinterpret_cast<const float4*>(a.x + int64_t(r) * a.in + k0);
+            return v;
+        };
+        auto stage = [&](int u, const float4 v) {
+            const int g = u / count, t = u - g * count;
+            stage_token<QT>(staged + g * unit, t, count, v, lane);
+        };
+        constexpr int kBatch = 4;
+        for (int u0 = wave; u0 < units; u0 += kWaves * kBatch) {
+            float4 x[kBatch];
 #pragma unroll
-    for (int mat = 0; mat < kMats; ++mat) v[mat] = sums[mat].total(split, outputs, red);
-    if (tid < outputs && o_t < count) {
-        const int pair = list[o_t];
-        float r;
-        if constexpr (UP) r = activate(v[0], a.act) * v[1];
-        else r = a.wts[pair] * v[0];
-        a.out[int64_t(pair) * a.rows + 16 * (tile0 + o_tile) + o_r] = r;
+            for (int i = 0; i < kBatch; ++i) x[i] = unit_x(min(u0 + kWaves * i, units - 1));
+            if (g0 == 0 && u0 == wave) {
+                load(S0{}, 0);
+                load(S1{}, 1);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                if (u0 + kWaves * i < units) stage(u0 + kWaves * i, x[i]);
+        }
+        if (g0 == 0 && units <= wave) {   // (a wave without a unit to stage)
+            load(S0{}, 0);
+            load(S1{}, 1);
+        }
+        lds_barrier();
+        // One load per computed group, without conditions, so that the compiler waits for exactly
+        // the group it needs; the next phase's weights are on their way when a phase ends.
+        for (const int end = g0 + phase >= a.groups ? items : j + phase / a.splits; j < end; j += 2) {
+            compute(S0{}, j, g0);
+            load(S0{}, j + 2);
+            if (j + 1 < end) compute(S1{}, j + 1, g0);
+            load(S1{}, j + 3);
+        }
+        lds_barrier();   // the staged activations are free
+    }
+    // The parts of a tile meet in LDS, in the order of ks.  red: [mat][wave][token][row]
+    constexpr int kPart = 4 * SETS * 16;
+#pragma unroll
+    for (int m = 0; m < kMats; ++m)
+#pragma unroll
+        for (int s = 0; s < SETS; ++s) red[(m * kWaves + wave) * kPart + (4 * s + q) * 16 + n] = acc[m][s];
+    lds_barrier();
+    for (int o = tid; o < tiles_wg * count * 16; o += kThreads) {
+        const int r = o & 15, rest = o >> 4;
+        const int t = rest % count, wt = rest / count;
+        const int tl = blockIdx.x * tiles_wg + wt;
+        if (16 * tl >= a.rows) continue;
+        float v[kMats];
+#pragma unroll
+        for (int m = 0; m < kMats; ++m) {
+            const float* p = red + (m * kWaves + wt * a.splits) * kPart + t * 16 + r;
+            v[m] = p[0];
+            for (int k = 1; k < a.splits; ++k) v[m] += p[k * kPart];
+        }
+        const int pair = list[t];
+        float y;
+        if constexpr (UP) y = activate(v[0], a.act) * v[1];
+        else y = a.wts[pair] * v[0];
+        a.out[int64_t(pair) * a.rows + 16 * tl + r] = y;
     }
 }
 
-template <int QT, bool UP, bool PAIRS>
-__global__ __launch_bounds__(kThreads, PAIRS ? 4 : 2) void moe_group_kernel(MoeArgs a) {
-    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    uint8_t* zero = smem;                                     // 128 zero bytes
-    unsigned* bits = reinterpret_cast<unsigned*>(smem + 128); // chosen experts, a bit each
-    int* count_lds = reinterpret_cast<int*>(smem + 128 + kMoeMaxExperts / 8);
-    float* red = reinterpret_cast<float*>(smem + 128 + kMoeMaxExperts / 8 + 16);
-    int* list = reinterpret_cast<int*>(red + kThreads);
-    const int list_room = PAIRS ? 4 : (a.pairs + 3) & ~3;
-    uint8_t* staged = reinterpret_cast<uint8_t*>(list + list_room);
+constexpr size_t red_bytes(int mats, int sets) { return size_t(mats) * kWaves * 4 * sets * 16 * 4; }
+
+// The blockIdx.y-th chosen expert (-1: there are fewer) and its pairs, in order: list, *count.
+__device__ __forceinline__ int expert_pairs(const MoeArgs& a, unsigned* bits, int* count, int* list) {
+    chosen_experts(a, bits);
     const int tid = threadIdx.x;
-    const int tile0 = blockIdx.x * a.tiles;
-    const int tiles = min(a.tiles, a.rows / 16 - tile0);
-    if (tid < 32) reinterpret_cast<unsigned*>(zero)[tid] = 0u;
-    if constexpr (PAIRS) {
+    int slot = blockIdx.y, expert = -1;   // the slot-th set bit
+    for (int w = 0; w < kMoeMaxExperts / 32; ++w) {
+        unsigned b = bits[w];
+        const int c = __popc(b);
+        if (slot < c) {
+            for (; slot > 0; --slot) b &= b - 1;
+            expert = 32 * w + __ffs(int(b)) - 1;
+            break;
+        }
+        slot -= c;
+    }
+    expert = __builtin_amdgcn_readfirstlane(expert);
+    if (expert < 0) return expert;
+    if (tid < 64) {
+        int n = 0;
+        for (int p0 = 0; p0 < a.pairs; p0 += 64) {
+            const int p = p0 + tid;
+            const bool mine = p < a.pairs && a.ids[p] == expert;
+            const unsigned long long m = __ballot(mine);
+            if (mine) list[n + __popcll(m & ((1ull << tid) - 1))] = p;
+            n += __popcll(m);
+        }
+        if (tid == 0) *count = n;
+    }
+    lds_barrier();
+    return expert;
+}
+
+// ------------------------------------------------------------------ many tokens
+// blockIdx.y: the slot-th chosen expert; its 16-row tiles are dealt to the waves of the gridDim.x
+// workgroups.  A workgroup stages all groups of up to four of the expert's tokens, then every wave walks
+// its tiles (of the gate matrix, then of the up matrix) by itself: the stream of weights never stops
+// between tiles, and nothing but the staging needs a barrier.  More tokens: again, the
+// weights then come from cache.  Two workgroups per CU where the staged tokens leave the room.
+template <int QT, bool UP>
+__global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    unsigned* bits = reinterpret_cast<unsigned*>(smem);
+    int* count_lds = reinterpret_cast<int*>(bits + kMoeMaxExperts / 32);
+    int* list = count_lds + 4;
+    uint8_t* slots = reinterpret_cast<uint8_t*>(list + ((a.pairs + 3) & ~3));
+    uint8_t* staged = slots + kWaves * Tile<QT>::kSlot;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, q = lane >> 4;
+    const int expert = expert_pairs(a, bits, count_lds, list);
+    if (expert < 0) return;   // (uniform)
+    const int total = __builtin_amdgcn_readfirstlane(*count_lds);
+
+    const int tiles = a.rows >> 4, stride = int(gridDim.x) * kWaves;
+    const int tile0 = int(blockIdx.x) * kWaves + wave;
+    const int blocks = row_blocks<QT>(a.in);
+    const uint32_t row_bytes = uint32_t(a.row_bytes), tile_bytes = 16 * row_bytes;
+    const uint32_t group_step = uint32_t(row_blocks_per_group<QT>() * a.stride);
+    const typename Tile<QT>::Lane lanes(lane, row_bytes);
+    uint8_t* slot = slots + wave * Tile<QT>::kSlot;
+    const int64_t expert_at = int64_t(expert) * a.rows * a.row_bytes;
+
+    for (int c0 = 0; c0 < total; c0 += a.set) {
+        const int count = min(a.set, total - c0);
+        const int* mine = list + c0;
+        const int unit = count * unit_bytes<QT>();
+        // units u = (group, token), dealt to the waves in batches
+        const int units = a.groups * count;
+        constexpr int kBatch = 4;
+        for (int u0 = wave; u0 < units; u0 += kWaves * kBatch) {
+            float4 x[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int u = min(u0 + kWaves * i, units - 1);
+                const int g = u / count, pair = mine[u - g * count];
+                const int k0 = 256 * g + 4 * lane;
+                x[i] = float4{0.f, 0.f, 0.f, 0.f};
+                if (k0 < a.in)
+                    x[i] = *reinterpret_cast<const float4*>(a.x + int64_t(UP ? pair / a.topk : pair) * a.in + k0);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int u = u0 + kWaves * i;
+                const int g = u / count;
+                if (u < units) stage_token<QT>(staged + g * unit, u - g * count, count, x[i], lane);
+            }
+        }
+        struct Cursor {
+            int tile, mat, g;
+        };
+        auto step = [&](Cursor& c) {
+            if (++c.g < a.groups) return;
+            c.g = 0;
+            if (UP && c.mat == 0) {
+                c.mat = 1;
+            } else {
+                c.mat = 0;
+                c.tile += stride;
+            }
+        };
+        Cursor ld = {tile0, 0, 0}, cp = ld;
+        Tile<QT> buf[kDepth];
+        // (past the last tile: the last group again)
+        auto load = [&](auto slot_c) __attribute__((always_inline)) {
+            const uint8_t* w = (UP && ld.mat ? a.w1 : a.w0) + expert_at + int64_t(ld.tile) * tile_bytes;
+            buf[decltype(slot_c)::value].load(w, lanes, uint32_t(ld.g) * group_step, tile_bytes);
+            Cursor next = ld;
+            step(next);
+            if (next.tile < tiles) ld = next;
+        };
+        const LaneTokens<QT> at(lane, 0, count);
+        const int pair = mine[min(q, count - 1)];
+        const float weight = UP ? 0.f : a.wts[pair];
+        float* out = a.out + int64_t(pair) * a.rows + n;
+        float acc = 0.f, gate = 0.f;
+        auto compute = [&](auto slot_c) __attribute__((always_inline)) {
+            // (one wave's LDS operations complete in order: the reads see these writes, and the next
+            // writes come after the reads)
+            buf[decltype(slot_c)::value].store(slot, lane);
+            __builtin_amdgcn_wave_barrier();
+            const uint32_t start =
+                whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(cp.g) * group_step) & 15u);
+            Group<QT> w;
+            decode(w, slot + n * Tile<QT>::kRow, start, q, cp.g, blocks, a.stride);
+            acc = group_dot<QT>(w, staged + cp.g * unit, at, acc);
+            __builtin_amdgcn_wave_barrier();
+            if (cp.g == a.groups - 1) {
+                if (UP && cp.mat == 0) {
+                    gate = acc;
+                } else if (q < count) {
+                    float y;
+                    if constexpr (UP) y = activate(gate, a.act) * acc;
+                    else y = weight * acc;
+                    out[16 * cp.tile] = y;
+                }
+                acc = 0.f;
+            }
+            step(cp);
+        };
+        using S0 = std::integral_constant<int, 0>;
+        using S1 = std::integral_constant<int, 1>;
+        static_assert(kDepth == 2, "the loop below names the slots");
+        if (tile0 < tiles) {
+            load(S0{});
+            load(S1{});
+        }
+        lds_barrier();
+        if (tile0 < tiles) {
+            while (true) {
+                compute(S0{});
+                if (cp.tile >= tiles) break;
+                load(S0{});
+                compute(S1{});
+                if (cp.tile >= tiles) break;
+                load(S1{});
+            }
+        }
+        lds_barrier();   // the staged activations are free
+    }
+}
+
+template <int QT, bool UP, bool ONE>
+__global__ __launch_bounds__(kThreads, ONE && whole_chunks<QT>() ? 4 : 2) void moe_expert_kernel(MoeArgs a) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    constexpr int kMats = UP ? 2 : 1;
+    float* red = reinterpret_cast<float*>(smem);
+    unsigned* bits = reinterpret_cast<unsigned*>(smem + red_bytes(kMats, ONE ? 1 : 2));
+    int* count_lds = reinterpret_cast<int*>(bits + kMoeMaxExperts / 32);
+    int* list = count_lds + 4;
+    const int list_room = ONE ? 4 : (a.pairs + 3) & ~3;
+    uint8_t* slots = reinterpret_cast<uint8_t*>(list + list_room);
+    uint8_t* staged = slots + kWaves * Tile<QT>::kSlot;
+    const int tid = threadIdx.x;
+    if constexpr (ONE) {
         const int pair = blockIdx.y;
-        const int expert = a.ids[pair];
+        const int expert = __builtin_amdgcn_readfirstlane(a.ids[pair]);
         if (unsigned(expert) >= unsigned(a.experts)) return;   // (uniform) not this layer's: adds nothing
         if (tid == 0) list[0] = pair;
         lds_barrier();
-        float* part = reinterpret_cast<float*>(staged + a.phase * kUnitBytes);
-        group_chunk<QT, UP, 1, 4>(a, expert, tile0, tiles, list, 1, staged, zero, part, red);
+        expert_tiles<QT, UP, 1>(a, expert, list, 1, staged, slots, red);
     } else {
-        const int words = (a.experts + 31) >> 5;
-        if (tid < words) bits[tid] = 0u;
-        lds_barrier();
-        for (int p = tid; p < a.pairs; p += kThreads) {
-            const int e = a.ids[p];
-            if (unsigned(e) < unsigned(a.experts)) atomicOr(&bits[e >> 5], 1u << (e & 31));
-        }
-        lds_barrier();
-        int slot = blockIdx.y, expert = -1;   // the slot-th set bit
-        for (int w = 0; w < words; ++w) {
-            unsigned b = bits[w];
-            const int c = __popc(b);
-            if (slot < c) {
-                for (; slot > 0; --slot) b &= b - 1;
-                expert = 32 * w + __ffs(int(b)) - 1;
-                break;
-            }
-            slot -= c;
-        }
+        const int expert = expert_pairs(a, bits, count_lds, list);
         if (expert < 0) return;   // (uniform) fewer chosen experts than slots
-        if (tid < 64) {           // the expert's pairs, in order
-            int n = 0;
-            for (int p0 = 0; p0 < a.pairs; p0 += 64) {
-                const int p = p0 + tid;
-                const bool mine = p < a.pairs && a.ids[p] == expert;
-                const unsigned long long m = __ballot(mine);
-                if (mine) list[n + __popcll(m & ((1ull << tid) - 1))] = p;
-                n += __popcll(m);
-            }
-            if (tid == 0) *count_lds = n;
-        }
-        lds_barrier();
-        const int count = *count_lds;
+        const int count = __builtin_amdgcn_readfirstlane(*count_lds);
         for (int c0 = 0; c0 < count; c0 += kTokens) {
             const int c = min(kTokens, count - c0);
-            const int* l = list + c0;
-            auto go = [&](auto t_c, auto depth_c) {
-                constexpr int T = decltype(t_c)::value;
-                float* part = reinterpret_cast<float*>(staged + a.phase * T * kUnitBytes);
-                group_chunk<QT, UP, T, decltype(depth_c)::value>(a, expert, tile0, tiles, l, c, staged, zero, part,
-                                                                 red);
-            };
-            if (c == 1) go(std::integral_constant<int, 1>{}, std::integral_constant<int, 4>{});
-            else if (c == 2) go(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
-            else if (c <= 4) go(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
-            else go(std::integral_constant<int, 8>{}, std::integral_constant<int, 2>{});
+            if (c <= 4) expert_tiles<QT, UP, 1>(a, expert, list + c0, c, staged, slots, red);
+            else expert_tiles<QT, UP, 2>(a, expert, list + c0, c, staged, slots, red);
             lds_barrier();
         }
     }
 }
 
-// ------------------------------------------------------------------ down with few pairs
-// blockIdx.x: `tiles` 16-row tiles of Y, for every pair.  A unit is one 256-value group of one
-// pair's h; an item is a unit with one tile.
-template <int QT>
-__global__ __launch_bounds__(kThreads, 4) void moe_down_pairs_kernel(MoeArgs a) {
+// ------------------------------------------------------------------ down with few tokens
+// blockIdx.x: one 16-row tile of Y.  The chosen experts are its slots; wave w takes part w % splits of
+// the groups of slots w / splits, w / splits + waves / splits, ..., and stages their tokens' h itself,
+// a group at a time, in LDS of its own (no workgroup barrier until the end).  Every (slot, part)
+// leaves its pairs' sums in LDS; a token's parts are added in order, weighted, in choice order.
+// A token that names an expert twice has one h there, used with both weights.
+// LDS of the kernel, in bytes (THREADS, CT: tokens at most).
+template <int QT, int THREADS, int CT>
+struct FewLds {
+    static constexpr int kWavesOf = THREADS / 64;
+    static constexpr int kTables = kMoeMaxExperts / 8 + 16 + kMoeFewPairs * 4 * (4 + CT);
+    static constexpr int kStage = kWavesOf * (CT * unit_bytes<QT>() + Tile<QT>::kSlot);   // staged tokens, weights
+    static size_t bytes(int pairs, int splits) { return kTables + kStage + size_t(pairs) * splits * 64; }
+};
+
+template <int QT, int THREADS, int CT>
+__global__ __launch_bounds__(THREADS) void moe_down_few_kernel(MoeArgs a) {
+    using Lds = FewLds<QT, THREADS, CT>;
+    constexpr int kNW = THREADS / 64;
+    constexpr int SETS = (CT + 3) / 4;
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    uint8_t* zero = smem;
-    int* count_lds = reinterpret_cast<int*>(smem + 128);
-    float* red = reinterpret_cast<float*>(smem + 128 + 16);
-    int* list = reinterpret_cast<int*>(red + kThreads);          // valid pairs
-    int* expert_of = list + kMoeFewPairs;
-    float* weight_of = reinterpret_cast<float*>(expert_of + kMoeFewPairs);
-    int* first_of = reinterpret_cast<int*>(weight_of + kMoeFewPairs);   // valid pairs before token m's; [tokens + 1]
-    uint8_t* staged = reinterpret_cast<uint8_t*>(first_of + kMoeFewPairs + 4);
-    float* part = reinterpret_cast<float*>(staged + a.phase * kUnitBytes);
+    unsigned* bits = reinterpret_cast<unsigned*>(smem);
+    int* expert_of = reinterpret_cast<int*>(smem + kMoeMaxExperts / 8 + 16);   // [pair] ids; -1: not this layer's
+    int* first_of = expert_of + kMoeFewPairs;      // [pair] the token's first pair of the same expert
+    int* slot_expert = first_of + kMoeFewPairs;    // [slot]
+    int* slot_count = slot_expert + kMoeFewPairs;  // [slot] tokens
+    int* slot_pairs = slot_count + kMoeFewPairs;   // [slot][CT]
+    uint8_t* stage_all = smem + Lds::kTables;
+    float* res = reinterpret_cast<float*>(stage_all + Lds::kStage);            // [pair][part][16 rows]
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, q = lane >> 4;
-    if (tid < 32) reinterpret_cast<unsigned*>(zero)[tid] = 0u;
-    if (tid < 64) {   // (kMoeFewPairs <= 64)
+    const int tokens = a.pairs / a.topk;
+
+    // (kMoeFewPairs <= THREADS)
+    if (tid < kMoeMaxExperts / 32) bits[tid] = 0u;
+    if (tid < kMoeFewPairs) {
+        slot_count[tid] = 0;
         const int e = tid < a.pairs ? a.ids[tid] : -1;
-        const bool ok = unsigned(e) < unsigned(a.experts);
-        const unsigned long long m = __ballot(ok);
-        if (ok) {
-            const int at = __popcll(m & ((1ull << tid) - 1));
-            list[at] = tid;
-            expert_of[at] = e;
-            weight_of[at] = a.wts[tid];
+        expert_of[tid] = unsigned(e) < unsigned(a.experts) ? e : -1;
+    }
+    lds_barrier();
+    const int my_e = tid < a.pairs ? expert_of[tid] : -1;
+    const int my_m = tid < a.pairs ? tid / a.topk : 0;
+    if (my_e >= 0) {
+        atomicOr(&bits[my_e >> 5], 1u << (my_e & 31));
+        int f = my_m * a.topk;
+        while (expert_of[f] != my_e) ++f;    // (ends at the pair itself)
+        first_of[tid] = f;
+    } else if (tid < a.pairs) {
+        first_of[tid] = -1;
+    }
+    lds_barrier();
+    int slots = 0, my_slot = 0;
+    for (int w = 0; w < kMoeMaxExperts / 32; ++w) {
+        const unsigned b = bits[w];
+        if (my_e >= 0 && (my_e >> 5) == w) my_slot = slots + __popc(b & ((1u << (my_e & 31)) - 1));
+        slots += __popc(b);
+    }
+    if (my_e >= 0 && first_of[tid] == tid) {
+        int t = 0;
+        for (int p = 0; p < my_m * a.topk; ++p) t += first_of[p] == p && expert_of[p] == my_e;
+        slot_expert[my_slot] = my_e;
+        slot_pairs[my_slot * CT + t] = tid;
+        atomicMax(&slot_count[my_slot], t + 1);
+    }
+    lds_barrier();
+
+    const int tile = blockIdx.x;
+    const int ks = wave % a.splits, slot0 = wave / a.splits, slot_step = kNW / a.splits;
+    const int per_slot = ks < a.groups ? (a.groups - ks + a.splits - 1) / a.splits : 0;
+    const int my_slots = slot0 < slots ? (slots - slot0 + slot_step - 1) / slot_step : 0;
+    const int items = per_slot * my_slots;
+    const int blocks = row_blocks<QT>(a.in);
+    uint8_t* staged = stage_all + wave * (CT * unit_bytes<QT>() + Tile<QT>::kSlot);
+    uint8_t* slot = staged + CT * unit_bytes<QT>();
+    const uint32_t row_bytes = uint32_t(a.row_bytes), tile_bytes = 16 * row_bytes;
+    const uint32_t group_step = uint32_t(row_blocks_per_group<QT>() * a.stride);
+    const typename Tile<QT>::Lane lanes(lane, row_bytes);
+    struct Cursor {
+        int slot, i;
+    };
+    auto step = [&](Cursor& c) {
+        if (++c.i == per_slot) {
+            c.i = 0;
+            c.slot += slot_step;
         }
-        if (tid == 0) *count_lds = __popcll(m);
-        if (tid <= a.pairs / a.topk) {   // (kMoeFewPairs < 64: no shift by 64)
-            const int before = tid * a.topk;
-            first_of[tid] = __popcll(m & ((1ull << before) - 1));
+    };
+    Tile<QT> buf[kDepth];
+    float4 xs[kDepth][CT];
+    Cursor ld = {slot0, 0}, cp = {slot0, 0};
+    // (loads past the last item read the last one again)
+    auto load = [&](auto slot_c) __attribute__((always_inline)) {
+        constexpr int S = decltype(slot_c)::value;
+        const int g = ks + a.splits * ld.i;
+        const int e = __builtin_amdgcn_readfirstlane(slot_expert[ld.slot]);
+        const int count = __builtin_amdgcn_readfirstlane(slot_count[ld.slot]);
+        const int k0 = 256 * g + 4 * lane;
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            const int pair = __builtin_amdgcn_readfirstlane(slot_pairs[ld.slot * CT + min(t, count - 1)]);
+            xs[S][t] = float4{0.f, 0.f, 0.f, 0.f};
+            if (k0 < a.in) xs[S][t] = *reinterpret_cast<const float4*>(a.x + int64_t(pair) * a.in + k0);
+        }
+        buf[S].load(a.w0 + (int64_t(e) * a.rows + 16 * tile) * a.row_bytes, lanes, uint32_t(g) * group_step, tile_bytes);
+        Cursor next = ld;
+        step(next);
+        if (next.slot < slots) ld = next;
+    };
+    float acc[SETS];
+#pragma unroll
+    for (int s = 0; s < SETS; ++s) acc[s] = 0.f;
+    auto compute = [&](auto slot_c) __attribute__((always_inline)) {
+        constexpr int S = decltype(slot_c)::value;
+        const int count = __builtin_amdgcn_readfirstlane(slot_count[cp.slot]);
+        // (one wave's LDS operations complete in order: the reads below see these writes, and the
+        // next group's writes come after them)
+#pragma unroll
+        for (int t = 0; t < CT; ++t)
+            if (t < count) stage_token<QT>(staged, t, count, xs[S][t], lane);
+        buf[S].store(slot, lane);
+        __builtin_amdgcn_wave_barrier();
+        const int g = ks + a.splits * cp.i;
+        const uint32_t start =
+            whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(g) * group_step) & 15u);
+        Group<QT> w;
+        decode(w, slot + n * Tile<QT>::kRow, start, q, g, blocks, a.stride);
+#pragma unroll
+        for (int s = 0; s < SETS; ++s)
+            if (s == 0 || count > 4) acc[s] = group_dot<QT>(w, staged, LaneTokens<QT>(lane, s, count), acc[s]);
+        __builtin_amdgcn_wave_barrier();
+        if (cp.i == per_slot - 1) {
+#pragma unroll
+            for (int s = 0; s < SETS; ++s) {
+                if (4 * s + q < count) res[(slot_pairs[cp.slot * CT + 4 * s + q] * a.splits + ks) * 16 + n] = acc[s];
+                acc[s] = 0.f;
+            }
+        }
+        step(cp);
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    static_assert(kDepth == 2, "the loops below name the slots");
+    if (items > 0) {
+        load(S0{});
+        load(S1{});
+        for (int j = 0; j < items; j += 2) {
+            compute(S0{});
+            load(S0{});
+            if (j + 1 < items) compute(S1{});
+            load(S1{});
         }
     }
     lds_barrier();
-    const int valid = *count_lds;
-    const int tile0 = blockIdx.x * a.tiles;
-    const int nt = min(a.tiles, a.rows / 16 - tile0);
-    const int blocks = QT == kQ4_K || QT == kQ5_K || QT == kQ6_K ? a.in >> 8 : a.in >> 5;
-    const int tokens = a.pairs / a.topk;
-    // outputs o = (tile, token, row)
-    const int outputs = nt * 16 * tokens;     // (at most kThreads)
-    const int units = valid * a.groups;
-    const bool split = 4 * outputs <= kThreads;
-    const int j = split ? tid / outputs : 0, o = tid - j * outputs;
-    const int o_tile = o / (16 * tokens), o_m = (o >> 4) - o_tile * tokens, o_r = o & 15;
-    const bool has_output = split ? j < 4 : tid < outputs;
-    const int my0 = has_output ? first_of[o_m] * a.groups : 0;            // its token's units
-    const int my1 = has_output ? first_of[o_m + 1] * a.groups : 0;
-    RowSums sums;
-    for (int u0 = 0; u0 < units; u0 += a.phase) {
-        const int nu = min(a.phase, units - u0);
-        const int items = nu * nt;
-        const int i0 = wave * items / kWaves, i1 = (wave + 1) * items / kWaves;
-        auto where = [&](int i) {
-            const int u = i / nt, tile = i - u * nt;
-            const int v = (u0 + u) / a.groups, g = (u0 + u) - v * a.groups;
-            const int64_t row = int64_t(expert_of[v]) * a.rows + 16 * (tile0 + tile) + n;
-            return ItemAt{a.w0 + row * a.row_bytes, g, u};
-        };
-        auto source = [&](int u, const float*& p, int& left) {
-            const int v = (u0 + u) / a.groups, g = (u0 + u) - v * a.groups;
-            p = a.x + int64_t(list[v]) * a.in + 256 * g;
-            left = a.in - 256 * g;
-        };
-        EarlyX ex;
-        early_x(ex, source, nu, wave, lane);
-        Bytes<QT> buf[4];
-        prime_items<QT, 1, 4>(buf, where, i0, i1, q, blocks, a.stride, a.off);
-        stage_units<QT>(ex, source, staged, nu, wave, lane);
-        lds_barrier();
-        run_items<QT, 1, 4>(buf, where, i0, i1, lane, staged, zero, part, blocks, a.stride, a.off);
-        lds_barrier();
-        // (units counted from the token's first)
-        sums.add(split, j, max(u0, my0) - my0, min(u0 + nu, my1) - my0, [&](int u) {
-            const int at = my0 + u;
-            return weight_of[at / a.groups] * part[((at - u0) * nt + o_tile) * 16 + o_r];
-        });
-        lds_barrier();
-    }
-    const float sum = sums.total(split, outputs, red);
-    if (tid < outputs) {
-        const int64_t at = int64_t(o_m) * a.rows + 16 * (tile0 + o_tile) + o_r;
-        a.out[at] = a.residual ? a.residual[at] + sum : sum;
+    if (tid < tokens * 16) {
+        const int m = tid >> 4, r = tid & 15;
+        const int64_t at = int64_t(m) * a.rows + 16 * tile + r;
+        float y = 0.f;
+        for (int c = 0; c < a.topk; ++c) {
+            const int p = m * a.topk + c;
+            if (expert_of[p] < 0) continue;
+            const float* v = res + first_of[p] * a.splits * 16 + r;
+            float s = v[0];
+            const int parts = min(a.splits, a.groups);
+            for (int k = 1; k < parts; ++k) s += v[k * 16];
+            y = fmaf(a.wts[p], s, y);
+        }
+        a.out[at] = a.residual ? a.residual[at] + y : y;
     }
 }
 
@@ -787,60 +974,101 @@ hipError_t with_type(int type, F&& f) {
     }
 }
 
-int64_t row_bytes_of(int type, BlockLayout lay, int64_t in) { return in / block_values_of(type) * lay.stride; }
+void set_layout(MoeArgs& a, int type, BlockLayout lay) {
+    a.stride = lay.stride;
+    a.off = lay.off;
+    a.row_bytes = int64_t(a.in / block_values_of(type)) * lay.stride;
+    a.groups = (a.in + 255) / 256;
+}
+
+// Largest power of two that is at most `v` (v >= 1).
+int pow2_floor(int64_t v) {
+    int p = 1;
+    while (2 * p <= v) p *= 2;
+    return p;
+}
+
+template <int QT>
+size_t expert_lds_fixed(int pairs) {   // besides the staged activations
+    return kMoeMaxExperts / 8 + 16 + size_t((pairs + 3) & ~3) * 4 + size_t(kWaves) * Tile<QT>::kSlot;
+}
+
+template <int QT, bool UP>
+hipError_t launch_expert_typed(MoeArgs a, hipStream_t s) {
+    const int tokens = a.pairs / a.topk, tiles = a.rows / 16;
+    const int slots = std::min(a.pairs, a.experts);
+    if (!moe_few(tokens, a.topk)) {
+        // tokens staged together: four, or what the LDS of a CU holds of very long rows (else phases, below)
+        const size_t fixed = expert_lds_fixed<QT>(a.pairs), per_token = size_t(a.groups) * unit_bytes<QT>();
+        const size_t room = kGfx950LdsBytes > fixed ? (kGfx950LdsBytes - fixed) / per_token : 0;
+        a.set = int(std::min<size_t>({4, room, size_t(a.pairs)}));
+        if (a.set >= 1) {
+            // about two rounds of two workgroups per CU, each wave with at least two tiles
+            const int want = std::max(1, 1024 / slots);
+            const int grid = std::max(1, std::min(want, tiles / (2 * kWaves)));
+            hipLaunchKernelGGL((moe_many_kernel<QT, UP>), dim3(grid, slots), dim3(kThreads),
+                               fixed + size_t(a.set) * per_token, s, a);
+            return hipGetLastError();
+        }
+    }
+    const bool one = UP && tokens == 1;
+    // A tile's groups over as many waves as fill the chip for one token (about 2048 waves), by the
+    // layer's sizes alone.  (At most four: a turn of eight tokens' groups has to fit the staging budget.)
+    const int64_t want = 2048 / std::max<int64_t>(1, int64_t(tiles) * a.topk);
+    a.splits = pow2_floor(std::max<int64_t>(1, std::min<int64_t>({want, 4, a.groups})));
+    const int tiles_wg = kWaves / a.splits;
+    const int count = one ? 1 : std::min(kTokens, a.pairs);
+    const int turn = kDepth * a.splits;
+    const int unit = count * unit_bytes<QT>();
+    const int phase = std::min(a.groups, kStageBudget / unit / turn * turn);
+    const size_t lds = expert_lds_fixed<QT>(one ? 4 : a.pairs) + red_bytes(UP ? 2 : 1, one ? 1 : 2) +
+                       std::min<size_t>(kStageBudget, size_t(phase) * unit + (one ? 0 : size_t(turn) * unit));
+    const dim3 grid((tiles + tiles_wg - 1) / tiles_wg, one ? a.pairs : slots);
+    if constexpr (UP) {
+        if (one) {
+            hipLaunchKernelGGL((moe_expert_kernel<QT, true, true>), grid, dim3(kThreads), lds, s, a);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((moe_expert_kernel<QT, UP, false>), grid, dim3(kThreads), lds, s, a);
+    return hipGetLastError();
+}
 
 template <bool UP>
-hipError_t launch_group(int type, BlockLayout lay, MoeArgs a, bool pairs_mode, int cus, hipStream_t s) {
-    constexpr int kMats = UP ? 2 : 1;
-    a.stride = lay.stride;
-    a.off = lay.off;
-    a.row_bytes = row_bytes_of(type, lay, a.in);
-    a.groups = (a.in + 255) / 256;
-    const int slots = pairs_mode ? a.pairs : std::min(a.pairs, a.experts);
-    const int tiles = a.rows / 16;
-    // up to four tiles per workgroup while two workgroups per CU remain
-    a.tiles = int(std::min<int64_t>(4, std::max<int64_t>(1, int64_t(slots) * tiles / (2 * cus))));
-    const int T = pairs_mode ? 1 : kTokens;
-    const int per_group = T * (kUnitBytes + a.tiles * kMats * 64);
-    a.phase = std::max(1, std::min(a.groups, kStageBudget / per_group));
-    const int list_room = pairs_mode ? 4 : (a.pairs + 3) & ~3;
-    const size_t lds = 128 + kMoeMaxExperts / 8 + 16 + kThreads * 4 + size_t(list_room) * 4 + size_t(a.phase) * per_group;
-    const dim3 grid((tiles + a.tiles - 1) / a.tiles, slots);
+hipError_t launch_expert(int type, BlockLayout lay, MoeArgs a, hipStream_t s) {
+    set_layout(a, type, lay);
+    return with_type(type, [&](auto qt) { return launch_expert_typed<decltype(qt)::value, UP>(a, s); });
+}
+
+hipError_t launch_down_few(int type, BlockLayout lay, MoeArgs a, hipStream_t s) {
+    set_layout(a, type, lay);
+    const int tokens = a.pairs / a.topk;
+    a.splits = pow2_floor(std::max<int64_t>(1, std::min<int64_t>({16 / a.topk, 8, a.groups})));
+    const dim3 grid(a.rows / 16);
     return with_type(type, [&](auto qt) {
         constexpr int QT = decltype(qt)::value;
-        if constexpr (UP) {
-            if (pairs_mode) {
-                hipLaunchKernelGGL((moe_group_kernel<QT, true, true>), grid, dim3(kThreads), lds, s, a);
-                return hipGetLastError();
-            }
-        }
-        hipLaunchKernelGGL((moe_group_kernel<QT, UP, false>), grid, dim3(kThreads), lds, s, a);
+        if (tokens == 1)
+            hipLaunchKernelGGL((moe_down_few_kernel<QT, 1024, 1>), grid, dim3(1024),
+                               (FewLds<QT, 1024, 1>::bytes(a.pairs, a.splits)), s, a);
+        else if (tokens <= 4)
+            hipLaunchKernelGGL((moe_down_few_kernel<QT, 512, 4>), grid, dim3(512),
+                               (FewLds<QT, 512, 4>::bytes(a.pairs, a.splits)), s, a);
+        else
+            hipLaunchKernelGGL((moe_down_few_kernel<QT, 512, 8>), grid, dim3(512),
+                               (FewLds<QT, 512, 8>::bytes(a.pairs, a.splits)), s, a);
         return hipGetLastError();
     });
 }
 
-hipError_t launch_down_pairs(int type, BlockLayout lay, MoeArgs a, hipStream_t s) {
-    a.stride = lay.stride;
-    a.off = lay.off;
-    a.row_bytes = row_bytes_of(type, lay, a.in);
-    a.groups = (a.in + 255) / 256;
-    a.tiles = 1;
-    const int per_unit = kUnitBytes + a.tiles * 64;
-    a.phase = std::max(1, std::min(a.pairs * a.groups, kStageBudget / per_unit));
-    const size_t lds = 128 + 16 + kThreads * 4 + kMoeFewPairs * 16 + 16 + size_t(a.phase) * per_unit;
-    const dim3 grid((a.rows / 16 + a.tiles - 1) / a.tiles);
-    return with_type(type, [&](auto qt) {
-        constexpr int QT = decltype(qt)::value;
-        hipLaunchKernelGGL((moe_down_pairs_kernel<QT>), grid, dim3(kThreads), lds, s, a);
-        return hipGetLastError();
-    });
-}
-
-#define MQ_MOE_INSTANCES(QT)                                          \
-    template __global__ void moe_group_kernel<QT, true, true>(MoeArgs);   \
-    template __global__ void moe_group_kernel<QT, true, false>(MoeArgs);  \
-    template __global__ void moe_group_kernel<QT, false, false>(MoeArgs); \
-    template __global__ void moe_down_pairs_kernel<QT>(MoeArgs);
+#define MQ_MOE_INSTANCES(QT)                                                  \
+    template __global__ void moe_expert_kernel<QT, true, true>(MoeArgs);      \
+    template __global__ void moe_expert_kernel<QT, true, false>(MoeArgs);     \
+    template __global__ void moe_expert_kernel<QT, false, false>(MoeArgs);    \
+    template __global__ void moe_many_kernel<QT, true>(MoeArgs);              \
+    template __global__ void moe_many_kernel<QT, false>(MoeArgs);             \
+    template __global__ void moe_down_few_kernel<QT, 1024, 1>(MoeArgs);       \
+    template __global__ void moe_down_few_kernel<QT, 512, 4>(MoeArgs);        \
+    template __global__ void moe_down_few_kernel<QT, 512, 8>(MoeArgs);
 MQ_MOE_INSTANCES(kQ4_0)
 MQ_MOE_INSTANCES(kQ4_1)
 MQ_MOE_INSTANCES(kQ5_0)
@@ -855,12 +1083,8 @@ size_t h_bytes(int64_t pairs, int64_t F) { return round_up256(size_t(pairs) * si
 
 }  // namespace
 
-// Few pairs (kMoeFewPairs): every pair is a slot of its own, and an expert that two tokens share
-// is read twice (the second time from cache).
-bool moe_few_pairs(int64_t pairs) { return pairs <= kMoeFewPairs; }
-
-size_t moe_scratch_bytes(int64_t pairs, int64_t F, int64_t K) {
-    return h_bytes(pairs, F) + (moe_few_pairs(pairs) ? 0 : round_up256(size_t(pairs) * size_t(K) * 4));
+size_t moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K) {
+    return h_bytes(M * topk, F) + (moe_few(M, topk) ? 0 : round_up256(size_t(M * topk) * size_t(K) * 4));
 }
 
 hipError_t moe_set_attributes(size_t lds_limit) {
@@ -869,10 +1093,14 @@ hipError_t moe_set_attributes(size_t lds_limit) {
     for (int type : {kQ4_0, kQ4_1, kQ5_0, kQ5_1, kQ8_0, kQ4_K, kQ5_K, kQ6_K})
         e = e != hipSuccess ? e : with_type(type, [&](auto qt) {
             constexpr int QT = decltype(qt)::value;
-            const void* const kernels[] = {reinterpret_cast<const void*>(&moe_group_kernel<QT, true, true>),
-                                           reinterpret_cast<const void*>(&moe_group_kernel<QT, true, false>),
-                                           reinterpret_cast<const void*>(&moe_group_kernel<QT, false, false>),
-                                           reinterpret_cast<const void*>(&moe_down_pairs_kernel<QT>)};
+            const void* const kernels[] = {reinterpret_cast<const void*>(&moe_expert_kernel<QT, true, true>),
+                                           reinterpret_cast<const void*>(&moe_expert_kernel<QT, true, false>),
+                                           reinterpret_cast<const void*>(&moe_expert_kernel<QT, false, false>),
+                                           reinterpret_cast<const void*>(&moe_many_kernel<QT, true>),
+                                           reinterpret_cast<const void*>(&moe_many_kernel<QT, false>),
+                                           reinterpret_cast<const void*>(&moe_down_few_kernel<QT, 1024, 1>),
+                                           reinterpret_cast<const void*>(&moe_down_few_kernel<QT, 512, 4>),
+                                           reinterpret_cast<const void*>(&moe_down_few_kernel<QT, 512, 8>)};
             hipError_t r = hipSuccess;
             for (const void* k : kernels)
                 if (r == hipSuccess) r = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, room);
@@ -883,10 +1111,10 @@ hipError_t moe_set_attributes(size_t lds_limit) {
 
 hipError_t launch_moe_ffn(const MoeLayer& l, hipStream_t s, const char** name) {
     const int64_t pairs = l.M * l.topk;
-    const bool few = moe_few_pairs(pairs);
+    const bool few = moe_few(l.M, l.topk);
     float* h = static_cast<float*>(l.scratch);
     float* rows = reinterpret_cast<float*>(static_cast<uint8_t*>(l.scratch) + h_bytes(pairs, l.F));
-    *name = few ? "moe_pairs" : "moe_grouped";
+    *name = few ? "moe_few" : "moe_many";
     MoeArgs a = {};
     a.ids = l.ids;
     a.wts = l.wts;
@@ -900,7 +1128,7 @@ hipError_t launch_moe_ffn(const MoeLayer& l, hipStream_t s, const char** name) {
     a.out = h;
     a.in = int(l.K);
     a.rows = int(l.F);
-    hipError_t e = launch_group<true>(l.gu_type, l.gu_layout, a, few, l.cu_count, s);
+    hipError_t e = launch_expert<true>(l.gu_type, l.gu_layout, a, s);
     if (e != hipSuccess) return e;
     a.w0 = l.Wd;
     a.w1 = nullptr;
@@ -910,10 +1138,10 @@ hipError_t launch_moe_ffn(const MoeLayer& l, hipStream_t s, const char** name) {
     if (few) {
         a.residual = l.residual;
         a.out = l.Y;
-        return launch_down_pairs(l.d_type, l.d_layout, a, s);
+        return launch_down_few(l.d_type, l.d_layout, a, s);
     }
     a.out = rows;
-    e = launch_group<false>(l.d_type, l.d_layout, a, false, l.cu_count, s);
+    e = launch_expert<false>(l.d_type, l.d_layout, a, s);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned(l.K) / 4 + 255) / 256, unsigned(l.M)), dim3(256), 0, s, rows,
                        l.ids, l.residual, l.Y, int(l.topk), int(l.E), int(l.K));

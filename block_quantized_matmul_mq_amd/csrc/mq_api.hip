@@ -470,7 +470,7 @@ size_t mq_moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K) {
     if (M <= 0 || topk <= 0 || F <= 0 || K <= 0 || F > MQ_MAX_K || K > MQ_MAX_K || M > MQ_MOE_MAX_PAIRS ||
         topk > MQ_MOE_MAX_PAIRS || M * topk > MQ_MOE_MAX_PAIRS)
         return 0;
-    return moe_scratch_bytes(M * topk, F, K);
+    return moe_scratch_bytes(M, topk, F, K);
 }
 
 int mq_moe_ffn(const void* Wg, const void* Wu, int gu_type, const void* Wd, int d_type, const float* X,
@@ -501,7 +501,7 @@ int mq_moe_ffn(const void* Wg, const void* Wu, int gu_type, const void* Wd, int 
     if (M > MQ_MOE_MAX_PAIRS || topk > MQ_MOE_MAX_PAIRS || M * topk > MQ_MOE_MAX_PAIRS)
         return fail(MQ_ERR_SHAPE, "%s: M=%lld topk=%lld are more than %d (token, choice) pairs", fn, (long long)M,
                     (long long)topk, MQ_MOE_MAX_PAIRS);
-    const size_t need = moe_scratch_bytes(M * topk, F, K);
+    const size_t need = moe_scratch_bytes(M, topk, F, K);
     if (scratch_bytes < need)
         return fail(MQ_ERR_SIZE, "%s: scratch of %zu bytes, %zu required", fn, scratch_bytes, need);
     if (!aligned(Wg, 16) || !aligned(Wu, 16) || !aligned(Wd, 16) || !aligned(X, 16) || !aligned(Y, 16) ||
@@ -525,7 +525,6 @@ int mq_moe_ffn(const void* Wg, const void* Wu, int gu_type, const void* Wd, int 
     l.F = F;
     l.K = K;
     l.act = act;
-    l.cu_count = device_info()->cu_count;
     const char* kernel = "moe_ffn";
     if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, kernel);
     hipError_t e = launch_moe_ffn(l, static_cast<hipStream_t>(stream), &kernel);

@@ -37,7 +37,7 @@ class Layer:
         M, k = ids.shape
         say(f"moe {NAMES[self.gu]}/{NAMES[self.down]} M={M} k={k} E={self.E} F={self.F} K={self.K} {what}")
         Y = self.run(X, ids, wts, act, residual)
-        assert mq.last_kernel() == ("moe_pairs" if M * k <= 32 else "moe_grouped")
+        assert mq.last_kernel() == ("moe_few" if M <= 8 and M * k <= 128 else "moe_many")
         ref, bound = oracle.moe_ffn(self.raw[0], self.raw[1], self.gu, self.raw[2], self.down, X, ids, wts, self.E, self.F,
                                     act, residual)
         err = np.abs(Y - ref)
@@ -60,7 +60,7 @@ def inputs(M, k, E, K, seed, distinct=True):
 
 
 @pytest.mark.parametrize("qtype", ALL_TYPES, ids=[NAMES[t] for t in ALL_TYPES])
-@pytest.mark.parametrize("M,k", [(1, 2), (3, 3), (20, 2), (33, 1)])
+@pytest.mark.parametrize("M,k", [(1, 2), (3, 3), (7, 2), (20, 2), (33, 1)])
 def test_every_type(qtype, M, k):
     b = BLOCK[qtype]
     E, F, K = 5, (256 if b == 256 else 160), (512 if b == 256 else 352)
@@ -90,7 +90,7 @@ def test_sizes_of_one_block():
     Layer(mq.Q8_0, mq.Q4_0, 1, 32, 32, seed=71).check(X, ids, wts)
 
 
-@pytest.mark.parametrize("M,k", [(1, 4), (2, 16), (3, 16), (64, 2)])
+@pytest.mark.parametrize("M,k", [(1, 4), (2, 16), (3, 16), (8, 16), (8, 17), (64, 2)])
 def test_long_rows_take_phases(M, k):
     # rows of many 256-value groups: more than fit the staging LDS at once
     E, F, K = 6, 2560, 5120
@@ -121,7 +121,7 @@ def test_invalid_ids_add_nothing(M):
     assert np.array_equal(lay.run(X, ids, wts, residual=res), res)
 
 
-@pytest.mark.parametrize("M", [1, 33])
+@pytest.mark.parametrize("M", [1, 6, 33])
 def test_repeated_expert_and_zero_weight(M):
     E, F, K = 3, 256, 512
     X, ids, wts = inputs(M, 4, E, K, 12, distinct=False)
@@ -130,7 +130,7 @@ def test_repeated_expert_and_zero_weight(M):
     Layer(mq.Q6_K, mq.Q8_0, E, F, K, seed=100).check(X, ids, wts)
 
 
-@pytest.mark.parametrize("M", [2, 40])
+@pytest.mark.parametrize("M", [2, 8, 40])
 def test_rows_do_not_depend_on_the_batch(M):
     """A token's bits are the same alone among other tokens of the same kernels."""
     E, F, K = 8, 512, 768
@@ -149,7 +149,7 @@ def test_a_token_alone_equals_itself_among_few():
     E, F, K = 8, 1024, 2048
     lay = Layer(mq.Q4_K, mq.Q4_K, E, F, K, seed=115)
     X, ids, wts = inputs(4, 8, E, K, 14)
-    Y = lay.run(X, ids, wts)                  # 32 pairs
+    Y = lay.run(X, ids, wts)
     for m in range(4):
         assert np.array_equal(lay.run(X[m:m + 1], ids[m:m + 1], wts[m:m + 1])[0], Y[m])
 
