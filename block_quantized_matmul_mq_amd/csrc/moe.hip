@@ -61,6 +61,7 @@ constexpr int kPlane = 288;                  // bytes of a staged digit plane: 2
 constexpr int kPlanes = 3 * kPlane;
 constexpr int kStageBudget = 64 * 1024;      // LDS of staged activations
 constexpr int kDepth = 2;                    // weight groups in flight per wave
+constexpr int kManyFixed = 64;               // many tokens: LDS of the slot's list
 
 // A wave-uniform pointer to device memory held in scalar registers: a load from it plus a 32-bit lane
 // offset then takes one vector register for its address (the compiler otherwise keeps a 64-bit pointer
@@ -602,131 +603,193 @@ __device__ __forceinline__ int expert_pairs(const MoeArgs& a, unsigned* bits, in
 }
 
 // ------------------------------------------------------------------ many tokens
-// blockIdx.y: the slot-th chosen expert; its 16-row tiles are dealt to the waves of the gridDim.x
-// workgroups.  A workgroup stages all groups of up to four of the expert's tokens, then every wave walks
-// its tiles (of the gate matrix, then of the up matrix) by itself: the stream of weights never stops
-// between tiles, and nothing but the staging needs a barrier.  More tokens: again, the
-// weights then come from cache.  Two workgroups per CU where the staged tokens leave the room.
+// blockIdx.y: a slot, `set` (at most four) tokens of one chosen expert; the expert's units (16 rows of
+// one matrix) are dealt to the waves of the gridDim.x workgroups.  A workgroup stages all groups of the
+// slot's tokens, then every wave walks its units by itself: nothing but the staging needs a barrier,
+// and the stream of weights does not stop between units.  The slots of an expert of more
+// tokens read the same weights at about the same time (from HBM once).
+//   up    leaves the gate and the up sums, f32 [pair][F] each: act(g) * u is formed where the down
+//         kernel stages h, so that a wave's unit is one matrix's 16 rows (at 48 tokens, 4096 x 1536,
+//         the last round of waves is then 1 of 7 and not 1 of 4)
+//   down  leaves the weighted rows, f32 [pair][K].
+
+// Slot blockIdx.y: its expert (-1: there are fewer slots), and its pairs in list[0 .. *count - 1].
+// LDS: counts [kMoeMaxExperts], tmp [16], list.  Slots are numbered expert by expert.
+__device__ __forceinline__ int slot_pairs_of(const MoeArgs& a, int* counts, int* tmp, int* count, int* list) {
+    static_assert(kMoeMaxExperts <= kThreads, "a thread per expert");
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    counts[tid] = 0;
+    if (tid == 0) tmp[8] = -1;
+    lds_barrier();
+    for (int p = tid; p < a.pairs; p += kThreads) {
+        const int e = a.ids[p];
+        if (unsigned(e) < unsigned(a.experts)) atomicAdd(&counts[e], 1);
+    }
+    lds_barrier();
+    // slots before expert tid's: a scan over the wave, then over the waves
+    const int mine = (counts[tid] + a.set - 1) / a.set;
+    int before = mine;
+    for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(before, off, 64);
+        if (lane >= off) before += v;
+    }
+    if (lane == 63) tmp[wave] = before;
+    lds_barrier();
+    for (int w = 0; w < wave; ++w) before += tmp[w];
+    before -= mine;
+    const int s = int(blockIdx.y) - before;
+    if (s >= 0 && s < mine) {
+        tmp[8] = tid;
+        tmp[9] = s * a.set;                                   // rank of the slot's first pair
+        *count = min(a.set, counts[tid] - s * a.set);
+    }
+    lds_barrier();
+    const int expert = __builtin_amdgcn_readfirstlane(tmp[8]);
+    if (expert < 0) return expert;
+    // ranks of the expert's pairs: wave w takes a consecutive part of them
+    const int first = tmp[9];
+    const int per = ((a.pairs + kWaves - 1) / kWaves + 63) & ~63;
+    const int p0 = wave * per, p1 = min(a.pairs, p0 + per);
+    int n = 0;
+    for (int p = p0 + lane; p - lane < p1; p += 64) n += __popcll(__ballot(p < p1 && a.ids[p] == expert));
+    lds_barrier();
+    if (lane == 0) tmp[wave] = n;
+    lds_barrier();
+    int rank = -first;
+    for (int w = 0; w < wave; ++w) rank += tmp[w];
+    for (int p = p0 + lane; p - lane < p1; p += 64) {
+        const bool is = p < p1 && a.ids[p] == expert;
+        const unsigned long long m = __ballot(is);
+        const int r = rank + __popcll(m & ((1ull << lane) - 1));
+        if (is && r >= 0 && r < a.set) list[r] = p;
+        rank += __popcll(m);
+    }
+    lds_barrier();
+    return expert;
+}
+
 template <int QT, bool UP>
 __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    unsigned* bits = reinterpret_cast<unsigned*>(smem);
-    int* count_lds = reinterpret_cast<int*>(bits + kMoeMaxExperts / 32);
-    int* list = count_lds + 4;
-    uint8_t* slots = reinterpret_cast<uint8_t*>(list + ((a.pairs + 3) & ~3));
+    int* tmp = reinterpret_cast<int*>(smem);   // [16], the count, the list of four
+    int* count_lds = tmp + 10;
+    int* list = tmp + 12;
+    uint8_t* slots = smem + kManyFixed;
     uint8_t* staged = slots + kWaves * Tile<QT>::kSlot;
+    int* counts = reinterpret_cast<int*>(slots);   // (before the first weights)
+    static_assert(kWaves * Tile<QT>::kSlot >= kMoeMaxExperts * 4, "room for the counts");
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, q = lane >> 4;
-    const int expert = expert_pairs(a, bits, count_lds, list);
+    const int expert = slot_pairs_of(a, counts, tmp, count_lds, list);
     if (expert < 0) return;   // (uniform)
-    const int total = __builtin_amdgcn_readfirstlane(*count_lds);
+    const int count = __builtin_amdgcn_readfirstlane(*count_lds);
 
-    const int tiles = a.rows >> 4, stride = int(gridDim.x) * kWaves;
-    const int tile0 = int(blockIdx.x) * kWaves + wave;
+    constexpr int kMats = UP ? 2 : 1;
+    const int units = (a.rows >> 4) * kMats, stride = int(gridDim.x) * kWaves;
+    const int unit0 = int(blockIdx.x) * kWaves + wave;
     const int blocks = row_blocks<QT>(a.in);
     const uint32_t row_bytes = uint32_t(a.row_bytes), tile_bytes = 16 * row_bytes;
     const uint32_t group_step = uint32_t(row_blocks_per_group<QT>() * a.stride);
     const typename Tile<QT>::Lane lanes(lane, row_bytes);
     uint8_t* slot = slots + wave * Tile<QT>::kSlot;
     const int64_t expert_at = int64_t(expert) * a.rows * a.row_bytes;
+    const int unit_size = count * unit_bytes<QT>();
 
-    for (int c0 = 0; c0 < total; c0 += a.set) {
-        const int count = min(a.set, total - c0);
-        const int* mine = list + c0;
-        const int unit = count * unit_bytes<QT>();
-        // units u = (group, token), dealt to the waves in batches
-        const int units = a.groups * count;
-        constexpr int kBatch = 4;
-        for (int u0 = wave; u0 < units; u0 += kWaves * kBatch) {
-            float4 x[kBatch];
+    // Stage the tokens: (group, token), dealt to the waves in batches.
+    const int staging = a.groups * count;
+    constexpr int kBatch = UP ? 4 : 2;
+    for (int u0 = wave; u0 < staging; u0 += kWaves * kBatch) {
+        float4 x[kBatch], y[kBatch];
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int u = min(u0 + kWaves * i, units - 1);
-                const int g = u / count, pair = mine[u - g * count];
-                const int k0 = 256 * g + 4 * lane;
-                x[i] = float4{0.f, 0.f, 0.f, 0.f};
-                if (k0 < a.in)
-                    x[i] = *reinterpret_cast<const float4*>(a.x + int64_t(UP ? pair / a.topk : pair) * a.in + k0);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int u = u0 + kWaves * i;
-                const int g = u / count;
-                if (u < units) stage_token<QT>(staged + g * unit, u - g * count, count, x[i], lane);
+        for (int i = 0; i < kBatch; ++i) {
+            const int u = min(u0 + kWaves * i, staging - 1);
+            const int g = u / count, pair = list[u - g * count];
+            const int k0 = 256 * g + 4 * lane;
+            x[i] = y[i] = float4{0.f, 0.f, 0.f, 0.f};
+            if (k0 < a.in) {
+                const float* p = a.x + int64_t(UP ? pair / a.topk : pair) * a.in + k0;
+                x[i] = *reinterpret_cast<const float4*>(p);
+                if constexpr (!UP) y[i] = *reinterpret_cast<const float4*>(p + int64_t(a.pairs) * a.in);
             }
         }
-        struct Cursor {
-            int tile, mat, g;
-        };
-        auto step = [&](Cursor& c) {
-            if (++c.g < a.groups) return;
-            c.g = 0;
-            if (UP && c.mat == 0) {
-                c.mat = 1;
-            } else {
-                c.mat = 0;
-                c.tile += stride;
-            }
-        };
-        Cursor ld = {tile0, 0, 0}, cp = ld;
-        Tile<QT> buf[kDepth];
-        // (past the last tile: the last group again)
-        auto load = [&](auto slot_c) __attribute__((always_inline)) {
-            const uint8_t* w = (UP && ld.mat ? a.w1 : a.w0) + expert_at + int64_t(ld.tile) * tile_bytes;
-            buf[decltype(slot_c)::value].load(w, lanes, uint32_t(ld.g) * group_step, tile_bytes);
-            Cursor next = ld;
-            step(next);
-            if (next.tile < tiles) ld = next;
-        };
-        const LaneTokens<QT> at(lane, 0, count);
-        const int pair = mine[min(q, count - 1)];
-        const float weight = UP ? 0.f : a.wts[pair];
-        float* out = a.out + int64_t(pair) * a.rows + n;
-        float acc = 0.f, gate = 0.f;
-        auto compute = [&](auto slot_c) __attribute__((always_inline)) {
-            // (one wave's LDS operations complete in order: the reads see these writes, and the next
-            // writes come after the reads)
-            buf[decltype(slot_c)::value].store(slot, lane);
-            __builtin_amdgcn_wave_barrier();
-            const uint32_t start =
-                whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(cp.g) * group_step) & 15u);
-            Group<QT> w;
-            decode(w, slot + n * Tile<QT>::kRow, start, q, cp.g, blocks, a.stride);
-            acc = group_dot<QT>(w, staged + cp.g * unit, at, acc);
-            __builtin_amdgcn_wave_barrier();
-            if (cp.g == a.groups - 1) {
-                if (UP && cp.mat == 0) {
-                    gate = acc;
-                } else if (q < count) {
-                    float y;
-                    if constexpr (UP) y = activate(gate, a.act) * acc;
-                    else y = weight * acc;
-                    out[16 * cp.tile] = y;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int u = u0 + kWaves * i;
+            const int g = u / count;
+            if (u < staging) {
+                float4 h = x[i];
+                if constexpr (!UP) {
+                    h.x = activate(h.x, a.act) * y[i].x;
+                    h.y = activate(h.y, a.act) * y[i].y;
+                    h.z = activate(h.z, a.act) * y[i].z;
+                    h.w = activate(h.w, a.act) * y[i].w;
                 }
-                acc = 0.f;
+                stage_token<QT>(staged + g * unit_size, u - g * count, count, h, lane);
             }
-            step(cp);
-        };
-        using S0 = std::integral_constant<int, 0>;
-        using S1 = std::integral_constant<int, 1>;
-        static_assert(kDepth == 2, "the loop below names the slots");
-        if (tile0 < tiles) {
+        }
+    }
+    struct Cursor {
+        int unit, g;
+    };
+    auto step = [&](Cursor& c) {
+        if (++c.g == a.groups) {
+            c.g = 0;
+            c.unit += stride;
+        }
+    };
+    Cursor ld = {unit0, 0}, cp = ld;
+    Tile<QT> buf[kDepth];
+    // (past the last unit: its last group again)
+    auto load = [&](auto slot_c) __attribute__((always_inline)) {
+        const uint8_t* w = (UP && (ld.unit & 1) ? a.w1 : a.w0) + expert_at + int64_t(UP ? ld.unit >> 1 : ld.unit) * tile_bytes;
+        buf[decltype(slot_c)::value].load(w, lanes, uint32_t(ld.g) * group_step, tile_bytes);
+        Cursor next = ld;
+        step(next);
+        if (next.unit < units) ld = next;
+    };
+    const LaneTokens<QT> at(lane, 0, count);
+    const int pair = list[min(q, count - 1)];
+    const float weight = UP ? 1.f : a.wts[pair];
+    float* out = a.out + int64_t(pair) * a.rows + n;
+    float acc = 0.f;
+    auto compute = [&](auto slot_c) __attribute__((always_inline)) {
+        // (one wave's LDS operations complete in order: the reads see these writes, and the next
+        // writes come after the reads)
+        buf[decltype(slot_c)::value].store(slot, lane);
+        __builtin_amdgcn_wave_barrier();
+        const uint32_t start =
+            whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(cp.g) * group_step) & 15u);
+        Group<QT> w;
+        decode(w, slot + n * Tile<QT>::kRow, start, q, cp.g, blocks, a.stride);
+        acc = group_dot<QT>(w, staged + cp.g * unit_size, at, acc);
+        __builtin_amdgcn_wave_barrier();
+        if (cp.g == a.groups - 1) {
+            if (q < count) {
+                if constexpr (UP) out[int64_t(cp.unit & 1) * a.pairs * a.rows + 16 * (cp.unit >> 1)] = acc;
+                else out[16 * cp.unit] = weight * acc;
+            }
+            acc = 0.f;
+        }
+        step(cp);
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    static_assert(kDepth == 2, "the loop below names the slots");
+    if (unit0 < units) {
+        load(S0{});
+        load(S1{});
+    }
+    lds_barrier();
+    if (unit0 < units) {
+        while (true) {
+            compute(S0{});
+            if (cp.unit >= units) break;
             load(S0{});
+            compute(S1{});
+            if (cp.unit >= units) break;
             load(S1{});
         }
-        lds_barrier();
-        if (tile0 < tiles) {
-            while (true) {
-                compute(S0{});
-                if (cp.tile >= tiles) break;
-                load(S0{});
-                compute(S1{});
-                if (cp.tile >= tiles) break;
-                load(S1{});
-            }
-        }
-        lds_barrier();   // the staged activations are free
     }
 }
 
@@ -998,15 +1061,18 @@ hipError_t launch_expert_typed(MoeArgs a, hipStream_t s) {
     const int tokens = a.pairs / a.topk, tiles = a.rows / 16;
     const int slots = std::min(a.pairs, a.experts);
     if (!moe_few(tokens, a.topk)) {
-        // tokens staged together: four, or what the LDS of a CU holds of very long rows (else phases, below)
-        const size_t fixed = expert_lds_fixed<QT>(a.pairs), per_token = size_t(a.groups) * unit_bytes<QT>();
-        const size_t room = kGfx950LdsBytes > fixed ? (kGfx950LdsBytes - fixed) / per_token : 0;
-        a.set = int(std::min<size_t>({4, room, size_t(a.pairs)}));
+        // tokens of a slot: four, or what the LDS of a CU holds of very long rows (else phases, below)
+        const size_t fixed = kManyFixed + size_t(kWaves) * Tile<QT>::kSlot;
+        const size_t per_token = size_t(a.groups) * unit_bytes<QT>();
+        a.set = int(std::min<size_t>({4, (kGfx950LdsBytes - fixed) / per_token, size_t(a.pairs)}));
         if (a.set >= 1) {
-            // about two rounds of two workgroups per CU, each wave with at least two tiles
-            const int want = std::max(1, 1024 / slots);
-            const int grid = std::max(1, std::min(want, tiles / (2 * kWaves)));
-            hipLaunchKernelGGL((moe_many_kernel<QT, UP>), dim3(grid, slots), dim3(kThreads),
+            const int many_slots = std::min(a.pairs, a.experts + a.pairs / a.set);
+            // about 16 KiB of weights per wave before it starts again with another slot
+            const int units = tiles * (UP ? 2 : 1);
+            const int64_t unit_bytes_of = 16 * a.row_bytes;
+            const int per_wave = int(std::max<int64_t>(1, 32768 / unit_bytes_of));
+            const int grid = std::max(1, units / (kWaves * per_wave));
+            hipLaunchKernelGGL((moe_many_kernel<QT, UP>), dim3(grid, many_slots), dim3(kThreads),
                                fixed + size_t(a.set) * per_token, s, a);
             return hipGetLastError();
         }
@@ -1084,7 +1150,9 @@ size_t h_bytes(int64_t pairs, int64_t F) { return round_up256(size_t(pairs) * si
 }  // namespace
 
 size_t moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K) {
-    return h_bytes(M * topk, F) + (moe_few(M, topk) ? 0 : round_up256(size_t(M * topk) * size_t(K) * 4));
+    // h of every pair; many tokens: its two factors, and the weighted rows
+    if (moe_few(M, topk)) return h_bytes(M * topk, F);
+    return h_bytes(2 * M * topk, F) + round_up256(size_t(M * topk) * size_t(K) * 4);
 }
 
 hipError_t moe_set_attributes(size_t lds_limit) {
@@ -1113,7 +1181,7 @@ hipError_t launch_moe_ffn(const MoeLayer& l, hipStream_t s, const char** name) {
     const int64_t pairs = l.M * l.topk;
     const bool few = moe_few(l.M, l.topk);
     float* h = static_cast<float*>(l.scratch);
-    float* rows = reinterpret_cast<float*>(static_cast<uint8_t*>(l.scratch) + h_bytes(pairs, l.F));
+    float* rows = reinterpret_cast<float*>(static_cast<uint8_t*>(l.scratch) + h_bytes(2 * pairs, l.F));
     *name = few ? "moe_few" : "moe_many";
     MoeArgs a = {};
     a.ids = l.ids;

@@ -66,7 +66,7 @@ def test_moe_sizes_and_refusals():
     size = mq.moe_scratch_bytes
     assert size(0, 2, 256, 512) == size(1, 0, 256, 512) == size(2049, 2, 256, 512) == size(1, 1, 1 << 16, 512) == 0
     assert size(1, 8, 256, 512) == 8 * 256 * 4                        # h of every pair
-    assert size(16, 8, 256, 512) == 128 * 256 * 4 + 128 * 512 * 4     # and the weighted rows
+    assert size(16, 8, 256, 512) == 2 * 128 * 256 * 4 + 128 * 512 * 4     # its two factors, and the weighted rows
     for name in ("Wg", "Wu", "Wd", "X", "ids", "wts", "Y", "s"):
         assert ffn(**{name: None}) == -1, name
     assert ffn(M=0) == -1 and ffn(k=-1) == -1 and ffn(E=0) == -1 and ffn(act=9) == -1 and ffn(F=0) == -1
