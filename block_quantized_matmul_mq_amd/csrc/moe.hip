@@ -6,15 +6,15 @@
 // times, so the floor is the chosen experts' bytes from HBM; everything here is arranged to
 // keep weight loads in flight and to spend few instructions per weight.
 //
-// Split.  Two launches, because every output of the down product needs every h of its token:
-//   up    one workgroup per (chosen expert, a few 16-row tiles of F), for all the expert's
-//         pairs: both the gate and the up rows, so that act(g) * u is formed where both sums
-//         meet; h goes to scratch, f32 [pair][F].
-//   down  up to kMoeFewTokens tokens: one workgroup per 16 rows of Y for every expert, which adds a
-//         token's choices itself (nothing is exchanged between workgroups); more tokens: one per
-//         (chosen expert, tiles), weighted partial rows to scratch [pair][K], and a third launch
-//         adds each token's rows in choice order.
-// An expert's weights are read once for all its tokens (eight at a time).
+// Split.  Two launches at least, because every output of the down product needs every h of its token.
+//   One token: `up`, a workgroup per (choice, a few 16-row tiles of F) that forms act(g) * u where both sums
+//   meet, h f32 [choice][F] to scratch; `down`, a workgroup per 16 rows of Y for every choice, which
+//   adds the choices itself (nothing is exchanged between workgroups).
+//   More tokens: a slot is up to `set` tokens of one chosen expert, whose weights are read once for all
+//   of them; `up` leaves the gate and the up sums, `down` the weighted rows of every pair, and a
+//   third launch adds a token's rows in choice order.  (Two tokens already gain from it: 64 experts of
+//   2048 x 1024, 8 choices, Q4_K: 35.2 us against 37.8 with the one-token kernels extended to few
+//   tokens, four tokens 44.3 against 65.5, eight 56.7 against 109.)
 //
 // Arithmetic.  The exact-integer scheme of the GEMV kernels: per 32-value block of the
 // activations x = 2^-s v with v an integer of at most 22 bits (relative to the block's largest
@@ -45,8 +45,8 @@
 
 namespace mq {
 
-// Few tokens: at most kMoeFewTokens of at most kMoeFewPairs pairs.
-bool moe_few(int64_t M, int64_t topk) { return M <= kMoeFewTokens && M * topk <= kMoeFewPairs; }
+// The kernels of one token: at most kMoeOneTopk choices.
+static bool moe_one(int64_t M, int64_t topk) { return M == 1 && topk <= kMoeOneTopk; }
 
 namespace {
 
@@ -56,11 +56,10 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kFracBits = 22;
-constexpr int kTokens = 8;                   // tokens of one expert computed together
 constexpr int kPlane = 288;                  // bytes of a staged digit plane: 256 and 32 (bank spread)
 constexpr int kPlanes = 3 * kPlane;
-constexpr int kStageBudget = 64 * 1024;      // LDS of staged activations
 constexpr int kDepth = 2;                    // weight groups in flight per wave
+constexpr int kOneUpWaves = 4096;            // waves of the one-token up kernel
 constexpr int kManyFixed = 64;               // many tokens: LDS of the slot's list
 
 // A wave-uniform pointer to device memory held in scalar registers: a load from it plus a 32-bit lane
@@ -392,15 +391,15 @@ __device__ __forceinline__ float group_dot(const Group<QT>& w, const uint8_t* st
 struct MoeArgs {
     const uint8_t* w0;     // up: gate weights; down: down weights
     const uint8_t* w1;     // up: up weights
-    const float* x;        // up: X [M][in]; down: h [pair][in]
+    const float* x;        // up: X [M][in]; down: h [choice][in], or its factors, each [pair][in]
     const int32_t* ids;    // [pairs]
     const float* wts;      // [pairs] (down)
-    const float* residual; // [M][rows] or null (down, few tokens)
-    float* out;            // up: h [pair][rows]; down: Y [M][rows], or weighted rows [pair][rows]
+    const float* residual; // [rows] or null (down, one token)
+    float* out;            // one token: h [choice][rows], Y [rows]; else the factors [pair][rows] each, weighted rows
     int pairs, topk, experts;
     int in, rows;          // values per weight row, weight rows per expert
     int groups;            // 256-value groups per row
-    int splits;            // waves that share a tile's groups (wave ks takes groups ks, ks + splits, ..)
+    int splits;            // one token: waves that share a tile's groups (part ks: groups ks, ks + splits, ..)
     int set;               // many tokens: tokens staged together
     int act;
     int stride, off;       // weight block layout
@@ -416,190 +415,6 @@ __device__ __forceinline__ int row_blocks(int in) {
 template <int QT>
 constexpr int row_blocks_per_group() {
     return QT == kQ4_K || QT == kQ5_K || QT == kQ6_K ? 1 : 8;
-}
-
-// The chosen experts as bits in LDS (`bits`, kMoeMaxExperts of them); ends with a barrier.
-__device__ __forceinline__ void chosen_experts(const MoeArgs& a, unsigned* bits) {
-    const int tid = threadIdx.x;
-    if (tid < kMoeMaxExperts / 32) bits[tid] = 0u;
-    lds_barrier();
-    for (int p = tid; p < a.pairs; p += kThreads) {
-        const int e = a.ids[p];
-        if (unsigned(e) < unsigned(a.experts)) atomicOr(&bits[e >> 5], 1u << (e & 31));
-    }
-    lds_barrier();
-}
-
-// ------------------------------------------------------------------ up, and down with many tokens
-// blockIdx.x: kWaves / splits 16-row tiles of the expert; blockIdx.y: the slot-th chosen expert, or
-// (ONE token) the token's choice.  Wave w: tile w / splits of the workgroup, part w % splits of its groups.
-// SETS: four tokens each.
-template <int QT, bool UP, int SETS>
-__device__ __forceinline__ void expert_tiles(const MoeArgs& a, int expert, const int* list, int count, uint8_t* staged,
-                                             uint8_t* slots, float* red) {
-    constexpr int kMats = UP ? 2 : 1;
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n = lane & 15, q = lane >> 4;
-    const int tiles_wg = kWaves / a.splits;
-    const int wtile = wave / a.splits, ks = wave - wtile * a.splits;
-    const int tile = blockIdx.x * tiles_wg + wtile;
-    const bool active = 16 * tile < a.rows;
-    const int blocks = row_blocks<QT>(a.in);
-    const int64_t at = (int64_t(expert) * a.rows + 16 * (active ? tile : 0)) * a.row_bytes;
-    const uint8_t* const w[2] = {a.w0 + at, UP ? a.w1 + at : nullptr};
-    const uint32_t row_bytes = uint32_t(a.row_bytes), tile_bytes = 16 * row_bytes;
-    const uint32_t group_step = uint32_t(row_blocks_per_group<QT>() * a.stride);
-    const typename Tile<QT>::Lane lanes(lane, row_bytes);
-    uint8_t* slot = slots + wave * Tile<QT>::kSlot;
-    // this wave's groups ks, ks + splits, ...: item j
-    const int items = active && ks < a.groups ? (a.groups - ks + a.splits - 1) / a.splits : 0;
-    Tile<QT> buf[kDepth][kMats];
-    // (past the last item: its first again)
-    auto load = [&](auto slot_c, int j) __attribute__((always_inline)) {
-        const uint32_t at_byte = uint32_t(ks + a.splits * (j < items ? j : 0)) * group_step;
-#pragma unroll
-        for (int m = 0; m < kMats; ++m)
-            buf[decltype(slot_c)::value][m].load(w[m], lanes, at_byte, tile_bytes);
-    };
-    float acc[kMats][SETS];
-#pragma unroll
-    for (int m = 0; m < kMats; ++m)
-#pragma unroll
-        for (int s = 0; s < SETS; ++s) acc[m][s] = 0.f;
-    const LaneTokens<QT> at0(lane, 0, count), at1(lane, SETS - 1, count);
-    const int unit = count * unit_bytes<QT>();
-    auto compute = [&](auto slot_c, int j, int g0) __attribute__((always_inline)) {
-        const int g = ks + a.splits * j;
-        const uint8_t* group = staged + (g - g0) * unit;
-        const uint8_t* mine = slot + n * Tile<QT>::kRow;
-        const uint32_t start =
-            whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(g) * group_step) & 15u);
-#pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-            // (one wave's LDS operations complete in order: the reads see these writes, and the next
-            // writes come after the reads)
-            buf[decltype(slot_c)::value][m].store(slot, lane);
-            __builtin_amdgcn_wave_barrier();
-            Group<QT> d;
-            decode(d, mine, start, q, g, blocks, a.stride);
-            acc[m][0] = group_dot<QT>(d, group, at0, acc[m][0]);
-            if constexpr (SETS == 2) acc[m][1] = group_dot<QT>(d, group, at1, acc[m][1]);
-            __builtin_amdgcn_sched_barrier(0);   // one matrix at a time: registers
-        }
-    };
-    using S0 = std::integral_constant<int, 0>;
-    using S1 = std::integral_constant<int, 1>;
-    static_assert(kDepth == 2, "the loops below name the slots");
-    // Groups staged at a time: what fits the budget, whole turns of two groups per wave.
-    const int turn = kDepth * a.splits;
-    const int phase = min(a.groups, kStageBudget / unit / turn * turn);
-    int j = 0;
-    for (int g0 = 0; g0 < a.groups; g0 += phase) {
-        const int ng = min(phase, a.groups - g0);
-        // Units u = (group, token) of this phase, dealt to the waves; x is requested before the
-        // weights (a wave's loads return in order).
-        const int units = ng * count;
-        auto unit_x = [&](int u) {
-            const int g = u / count, t = u - g * count;
-            const int pair = list[t];
-            const int r = UP ? pair / a.topk : pair;
-            const int k0 = 256 * (g0 + g) + 4 * lane;
-            float4 v = {0.f, 0.f, 0.f, 0.f};
-            if (k0 < a.in) v = *reinterpret_cast<const float4*>(a.x + int64_t(r) * a.in + k0);
-            return v;
-        };
-        auto stage = [&](int u, const float4 v) {
-            const int g = u / count, t = u - g * count;
-            stage_token<QT>(staged + g * unit, t, count, v, lane);
-        };
-        constexpr int kBatch = 4;
-        for (int u0 = wave; u0 < units; u0 += kWaves * kBatch) {
-            float4 x[kBatch];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) x[i] = unit_x(min(u0 + kWaves * i, units - 1));
-            if (g0 == 0 && u0 == wave) {
-                load(S0{}, 0);
-                load(S1{}, 1);
-            }
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-                if (u0 + kWaves * i < units) stage(u0 + kWaves * i, x[i]);
-        }
-        if (g0 == 0 && units <= wave) {   // (a wave without a unit to stage)
-            load(S0{}, 0);
-            load(S1{}, 1);
-        }
-        lds_barrier();
-        // One load per computed group, without conditions, so that the compiler waits for exactly
-        // the group it needs; the next phase's weights are on their way when a phase ends.
-        for (const int end = g0 + phase >= a.groups ? items : j + phase / a.splits; j < end; j += 2) {
-            compute(S0{}, j, g0);
-            load(S0{}, j + 2);
-            if (j + 1 < end) compute(S1{}, j + 1, g0);
-            load(S1{}, j + 3);
-        }
-        lds_barrier();   // the staged activations are free
-    }
-    // The parts of a tile meet in LDS, in the order of ks.  red: [mat][wave][token][row]
-    constexpr int kPart = 4 * SETS * 16;
-#pragma unroll
-    for (int m = 0; m < kMats; ++m)
-#pragma unroll
-        for (int s = 0; s < SETS; ++s) red[(m * kWaves + wave) * kPart + (4 * s + q) * 16 + n] = acc[m][s];
-    lds_barrier();
-    for (int o = tid; o < tiles_wg * count * 16; o += kThreads) {
-        const int r = o & 15, rest = o >> 4;
-        const int t = rest % count, wt = rest / count;
-        const int tl = blockIdx.x * tiles_wg + wt;
-        if (16 * tl >= a.rows) continue;
-        float v[kMats];
-#pragma unroll
-        for (int m = 0; m < kMats; ++m) {
-            const float* p = red + (m * kWaves + wt * a.splits) * kPart + t * 16 + r;
-            v[m] = p[0];
-            for (int k = 1; k < a.splits; ++k) v[m] += p[k * kPart];
-        }
-        const int pair = list[t];
-        float y;
-        if constexpr (UP) y = activate(v[0], a.act) * v[1];
-        else y = a.wts[pair] * v[0];
-        a.out[int64_t(pair) * a.rows + 16 * tl + r] = y;
-    }
-}
-
-constexpr size_t red_bytes(int mats, int sets) { return size_t(mats) * kWaves * 4 * sets * 16 * 4; }
-
-// The blockIdx.y-th chosen expert (-1: there are fewer) and its pairs, in order: list, *count.
-__device__ __forceinline__ int expert_pairs(const MoeArgs& a, unsigned* bits, int* count, int* list) {
-    chosen_experts(a, bits);
-    const int tid = threadIdx.x;
-    int slot = blockIdx.y, expert = -1;   // the slot-th set bit
-    for (int w = 0; w < kMoeMaxExperts / 32; ++w) {
-        unsigned b = bits[w];
-        const int c = __popc(b);
-        if (slot < c) {
-            for (; slot > 0; --slot) b &= b - 1;
-            expert = 32 * w + __ffs(int(b)) - 1;
-            break;
-        }
-        slot -= c;
-    }
-    expert = __builtin_amdgcn_readfirstlane(expert);
-    if (expert < 0) return expert;
-    if (tid < 64) {
-        int n = 0;
-        for (int p0 = 0; p0 < a.pairs; p0 += 64) {
-            const int p = p0 + tid;
-            const bool mine = p < a.pairs && a.ids[p] == expert;
-            const unsigned long long m = __ballot(mine);
-            if (mine) list[n + __popcll(m & ((1ull << tid) - 1))] = p;
-            n += __popcll(m);
-        }
-        if (tid == 0) *count = n;
-    }
-    lds_barrier();
-    return expert;
 }
 
 // ------------------------------------------------------------------ many tokens
@@ -793,158 +608,169 @@ __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
     }
 }
 
-template <int QT, bool UP, bool ONE>
-__global__ __launch_bounds__(kThreads, ONE && whole_chunks<QT>() ? 4 : 2) void moe_expert_kernel(MoeArgs a) {
+// ------------------------------------------------------------------ one token
+// blockIdx.y: choice; blockIdx.x: kWaves / (2 splits) 16-row tiles of its expert.  Wave w: part w % splits of
+// the groups (part ks: ks, ks + splits, ...) of matrix w / splits % 2 (gate, up), tile w / (2 splits) of
+// the workgroup; the sums meet in LDS, parts in order.
+template <int QT>
+__global__ __launch_bounds__(kThreads, 4) void moe_one_up_kernel(MoeArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    constexpr int kMats = UP ? 2 : 1;
-    float* red = reinterpret_cast<float*>(smem);
-    unsigned* bits = reinterpret_cast<unsigned*>(smem + red_bytes(kMats, ONE ? 1 : 2));
-    int* count_lds = reinterpret_cast<int*>(bits + kMoeMaxExperts / 32);
-    int* list = count_lds + 4;
-    const int list_room = ONE ? 4 : (a.pairs + 3) & ~3;
-    uint8_t* slots = reinterpret_cast<uint8_t*>(list + list_room);
+    float* red = reinterpret_cast<float*>(smem);   // [wave][16 rows]
+    uint8_t* slots = smem + kWaves * 64;
     uint8_t* staged = slots + kWaves * Tile<QT>::kSlot;
-    const int tid = threadIdx.x;
-    if constexpr (ONE) {
-        const int pair = blockIdx.y;
-        const int expert = __builtin_amdgcn_readfirstlane(a.ids[pair]);
-        if (unsigned(expert) >= unsigned(a.experts)) return;   // (uniform) not this layer's: adds nothing
-        if (tid == 0) list[0] = pair;
-        lds_barrier();
-        expert_tiles<QT, UP, 1>(a, expert, list, 1, staged, slots, red);
-    } else {
-        const int expert = expert_pairs(a, bits, count_lds, list);
-        if (expert < 0) return;   // (uniform) fewer chosen experts than slots
-        const int count = __builtin_amdgcn_readfirstlane(*count_lds);
-        for (int c0 = 0; c0 < count; c0 += kTokens) {
-            const int c = min(kTokens, count - c0);
-            if (c <= 4) expert_tiles<QT, UP, 1>(a, expert, list + c0, c, staged, slots, red);
-            else expert_tiles<QT, UP, 2>(a, expert, list + c0, c, staged, slots, red);
-            lds_barrier();
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int n = lane & 15, q = lane >> 4;
+    // x is requested before anything that depends on the choice: group `wave` of it
+    auto group_x = [&](int g) {
+        const int k0 = 256 * g + 4 * lane;
+        float4 v = {0.f, 0.f, 0.f, 0.f};
+        if (k0 < a.in) v = *reinterpret_cast<const float4*>(a.x + k0);
+        return v;
+    };
+    const float4 x0 = group_x(wave);
+    const int expert = __builtin_amdgcn_readfirstlane(a.ids[blockIdx.y]);
+    if (unsigned(expert) >= unsigned(a.experts)) return;   // (uniform) not this layer's: adds nothing
+    const int tiles_wg = kWaves / (2 * a.splits);
+    const int ks = wave % a.splits, mat = wave / a.splits & 1, wtile = wave / (2 * a.splits);
+    const int tile = blockIdx.x * tiles_wg + wtile;
+    const bool active = 16 * tile < a.rows;
+    const int blocks = row_blocks<QT>(a.in);
+    const uint8_t* const w =
+        (mat ? a.w1 : a.w0) + (int64_t(expert) * a.rows + 16 * (active ? tile : 0)) * a.row_bytes;
+    const uint32_t row_bytes = uint32_t(a.row_bytes), tile_bytes = 16 * row_bytes;
+    const uint32_t group_step = uint32_t(row_blocks_per_group<QT>() * a.stride);
+    const typename Tile<QT>::Lane lanes(lane, row_bytes);
+    uint8_t* slot = slots + wave * Tile<QT>::kSlot;
+    const int items = active ? (a.groups - ks + a.splits - 1) / a.splits : 0;   // (splits <= groups)
+    Tile<QT> buf[kDepth];
+    // (past the last item: it again)
+    auto load = [&](auto slot_c, int j) __attribute__((always_inline)) {
+        buf[decltype(slot_c)::value].load(w, lanes, uint32_t(ks + a.splits * max(0, min(j, items - 1))) * group_step,
+                                          tile_bytes);
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    static_assert(kDepth == 2, "the loop below names the slots");
+    load(S0{}, 0);
+    load(S1{}, 1);
+    if (wave < a.groups) stage_token<QT>(staged + wave * unit_bytes<QT>(), 0, 1, x0, lane);
+    for (int g = wave + kWaves; g < a.groups; g += kWaves)
+        stage_token<QT>(staged + g * unit_bytes<QT>(), 0, 1, group_x(g), lane);
+    lds_barrier();
+    float acc = 0.f;
+    const LaneTokens<QT> lt(lane, 0, 1);
+    auto compute = [&](auto slot_c, int j) __attribute__((always_inline)) {
+        const int g = ks + a.splits * j;
+        const uint32_t start =
+            whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(g) * group_step) & 15u);
+        // (one wave's LDS operations complete in order: the reads see these writes, and the next
+        // writes come after the reads)
+        buf[decltype(slot_c)::value].store(slot, lane);
+        __builtin_amdgcn_wave_barrier();
+        Group<QT> d;
+        decode(d, slot + n * Tile<QT>::kRow, start, q, g, blocks, a.stride);
+        acc = group_dot<QT>(d, staged + g * unit_bytes<QT>(), lt, acc);
+        __builtin_amdgcn_wave_barrier();
+    };
+    for (int j = 0; j < items; j += 2) {
+        compute(S0{}, j);
+        load(S0{}, j + 2);
+        if (j + 1 < items) compute(S1{}, j + 1);
+        load(S1{}, j + 3);
+    }
+    if (q == 0) red[wave * 16 + n] = acc;
+    lds_barrier();
+    if (tid < tiles_wg * 16) {
+        const int r = tid & 15, wt = tid >> 4;
+        const int row = 16 * (blockIdx.x * tiles_wg + wt) + r;
+        if (row < a.rows) {
+            float v[2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const float* p = red + (2 * wt + m) * a.splits * 16 + r;
+                v[m] = p[0];
+                for (int k = 1; k < a.splits; ++k) v[m] += p[16 * k];
+            }
+            a.out[int64_t(blockIdx.y) * a.rows + row] = activate(v[0], a.act) * v[1];
         }
     }
 }
 
-// ------------------------------------------------------------------ down with few tokens
-// blockIdx.x: one 16-row tile of Y.  The chosen experts are its slots; wave w takes part w % splits of
-// the groups of slots w / splits, w / splits + waves / splits, ..., and stages their tokens' h itself,
-// a group at a time, in LDS of its own (no workgroup barrier until the end).  Every (slot, part)
-// leaves its pairs' sums in LDS; a token's parts are added in order, weighted, in choice order.
-// A token that names an expert twice has one h there, used with both weights.
-// LDS of the kernel, in bytes (THREADS, CT: tokens at most).
-template <int QT, int THREADS, int CT>
-struct FewLds {
-    static constexpr int kWavesOf = THREADS / 64;
-    static constexpr int kTables = kMoeMaxExperts / 8 + 16 + kMoeFewPairs * 4 * (4 + CT);
-    static constexpr int kStage = kWavesOf * (CT * unit_bytes<QT>() + Tile<QT>::kSlot);   // staged tokens, weights
-    static size_t bytes(int pairs, int splits) { return kTables + kStage + size_t(pairs) * splits * 64; }
-};
-
-template <int QT, int THREADS, int CT>
-__global__ __launch_bounds__(THREADS) void moe_down_few_kernel(MoeArgs a) {
-    using Lds = FewLds<QT, THREADS, CT>;
-    constexpr int kNW = THREADS / 64;
-    constexpr int SETS = (CT + 3) / 4;
+// blockIdx.x: one 16-row tile of Y.  Wave w takes part w % splits of the groups of choices w / splits,
+// w / splits + waves / splits, ..., and stages their h itself, a group at a time, in LDS of its own (no
+// workgroup barrier until the end).  Every (choice, part) leaves its sum in LDS; a choice's parts are
+// added in order, weighted, and the choices in order.
+constexpr int kOneThreads = 1024;
+constexpr int kOneWaves = kOneThreads / 64;
+constexpr int kOneTables = 16 + 2 * 4 * kMoeOneTopk;
+template <int QT>
+__global__ __launch_bounds__(kOneThreads) void moe_one_down_kernel(MoeArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    unsigned* bits = reinterpret_cast<unsigned*>(smem);
-    int* expert_of = reinterpret_cast<int*>(smem + kMoeMaxExperts / 8 + 16);   // [pair] ids; -1: not this layer's
-    int* first_of = expert_of + kMoeFewPairs;      // [pair] the token's first pair of the same expert
-    int* slot_expert = first_of + kMoeFewPairs;    // [slot]
-    int* slot_count = slot_expert + kMoeFewPairs;  // [slot] tokens
-    int* slot_pairs = slot_count + kMoeFewPairs;   // [slot][CT]
-    uint8_t* stage_all = smem + Lds::kTables;
-    float* res = reinterpret_cast<float*>(stage_all + Lds::kStage);            // [pair][part][16 rows]
+    int* valid_lds = reinterpret_cast<int*>(smem);
+    int* list = reinterpret_cast<int*>(smem + 16);   // the choices that are this layer's,
+    int* expert_of = list + kMoeOneTopk;             // and their experts
+    float* res = reinterpret_cast<float*>(smem + kOneTables);                       // [choice][part][16 rows]
+    uint8_t* mine = reinterpret_cast<uint8_t*>(res + a.topk * a.splits * 16);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, q = lane >> 4;
-    const int tokens = a.pairs / a.topk;
-
-    // (kMoeFewPairs <= THREADS)
-    if (tid < kMoeMaxExperts / 32) bits[tid] = 0u;
-    if (tid < kMoeFewPairs) {
-        slot_count[tid] = 0;
-        const int e = tid < a.pairs ? a.ids[tid] : -1;
-        expert_of[tid] = unsigned(e) < unsigned(a.experts) ? e : -1;
+    uint8_t* staged = mine + wave * (unit_bytes<QT>() + Tile<QT>::kSlot);
+    uint8_t* slot = staged + unit_bytes<QT>();
+    if (wave == 0) {   // (kMoeOneTopk lanes)
+        const int e = lane < a.topk ? a.ids[lane] : -1;
+        const bool ok = unsigned(e) < unsigned(a.experts);
+        const unsigned long long m = __ballot(ok);
+        if (ok) {
+            const int at = __popcll(m & ((1ull << lane) - 1));
+            list[at] = lane;
+            expert_of[at] = e;
+        }
+        if (lane == 0) *valid_lds = __popcll(m);
     }
     lds_barrier();
-    const int my_e = tid < a.pairs ? expert_of[tid] : -1;
-    const int my_m = tid < a.pairs ? tid / a.topk : 0;
-    if (my_e >= 0) {
-        atomicOr(&bits[my_e >> 5], 1u << (my_e & 31));
-        int f = my_m * a.topk;
-        while (expert_of[f] != my_e) ++f;    // (ends at the pair itself)
-        first_of[tid] = f;
-    } else if (tid < a.pairs) {
-        first_of[tid] = -1;
-    }
-    lds_barrier();
-    int slots = 0, my_slot = 0;
-    for (int w = 0; w < kMoeMaxExperts / 32; ++w) {
-        const unsigned b = bits[w];
-        if (my_e >= 0 && (my_e >> 5) == w) my_slot = slots + __popc(b & ((1u << (my_e & 31)) - 1));
-        slots += __popc(b);
-    }
-    if (my_e >= 0 && first_of[tid] == tid) {
-        int t = 0;
-        for (int p = 0; p < my_m * a.topk; ++p) t += first_of[p] == p && expert_of[p] == my_e;
-        slot_expert[my_slot] = my_e;
-        slot_pairs[my_slot * CT + t] = tid;
-        atomicMax(&slot_count[my_slot], t + 1);
-    }
-    lds_barrier();
-
+    const int valid = __builtin_amdgcn_readfirstlane(*valid_lds);
     const int tile = blockIdx.x;
-    const int ks = wave % a.splits, slot0 = wave / a.splits, slot_step = kNW / a.splits;
-    const int per_slot = ks < a.groups ? (a.groups - ks + a.splits - 1) / a.splits : 0;
-    const int my_slots = slot0 < slots ? (slots - slot0 + slot_step - 1) / slot_step : 0;
-    const int items = per_slot * my_slots;
+    const int ks = wave % a.splits, first = wave / a.splits, step_of = kOneWaves / a.splits;
+    const int per = (a.groups - ks + a.splits - 1) / a.splits;   // (splits <= groups)
+    const int items = first < valid ? per * ((valid - first + step_of - 1) / step_of) : 0;
     const int blocks = row_blocks<QT>(a.in);
-    uint8_t* staged = stage_all + wave * (CT * unit_bytes<QT>() + Tile<QT>::kSlot);
-    uint8_t* slot = staged + CT * unit_bytes<QT>();
     const uint32_t row_bytes = uint32_t(a.row_bytes), tile_bytes = 16 * row_bytes;
     const uint32_t group_step = uint32_t(row_blocks_per_group<QT>() * a.stride);
     const typename Tile<QT>::Lane lanes(lane, row_bytes);
     struct Cursor {
-        int slot, i;
+        int at, i;   // choice list[at], item i of its groups
     };
     auto step = [&](Cursor& c) {
-        if (++c.i == per_slot) {
+        if (++c.i == per) {
             c.i = 0;
-            c.slot += slot_step;
+            c.at += step_of;
         }
     };
     Tile<QT> buf[kDepth];
-    float4 xs[kDepth][CT];
-    Cursor ld = {slot0, 0}, cp = {slot0, 0};
-    // (loads past the last item read the last one again)
+    float4 xs[kDepth];
+    Cursor ld = {first, 0}, cp = ld;
+    // (past the last item: the last one again)
     auto load = [&](auto slot_c) __attribute__((always_inline)) {
         constexpr int S = decltype(slot_c)::value;
         const int g = ks + a.splits * ld.i;
-        const int e = __builtin_amdgcn_readfirstlane(slot_expert[ld.slot]);
-        const int count = __builtin_amdgcn_readfirstlane(slot_count[ld.slot]);
+        const int e = __builtin_amdgcn_readfirstlane(expert_of[ld.at]);
+        const int choice = __builtin_amdgcn_readfirstlane(list[ld.at]);
         const int k0 = 256 * g + 4 * lane;
-#pragma unroll
-        for (int t = 0; t < CT; ++t) {
-            const int pair = __builtin_amdgcn_readfirstlane(slot_pairs[ld.slot * CT + min(t, count - 1)]);
-            xs[S][t] = float4{0.f, 0.f, 0.f, 0.f};
-            if (k0 < a.in) xs[S][t] = *reinterpret_cast<const float4*>(a.x + int64_t(pair) * a.in + k0);
-        }
+        xs[S] = float4{0.f, 0.f, 0.f, 0.f};
+        if (k0 < a.in) xs[S] = *reinterpret_cast<const float4*>(a.x + int64_t(choice) * a.in + k0);
         buf[S].load(a.w0 + (int64_t(e) * a.rows + 16 * tile) * a.row_bytes, lanes, uint32_t(g) * group_step, tile_bytes);
         Cursor next = ld;
         step(next);
-        if (next.slot < slots) ld = next;
+        if (next.at < valid) ld = next;
     };
-    float acc[SETS];
-#pragma unroll
-    for (int s = 0; s < SETS; ++s) acc[s] = 0.f;
+    float acc = 0.f;
+    const LaneTokens<QT> lt(lane, 0, 1);
     auto compute = [&](auto slot_c) __attribute__((always_inline)) {
         constexpr int S = decltype(slot_c)::value;
-        const int count = __builtin_amdgcn_readfirstlane(slot_count[cp.slot]);
         // (one wave's LDS operations complete in order: the reads below see these writes, and the
         // next group's writes come after them)
-#pragma unroll
-        for (int t = 0; t < CT; ++t)
-            if (t < count) stage_token<QT>(staged, t, count, xs[S][t], lane);
+        stage_token<QT>(staged, 0, 1, xs[S], lane);
         buf[S].store(slot, lane);
         __builtin_amdgcn_wave_barrier();
         const int g = ks + a.splits * cp.i;
@@ -952,22 +778,17 @@ __global__ __launch_bounds__(THREADS) void moe_down_few_kernel(MoeArgs a) {
             whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(g) * group_step) & 15u);
         Group<QT> w;
         decode(w, slot + n * Tile<QT>::kRow, start, q, g, blocks, a.stride);
-#pragma unroll
-        for (int s = 0; s < SETS; ++s)
-            if (s == 0 || count > 4) acc[s] = group_dot<QT>(w, staged, LaneTokens<QT>(lane, s, count), acc[s]);
+        acc = group_dot<QT>(w, staged, lt, acc);
         __builtin_amdgcn_wave_barrier();
-        if (cp.i == per_slot - 1) {
-#pragma unroll
-            for (int s = 0; s < SETS; ++s) {
-                if (4 * s + q < count) res[(slot_pairs[cp.slot * CT + 4 * s + q] * a.splits + ks) * 16 + n] = acc[s];
-                acc[s] = 0.f;
-            }
+        if (cp.i == per - 1) {
+            if (q == 0) res[(list[cp.at] * a.splits + ks) * 16 + n] = acc;
+            acc = 0.f;
         }
         step(cp);
     };
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
-    static_assert(kDepth == 2, "the loops below name the slots");
+    static_assert(kDepth == 2, "the loop below names the slots");
     if (items > 0) {
         load(S0{});
         load(S1{});
@@ -979,18 +800,15 @@ __global__ __launch_bounds__(THREADS) void moe_down_few_kernel(MoeArgs a) {
         }
     }
     lds_barrier();
-    if (tid < tokens * 16) {
-        const int m = tid >> 4, r = tid & 15;
-        const int64_t at = int64_t(m) * a.rows + 16 * tile + r;
+    if (tid < 16) {
+        const int64_t at = 16 * tile + tid;
         float y = 0.f;
-        for (int c = 0; c < a.topk; ++c) {
-            const int p = m * a.topk + c;
-            if (expert_of[p] < 0) continue;
-            const float* v = res + first_of[p] * a.splits * 16 + r;
-            float s = v[0];
-            const int parts = min(a.splits, a.groups);
-            for (int k = 1; k < parts; ++k) s += v[k * 16];
-            y = fmaf(a.wts[p], s, y);
+        for (int v = 0; v < valid; ++v) {
+            const int c = list[v];
+            const float* p = res + c * a.splits * 16 + tid;
+            float s = p[0];
+            for (int k = 1; k < a.splits; ++k) s += p[16 * k];
+            y = fmaf(a.wts[c], s, y);
         }
         a.out[at] = a.residual ? a.residual[at] + y : y;
     }
@@ -1051,90 +869,52 @@ int pow2_floor(int64_t v) {
     return p;
 }
 
-template <int QT>
-size_t expert_lds_fixed(int pairs) {   // besides the staged activations
-    return kMoeMaxExperts / 8 + 16 + size_t((pairs + 3) & ~3) * 4 + size_t(kWaves) * Tile<QT>::kSlot;
-}
-
 template <int QT, bool UP>
-hipError_t launch_expert_typed(MoeArgs a, hipStream_t s) {
-    const int tokens = a.pairs / a.topk, tiles = a.rows / 16;
-    const int slots = std::min(a.pairs, a.experts);
-    if (!moe_few(tokens, a.topk)) {
-        // tokens of a slot: four, or what the LDS of a CU holds of very long rows (else phases, below)
-        const size_t fixed = kManyFixed + size_t(kWaves) * Tile<QT>::kSlot;
-        const size_t per_token = size_t(a.groups) * unit_bytes<QT>();
-        a.set = int(std::min<size_t>({4, (kGfx950LdsBytes - fixed) / per_token, size_t(a.pairs)}));
-        if (a.set >= 1) {
-            const int many_slots = std::min(a.pairs, a.experts + a.pairs / a.set);
-            // about 16 KiB of weights per wave before it starts again with another slot
-            const int units = tiles * (UP ? 2 : 1);
-            const int64_t unit_bytes_of = 16 * a.row_bytes;
-            const int per_wave = int(std::max<int64_t>(1, 32768 / unit_bytes_of));
-            const int grid = std::max(1, units / (kWaves * per_wave));
-            hipLaunchKernelGGL((moe_many_kernel<QT, UP>), dim3(grid, many_slots), dim3(kThreads),
-                               fixed + size_t(a.set) * per_token, s, a);
-            return hipGetLastError();
-        }
-    }
-    const bool one = UP && tokens == 1;
-    // A tile's groups over as many waves as fill the chip for one token (about 2048 waves), by the
-    // layer's sizes alone.  (At most four: a turn of eight tokens' groups has to fit the staging budget.)
-    const int64_t want = 2048 / std::max<int64_t>(1, int64_t(tiles) * a.topk);
-    a.splits = pow2_floor(std::max<int64_t>(1, std::min<int64_t>({want, 4, a.groups})));
-    const int tiles_wg = kWaves / a.splits;
-    const int count = one ? 1 : std::min(kTokens, a.pairs);
-    const int turn = kDepth * a.splits;
-    const int unit = count * unit_bytes<QT>();
-    const int phase = std::min(a.groups, kStageBudget / unit / turn * turn);
-    const size_t lds = expert_lds_fixed<QT>(one ? 4 : a.pairs) + red_bytes(UP ? 2 : 1, one ? 1 : 2) +
-                       std::min<size_t>(kStageBudget, size_t(phase) * unit + (one ? 0 : size_t(turn) * unit));
-    const dim3 grid((tiles + tiles_wg - 1) / tiles_wg, one ? a.pairs : slots);
-    if constexpr (UP) {
-        if (one) {
-            hipLaunchKernelGGL((moe_expert_kernel<QT, true, true>), grid, dim3(kThreads), lds, s, a);
-            return hipGetLastError();
-        }
-    }
-    hipLaunchKernelGGL((moe_expert_kernel<QT, UP, false>), grid, dim3(kThreads), lds, s, a);
+hipError_t launch_many(MoeArgs a, hipStream_t s) {
+    // Tokens of a slot: four.  (The LDS of a CU holds them of rows of up to 38 groups, and one of the longest.)
+    constexpr size_t kFixed = kManyFixed + size_t(kWaves) * Tile<QT>::kSlot;
+    static_assert(kFixed + 128 * size_t(unit_bytes<QT>()) <= kGfx950LdsBytes, "a token of the longest rows fits");
+    const size_t per_token = size_t(a.groups) * unit_bytes<QT>();
+    a.set = int(std::min<size_t>({4, (kGfx950LdsBytes - kFixed) / per_token, size_t(a.pairs)}));
+    const int slots = std::min(a.pairs, a.experts + a.pairs / a.set);
+    // units of 32 KiB of weights or more per wave: enough to outlast the staging, and short enough
+    // that the last round of workgroups costs little
+    const int units = a.rows / 16 * (UP ? 2 : 1);
+    const int per_wave = int(std::max<int64_t>(1, 32768 / (16 * a.row_bytes)));
+    const int grid = std::max(1, units / (kWaves * per_wave));
+    hipLaunchKernelGGL((moe_many_kernel<QT, UP>), dim3(grid, slots), dim3(kThreads), kFixed + size_t(a.set) * per_token,
+                       s, a);
     return hipGetLastError();
 }
 
-template <bool UP>
-hipError_t launch_expert(int type, BlockLayout lay, MoeArgs a, hipStream_t s) {
-    set_layout(a, type, lay);
-    return with_type(type, [&](auto qt) { return launch_expert_typed<decltype(qt)::value, UP>(a, s); });
+template <int QT>
+hipError_t launch_one_up(MoeArgs a, hipStream_t s) {
+    constexpr size_t kFixed = kWaves * 64 + size_t(kWaves) * Tile<QT>::kSlot;
+    static_assert(kFixed + 128 * size_t(unit_bytes<QT>()) <= kGfx950LdsBytes, "the longest token fits");
+    // A tile's groups over as many waves as fill the chip (about kOneUpWaves).
+    const int tiles = a.rows / 16;
+    const int64_t want = kOneUpWaves / std::max<int64_t>(1, int64_t(tiles) * 2 * a.topk);
+    a.splits = pow2_floor(std::max<int64_t>(1, std::min<int64_t>({want, kWaves / 2, a.groups})));
+    const int tiles_wg = kWaves / (2 * a.splits);
+    hipLaunchKernelGGL((moe_one_up_kernel<QT>), dim3((tiles + tiles_wg - 1) / tiles_wg, a.topk), dim3(kThreads),
+                       kFixed + size_t(a.groups) * unit_bytes<QT>(), s, a);
+    return hipGetLastError();
 }
 
-hipError_t launch_down_few(int type, BlockLayout lay, MoeArgs a, hipStream_t s) {
-    set_layout(a, type, lay);
-    const int tokens = a.pairs / a.topk;
-    a.splits = pow2_floor(std::max<int64_t>(1, std::min<int64_t>({16 / a.topk, 8, a.groups})));
-    const dim3 grid(a.rows / 16);
-    return with_type(type, [&](auto qt) {
-        constexpr int QT = decltype(qt)::value;
-        if (tokens == 1)
-            hipLaunchKernelGGL((moe_down_few_kernel<QT, 1024, 1>), grid, dim3(1024),
-                               (FewLds<QT, 1024, 1>::bytes(a.pairs, a.splits)), s, a);
-        else if (tokens <= 4)
-            hipLaunchKernelGGL((moe_down_few_kernel<QT, 512, 4>), grid, dim3(512),
-                               (FewLds<QT, 512, 4>::bytes(a.pairs, a.splits)), s, a);
-        else
-            hipLaunchKernelGGL((moe_down_few_kernel<QT, 512, 8>), grid, dim3(512),
-                               (FewLds<QT, 512, 8>::bytes(a.pairs, a.splits)), s, a);
-        return hipGetLastError();
-    });
+template <int QT>
+hipError_t launch_one_down(MoeArgs a, hipStream_t s) {
+    a.splits = pow2_floor(std::max<int64_t>(1, std::min<int64_t>({kOneWaves / a.topk, kOneWaves, a.groups})));
+    const size_t lds = kOneTables + size_t(a.topk) * a.splits * 64 +
+                       size_t(kOneWaves) * (unit_bytes<QT>() + Tile<QT>::kSlot);
+    hipLaunchKernelGGL((moe_one_down_kernel<QT>), dim3(a.rows / 16), dim3(kOneThreads), lds, s, a);
+    return hipGetLastError();
 }
 
-#define MQ_MOE_INSTANCES(QT)                                                  \
-    template __global__ void moe_expert_kernel<QT, true, true>(MoeArgs);      \
-    template __global__ void moe_expert_kernel<QT, true, false>(MoeArgs);     \
-    template __global__ void moe_expert_kernel<QT, false, false>(MoeArgs);    \
-    template __global__ void moe_many_kernel<QT, true>(MoeArgs);              \
-    template __global__ void moe_many_kernel<QT, false>(MoeArgs);             \
-    template __global__ void moe_down_few_kernel<QT, 1024, 1>(MoeArgs);       \
-    template __global__ void moe_down_few_kernel<QT, 512, 4>(MoeArgs);        \
-    template __global__ void moe_down_few_kernel<QT, 512, 8>(MoeArgs);
+#define MQ_MOE_INSTANCES(QT)                                     \
+    template __global__ void moe_one_up_kernel<QT>(MoeArgs);     \
+    template __global__ void moe_one_down_kernel<QT>(MoeArgs);   \
+    template __global__ void moe_many_kernel<QT, true>(MoeArgs); \
+    template __global__ void moe_many_kernel<QT, false>(MoeArgs);
 MQ_MOE_INSTANCES(kQ4_0)
 MQ_MOE_INSTANCES(kQ4_1)
 MQ_MOE_INSTANCES(kQ5_0)
@@ -1150,8 +930,8 @@ size_t h_bytes(int64_t pairs, int64_t F) { return round_up256(size_t(pairs) * si
 }  // namespace
 
 size_t moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K) {
-    // h of every pair; many tokens: its two factors, and the weighted rows
-    if (moe_few(M, topk)) return h_bytes(M * topk, F);
+    // one token: h of every choice; more: its two factors for every pair, and the weighted rows
+    if (moe_one(M, topk)) return h_bytes(topk, F);
     return h_bytes(2 * M * topk, F) + round_up256(size_t(M * topk) * size_t(K) * 4);
 }
 
@@ -1161,14 +941,10 @@ hipError_t moe_set_attributes(size_t lds_limit) {
     for (int type : {kQ4_0, kQ4_1, kQ5_0, kQ5_1, kQ8_0, kQ4_K, kQ5_K, kQ6_K})
         e = e != hipSuccess ? e : with_type(type, [&](auto qt) {
             constexpr int QT = decltype(qt)::value;
-            const void* const kernels[] = {reinterpret_cast<const void*>(&moe_expert_kernel<QT, true, true>),
-                                           reinterpret_cast<const void*>(&moe_expert_kernel<QT, true, false>),
-                                           reinterpret_cast<const void*>(&moe_expert_kernel<QT, false, false>),
+            const void* const kernels[] = {reinterpret_cast<const void*>(&moe_one_up_kernel<QT>),
+                                           reinterpret_cast<const void*>(&moe_one_down_kernel<QT>),
                                            reinterpret_cast<const void*>(&moe_many_kernel<QT, true>),
-                                           reinterpret_cast<const void*>(&moe_many_kernel<QT, false>),
-                                           reinterpret_cast<const void*>(&moe_down_few_kernel<QT, 1024, 1>),
-                                           reinterpret_cast<const void*>(&moe_down_few_kernel<QT, 512, 4>),
-                                           reinterpret_cast<const void*>(&moe_down_few_kernel<QT, 512, 8>)};
+                                           reinterpret_cast<const void*>(&moe_many_kernel<QT, false>)};
             hipError_t r = hipSuccess;
             for (const void* k : kernels)
                 if (r == hipSuccess) r = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, room);
@@ -1179,10 +955,10 @@ hipError_t moe_set_attributes(size_t lds_limit) {
 
 hipError_t launch_moe_ffn(const MoeLayer& l, hipStream_t s, const char** name) {
     const int64_t pairs = l.M * l.topk;
-    const bool few = moe_few(l.M, l.topk);
+    const bool one = moe_one(l.M, l.topk);
     float* h = static_cast<float*>(l.scratch);
     float* rows = reinterpret_cast<float*>(static_cast<uint8_t*>(l.scratch) + h_bytes(2 * pairs, l.F));
-    *name = few ? "moe_few" : "moe_many";
+    *name = one ? "moe_one" : "moe_many";
     MoeArgs a = {};
     a.ids = l.ids;
     a.wts = l.wts;
@@ -1196,21 +972,25 @@ hipError_t launch_moe_ffn(const MoeLayer& l, hipStream_t s, const char** name) {
     a.out = h;
     a.in = int(l.K);
     a.rows = int(l.F);
-    hipError_t e = launch_expert<true>(l.gu_type, l.gu_layout, a, s);
+    set_layout(a, l.gu_type, l.gu_layout);
+    hipError_t e = with_type(l.gu_type, [&](auto qt) {
+        constexpr int QT = decltype(qt)::value;
+        return one ? launch_one_up<QT>(a, s) : launch_many<QT, true>(a, s);
+    });
     if (e != hipSuccess) return e;
     a.w0 = l.Wd;
     a.w1 = nullptr;
     a.x = h;
     a.in = int(l.F);
     a.rows = int(l.K);
-    if (few) {
-        a.residual = l.residual;
-        a.out = l.Y;
-        return launch_down_few(l.d_type, l.d_layout, a, s);
-    }
-    a.out = rows;
-    e = launch_expert<false>(l.d_type, l.d_layout, a, s);
-    if (e != hipSuccess) return e;
+    a.residual = l.residual;
+    a.out = one ? l.Y : rows;
+    set_layout(a, l.d_type, l.d_layout);
+    e = with_type(l.d_type, [&](auto qt) {
+        constexpr int QT = decltype(qt)::value;
+        return one ? launch_one_down<QT>(a, s) : launch_many<QT, false>(a, s);
+    });
+    if (one || e != hipSuccess) return e;
     hipLaunchKernelGGL(moe_combine_kernel, dim3((unsigned(l.K) / 4 + 255) / 256, unsigned(l.M)), dim3(256), 0, s, rows,
                        l.ids, l.residual, l.Y, int(l.topk), int(l.E), int(l.K));
     return hipGetLastError();

@@ -173,13 +173,11 @@ hipError_t gemv_q8_set_attributes(size_t lds_limit);
 hipError_t launch_gemv_q8(int type, BlockLayout lay, const uint8_t* W, const int8_t* codes, const float* scales,
                           const int32_t* sums, float* Y, int32_t* dots, int64_t M, int64_t N, int64_t K,
                           const Epilogue* ep, hipStream_t s, const char** kernel_name);
-// mq_moe_ffn (moe.hip): at most kMoeMaxPairs (token, choice) pairs and kMoeMaxExperts experts; up to
-// kMoeFewTokens tokens of up to kMoeFewPairs pairs take the kernels that exchange nothing between
-// workgroups.
+// mq_moe_ffn (moe.hip): at most kMoeMaxPairs (token, choice) pairs and kMoeMaxExperts experts; one
+// token of up to kMoeOneTopk choices takes kernels of its own.
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxPairs = 4096;
-constexpr int kMoeFewTokens = 8;
-constexpr int kMoeFewPairs = 128;
+constexpr int kMoeOneTopk = 64;
 constexpr int kMoeMaxTopk = 64;   // choices per token of mq_moe_route (a lane each)
 struct MoeLayer {
     const uint8_t *Wg, *Wu, *Wd;
@@ -194,7 +192,6 @@ struct MoeLayer {
     int64_t M, topk, E, F, K;
     int act;
 };
-bool moe_few(int64_t M, int64_t topk);
 size_t moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K);
 hipError_t moe_set_attributes(size_t lds_limit);
 hipError_t launch_moe_ffn(const MoeLayer& layer, hipStream_t s, const char** kernel_name);

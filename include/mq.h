@@ -322,10 +322,10 @@ int mq_moe_route(const float* X, const float* Wr, const float* bias, int32_t* id
  * f32 accuracy: activations keep 22 bits relative to the largest of their 32-value block, block dots
  * are exact integers, all sums f32.  A token with an infinity or a NaN gets NaN outputs.
  * Deterministic: a token's bits depend on its own row, ids and weights and on which kernels run
- * (M <= 8 and M * topk <= 128, or more), not on the other tokens.
+ * (one token of at most 64 choices, or more), not on the other tokens.
  * scratch: mq_moe_scratch_bytes(M, topk, F, K) bytes (0 for sizes the call refuses), 16-byte
  * aligned, no initial value; calls that share one buffer must be ordered on one stream.
- * Runs two launches, or three beyond M = 8 or 128 pairs.
+ * Runs two launches for one token (of at most 64 choices), else three.
  */
 size_t mq_moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K);
 int mq_moe_ffn(const void* Wg, const void* Wu, int gu_type, const void* Wd, int d_type, const float* X,
@@ -425,7 +425,7 @@ int mq_device_lds_bytes(void);
  *     "gemv_q8<type>" (other M <= 8 shapes that fit LDS), "mmq_kw<q4_K>" (Q4_K,
  *     GGUF payload, few output tiles: see mq_gemm_scratch_bytes), else "mmq<type>";
  *   mq_gemv_ep, mq_gemm_ep: the name of the product's kernel; mq_moe_route: "moe_route";
- *   mq_moe_ffn: "moe_few" (M <= 8, M * topk <= 128) or "moe_many". */
+ *   mq_moe_ffn: "moe_one" (one token, topk <= 64) or "moe_many". */
 const char* mq_last_kernel(void);
 
 /* Library version string. */

@@ -37,7 +37,7 @@ class Layer:
         M, k = ids.shape
         say(f"moe {NAMES[self.gu]}/{NAMES[self.down]} M={M} k={k} E={self.E} F={self.F} K={self.K} {what}")
         Y = self.run(X, ids, wts, act, residual)
-        assert mq.last_kernel() == ("moe_few" if M <= 8 and M * k <= 128 else "moe_many")
+        assert mq.last_kernel() == ("moe_one" if M == 1 and k <= 64 else "moe_many")
         ref, bound = oracle.moe_ffn(self.raw[0], self.raw[1], self.gu, self.raw[2], self.down, X, ids, wts, self.E, self.F,
                                     act, residual)
         err = np.abs(Y - ref)
@@ -145,13 +145,14 @@ def test_rows_do_not_depend_on_the_batch(M):
     assert np.array_equal(lay.run(X, ids, wts), Y)
 
 
-def test_a_token_alone_equals_itself_among_few():
-    E, F, K = 8, 1024, 2048
-    lay = Layer(mq.Q4_K, mq.Q4_K, E, F, K, seed=115)
-    X, ids, wts = inputs(4, 8, E, K, 14)
-    Y = lay.run(X, ids, wts)
-    for m in range(4):
-        assert np.array_equal(lay.run(X[m:m + 1], ids[m:m + 1], wts[m:m + 1])[0], Y[m])
+def test_one_token_takes_many_choices():
+    """More choices than waves, repeated experts, and the switch to the other kernels past 64."""
+    E, F, K = 40, 256, 512
+    lay = Layer(mq.Q4_K, mq.Q8_0, E, F, K, seed=115)
+    for k in (16, 33, 64, 65, 200):
+        X, ids, wts = inputs(1, k, E, K, k, distinct=False)
+        ids[0, 1] = -1
+        lay.check(X, ids, wts, what=f"k={k}")
 
 
 @pytest.mark.parametrize("M", [4, 40])
