@@ -329,14 +329,14 @@ template <> struct WeightRegs<kQ6_K> {
             const int u = t + 256 * it, row = u >> 3, p = u & 7;
             const int n = min(n0 + row, N - 1);
             const uint8_t* blk = W + int64_t(n) * rb + bs * sb + bo;
-            ql0[it] = load_u32_a2(blk + 64 * h + 4 * p);
-            ql1[it] = load_u32_a2(blk + 64 * h + 32 + 4 * p);
-            qh[it] = load_u32_a2(blk + 128 + 32 * h + 4 * p);
+            ql0[it] = load_u32_unaligned(blk + 64 * h + 4 * p);
+            ql1[it] = load_u32_unaligned(blk + 64 * h + 32 + 4 * p);
+            qh[it] = load_u32_unaligned(blk + 128 + 32 * h + 4 * p);
         }
         const int n = min(n0 + (t & (BN - 1)), N - 1);
         const uint8_t* blk = W + int64_t(n) * rb + bs * sb + bo;
-        s0 = load_u32_a2(blk + 192 + 8 * h);
-        s1 = load_u32_a2(blk + 192 + 8 * h + 4);
+        s0 = load_u32_unaligned(blk + 192 + 8 * h);
+        s1 = load_u32_unaligned(blk + 192 + 8 * h + 4);
         dbits = load_u16(blk + 208);
     }
     template <int BM>

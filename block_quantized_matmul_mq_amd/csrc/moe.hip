@@ -357,6 +357,7 @@ __device__ __forceinline__ float group_dot(const Group<QT>& w, const uint8_t* st
         for (int i = 0; i < kSums; i += 4)
             *reinterpret_cast<int4*>(sum.i + i) = *reinterpret_cast<const int4*>(staged + l.sums + 4 * i);
     }
+    // the three plane sums as one integer, modulo 2^32
     auto joined = [](const v4i& c) { return (((uint32_t(c[2]) << 8) + uint32_t(c[1])) << 8) + uint32_t(c[0]); };
     float codes = 0.f, mins = 0.f;
 #pragma unroll
@@ -703,14 +704,15 @@ __global__ __launch_bounds__(kThreads, 4) void moe_one_up_kernel(MoeArgs a) {
 // added in order, weighted, and the choices in order.
 constexpr int kOneThreads = 1024;
 constexpr int kOneWaves = kOneThreads / 64;
-constexpr int kOneTables = 16 + 2 * 4 * kMoeOneTopk;
+constexpr int kOneTables = 16 + 3 * 4 * kMoeOneTopk;
 template <int QT>
 __global__ __launch_bounds__(kOneThreads) void moe_one_down_kernel(MoeArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
     int* valid_lds = reinterpret_cast<int*>(smem);
     int* list = reinterpret_cast<int*>(smem + 16);   // the choices that are this layer's,
-    int* expert_of = list + kMoeOneTopk;             // and their experts
-    float* res = reinterpret_cast<float*>(smem + kOneTables);                       // [choice][part][16 rows]
+    int* expert_of = list + kMoeOneTopk;             // their experts
+    float* weight_of = reinterpret_cast<float*>(expert_of + kMoeOneTopk);           // and weights
+    float* res = reinterpret_cast<float*>(smem + kOneTables);                       // [entry of list][part][16 rows]
     uint8_t* mine = reinterpret_cast<uint8_t*>(res + a.topk * a.splits * 16);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -719,12 +721,14 @@ __global__ __launch_bounds__(kOneThreads) void moe_one_down_kernel(MoeArgs a) {
     uint8_t* slot = staged + unit_bytes<QT>();
     if (wave == 0) {   // (kMoeOneTopk lanes)
         const int e = lane < a.topk ? a.ids[lane] : -1;
+        const float weight = lane < a.topk ? a.wts[lane] : 0.f;
         const bool ok = unsigned(e) < unsigned(a.experts);
         const unsigned long long m = __ballot(ok);
         if (ok) {
             const int at = __popcll(m & ((1ull << lane) - 1));
             list[at] = lane;
             expert_of[at] = e;
+            weight_of[at] = weight;
         }
         if (lane == 0) *valid_lds = __popcll(m);
     }
@@ -781,7 +785,7 @@ __global__ __launch_bounds__(kOneThreads) void moe_one_down_kernel(MoeArgs a) {
         acc = group_dot<QT>(w, staged, lt, acc);
         __builtin_amdgcn_wave_barrier();
         if (cp.i == per - 1) {
-            if (q == 0) res[(list[cp.at] * a.splits + ks) * 16 + n] = acc;
+            if (q == 0) res[(cp.at * a.splits + ks) * 16 + n] = acc;
             acc = 0.f;
         }
         step(cp);
@@ -800,17 +804,21 @@ __global__ __launch_bounds__(kOneThreads) void moe_one_down_kernel(MoeArgs a) {
         }
     }
     lds_barrier();
+    // a choice's parts (a thread per choice and row), then the choices of a row
+    if (tid < 16 * valid) {   // (16 kMoeOneTopk <= kOneThreads)
+        float* p = res + (tid >> 4) * a.splits * 16 + (tid & 15);
+        float s = p[0];
+        for (int k = 1; k < a.splits; ++k) s += p[16 * k];
+        p[0] = s;
+    }
+    lds_barrier();
     if (tid < 16) {
         const int64_t at = 16 * tile + tid;
+        const float before = a.residual ? a.residual[at] : 0.f;
         float y = 0.f;
-        for (int v = 0; v < valid; ++v) {
-            const int c = list[v];
-            const float* p = res + c * a.splits * 16 + tid;
-            float s = p[0];
-            for (int k = 1; k < a.splits; ++k) s += p[16 * k];
-            y = fmaf(a.wts[c], s, y);
-        }
-        a.out[at] = a.residual ? a.residual[at] + y : y;
+#pragma unroll 4
+        for (int v = 0; v < valid; ++v) y = fmaf(weight_of[v], res[v * a.splits * 16 + tid], y);
+        a.out[at] = before + y;
     }
 }
 
@@ -824,11 +832,21 @@ __global__ __launch_bounds__(256) void moe_combine_kernel(const float* __restric
     const int c = blockIdx.x * 256 + threadIdx.x;
     if (4 * c >= K) return;
     float4 s = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < topk; ++j) {
-        const int64_t p = int64_t(m) * topk + j;
-        if (unsigned(ids[p]) >= unsigned(experts)) continue;
-        const float4 v = reinterpret_cast<const float4*>(rows_of + p * K)[c];
-        s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    constexpr int kBatch = 4;   // rows in flight
+    for (int j0 = 0; j0 < topk; j0 += kBatch) {
+        float4 v[kBatch];
+        bool live[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int64_t p = int64_t(m) * topk + min(j0 + i, topk - 1);
+            live[i] = j0 + i < topk && unsigned(ids[p]) < unsigned(experts);
+            v[i] = reinterpret_cast<const float4*>(rows_of + p * K)[c];   // (anything where nothing was written)
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (live[i]) {
+                s.x += v[i].x; s.y += v[i].y; s.z += v[i].z; s.w += v[i].w;
+            }
     }
     const int64_t at = int64_t(m) * K + 4 * c;
     if (residual) {

@@ -9,7 +9,7 @@
 // row l % 16 and k = l / 16 of both operands; a lane loads four consecutive k as one float4 and
 // feeds element j to instruction j, which only permutes the sum).
 //
-// Split.  A workgroup owns 16 tokens x 32 experts x one of S ranges of K, its 8 waves parts of
+// Split.  A workgroup owns 16 tokens x 32 experts x one of S ranges of K, its 16 waves parts of
 // that range, summed in LDS in wave order.  Few tokens leave few such tiles, so K is cut until
 // about 256 workgroups run (latency bound: one decoded token reads E K floats that one CU
 // could not fetch in time).  Each workgroup stores its partial logits to scratch and counts
@@ -17,6 +17,7 @@
 // ranges in order and selects: a wave per token, E / 64 logits per lane, k rounds of a
 // maximum over the wave on 64-bit keys that order like the f64 values (ties: lowest index).
 #include <algorithm>
+#include <type_traits>
 
 #include "mmq_splitk.h"
 #include "mq_device.h"
@@ -28,11 +29,14 @@ namespace {
 
 typedef double v4d __attribute__((ext_vector_type(4)));
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
 constexpr int kTileM = 16, kTileE = 32;
 constexpr int kStep = 16;                     // K values per wave step (K % 32 == 0)
 constexpr int kTargetWorkgroups = 256;
+// Steps of a wave at least: one where there is one token tile, else two, for fewer ranges that the last
+// workgroup has to add (K = 4096, E = 128: one token 8.3 us with one step, 9.3 with two; 64 tokens 19.2 and 17.4).
+constexpr int kMinStepsFew = 1, kMinSteps = 2;
 constexpr int kCounters = 65536;              // token tiles: MQ_MAX_M / 16
 constexpr uint64_t kTaken = 0;
 
@@ -60,22 +64,45 @@ __device__ __forceinline__ uint64_t dpp_u64(uint64_t v) {
     const uint32_t hi = uint32_t(__builtin_amdgcn_mov_dpp(int(uint32_t(v >> 32)), CTRL, 0xF, 0xF, false));
     return (uint64_t(hi) << 32) | lo;
 }
-__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+// The values of lanes l ^ 16 (or l ^ 32) and l, in some order that is the same for both.
+template <int STEP>
+__device__ __forceinline__ void swap_u64(uint64_t v, uint64_t& a, uint64_t& b) {
+    const uint32_t l = uint32_t(v), h = uint32_t(v >> 32);
+    if constexpr (STEP == 16) {
+        const auto x = __builtin_amdgcn_permlane16_swap(l, l, false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(h, h, false, false);
+        a = (uint64_t(y[0]) << 32) | x[0];
+        b = (uint64_t(y[1]) << 32) | x[1];
+    } else {
+        const auto x = __builtin_amdgcn_permlane32_swap(l, l, false, false);
+        const auto y = __builtin_amdgcn_permlane32_swap(h, h, false, false);
+        a = (uint64_t(y[0]) << 32) | x[0];
+        b = (uint64_t(y[1]) << 32) | x[1];
+    }
+}
+// op over all lanes, in registers (no LDS trips)
+template <class T, class Op>
+__device__ __forceinline__ T wave_all(T v, const Op& op) {
+    auto bits = [](T x) { return __builtin_bit_cast(uint64_t, x); };
+    auto value = [](uint64_t x) { return __builtin_bit_cast(T, x); };
+    v = op(v, value(dpp_u64<0xB1>(bits(v))));    // lane ^ 1
+    v = op(v, value(dpp_u64<0x4E>(bits(v))));    // lane ^ 2
+    v = op(v, value(dpp_u64<0x141>(bits(v))));   // the other quad of eight
+    v = op(v, value(dpp_u64<0x140>(bits(v))));   // the other eight of sixteen (row mirror)
+    uint64_t a, b;
+    swap_u64<16>(bits(v), a, b);
+    v = op(value(a), value(b));
+    swap_u64<32>(bits(v), a, b);
+    return op(value(a), value(b));
+}
 __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
-    v = max_u64(v, dpp_u64<0xB1>(v));    // lane ^ 1
-    v = max_u64(v, dpp_u64<0x4E>(v));    // lane ^ 2
-    v = max_u64(v, dpp_u64<0x141>(v));   // the other quad of eight
-    v = max_u64(v, dpp_u64<0x140>(v));   // the other eight of sixteen (row mirror)
-    v = max_u64(v, __shfl_xor(v, 16, 64));
-    return max_u64(v, __shfl_xor(v, 32, 64));
+    return wave_all(v, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
 }
-__device__ __forceinline__ double wave_max_f64(double v) {
-    for (int off = 1; off < 64; off <<= 1) v = fmax(v, __shfl_xor(v, off, 64));
-    return v;
-}
-__device__ __forceinline__ double wave_sum_f64(double v) {
-    for (int off = 1; off < 64; off <<= 1) v += __shfl_xor(v, off, 64);
-    return v;
+__device__ __forceinline__ double lane_f64(double v, int lane) {   // lane: uniform
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(u)), lane));
+    const uint32_t hi = uint32_t(__builtin_amdgcn_readlane(int(uint32_t(u >> 32)), lane));
+    return __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
 }
 
 // One token's choices: lane l holds the logits of experts l, l + 64, ...
@@ -88,7 +115,7 @@ __device__ __forceinline__ void select(const RouteArgs& a, int m, const double (
 #pragma unroll
     for (int i = 0; i < PER; ++i)
         if (64 * i + lane < a.E) top = fmax(top, z[i]);
-    top = wave_max_f64(top);
+    top = wave_all(top, [](double x, double y) { return fmax(x, y); });
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -102,7 +129,7 @@ __device__ __forceinline__ void select(const RouteArgs& a, int m, const double (
         if constexpr (PER > 4) __builtin_amdgcn_sched_barrier(0);   // one exp at a time (registers)
     }
     if (softmax && (a.bias || !a.norm)) {
-        sum = wave_sum_f64(sum);
+        sum = wave_all(sum, [](double x, double y) { return x + y; });
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             p[i] /= sum;
@@ -134,7 +161,7 @@ __device__ __forceinline__ void select(const RouteArgs& a, int m, const double (
             for (int off = 1; off < 64; off <<= 1) low = min(low, __shfl_xor(low, off, 64));
             who = __ballot(best == all && e == low);
         }
-        const int src = __ffsll(who) - 1;
+        const int src = __builtin_amdgcn_readfirstlane(__ffsll(who) - 1);
         double pv = 0.0;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
@@ -142,8 +169,8 @@ __device__ __forceinline__ void select(const RouteArgs& a, int m, const double (
                 pv = p[i];
                 if (lane == src) key[i] = kTaken;
             }
-        e = __shfl(e, src, 64);
-        pv = __shfl(pv, src, 64);
+        e = __builtin_amdgcn_readlane(e, src);
+        pv = lane_f64(pv, src);
         chosen += pv;
         if (lane == j) {
             mine = pv;
@@ -160,7 +187,7 @@ __device__ __forceinline__ void select(const RouteArgs& a, int m, const double (
 // PER: logits a lane holds when the last workgroup selects (E <= 64 PER).
 template <int PER>
 __global__ __launch_bounds__(kThreads) void moe_route_kernel(RouteArgs a) {
-    __shared__ double red[kWaves][kTileM * kTileE];   // 32 KiB: the waves' partial tiles
+    __shared__ double red[kWaves][kTileM * kTileE];   // 64 KiB: the waves' partial tiles
     __shared__ unsigned ticket;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -197,31 +224,50 @@ __global__ __launch_bounds__(kThreads) void moe_route_kernel(RouteArgs a) {
         red[wave][(4 * i + q) * kTileE + 16 + r] = c1[i];
     }
     __syncthreads();
-    const int t = tid / kTileE, e = tid % kTileE;   // 512 threads: one element each
+    const int t = tid / kTileE, e = tid % kTileE;   // the first 512 threads: one element each
     double z = 0.0;
+    if (tid < kTileM * kTileE)
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) z += red[w][tid];
+        for (int w = 0; w < kWaves; ++w) z += red[w][tid];
     double* slots = a.partial + int64_t(mt) * a.ranges * kTileM * a.E;
-    const bool ok = m0 + t < a.M && e0 + e < a.E;
+    const bool ok = t < kTileM && m0 + t < a.M && e0 + e < a.E;
     if (ok)   // written through to the device-coherent level (mmq_splitk.h)
         __hip_atomic_store(slots + (int64_t(range) * kTileM + t) * a.E + e0 + e, z, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
     if (!splitk_arrive(a.counters + mt, a.etiles * a.ranges, &ticket)) return;
-    // the last workgroup of this token tile
-    for (int tt = wave; tt < kTileM && m0 + tt < a.M; tt += kWaves) {
-        double logit[PER];
+    // The last workgroup of this token tile: the logits summed over the ranges in order (16 or 4 loads in
+    // flight: each is a trip to the device-coherent level), then one token per wave selected from LDS.
+    double* logits = &red[0][0];   // [token][E]
+    static_assert(sizeof(red) >= sizeof(double) * kWaves * kMoeMaxExperts, "the logits of the tile");
+    static_assert(kWaves == kTileM, "a wave per token");
+    const int count = min(kTileM, a.M - m0) * a.E;
+    for (int i = tid; i < count; i += kThreads) {
+        const double* from = slots + i;   // (tokens of a range are E apart, as here)
+        double sum = 0.0;
+        int g = 0;
+        auto batch = [&](auto n_c) {
+            constexpr int kN = decltype(n_c)::value;
+            for (; g + kN <= a.ranges; g += kN) {
+                double v[kN];
 #pragma unroll
-        for (int i = 0; i < PER; ++i) logit[i] = 0.0;
-#pragma unroll 2
-        for (int g = 0; g < a.ranges; ++g) {
+                for (int j = 0; j < kN; ++j)
+                    v[j] = __hip_atomic_load(from + int64_t(g + j) * kTileM * a.E, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int ex = min(64 * i + lane, a.E - 1);
-                logit[i] += __hip_atomic_load(slots + (int64_t(g) * kTileM + tt) * a.E + ex, __ATOMIC_RELAXED,
-                                              __HIP_MEMORY_SCOPE_AGENT);
+                for (int j = 0; j < kN; ++j) sum += v[j];
             }
-        }
-        select<PER>(a, m0 + tt, logit, lane);
+        };
+        batch(std::integral_constant<int, 16>{});
+        batch(std::integral_constant<int, 4>{});
+        batch(std::integral_constant<int, 1>{});
+        logits[i] = sum;
+    }
+    __syncthreads();
+    if (m0 + wave < a.M) {
+        double mine[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) mine[i] = logits[wave * a.E + min(64 * i + lane, a.E - 1)];
+        select<PER>(a, m0 + wave, mine, lane);
     }
 }
 
@@ -230,10 +276,10 @@ template __global__ void moe_route_kernel<2>(RouteArgs);
 template __global__ void moe_route_kernel<4>(RouteArgs);
 template __global__ void moe_route_kernel<8>(RouteArgs);
 
-// Ranges of K: about kTargetWorkgroups workgroups in all, each wave with at least one step.
+// Ranges of K: about kTargetWorkgroups workgroups in all.
 int route_ranges(int64_t M, int64_t K, int64_t E) {
     const int64_t tiles = ((M + kTileM - 1) / kTileM) * ((E + kTileE - 1) / kTileE);
-    return int(std::max<int64_t>(1, std::min<int64_t>(kTargetWorkgroups / tiles, K / (kStep * kWaves))));
+    return int(std::max<int64_t>(1, std::min<int64_t>(kTargetWorkgroups / tiles, K / (kStep * kWaves * (M <= kTileM ? kMinStepsFew : kMinSteps)))));
 }
 
 }  // namespace

@@ -59,15 +59,13 @@ __device__ __forceinline__ uint32_t align_byte(uint32_t hi, uint32_t lo, uint32_
     return __builtin_amdgcn_alignbyte(hi, lo, sel);
 }
 
-// A dword at an address that is only 2-byte aligned, built from the one or two
-// naturally aligned dwords that contain it.  Never touches a dword that holds
-// none of the requested bytes, so it cannot read past the end of a buffer.
-__device__ __forceinline__ uint32_t load_u32_a2(const uint8_t* p) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    const uint32_t* q = reinterpret_cast<const uint32_t*>(a & ~uintptr_t(3));
-    const uint32_t lo = q[0];
-    if (a & 2) return align_byte(q[1], lo, 2);
-    return lo;
+// A dword at any address, as one unaligned load of exactly its four bytes.  (Built from the one or two
+// aligned dwords that hold it, the second behind a branch on the address, each such load was waited
+// for where it stood: Q6_K's 14 per K-step took most of the MMQ kernel's time.)
+__device__ __forceinline__ uint32_t load_u32_unaligned(const uint8_t* p) {
+    uint32_t v;
+    __builtin_memcpy(&v, p, 4);
+    return v;
 }
 
 __device__ __forceinline__ uint32_t load_u16(const uint8_t* p) {

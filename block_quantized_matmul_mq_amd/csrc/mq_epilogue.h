@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace mq {
 
 constexpr int kActNone = 0;
@@ -79,9 +81,15 @@ struct Epilogue {
         if (bias)
 #pragma unroll
             for (int v = 0; v < C; ++v) y[v] += b;
-        if (act != kActNone)
+        // (one branch for the column: with the choice inside the loop the elements run one by one)
+        auto all = [&](auto act_c) {
 #pragma unroll
-            for (int v = 0; v < C; ++v) y[v] = activate(y[v], act);
+            for (int v = 0; v < C; ++v) y[v] = activate(y[v], decltype(act_c)::value);
+        };
+        if (act == kActSilu) all(std::integral_constant<int, kActSilu>{});
+        else if (act == kActGeluTanh) all(std::integral_constant<int, kActGeluTanh>{});
+        else if (act == kActGeluErf) all(std::integral_constant<int, kActGeluErf>{});
+        else if (act == kActRelu) all(std::integral_constant<int, kActRelu>{});
         if (mul)
 #pragma unroll
             for (int v = 0; v < C; ++v) y[v] *= f[v];
