@@ -60,7 +60,7 @@ constexpr int kPlane = 288;                  // bytes of a staged digit plane: 2
 constexpr int kPlanes = 3 * kPlane;
 constexpr int kDepth = 2;                    // weight groups in flight per wave
 constexpr int kOneUpWaves = 4096;            // waves of the one-token up kernel
-constexpr int kManyFixed = 64;               // many tokens: LDS of the slot's list
+constexpr int kManyFixed = 48 + 16 * kWaves;  // many tokens: LDS of the slot's lists
 
 // A wave-uniform pointer to device memory held in scalar registers: a load from it plus a 32-bit lane
 // offset then takes one vector register for its address (the compiler otherwise keeps a 64-bit pointer
@@ -429,6 +429,31 @@ constexpr int row_blocks_per_group() {
 //         the last round of waves is then 1 of 7 and not 1 of 4)
 //   down  leaves the weighted rows, f32 [pair][K].
 
+// The same for at most 64 pairs, a lane each, in every wave by itself (no trip through LDS, no barrier):
+// slots in the order of their first pairs; `list` is the wave's own.
+__device__ __forceinline__ int slot_pairs_of_64(const MoeArgs& a, int lane, int* count, int* list) {
+    const int e = lane < a.pairs ? a.ids[lane] : -1;
+    const bool valid = unsigned(e) < unsigned(a.experts);
+    unsigned long long same = __ballot(valid);   // the lanes of this lane's expert
+#pragma unroll
+    for (int b = 1; b < kMoeMaxExperts; b <<= 1) {
+        const unsigned long long m = __ballot((e & b) != 0);
+        same &= (e & b) ? m : ~m;
+    }
+    const unsigned long long below = (1ull << lane) - 1;
+    const int rank = __popcll(same & below);
+    const unsigned long long heads = __ballot(valid && rank % a.set == 0);   // a slot's first pair each
+    const bool mine = valid && rank % a.set == 0 && __popcll(heads & below) == int(blockIdx.y);
+    const unsigned long long head = __ballot(mine);
+    if (head == 0) return -1;
+    const int src = __builtin_amdgcn_readfirstlane(__ffsll(head) - 1);
+    const int expert = __builtin_amdgcn_readlane(e, src), first = __builtin_amdgcn_readlane(rank, src);
+    const bool in = valid && e == expert && rank >= first && rank < first + a.set;
+    if (in) list[rank - first] = lane;
+    *count = __popcll(__ballot(in));
+    return expert;
+}
+
 // Slot blockIdx.y: its expert (-1: there are fewer slots), and its pairs in list[0 .. *count - 1].
 // LDS: counts [kMoeMaxExperts], tmp [16], list.  Slots are numbered expert by expert.
 __device__ __forceinline__ int slot_pairs_of(const MoeArgs& a, int* counts, int* tmp, int* count, int* list) {
@@ -487,9 +512,8 @@ __device__ __forceinline__ int slot_pairs_of(const MoeArgs& a, int* counts, int*
 template <int QT, bool UP>
 __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
     extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-    int* tmp = reinterpret_cast<int*>(smem);   // [16], the count, the list of four
+    int* tmp = reinterpret_cast<int*>(smem);   // of slot_pairs_of, with the count; then a list of four per wave
     int* count_lds = tmp + 10;
-    int* list = tmp + 12;
     uint8_t* slots = smem + kManyFixed;
     uint8_t* staged = slots + kWaves * Tile<QT>::kSlot;
     int* counts = reinterpret_cast<int*>(slots);   // (before the first weights)
@@ -497,9 +521,17 @@ __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n = lane & 15, q = lane >> 4;
-    const int expert = slot_pairs_of(a, counts, tmp, count_lds, list);
+    const bool few = a.pairs <= 64;
+    int* list = tmp + 12 + (few ? 4 * wave : 0);
+    int expert, count;
+    if (few) {
+        expert = slot_pairs_of_64(a, lane, &count, list);
+        __builtin_amdgcn_wave_barrier();
+    } else {
+        expert = slot_pairs_of(a, counts, tmp, count_lds, list);
+        count = __builtin_amdgcn_readfirstlane(*count_lds);
+    }
     if (expert < 0) return;   // (uniform)
-    const int count = __builtin_amdgcn_readfirstlane(*count_lds);
 
     constexpr int kMats = UP ? 2 : 1;
     const int units = (a.rows >> 4) * kMats, stride = int(gridDim.x) * kWaves;
@@ -512,11 +544,31 @@ __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
     const int64_t expert_at = int64_t(expert) * a.rows * a.row_bytes;
     const int unit_size = count * unit_bytes<QT>();
 
-    // Stage the tokens: (group, token), dealt to the waves in batches.
+    struct Cursor {
+        int unit, g;
+    };
+    auto step = [&](Cursor& c) {
+        if (++c.g == a.groups) {
+            c.g = 0;
+            c.unit += stride;
+        }
+    };
+    Cursor ld = {min(unit0, units - 1), 0}, cp = {unit0, 0};
+    Tile<QT> buf[kDepth];
+    // (past the last unit: its last group again)
+    auto load = [&](auto slot_c) __attribute__((always_inline)) {
+        const uint8_t* w = (UP && (ld.unit & 1) ? a.w1 : a.w0) + expert_at + int64_t(UP ? ld.unit >> 1 : ld.unit) * tile_bytes;
+        buf[decltype(slot_c)::value].load(w, lanes, uint32_t(ld.g) * group_step, tile_bytes);
+        Cursor next = ld;
+        step(next);
+        if (next.unit < units) ld = next;
+    };
+    // Stage the tokens: (group, token), dealt to the waves in batches.  The first batch's activations are
+    // requested before the first weights (a wave's loads return in order), and those before it is staged.
     const int staging = a.groups * count;
     constexpr int kBatch = UP ? 4 : 2;
-    for (int u0 = wave; u0 < staging; u0 += kWaves * kBatch) {
-        float4 x[kBatch], y[kBatch];
+    float4 x[kBatch], y[kBatch];
+    auto fetch = [&](int u0) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int u = min(u0 + kWaves * i, staging - 1);
@@ -529,6 +581,8 @@ __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
                 if constexpr (!UP) y[i] = *reinterpret_cast<const float4*>(p + int64_t(a.pairs) * a.in);
             }
         }
+    };
+    auto stage = [&](int u0) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
             const int u = u0 + kWaves * i;
@@ -544,26 +598,18 @@ __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
                 stage_token<QT>(staged + g * unit_size, u - g * count, count, h, lane);
             }
         }
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    static_assert(kDepth == 2, "the loops below name the slots");
+    fetch(wave);
+    load(S0{});
+    load(S1{});
+    stage(wave);
+    for (int u0 = wave + kWaves * kBatch; u0 < staging; u0 += kWaves * kBatch) {
+        fetch(u0);
+        stage(u0);
     }
-    struct Cursor {
-        int unit, g;
-    };
-    auto step = [&](Cursor& c) {
-        if (++c.g == a.groups) {
-            c.g = 0;
-            c.unit += stride;
-        }
-    };
-    Cursor ld = {unit0, 0}, cp = ld;
-    Tile<QT> buf[kDepth];
-    // (past the last unit: its last group again)
-    auto load = [&](auto slot_c) __attribute__((always_inline)) {
-        const uint8_t* w = (UP && (ld.unit & 1) ? a.w1 : a.w0) + expert_at + int64_t(UP ? ld.unit >> 1 : ld.unit) * tile_bytes;
-        buf[decltype(slot_c)::value].load(w, lanes, uint32_t(ld.g) * group_step, tile_bytes);
-        Cursor next = ld;
-        step(next);
-        if (next.unit < units) ld = next;
-    };
     const LaneTokens<QT> at(lane, 0, count);
     const int pair = list[min(q, count - 1)];
     const float weight = UP ? 1.f : a.wts[pair];
@@ -589,13 +635,6 @@ __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
         }
         step(cp);
     };
-    using S0 = std::integral_constant<int, 0>;
-    using S1 = std::integral_constant<int, 1>;
-    static_assert(kDepth == 2, "the loop below names the slots");
-    if (unit0 < units) {
-        load(S0{});
-        load(S1{});
-    }
     lds_barrier();
     if (unit0 < units) {
         while (true) {
