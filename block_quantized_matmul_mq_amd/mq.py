@@ -362,6 +362,17 @@ def _call(fn, tensor, stream, *args):
     _check(fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream))
 
 
+def _new(stream, make, shape, dtype, device):
+    """make(shape) (torch.empty or torch.zeros), in order on the call's stream: memory that the allocator
+    takes back may otherwise be reused, or be cleared, while the call runs."""
+    import torch
+    if stream is None or device.type != "cuda":
+        return make(shape, dtype=dtype, device=device)
+    handle = stream if isinstance(stream, int) else stream.value or 0
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+        return make(shape, dtype=dtype, device=device)
+
+
 def _terms(fn, M, N, bias, mul, residual):
     """The epilogue's tensors that are given, checked."""
     given = []
@@ -380,7 +391,7 @@ def gemv_ep(W, qtype, x, N, K, bias=None, act=ACT_NONE, mul=None, residual=None,
     _f32(x, K, "gemv_ep", "x")
     given = _terms("gemv_ep", 1, N, bias, mul, residual)
     if y is None:
-        y = torch.empty(N, dtype=torch.float32, device=x.device)
+        y = _new(stream, torch.empty, N, torch.float32, x.device)
     else:
         _f32(y, N, "gemv_ep", "y")
     _same_device("gemv_ep", W, x, y, *given)
@@ -398,12 +409,12 @@ def gemm_ep(W, qtype, Xq, M, N, K, bias=None, act=ACT_NONE, mul=None, residual=N
     _act_plane(Xq, M, K, "gemm_ep")
     given = _terms("gemm_ep", M, N, bias, mul, residual)
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=Xq.device)
+        Y = _new(stream, torch.empty, (M, N), torch.float32, Xq.device)
     else:
         _f32(Y, M * N, "gemm_ep", "Y")
     need = gemm_scratch_bytes(qtype, M, N, K)
     if scratch is None and need:
-        scratch = torch.zeros(need, dtype=torch.uint8, device=Xq.device)
+        scratch = _new(stream, torch.zeros, need, torch.uint8, Xq.device)
     if scratch is not None:
         _buffer(scratch, need, "gemm_ep", "scratch")
         given.append(scratch)
@@ -445,7 +456,7 @@ def moe_route(X, Wr, topk, bias=None, score=SCORE_SOFTMAX, norm=True, scale=1.0,
     _f32(Wr, E * K, "moe_route", "Wr")
     need = moe_route_scratch_bytes(M, K, E)
     if scratch is None:
-        scratch = torch.zeros(max(need, 16), dtype=torch.uint8, device=X.device)
+        scratch = _new(stream, torch.zeros, max(need, 16), torch.uint8, X.device)
     else:
         _buffer(scratch, need, "moe_route", "scratch")
     tensors = [X, Wr, scratch]
@@ -453,11 +464,11 @@ def moe_route(X, Wr, topk, bias=None, score=SCORE_SOFTMAX, norm=True, scale=1.0,
         _f32(bias, E, "moe_route", "bias")
         tensors.append(bias)
     if ids is None:
-        ids = torch.empty((M, topk), dtype=torch.int32, device=X.device)
+        ids = _new(stream, torch.empty, (M, topk), torch.int32, X.device)
     else:
         _i32(ids, M * topk, "moe_route", "ids")
     if wts is None:
-        wts = torch.empty((M, topk), dtype=torch.float32, device=X.device)
+        wts = _new(stream, torch.empty, (M, topk), torch.float32, X.device)
     else:
         _f32(wts, M * topk, "moe_route", "wts")
     _same_device("moe_route", ids, wts, *tensors)
@@ -492,12 +503,12 @@ def moe_ffn(Wg, Wu, gu_type, Wd, d_type, X, ids, wts, E, F, act=ACT_SILU, residu
         _f32(residual, M * K, "moe_ffn", "residual")
         tensors.append(residual)
     if Y is None:
-        Y = torch.empty((M, K), dtype=torch.float32, device=X.device)
+        Y = _new(stream, torch.empty, (M, K), torch.float32, X.device)
     else:
         _f32(Y, M * K, "moe_ffn", "Y")
     need = moe_scratch_bytes(M, topk, F, K)
     if scratch is None:
-        scratch = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
+        scratch = _new(stream, torch.empty, max(need, 16), torch.uint8, X.device)
     else:
         _buffer(scratch, need, "moe_ffn", "scratch")
     _same_device("moe_ffn", Y, scratch, *tensors)

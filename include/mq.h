@@ -320,7 +320,8 @@ int mq_moe_route(const float* X, const float* Wr, const float* bias, int32_t* id
  * E <= MQ_MOE_MAX_EXPERTS; M * topk <= MQ_MOE_MAX_PAIRS (a larger batch belongs to mq_gemm,
  * expert by expert).  Y may be X or residual.
  * f32 accuracy: activations keep 22 bits relative to the largest of their 32-value block, block dots
- * are exact integers, all sums f32.  A token with an infinity or a NaN gets NaN outputs.
+ * are exact integers, all sums f32.  A token with an infinity or a NaN (in X, or in
+ * act(Wg X) * (Wu X), which may overflow) gets NaN outputs.
  * Deterministic: a token's bits depend on its own row, ids and weights and on which kernels run
  * (one token of at most 64 choices, or more), not on the other tokens.
  * scratch: mq_moe_scratch_bytes(M, topk, F, K) bytes (0 for sizes the call refuses), 16-byte
