@@ -343,7 +343,7 @@ __global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restric
         *reinterpret_cast<uint32_t*>(p0 + off) = d0;
         *reinterpret_cast<uint32_t*>(p1 + off) = d1;
         *reinterpret_cast<uint32_t*>(p2 + off) = d2;
-        float sm = (v.x + v.y) + (v.z + v.w);
+        float sm = staged_sum<EP>(v, k);
         sm = lanes8_sum<2>(sm);
         if constexpr (QT == kQ6_K) {
             if ((i & 3) == 0) {            // one 16-run = chunk kc of unit uu

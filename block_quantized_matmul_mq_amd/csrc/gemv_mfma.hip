@@ -204,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void gemv_mfma_q4k_kernel(const uint8_t* 
         *reinterpret_cast<uint32_t*>(xp + 4 * tid) = d0;
         *reinterpret_cast<uint32_t*>(xp + K + 4 * tid) = d1;
         *reinterpret_cast<uint32_t*>(xp + 2 * K + 4 * tid) = d2;
-        float sm = (v.x + v.y) + (v.z + v.w);
+        float sm = staged_sum<EP>(v, k);
         sm = lanes8_sum(sm);
         if ((tid & 7) == 0) {
             sums[tid >> 3] = sm;
@@ -401,7 +401,7 @@ __global__ __launch_bounds__(kThreads) void gemv_mfma_q4k_long_kernel(const uint
         *reinterpret_cast<uint32_t*>(my_xs + 4 * lane) = d0;
         *reinterpret_cast<uint32_t*>(my_xs + 256 + 4 * lane) = d1;
         *reinterpret_cast<uint32_t*>(my_xs + 512 + 4 * lane) = d2;
-        float sm = (v.x + v.y) + (v.z + v.w);
+        float sm = staged_sum<EP>(v, k);
         sm = lanes8_sum(sm);
         if ((lane & 7) == 0) {
             my_sum[lane >> 3] = sm;
@@ -715,7 +715,7 @@ __global__ __launch_bounds__(kThreads) void gemv_tiled_kernel(const uint8_t* __r
         *reinterpret_cast<uint32_t*>(xp + 4 * tid) = d0;
         *reinterpret_cast<uint32_t*>(xp + K + 4 * tid) = d1;
         *reinterpret_cast<uint32_t*>(xp + 2 * K + 4 * tid) = d2;
-        float sm = (v.x + v.y) + (v.z + v.w);
+        float sm = staged_sum<EP>(v, k);
         sm = lanes8_sum<2>(sm);
         if ((tid & 3) == 0) sums[tid >> 2] = sm;
         if ((tid & 7) == 0) ex[tid >> 3] = -k;
@@ -1121,7 +1121,7 @@ __global__ __launch_bounds__(kThreads) void gemv_wide_kernel(const uint8_t* __re
         *reinterpret_cast<uint32_t*>(xp + 4 * tid) = d0;
         *reinterpret_cast<uint32_t*>(xp + K + 4 * tid) = d1;
         *reinterpret_cast<uint32_t*>(xp + 2 * K + 4 * tid) = d2;
-        float sm = (v.x + v.y) + (v.z + v.w);
+        float sm = staged_sum<EP>(v, k);
         sm = lanes8_sum<2>(sm);
         if ((tid & 3) == 0) sums[tid >> 2] = sm;
         if ((tid & 7) == 0) ex[tid >> 3] = -k;

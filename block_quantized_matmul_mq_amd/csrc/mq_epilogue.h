@@ -19,8 +19,8 @@ constexpr int kActs = 5;
 // 1 / (1 + e^-u).  e^-u as 2^t by the exp2 instruction, t = -u log2(e) rounded to f32, times 1 + r ln 2
 // for what the rounding of t left out (r: an fma's exact remainder and log2(e)'s own low part), so
 // the relative error stays at about two roundings for large |u| too; then one reciprocal
-// instruction.  (expf and an IEEE division took 16 us of the 164 us of 512 x 18944 x 3584 with silu,
-// this 4.)  e^-u overflows to infinity (1 / inf = 0) and keeps a NaN.
+// instruction.  (512 x 18944 x 3584 Q4_K with silu and mul: 164 us with expf and an IEEE
+// division, 146 with this.)  e^-u overflows to infinity (1 / inf = 0) and keeps a NaN.
 __device__ __forceinline__ float logistic(float u) {
     constexpr float kLog2e = 1.44269502162933349609375f;        // f32(log2 e)
     constexpr float kLog2eLow = 1.92596299112661746887e-8f;     // log2 e - f32(log2 e)
@@ -66,7 +66,7 @@ struct Epilogue {
     }
     // The same for C elements of one column n, at(v) the (valid) place of element v: each term's
     // loads are issued together and before the activations, instead of one round trip per element
-    // (512 x 18944 x 3584 Q4_K with silu and mul: 195 -> 178 us).
+    // (512 x 18944 x 3584 Q4_K with silu and mul: 195 -> 164 us).
     template <int C, class At>
     __device__ __forceinline__ void column(float (&y)[C], int n, const At& at) const {
         float f[C], r[C];
@@ -104,6 +104,18 @@ struct Epilogue {
 inline void* epilogue_arg(const Epilogue* ep) {
     static NoEpilogue none;
     return ep ? const_cast<void*>(static_cast<const void*>(ep)) : static_cast<void*>(&none);
+}
+
+// The sum of four activations of a block staged as integers, x = 2^-k rint(2^k x) with |2^k x| <= 2^21: of
+// the staged x in the kernels with an epilogue (exact), of x itself in those without, whose results are
+// fixed.  A code's offset and a minimum then multiply the same x that the codes meet, so that staging's error of
+// x carries through the weight and not through the code (Q4_0, 9872 x 5408: 9.8e-7 -> 5.1e-7 relative).
+template <class EP>
+__device__ __forceinline__ float staged_sum(const float4 v, int k) {
+    if constexpr (!EP::kIs) return (v.x + v.y) + (v.z + v.w);
+    constexpr float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to whole numbers
+    auto rounded = [&](float x) { return (ldexpf(x, k) + kRound) - kRound; };
+    return ldexpf((rounded(v.x) + rounded(v.y)) + (rounded(v.z) + rounded(v.w)), -k);
 }
 
 // An f32 (its bits) as three bf16 pieces of 8 bits each, high + mid + low exactly; each piece

@@ -277,9 +277,11 @@ int mq_gemm(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_
  * So a gated feed-forward layer takes three products and no other launch:
  *   u = mq_gemv(Wup), h = mq_gemv_ep(Wgate, act = MQ_ACT_SILU, mul = u),
  *   y = mq_gemv_ep(Wdown, h, residual = y).
- * The min term of Q4_K, Q5_K, Q4_1 and Q5_1 on the int8 kernels is formed to f32 precision
- * here (mq_gemm forms it to 2^-16), so an mq_gemm_ep without terms agrees with mq_gemm to
- * mq_gemm's accuracy, for those types not bit for bit; the other types' acc are the same bits.
+ * Two sums are formed more precisely here, so that a call without terms agrees with mq_gemv or
+ * mq_gemm to their accuracy and, for the types named, not bit for bit: mq_gemm_ep forms the min term
+ * of Q4_K, Q5_K, Q4_1 and Q5_1 on the int8 kernels to f32 precision (mq_gemm: to 2^-16);
+ * mq_gemv_ep forms the offset and min terms (every type but Q8_0) from the staged activations that
+ * the codes meet (mq_gemv: from x).
  */
 int mq_gemv_ep(const void* W, int type, const float* x, float* y, int64_t N, int64_t K, const float* bias, int act,
                const float* mul, const float* residual, void* stream);

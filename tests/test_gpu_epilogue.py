@@ -1,8 +1,8 @@
 """GPU parity of mq_gemv_ep and mq_gemm_ep, on every kernel that they run.
 
-* Without terms they give the bits of mq_gemv / mq_gemm (for mq_gemm's types with a minimum on the
-  int8 kernels, whose min term is formed to f32 precision here: the f64 product within the bound of
-  f32 sums).
+* Without terms they give the bits of mq_gemv / mq_gemm, but for what is formed more precisely here: mq_gemv's
+  offset and min terms (from the staged activations) and mq_gemm's min terms on the int8 kernels (to f32
+  precision); there the f64 product within the bound of f32 sums.
 * With terms the result is the oracle's epilogue of that accumulator, within the roundings of the
   epilogue's own f32 steps.
 """
@@ -96,14 +96,28 @@ def test_gemv(qtype, N, K, kernel):
     say(f"gemv_ep {kernel} N={N} K={K}")
     raw = weights(qtype & 0xFF, N, K, "quantized", 700)
     W = laid_out(raw, qtype, N, K, dev)
-    x = to_dev(synth.activations(1, K, config_index=14, tensor_index=7)[0], dev)
+    X = synth.activations(1, K, config_index=14, tensor_index=7)
+    x = to_dev(X[0], dev)
     acc = mq.gemv(W, qtype, x, N, K)
     assert mq.last_kernel() == kernel, mq.last_kernel()
     y = mq.gemv_ep(W, qtype, x, N, K)
     assert mq.last_kernel() == kernel
     torch.cuda.synchronize()
-    acc = acc.cpu().numpy()
-    assert np.array_equal(y.cpu().numpy(), acc)
+    acc, plain = y.cpu().numpy(), acc.cpu().numpy()
+    base = qtype & 0xFF
+    if base == mq.Q8_0:
+        assert np.array_equal(acc, plain)
+    else:
+        # x staged within 2^-21 of its block's largest (half a unit, the largest at least 2^20 units), met by the
+        # weight; K / 32 block terms and their offset or min terms, summed in f32 (any order), each product rounded
+        w = oracle.decode(raw, base, N, K)
+        top = np.abs(X.reshape(-1, 32)).max(1).astype(np.float64).repeat(32)
+        bound = 2.0 ** -21 * (np.abs(w) @ top) + (K / 32 + 24) * HALF * (oracle.magnitude(raw, base, N, K) @ np.abs(X[0]))
+        ref = w @ X[0].astype(np.float64)
+        err = np.abs(acc - ref)
+        rel = [float(np.linalg.norm(v - ref) / np.linalg.norm(ref)) for v in (acc, plain)]
+        say(f"  worst error / bound {float((err / bound).max()):.3f}, relative {rel[0]:.2e} (mq_gemv {rel[1]:.2e})")
+        assert np.all(err <= bound)
     check_terms(lambda **t: mq.gemv_ep(W, qtype, x, N, K, **t), acc[None], 1, N, kernel)
 
 
