@@ -162,6 +162,8 @@ def _weights(W, qtype, N, K, fn):
 
 def _f32(t, numel, fn, name):
     import torch
+    if t.dtype is torch.float32 and t.numel() == numel and t.is_contiguous():
+        return
     if t.dtype != torch.float32:
         _refuse(-1, fn, f"{name} must be float32, not {t.dtype}")
     _contiguous(t, fn, name)
@@ -176,9 +178,13 @@ def _buffer(t, min_bytes, fn, name):
 
 
 def _same_device(fn, *tensors):
-    d = tensors[0].device
-    if d.type == "cuda" and all([t.device == d for t in tensors]):
-        return
+    d = tensors[0].get_device()      # (-1 on the CPU; no device objects: 0.7 -> 0.3 us per call)
+    if d >= 0:
+        for t in tensors:
+            if t.get_device() != d:
+                break
+        else:
+            return
     devs = {(t.device.type, t.device.index) for t in tensors}
     if len(devs) != 1 or next(iter(devs))[0] != "cuda":
         _refuse(-6, fn, f"every tensor must be on one GPU device, got {sorted(map(str, devs))}")
@@ -355,22 +361,26 @@ def _ptr(t):
 def _call(fn, tensor, stream, *args):
     """fn(*args, stream) on the device of the (checked) tensors, on `stream` or that device's current one."""
     import torch
-    device = tensor.device.index
-    if device != torch.cuda.current_device():
+    device = tensor.get_device()
+    if device == torch._C._cuda_getDevice():
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream)
+    else:
         with torch.cuda.device(device):
-            return _check(fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream))
-    _check(fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream))
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream)
+    if code != MQ_OK:
+        _check(code)
 
 
-def _new(stream, make, shape, dtype, device):
-    """make(shape) (torch.empty or torch.zeros), in order on the call's stream: memory that the allocator
+def _new(stream, like, shape, dtype, zero=False):
+    """A tensor on `like`'s device, empty or zero, in order on the call's stream: memory that the allocator
     takes back may otherwise be reused, or be cleared, while the call runs."""
     import torch
-    if stream is None or device.type != "cuda":
-        return make(shape, dtype=dtype, device=device)
+    make = like.new_zeros if zero else like.new_empty
+    if stream is None or not like.is_cuda:
+        return make(shape, dtype=dtype)
     handle = stream if isinstance(stream, int) else stream.value or 0
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
-        return make(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=like.device)):
+        return make(shape, dtype=dtype)
 
 
 def _terms(fn, M, N, bias, mul, residual):
@@ -391,7 +401,7 @@ def gemv_ep(W, qtype, x, N, K, bias=None, act=ACT_NONE, mul=None, residual=None,
     _f32(x, K, "gemv_ep", "x")
     given = _terms("gemv_ep", 1, N, bias, mul, residual)
     if y is None:
-        y = _new(stream, torch.empty, N, torch.float32, x.device)
+        y = _new(stream, x, N, torch.float32)
     else:
         _f32(y, N, "gemv_ep", "y")
     _same_device("gemv_ep", W, x, y, *given)
@@ -409,12 +419,12 @@ def gemm_ep(W, qtype, Xq, M, N, K, bias=None, act=ACT_NONE, mul=None, residual=N
     _act_plane(Xq, M, K, "gemm_ep")
     given = _terms("gemm_ep", M, N, bias, mul, residual)
     if Y is None:
-        Y = _new(stream, torch.empty, (M, N), torch.float32, Xq.device)
+        Y = _new(stream, Xq, (M, N), torch.float32)
     else:
         _f32(Y, M * N, "gemm_ep", "Y")
     need = gemm_scratch_bytes(qtype, M, N, K)
     if scratch is None and need:
-        scratch = _new(stream, torch.zeros, need, torch.uint8, Xq.device)
+        scratch = _new(stream, Xq, need, torch.uint8, zero=True)
     if scratch is not None:
         _buffer(scratch, need, "gemm_ep", "scratch")
         given.append(scratch)
@@ -456,7 +466,7 @@ def moe_route(X, Wr, topk, bias=None, score=SCORE_SOFTMAX, norm=True, scale=1.0,
     _f32(Wr, E * K, "moe_route", "Wr")
     need = moe_route_scratch_bytes(M, K, E)
     if scratch is None:
-        scratch = _new(stream, torch.zeros, max(need, 16), torch.uint8, X.device)
+        scratch = _new(stream, X, max(need, 16), torch.uint8, zero=True)
     else:
         _buffer(scratch, need, "moe_route", "scratch")
     tensors = [X, Wr, scratch]
@@ -464,11 +474,11 @@ def moe_route(X, Wr, topk, bias=None, score=SCORE_SOFTMAX, norm=True, scale=1.0,
         _f32(bias, E, "moe_route", "bias")
         tensors.append(bias)
     if ids is None:
-        ids = _new(stream, torch.empty, (M, topk), torch.int32, X.device)
+        ids = _new(stream, X, (M, topk), torch.int32)
     else:
         _i32(ids, M * topk, "moe_route", "ids")
     if wts is None:
-        wts = _new(stream, torch.empty, (M, topk), torch.float32, X.device)
+        wts = _new(stream, X, (M, topk), torch.float32)
     else:
         _f32(wts, M * topk, "moe_route", "wts")
     _same_device("moe_route", ids, wts, *tensors)
@@ -503,12 +513,12 @@ def moe_ffn(Wg, Wu, gu_type, Wd, d_type, X, ids, wts, E, F, act=ACT_SILU, residu
         _f32(residual, M * K, "moe_ffn", "residual")
         tensors.append(residual)
     if Y is None:
-        Y = _new(stream, torch.empty, (M, K), torch.float32, X.device)
+        Y = _new(stream, X, (M, K), torch.float32)
     else:
         _f32(Y, M * K, "moe_ffn", "Y")
     need = moe_scratch_bytes(M, topk, F, K)
     if scratch is None:
-        scratch = _new(stream, torch.empty, max(need, 16), torch.uint8, X.device)
+        scratch = _new(stream, X, max(need, 16), torch.uint8)
     else:
         _buffer(scratch, need, "moe_ffn", "scratch")
     _same_device("moe_ffn", Y, scratch, *tensors)
