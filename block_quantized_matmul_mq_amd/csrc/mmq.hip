@@ -804,8 +804,8 @@ hipError_t launch_shaped(const uint8_t* W, const int8_t* codes, const float* xs,
 template <int QT>
 hipError_t launch_typed(const uint8_t* W, const int8_t* codes, const float* xs, const int32_t* xsum,
                         float* Y, int32_t* dots, float* partial, unsigned* counters, int64_t M, int64_t N,
-                        int64_t K, BlockLayout lay, const Epilogue* ep, hipStream_t s) {
-    const MmqPlan plan = mmq_plan(QT, M, N, K);
+                        int64_t K, BlockLayout lay, const Epilogue* ep, bool filled, hipStream_t s) {
+    const MmqPlan plan = filled ? mmq_filled_plan(QT, M, N, K) : mmq_plan(QT, M, N, K);
     if (!counters && partial) {   // the caller's scratch: counters, then the partial tiles
         counters = reinterpret_cast<unsigned*>(partial);
         partial = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(partial) + kSplitkCounterBytes);
@@ -866,6 +866,46 @@ MmqPlan mmq_plan(int /*type*/, int64_t M, int64_t N, int64_t K) {
     return p;
 }
 
+MmqPlan mmq_filled_plan(int type, int64_t M, int64_t N, int64_t K) {
+    // mmq_plan's cuts stop at one workgroup per CU, and from 257 tiles of 32 rows on cut nothing, which leaves
+    // a product of a long K and few columns with half the chip idle.  Here all tiles are cut alike into as
+    // many K ranges (of at least kRange steps) as fill both workgroups of every CU, and the tile rows are
+    // those of the lower cost in row steps per workgroup: a row step of a 32-row tile costs 1.7 of a
+    // 128-row tile's, writing and adding a round of partial tiles as much as 640 row steps (128 rows) or 160 (32).
+    // (us, mmq_plan -> this: Q6_K 333 x 5120 x 13824 248 -> 169, Q8_0 141 -> 109; Q6_K 128 x 8192 x 8192
+    // 105 -> 78, 512 x 8192 x 8192 261 -> 199;
+    // Q5_1 64 x 8192 x 8192 50 -> 36; Q8_0 384 x 2048 x 8192 87 -> 54.)
+    constexpr int kRange = 7;
+    const MmqPlan plain = mmq_plan(type, M, N, K);
+    auto cut = [&](int bm) {
+        MmqPlan p = plain;
+        p.bm = bm;
+        const int64_t tiles = ((M + bm - 1) / bm) * ((N + BN - 1) / BN);
+        p.full = 0;
+        p.split_tiles = int(tiles);
+        p.splits = tiles > kTargetWorkgroups / 2
+                       ? 0
+                       : int(std::min<int64_t>(kTargetWorkgroups / tiles, p.steps / kRange));
+        return p;   // (splits of 0 or 1: nothing to cut)
+    };
+    const MmqPlan wide = cut(128), narrow = cut(32);
+    if (wide.splits == 0 && narrow.splits == 0) return plain;
+    auto row_steps = [&](int bm) { return (bm == 32 ? 1.7 * 32 : 128.0) * plain.steps; };
+    const auto partials = [](int bm) { return bm == 32 ? 160.0 : 640.0; };
+    auto cost = [&](const MmqPlan& p) { return p.splits < 2 ? 1e30 : row_steps(p.bm) / p.splits + partials(p.bm); };
+    const double wide_cost = M <= kSmallM ? 1e30 : cost(wide), narrow_cost = cost(narrow);
+    double plain_cost = row_steps(plain.bm) * ((plain.full + kTargetWorkgroups - 1) / kTargetWorkgroups);
+    if (plain.split_tiles) plain_cost += row_steps(plain.bm) / plain.splits + partials(plain.bm) / 2;
+    if (plain_cost <= std::min(wide_cost, narrow_cost)) return plain;
+    return wide_cost < narrow_cost ? wide : narrow;
+}
+
+size_t mmq_filled_scratch_bytes(int type, int64_t M, int64_t N, int64_t K) {
+    if (gemv_q8_applies(type, M, K) || mmq_kw_applies(type, BlockLayout{144, 0}, M, N, K)) return 0;
+    const MmqPlan p = mmq_filled_plan(type, M, N, K);
+    return splitk_scratch_bytes(p.split_tiles, p.splits, int64_t(p.bm) * BN);
+}
+
 size_t mmq_scratch_bytes(int type, int64_t M, int64_t N, int64_t K) {
     if (gemv_q8_applies(type, M, K) || mmq_kw_applies(type, BlockLayout{144, 0}, M, N, K)) return 0;
     const MmqPlan p = mmq_plan(type, M, N, K);
@@ -880,7 +920,7 @@ size_t mmq_partial_bytes(int type, int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_mmq(int type, BlockLayout lay, const uint8_t* W, const int8_t* codes, const float* xs,
                       const int32_t* xsum, float* Y, int32_t* dots, void* scratch, unsigned* counters, int64_t M,
-                      int64_t N, int64_t K, const Epilogue* ep, hipStream_t s, const char** name) {
+                      int64_t N, int64_t K, const Epilogue* ep, bool filled, hipStream_t s, const char** name) {
     if (gemv_q8_applies(type, M, K)) return launch_gemv_q8(type, lay, W, codes, xs, xsum, Y, dots, M, N, K, ep, s, name);
     if (mmq_kw_applies(type, lay, M, N, K)) return launch_mmq_kw(W, codes, xs, xsum, Y, dots, M, N, K, ep, s, name);
     float* partial = static_cast<float*>(scratch);
@@ -888,28 +928,28 @@ hipError_t launch_mmq(int type, BlockLayout lay, const uint8_t* W, const int8_t*
     switch (type) {
         case kQ8_0:
             *name = repacked ? "mmq<q8_0 repacked>" : "mmq<q8_0>";
-            return launch_typed<kQ8_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
+            return launch_typed<kQ8_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, filled, s);
         case kQ4_K:
             *name = "mmq<q4_K>";
-            return launch_typed<kQ4_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
+            return launch_typed<kQ4_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, filled, s);
         case kQ6_K:
             *name = repacked ? "mmq<q6_K repacked>" : "mmq<q6_K>";
-            return launch_typed<kQ6_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
+            return launch_typed<kQ6_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, filled, s);
         case kQ5_K:
             *name = "mmq<q5_K>";
-            return launch_typed<kQ5_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
+            return launch_typed<kQ5_K>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, filled, s);
         case kQ4_0:
             *name = "mmq<q4_0>";
-            return launch_typed<kQ4_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
+            return launch_typed<kQ4_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, filled, s);
         case kQ4_1:
             *name = "mmq<q4_1>";
-            return launch_typed<kQ4_1>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
+            return launch_typed<kQ4_1>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, filled, s);
         case kQ5_0:
             *name = "mmq<q5_0>";
-            return launch_typed<kQ5_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
+            return launch_typed<kQ5_0>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, filled, s);
         case kQ5_1:
             *name = "mmq<q5_1>";
-            return launch_typed<kQ5_1>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, s);
+            return launch_typed<kQ5_1>(W, codes, xs, xsum, Y, dots, partial, counters, M, N, K, lay, ep, filled, s);
         default: return hipErrorInvalidValue;
     }
 }

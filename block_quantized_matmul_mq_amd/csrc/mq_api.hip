@@ -7,6 +7,7 @@
 // returns are read at the call site, device limits are queried at run time).
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -276,6 +277,16 @@ size_t mq_gemm_scratch_bytes(int type, int64_t M, int64_t N, int64_t K) {
     return mmq_scratch_bytes(type, M, N, K);
 }
 
+size_t mq_gemm_ep_scratch_bytes(int type, int64_t M, int64_t N, int64_t K) {
+    const size_t plain = mq_gemm_scratch_bytes(type, M, N, K);
+    BlockLayout lay;
+    type = parse_type(type, lay);
+    if (type == 0 || is_plane(lay) || lay.row_tiled || M <= 0 || N <= 0 || K <= 0 || M > MQ_MAX_M || N > MQ_MAX_N ||
+        K > MQ_MAX_K || K % block_values(type) != 0)
+        return plain;
+    return std::max(plain, mmq_filled_scratch_bytes(type, M, N, K));
+}
+
 int mq_quantize_act(const float* X, void* Xq, int64_t M, int64_t K, void* stream) {
     const char* fn = "mq_quantize_act";
     if (!X || !Xq) return fail(MQ_ERR_ARG, "%s: null pointer (X=%p Xq=%p)", fn, (const void*)X, Xq);
@@ -357,7 +368,7 @@ int mq_gemv_ep(const void* W, int type, const float* x, float* y, int64_t N, int
 
 static int gemm_common(const char* fn, const void* W, int type, const void* Xq, float* Y, int32_t* D,
                        void* scratch, unsigned* counters, int64_t M, int64_t N, int64_t K, const Epilogue* ep,
-                       void* stream) {
+                       bool filled, void* stream) {
     if (!W || !Xq || (!Y && !D))
         return fail(MQ_ERR_ARG, "%s: null pointer (W=%p Xq=%p out=%p)", fn, W, Xq, Y ? (void*)Y : (void*)D);
     BlockLayout lay;
@@ -392,7 +403,7 @@ static int gemm_common(const char* fn, const void* W, int type, const void* Xq, 
     hipError_t e = launch_mmq(type, lay, static_cast<const uint8_t*>(W), reinterpret_cast<const int8_t*>(xq),
                               reinterpret_cast<const float*>(xq + act_scale_offset(M, K)),
                               reinterpret_cast<const int32_t*>(xq + act_sum_offset(M, K)), Yout, D, scratch,
-                              counters, M, N, K, ep, static_cast<hipStream_t>(stream), &kernel);
+                              counters, M, N, K, ep, filled, static_cast<hipStream_t>(stream), &kernel);
     return launch_status(fn, e, kernel);
 }
 
@@ -402,9 +413,12 @@ static int gemm_with_scratch(const char* fn, const void* W, int type, const void
     const size_t need = mq_gemm_scratch_bytes(type, M, N, K);
     if (scratch_bytes < need || (need && !scratch))
         return fail(MQ_ERR_SIZE, "%s: scratch of %zu bytes at %p, %zu required", fn, scratch_bytes, scratch, need);
-    if (need && !aligned(scratch, 16))
+    const size_t fill = ep && scratch ? mq_gemm_ep_scratch_bytes(type, M, N, K) : 0;
+    const bool filled = fill && scratch_bytes >= fill;
+    if ((need || filled) && !aligned(scratch, 16))
         return fail(MQ_ERR_ALIGN, "%s: scratch must be 16-byte aligned (%p)", fn, scratch);
-    return gemm_common(fn, W, type, Xq, Y, nullptr, need ? scratch : nullptr, nullptr, M, N, K, ep, stream);
+    return gemm_common(fn, W, type, Xq, Y, nullptr, need || filled ? scratch : nullptr, nullptr, M, N, K, ep, filled,
+                       stream);
 }
 
 int mq_gemm(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N, int64_t K, void* scratch,
@@ -437,7 +451,7 @@ int mq_gemm_noalloc(const void* W, int type, const void* Xq, float* Y, int64_t M
     if (rc) return rc;
     uint8_t* base = device_info()->noalloc_scratch;
     return gemm_common(fn, W, type, Xq, Y, nullptr, base + kNoAllocCounterBytes, reinterpret_cast<unsigned*>(base),
-                       M, N, K, nullptr, stream);
+                       M, N, K, nullptr, false, stream);
 }
 
 size_t mq_debug_lds_bytes(int what, int type, int64_t K) {
@@ -463,7 +477,7 @@ int mq_debug_gemm_blockdots(const void* W, int type, const void* Xq, int32_t* D,
                             void* stream) {
     const char* fn = "mq_debug_gemm_blockdots";
     if (!D) return fail(MQ_ERR_ARG, "%s: null D", fn);
-    return gemm_common(fn, W, type, Xq, nullptr, D, nullptr, nullptr, M, N, K, nullptr, stream);
+    return gemm_common(fn, W, type, Xq, nullptr, D, nullptr, nullptr, M, N, K, nullptr, false, stream);
 }
 
 size_t mq_moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K) {

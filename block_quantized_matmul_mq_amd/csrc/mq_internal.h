@@ -138,13 +138,17 @@ struct MmqPlan {
 MmqPlan mmq_plan(int type, int64_t M, int64_t N, int64_t K);
 size_t mmq_scratch_bytes(int type, int64_t M, int64_t N, int64_t K);
 size_t mmq_partial_bytes(int type, int64_t M, int64_t N, int64_t K);
+// The work split of mq_gemm_ep with mq_gemm_ep_scratch_bytes of scratch: enough K ranges for two workgroups
+// per CU.
+MmqPlan mmq_filled_plan(int type, int64_t M, int64_t N, int64_t K);
+size_t mmq_filled_scratch_bytes(int type, int64_t M, int64_t N, int64_t K);
 // Y: the product (null for the block-dot export); dots: the export (null for the product);
 // scratch: at least mmq_scratch_bytes of device memory when the plan has splits > 1;
 // counters: the cut tiles' counters (zero between calls) with scratch holding only the
-// partial tiles, or null when scratch holds both (mmq_splitk.h's layout).
+// partial tiles, or null when scratch holds both (mmq_splitk.h's layout).  filled: mmq_filled_plan.
 hipError_t launch_mmq(int type, BlockLayout layout, const uint8_t* W, const int8_t* codes, const float* scales,
                       const int32_t* sums, float* Y, int32_t* dots, void* scratch, unsigned* counters, int64_t M,
-                      int64_t N, int64_t K, const Epilogue* ep, hipStream_t s, const char** kernel_name);
+                      int64_t N, int64_t K, const Epilogue* ep, bool filled, hipStream_t s, const char** kernel_name);
 // Q4_K (GGUF layout) with few output tiles: one 32 x 32 tile per workgroup, its K range
 // split over the workgroup's waves (mmq_kw.hip); taken by launch_mmq whenever
 // mmq_kw_applies.  It needs no scratch.

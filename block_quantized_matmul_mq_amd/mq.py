@@ -56,6 +56,7 @@ _SIGNATURES = {
     "mq_gemm_ep": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                   ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mq_gemm_ep_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
     "mq_moe_route_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64]),
     "mq_moe_route": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
@@ -371,16 +372,21 @@ def _call(fn, tensor, stream, *args):
         _check(code)
 
 
-def _new(stream, like, shape, dtype, zero=False):
-    """A tensor on `like`'s device, empty or zero, in order on the call's stream: memory that the allocator
-    takes back may otherwise be reused, or be cleared, while the call runs."""
+_GEMM_COUNTER_BYTES, _ROUTE_COUNTER_BYTES = 1024, 256 * 1024    # of the workspaces (include/mq.h)
+
+
+def _new(stream, like, shape, dtype, zero=0):
+    """A tensor on `like`'s device, its first `zero` elements zero, in order on the call's stream: memory that
+    the allocator takes back may otherwise be reused, or be cleared, while the call runs."""
     import torch
-    make = like.new_zeros if zero else like.new_empty
-    if stream is None or not like.is_cuda:
-        return make(shape, dtype=dtype)
-    handle = stream if isinstance(stream, int) else stream.value or 0
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=like.device)):
-        return make(shape, dtype=dtype)
+    if stream is not None and like.is_cuda:
+        handle = stream if isinstance(stream, int) else stream.value or 0
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=like.device)):
+            return _new(None, like, shape, dtype, zero)
+    t = like.new_empty(shape, dtype=dtype)
+    if zero:
+        t[:zero].zero_()
+    return t
 
 
 def _terms(fn, M, N, bias, mul, residual):
@@ -410,10 +416,16 @@ def gemv_ep(W, qtype, x, N, K, bias=None, act=ACT_NONE, mul=None, residual=None,
     return y
 
 
+@functools.lru_cache(maxsize=4096)
+def gemm_ep_scratch_bytes(qtype, M, N, K):
+    return load().mq_gemm_ep_scratch_bytes(qtype, M, N, K)
+
+
 def gemm_ep(W, qtype, Xq, M, N, K, bias=None, act=ACT_NONE, mul=None, residual=None, Y=None, scratch=None,
             stream=None):
     """Y[M, N] = act(product + bias) * mul + residual, the product of gemm (bias: f32 [N]; mul, residual:
-    f32 [M, N]; each may be None; Y may be mul or residual)."""
+    f32 [M, N]; each may be None; Y may be mul or residual).  scratch: gemm_scratch_bytes, or
+    gemm_ep_scratch_bytes for its own work split; its first KiB zero before its first use."""
     import torch
     _weights(W, qtype, N, K, "gemm_ep")
     _act_plane(Xq, M, K, "gemm_ep")
@@ -422,11 +434,13 @@ def gemm_ep(W, qtype, Xq, M, N, K, bias=None, act=ACT_NONE, mul=None, residual=N
         Y = _new(stream, Xq, (M, N), torch.float32)
     else:
         _f32(Y, M * N, "gemm_ep", "Y")
-    need = gemm_scratch_bytes(qtype, M, N, K)
-    if scratch is None and need:
-        scratch = _new(stream, Xq, need, torch.uint8, zero=True)
-    if scratch is not None:
-        _buffer(scratch, need, "gemm_ep", "scratch")
+    if scratch is None:
+        need = gemm_ep_scratch_bytes(qtype, M, N, K)
+        if need:
+            scratch = _new(stream, Xq, need, torch.uint8, zero=_GEMM_COUNTER_BYTES)
+            given.append(scratch)
+    else:
+        _buffer(scratch, gemm_scratch_bytes(qtype, M, N, K), "gemm_ep", "scratch")
         given.append(scratch)
     _same_device("gemm_ep", W, Xq, Y, *given)
     _call(load().mq_gemm_ep, Xq, stream, W.data_ptr(), qtype, Xq.data_ptr(), Y.data_ptr(), M, N, K, _ptr(bias), act,
@@ -466,7 +480,7 @@ def moe_route(X, Wr, topk, bias=None, score=SCORE_SOFTMAX, norm=True, scale=1.0,
     _f32(Wr, E * K, "moe_route", "Wr")
     need = moe_route_scratch_bytes(M, K, E)
     if scratch is None:
-        scratch = _new(stream, X, max(need, 16), torch.uint8, zero=True)
+        scratch = _new(stream, X, max(need, 16), torch.uint8, zero=_ROUTE_COUNTER_BYTES)
     else:
         _buffer(scratch, need, "moe_route", "scratch")
     tensors = [X, Wr, scratch]

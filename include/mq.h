@@ -271,18 +271,24 @@ int mq_gemm(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_
  * with acc the product of mq_gemv (M = 1) or mq_gemm and act an MQ_ACT_* id.  bias (N f32),
  * mul and residual (M x N f32, row-major, as Y) are device memory or NULL; a NULL term is left
  * out.  Everything else -- types and layouts, shapes, limits, the accuracy of acc, the
- * quantized plane Xq, scratch (mq_gemm_scratch_bytes), errors -- is as for mq_gemv and mq_gemm.
+ * quantized plane Xq, scratch, errors -- is as for mq_gemv and mq_gemm.
+ * mq_gemm_ep takes mq_gemm_scratch_bytes of scratch, as mq_gemm, and is faster with mq_gemm_ep_scratch_bytes
+ * (never less, at most 32 MiB and 1 KiB; the counters at the start as there): the int8 kernel then cuts a
+ * product of few tiles and a long K into ranges for both workgroups of every CU, whose sums
+ * are another order of the same terms.  The split depends on the shape and on which of the two the
+ * scratch holds.
  * mul and residual may be the output itself (the residual stream updated in place), or the
  * same buffer; no input may overlap the output otherwise.  MQ_ERR_ARG for an unknown act.
  * So a gated feed-forward layer takes three products and no other launch:
  *   u = mq_gemv(Wup), h = mq_gemv_ep(Wgate, act = MQ_ACT_SILU, mul = u),
  *   y = mq_gemv_ep(Wdown, h, residual = y).
  * Two sums are formed more precisely here, so that a call without terms agrees with mq_gemv or
- * mq_gemm to their accuracy and, for the types named, not bit for bit: mq_gemm_ep forms the min term
+ * mq_gemm to their accuracy and, for the types named (and for a split of its own), not bit for bit: mq_gemm_ep forms the min term
  * of Q4_K, Q5_K, Q4_1 and Q5_1 on the int8 kernels to f32 precision (mq_gemm: to 2^-16);
  * mq_gemv_ep forms the offset and min terms (every type but Q8_0) from the staged activations that
  * the codes meet (mq_gemv: from x).
  */
+size_t mq_gemm_ep_scratch_bytes(int type, int64_t M, int64_t N, int64_t K);
 int mq_gemv_ep(const void* W, int type, const float* x, float* y, int64_t N, int64_t K, const float* bias, int act,
                const float* mul, const float* residual, void* stream);
 int mq_gemm_ep(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N, int64_t K, const float* bias,

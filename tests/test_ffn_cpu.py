@@ -46,6 +46,29 @@ def test_epilogue_refusals():
     assert gemm_ep(s=FAKE + 4, sb=need, **big) == -5
 
 
+def test_epilogue_scratch():
+    """gemm_ep's own work split: 1 KiB of counters and a partial tile for each of at most 512 workgroups."""
+    def tiles(count, splits, rows):
+        return 1024 + count * splits * rows * 128 * 4
+
+    size = mq.gemm_ep_scratch_bytes
+    assert size(mq.Q6_K, 333, 5120, 13824) == tiles(120, 4, 128)
+    assert size(mq.Q8_0, 512, 8192, 8192) == tiles(256, 2, 128)
+    assert size(mq.Q5_1, 64, 8192, 8192) == tiles(128, 4, 32)
+    assert size(mq.Q8_0, 512, 3584, 3584) == 0 == mq.gemm_scratch_bytes(mq.Q8_0, 512, 3584, 3584)
+    for t in (mq.Q4_0, mq.Q4_1, mq.Q5_0, mq.Q5_1, mq.Q8_0, mq.Q4_K, mq.Q5_K, mq.Q6_K):
+        block = 256 if t in (mq.Q4_K, mq.Q5_K, mq.Q6_K) else 32
+        for M in (1, 8, 9, 31, 33, 100, 129, 333, 512, 1000, 4096):
+            for N in (1, 130, 1000, 4096, 8200, 18944):
+                for K in (block, 7 * 256, 3584, 8192, 32768):
+                    plain, own = mq.gemm_scratch_bytes(t, M, N, K), size(t, M, N, K)
+                    assert plain <= own <= 1024 + (32 << 20) or own == plain, (t, M, N, K)
+    plane = mq.Q4_K | mq.REPACKED
+    assert size(plane, 512, 18944, 3584) == mq.gemm_scratch_bytes(plane, 512, 18944, 3584)
+    assert size(mq.Q4_K, 0, 10, 256) == size(mq.Q4_K, 40, 10, 100) == size(99, 40, 10, 256) == 0
+    assert size(mq.Q4_K | mq.ROW_TILED, 40, 10, 256) == 0
+
+
 def test_route_sizes_and_refusals():
     size = mq.moe_route_scratch_bytes
     assert size(0, 64, 8) == size(4, 48, 8) == size(4, 64, 0) == size(4, 64, 513) == size(1, 1 << 16, 8) == 0

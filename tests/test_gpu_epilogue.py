@@ -169,6 +169,59 @@ def test_gemm(qtype, M, N, K, kernel):
     check_terms(lambda **t: mq.gemm_ep(W, qtype, Xq, M, N, K, scratch=scratch, **t), acc, M, N, kernel)
 
 
+FILLED = [  # (type, M, N, K, tile rows of the split)
+    (mq.Q6_K, 333, 5120, 4096, 128), (mq.Q8_0, 200, 4100, 8192, 128), (mq.Q4_0, 384, 2047, 8192, 128),
+    (mq.Q4_K, 333, 8190, 8192, 128), (mq.Q5_1, 64, 8192, 4096, 32), (mq.Q5_0, 128, 4096, 4096 + 32, 32),
+    (mq.Q4_1, 30, 16001, 4096, 32), (mq.Q5_K, 9, 8000, 8192, 32), (mq.Q8_0 | mq.REPACKED, 137, 3155, 8192, 32),
+]
+
+
+@pytest.mark.parametrize("qtype,M,N,K,rows", FILLED, ids=[f"{NAMES[f[0] & 0xFF]}-{f[1]}x{f[2]}x{f[3]}" for f in FILLED])
+def test_gemm_with_its_own_split(qtype, M, N, K, rows):
+    """With gemm_ep_scratch_bytes of scratch the tiles are cut into other K ranges: the f64 product within
+    the bound of f32 sums, the same bits from call to call (with other bytes in the partial tiles), and the
+    counters left at zero; with less, mq_gemm's split."""
+    import torch
+    dev = device()
+    base = qtype & 0xFF
+    say(f"gemm_ep own split {NAMES[base]} M={M} N={N} K={K}")
+    need, plain = mq.gemm_ep_scratch_bytes(qtype, M, N, K), mq.gemm_scratch_bytes(qtype, M, N, K)
+    tile_bytes = -(-M // rows) * -(-N // 128) * rows * 128 * 4
+    assert need > plain and (need - 1024) % tile_bytes == 0 and (need - 1024) // tile_bytes >= 2
+    raw = weights(base, N, K, "quantized", 720)
+    W = laid_out(raw, qtype, N, K, dev)
+    X = synth.activations(M, K, config_index=14, tensor_index=9)
+    Xq = mq.quantize_act(to_dev(X, dev))
+    own = torch.zeros(need, dtype=torch.uint8, device=dev)
+    Y = mq.gemm_ep(W, qtype, Xq, M, N, K, scratch=own)
+    assert mq.last_kernel().startswith("mmq<")
+    own[1024:] = 255     # (f32 NaN)
+    again = mq.gemm_ep(W, qtype, Xq, M, N, K, scratch=own)
+    alone = mq.gemm_ep(W, qtype, Xq, M, N, K)
+    less = mq.gemm_ep(W, qtype, Xq, M, N, K, scratch=torch.zeros(max(plain, 16), dtype=torch.uint8, device=dev))
+    torch.cuda.synchronize()
+    assert int(own[:1024].sum()) == 0
+    assert torch.equal(Y, again) and torch.equal(Y, alone)
+    # K / 32 block terms and their min terms, summed in f32 (any order), each product rounded; some columns
+    cols = np.unique(np.concatenate([np.arange(min(N, 40)), np.arange(max(0, N - 140), N), np.arange(0, N, 97)]))
+    q, d, _ = oracle.quantize_act(X)
+    part = np.ascontiguousarray(raw.reshape(N, -1)[cols])
+    ref = oracle.mmq(part, base, q, d, len(cols), K)
+    xh = np.abs(q.reshape(M, -1, 32) * d[..., None].astype(np.float64)).reshape(M, K)
+    bound = (K / 32 + 24) * HALF * (xh @ oracle.magnitude(part, base, len(cols), K).T)
+    for y in (Y, less):
+        acc = y.cpu().numpy()[:, cols]
+        err = np.abs(acc - ref)
+        say(f"  worst error / bound {float((err / bound).max()):.3f}, relative {np.linalg.norm(acc - ref) / np.linalg.norm(ref):.2e}")
+        assert np.all(err <= bound)
+    acc = Y.cpu().numpy()
+    rng = np.random.default_rng(M)
+    mul, res = rng.standard_normal((M, N)).astype(np.float32), rng.standard_normal((M, N)).astype(np.float32)
+    y = mq.gemm_ep(W, qtype, Xq, M, N, K, act=mq.ACT_SILU, mul=to_dev(mul, dev), residual=to_dev(res, dev), scratch=own)
+    err = np.abs(y.cpu().numpy() - oracle.epilogue(acc, None, mq.ACT_SILU, mul, res))
+    assert np.all(err <= terms_bound(acc, None, mq.ACT_SILU, mul, res))
+
+
 def test_the_output_may_be_a_term():
     import torch
     dev = device()
