@@ -13,8 +13,9 @@
 //   More tokens: a slot is up to `set` tokens of one chosen expert, whose weights are read once for all
 //   of them; `up` leaves the gate and the up sums, `down` the weighted rows of every pair, and a
 //   third launch adds a token's rows in choice order.  (Two tokens already gain from it: 64 experts of
-//   2048 x 1024, 8 choices, Q4_K: 35.2 us against 37.8 with the one-token kernels extended to few
-//   tokens, four tokens 44.3 against 65.5, eight 56.7 against 109.)
+//   2048 x 1024, 8 choices, Q4_K: 29.9 us, four tokens 39.1, eight 51.3, where the one-token kernels
+//   extended to few tokens took 37.8, 65.5 and 109.  The third launch's work in the down kernel's last
+//   workgroups instead was slower: eight tokens 62.2.)
 //
 // Arithmetic.  The exact-integer scheme of the GEMV kernels: per 32-value block of the
 // activations x = 2^-s v with v an integer of at most 22 bits (relative to the block's largest
@@ -56,9 +57,10 @@ typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
 constexpr int kFracBits = 22;
-constexpr int kPlane = 288;                  // bytes of a staged digit plane: 256 and 32 (bank spread)
+constexpr int kPlane = 272;                  // bytes of a staged digit plane: 256 and 16, so that the twelve planes of
+                                             // four tokens start in different quads of the 64 LDS banks
 constexpr int kPlanes = 3 * kPlane;
-constexpr int kDepth = 2;                    // weight groups in flight per wave
+constexpr int kDepth = 2;                    // weight groups in flight per wave (48 tokens: 421 us; with 4, 448)
 constexpr int kOneUpWaves = 4096;            // waves of the one-token up kernel
 constexpr int kManyFixed = 48 + 16 * kWaves;  // many tokens: LDS of the slot's lists
 
@@ -115,10 +117,12 @@ constexpr int row_chunks() {
 }
 
 // One group of a wave's 16 rows: chunk c (row c / row_chunks, 16 bytes c % row_chunks of the row's
-// group) in register c / 64 of lane c % 64, then at byte 16 c of the wave's LDS slot.
+// group) in register c / 64 of lane c % 64, then in its row of the wave's LDS slot.
 template <int QT>
 struct Tile {
-    static constexpr int kRow = row_chunks<QT>() * 16;      // LDS bytes of a row
+    static constexpr int kRow = (row_chunks<QT>() | 1) * 16;   // LDS bytes of a row: an odd number of bank quads, so
+                                                               // that the 16 rows' start in different ones
+    static constexpr bool kPadded = kRow != row_chunks<QT>() * 16;
     static constexpr int kSlot = 16 * kRow;
     static constexpr int kChunks = 16 * row_chunks<QT>();
     static constexpr int kLoads = (kChunks + 63) / 64;
@@ -126,13 +130,14 @@ struct Tile {
 
     // lane constants: byte offsets of its chunks' rows in the tile, and of the chunks in the row
     struct Lane {
-        uint32_t row[kLoads], col[kLoads];
+        uint32_t row[kLoads], col[kLoads], at[kLoads];   // (at: its byte in the slot)
         __device__ Lane(int lane, uint32_t row_bytes) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
                 const int c = min(lane + 64 * i, kChunks - 1);
                 row[i] = uint32_t(c / row_chunks<QT>()) * row_bytes;
                 col[i] = uint32_t(c % row_chunks<QT>()) * 16;
+                at[i] = kPadded ? uint32_t(c / row_chunks<QT>()) * kRow + col[i] : uint32_t(lane + 64 * i) * 16;
             }
         }
     };
@@ -147,11 +152,11 @@ struct Tile {
             r[i] = *(const __attribute__((address_space(1))) v4u*)(b + (o + l.col[i]));
         }
     }
-    __device__ void store(uint8_t* slot, int lane) const {
+    __device__ void store(uint8_t* slot, int lane, const Lane& l) const {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             if (64 * (i + 1) <= kChunks || lane + 64 * i < kChunks)
-                *reinterpret_cast<v4u*>(slot + 16 * (lane + 64 * i)) = r[i];
+                *reinterpret_cast<v4u*>(slot + l.at[i]) = r[i];
     }
 };
 
@@ -424,12 +429,16 @@ constexpr int row_blocks_per_group() {
 // slot's tokens, then every wave walks its units by itself: nothing but the staging needs a barrier,
 // and the stream of weights does not stop between units.  The slots of an expert of more
 // tokens read the same weights at about the same time (from HBM once).
+// (48 tokens, 8 of 128 experts each, 4096 x 1536, graph replay: up Q4_K 212 us, 4.1 TB/s of chosen
+// weights; down Q6_K 186 us, 3.4 TB/s.  By the counters the vector ALU issues 60% (Q6_K 75%) of the time:
+// decoding a group and joining its plane sums.  LDS bank conflicts are 11% and 15%, 20% and 35% before
+// planes and rows were padded to odd bank quads, 429 -> 414 us for the layer.)
 //   up    leaves the gate and the up sums, f32 [pair][F] each: act(g) * u is formed where the down
 //         kernel stages h, so that a wave's unit is one matrix's 16 rows (at 48 tokens, 4096 x 1536,
 //         the last round of waves is then 1 of 7 and not 1 of 4)
 //   down  leaves the weighted rows, f32 [pair][K].
 
-// The same for at most 64 pairs, a lane each, in every wave by itself (no trip through LDS, no barrier):
+// A slot's pairs (as slot_pairs_of below) for at most 64 pairs, a lane each, in every wave by itself (no trip through LDS, no barrier):
 // slots in the order of their first pairs; `list` is the wave's own.
 __device__ __forceinline__ int slot_pairs_of_64(const MoeArgs& a, int lane, int* count, int* list) {
     const int e = lane < a.pairs ? a.ids[lane] : -1;
@@ -618,7 +627,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
     auto compute = [&](auto slot_c) __attribute__((always_inline)) {
         // (one wave's LDS operations complete in order: the reads see these writes, and the next
         // writes come after the reads)
-        buf[decltype(slot_c)::value].store(slot, lane);
+        buf[decltype(slot_c)::value].store(slot, lane, lanes);
         __builtin_amdgcn_wave_barrier();
         const uint32_t start =
             whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(cp.g) * group_step) & 15u);
@@ -649,6 +658,8 @@ __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
 }
 
 // ------------------------------------------------------------------ one token
+// (8 of 64 experts of 2048 x 1024, Q4_K: up 7.4 us, down 6.7, 2.5 and 1.4 TB/s: two launches' ramps and
+// round trips, not bytes.  4 of 32 of 4096 x 2048: up Q4_K 10.4 us, down Q6_K 9.8, 3.6 and 2.8 TB/s.)
 // blockIdx.y: choice; blockIdx.x: kWaves / (2 splits) 16-row tiles of its expert.  Wave w: part w % splits of
 // the groups (part ks: ks, ks + splits, ...) of matrix w / splits % 2 (gate, up), tile w / (2 splits) of
 // the workgroup; the sums meet in LDS, parts in order.
@@ -706,7 +717,7 @@ __global__ __launch_bounds__(kThreads, 4) void moe_one_up_kernel(MoeArgs a) {
             whole_chunks<QT>() ? 0u : a.off + ((uint32_t(n) * row_bytes + uint32_t(g) * group_step) & 15u);
         // (one wave's LDS operations complete in order: the reads see these writes, and the next
         // writes come after the reads)
-        buf[decltype(slot_c)::value].store(slot, lane);
+        buf[decltype(slot_c)::value].store(slot, lane, lanes);
         __builtin_amdgcn_wave_barrier();
         Group<QT> d;
         decode(d, slot + n * Tile<QT>::kRow, start, q, g, blocks, a.stride);
@@ -814,7 +825,7 @@ __global__ __launch_bounds__(kOneThreads) void moe_one_down_kernel(MoeArgs a) {
         // (one wave's LDS operations complete in order: the reads below see these writes, and the
         // next group's writes come after them)
         stage_token<QT>(staged, 0, 1, xs[S], lane);
-        buf[S].store(slot, lane);
+        buf[S].store(slot, lane, lanes);
         __builtin_amdgcn_wave_barrier();
         const int g = ks + a.splits * cp.i;
         const uint32_t start =

@@ -16,6 +16,9 @@
 // itself in on its token tile's counter (mmq_splitk.h's exchange); the last one adds the
 // ranges in order and selects: a wave per token, E / 64 logits per lane, k rounds of a
 // maximum over the wave on 64-bit keys that order like the f64 values (ties: lowest index).
+//
+// One token, K = 2048, E = 64: 7.9 us, all of it latency (0.5 MB); 512 tokens, K = 4096, E = 128: 22 us, of which
+// the f64 matrix products are about 7.
 #include <algorithm>
 #include <type_traits>
 
