@@ -261,8 +261,7 @@ def quantize_act(X, Xq=None, stream=None):
     else:
         _buffer(Xq, need, "quantize_act", "Xq")
     _same_device("quantize_act", X, Xq)
-    _check(load().mq_quantize_act(ctypes.c_void_p(X.data_ptr()), ctypes.c_void_p(Xq.data_ptr()), M, K,
-                                  _stream(stream)))
+    _call(load().mq_quantize_act, X, stream, X.data_ptr(), Xq.data_ptr(), M, K)
     return Xq
 
 
