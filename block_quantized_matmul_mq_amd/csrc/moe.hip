@@ -13,9 +13,9 @@
 //   More tokens: a slot is up to `set` tokens of one chosen expert, whose weights are read once for all
 //   of them; `up` leaves the gate and the up sums, `down` the weighted rows of every pair, and a
 //   third launch adds a token's rows in choice order.  (Two tokens already gain from it: 64 experts of
-//   2048 x 1024, 8 choices, Q4_K: 29.9 us, four tokens 39.1, eight 51.3, where the one-token kernels
+//   2048 x 1024, 8 choices, Q4_K: 21.9 us, four tokens 32.3, eight 48.8, where the one-token kernels
 //   extended to few tokens took 37.8, 65.5 and 109.  The third launch's work in the down kernel's last
-//   workgroups instead was slower: eight tokens 62.2.)
+//   workgroups instead was slower: eight tokens 51.3 -> 62.2.)
 //
 // Arithmetic.  The exact-integer scheme of the GEMV kernels: per 32-value block of the
 // activations x = 2^-s v with v an integer of at most 22 bits (relative to the block's largest
@@ -946,9 +946,12 @@ hipError_t launch_many(MoeArgs a, hipStream_t s) {
     a.set = int(std::min<size_t>({4, (kGfx950LdsBytes - kFixed) / per_token, size_t(a.pairs)}));
     const int slots = std::min(a.pairs, a.experts + a.pairs / a.set);
     // units of 32 KiB of weights or more per wave: enough to outlast the staging, and short enough
-    // that the last round of workgroups costs little
+    // that the last round of workgroups costs little; fewer while there are not two workgroups per CU
+    // (64 experts of 2048 x 1024, k = 8, Q4_K: two tokens 30.0 -> 21.9 us, four 38.9 -> 32.3, eight 51.4 -> 48.8; one or
+    // four per CU instead: eight 51.3 and 48.3, twelve 63.7 and 63.1 against 59.5)
     const int units = a.rows / 16 * (UP ? 2 : 1);
-    const int per_wave = int(std::max<int64_t>(1, 32768 / (16 * a.row_bytes)));
+    const int64_t filled = int64_t(units) * slots / (kWaves * 512);
+    const int per_wave = int(std::max<int64_t>(1, std::min<int64_t>(filled, 32768 / (16 * a.row_bytes))));
     const int grid = std::max(1, units / (kWaves * per_wave));
     hipLaunchKernelGGL((moe_many_kernel<QT, UP>), dim3(grid, slots), dim3(kThreads), kFixed + size_t(a.set) * per_token,
                        s, a);
