@@ -38,7 +38,7 @@ __device__ __forceinline__ float activate(float v, int act) {
         case kActSilu: return v * logistic(v);
         case kActGeluTanh: return v * logistic(1.5957691216057308f * fmaf(0.044715f * v, v * v, v));
         case kActGeluErf: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-        case kActRelu: return fmaxf(v, 0.0f);
+        case kActRelu: return v <= 0.0f ? 0.0f : v;   // (the maximum instruction would turn a NaN into 0)
         default: return v;
     }
 }

@@ -119,7 +119,7 @@ extern "C" {
 #define MQ_ACT_SILU 1      /* v / (1 + e^-v)                                             */
 #define MQ_ACT_GELU_TANH 2 /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2          */
 #define MQ_ACT_GELU_ERF 3  /* v (1 + erf(v / sqrt 2)) / 2                                */
-#define MQ_ACT_RELU 4      /* max(v, 0)                                                  */
+#define MQ_ACT_RELU 4      /* max(v, 0), a NaN for a NaN                                 */
 
 /* Router scores of mq_moe_route. */
 #define MQ_SCORE_SOFTMAX 0
