@@ -115,10 +115,17 @@ __device__ __forceinline__ void select(const RouteArgs& a, int m, const double (
     uint64_t key[PER];
     const bool softmax = a.score == 0;
     double top = -__builtin_inf();
+    bool nan = false;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-        if (64 * i + lane < a.E) top = fmax(top, z[i]);
+        if (64 * i + lane < a.E) {
+            top = fmax(top, z[i]);
+            nan |= !(z[i] == z[i]);
+        }
     top = wave_all(top, [](double x, double y) { return fmax(x, y); });
+    // The softmax's sum holds every expert's exp: a NaN logit makes all of them NaN, also where only the chosen
+    // ones' are summed below.
+    if (__ballot(nan) != 0) top = __builtin_nan("");
     double sum = 0.0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {

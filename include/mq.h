@@ -301,7 +301,8 @@ int mq_gemm_ep(const void* W, int type, const void* Xq, float* Y, int64_t M, int
  *   p = softmax of z[m] over the E experts (MQ_SCORE_SOFTMAX), or 1 / (1 + e^-z) (MQ_SCORE_SIGMOID)
  *   ids[m][0..topk-1] = the topk experts of largest z, or of largest p + bias when bias (f32 [E],
  *     a selection bias that does not enter the weights) is not NULL, in falling order; of equal
- *     ones the lower index first, a NaN after every number
+ *     ones the lower index first, a NaN after every number (under softmax a NaN z makes every p of its
+ *     token NaN)
  *   wts[m][j] = scale * p[ids[m][j]], divided by the sum of the topk chosen p when norm != 0.
  * ids int32 and wts f32, [M][topk], as mq_moe_ffn reads them.  K % 32 == 0; 1 <= topk <= E and
  * <= MQ_MOE_MAX_TOPK.  Every id is in [0, E) and a token's ids differ, whatever X holds.

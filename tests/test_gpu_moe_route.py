@@ -125,3 +125,36 @@ def test_deterministic():
     for _ in range(3):
         b = run(X, Wr, 8)
         assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("E", [40, 130, 512])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("score", [mq.SCORE_SOFTMAX, mq.SCORE_SIGMOID], ids=["softmax", "sigmoid"])
+def test_weights_of_non_finite_logits(E, norm, score):
+    """An expert whose logit is NaN is in the softmax of every expert: its token's weights are NaN, chosen or not,
+    normalized or not; a sigmoid is NaN for that expert alone.  Infinite logits as the formula has them."""
+    rng = np.random.default_rng(11)
+    M, K = 5, 64
+    X = np.abs(rng.standard_normal((M, K))).astype(np.float32)
+    Wr = (rng.standard_normal((E, K)) * 0.2).astype(np.float32)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+
+    def same(Wr, bias, k):
+        ids, wts = run(X, Wr, k, bias, score=score, norm=norm)
+        with np.errstate(all="ignore"):
+            ref_ids, ref = oracle.moe_route(X, Wr, k, bias, score=score, norm=norm)
+        assert np.array_equal(ids, ref_ids)
+        assert np.array_equal(np.isnan(wts), np.isnan(ref)), (wts, ref)
+        ok = ~np.isnan(ref)
+        assert np.all(np.abs(wts[ok] - ref[ok]) <= 2.0 ** -23 * np.abs(ref[ok]) + 1e-45)
+        return wts
+
+    for value in (np.nan, np.inf, -np.inf):
+        bad = Wr.copy()
+        bad[6] = value
+        for k in (1, 5, min(E, 64)):
+            w = same(bad, None, k)
+            if np.isnan(value) and score == mq.SCORE_SOFTMAX:
+                assert np.all(np.isnan(w))
+        same(bad, bias, 5)
+    same(np.full_like(Wr, -np.inf), None, 3)
