@@ -18,9 +18,10 @@ constexpr int kActs = 5;
 
 // 1 / (1 + e^-u).  e^-u as 2^t by the exp2 instruction, t = -u log2(e) rounded to f32, times 1 + r ln 2
 // for what the rounding of t left out (r: an fma's exact remainder and log2(e)'s own low part), so
-// the relative error stays at about two roundings for large |u| too; then one reciprocal
-// instruction.  (512 x 18944 x 3584 Q4_K with silu and mul: 164 us with expf and an IEEE
-// division, 146 with this.)  e^-u overflows to infinity (1 / inf = 0) and keeps a NaN.
+// the relative error stays at a few roundings for large |u| too; then one reciprocal
+// instruction, which gives 0 for a quotient below 2^-126 (u < -87.3).  (512 x 18944 x 3584 Q4_K with silu and mul:
+// 164 us with expf and an IEEE division, 146 with this.)  e^-u overflows to infinity (1 / inf = 0; its r
+// may be NaN, as that of e^-u = 0) and keeps a NaN.
 __device__ __forceinline__ float logistic(float u) {
     constexpr float kLog2e = 1.44269502162933349609375f;        // f32(log2 e)
     constexpr float kLog2eLow = 1.92596299112661746887e-8f;     // log2 e - f32(log2 e)
@@ -28,7 +29,7 @@ __device__ __forceinline__ float logistic(float u) {
     const float t = -u * kLog2e;
     const float r = fmaf(-u, kLog2eLow, fmaf(-u, kLog2e, -t));
     const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_amdgcn_rcpf(1.0f + (e > 0.0f && e < 1e30f ? fmaf(e, r * kLn2, e) : e));
+    return __builtin_amdgcn_rcpf(1.0f + (e > 0.0f && e < __builtin_inff() ? fmaf(e, r * kLn2, e) : e));
 }
 
 // (act is uniform: one branch.  Both gelus in the forms that lose nothing to cancellation for
