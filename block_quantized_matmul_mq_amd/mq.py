@@ -380,7 +380,9 @@ def _new(stream, like, shape, dtype, zero=0):
     import torch
     if stream is not None and like.is_cuda:
         handle = stream if isinstance(stream, int) else stream.value or 0
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=like.device)):
+        # (0 is the default stream's handle; an ExternalStream of 0 would be a new stream, ordered with nothing)
+        on = torch.cuda.ExternalStream(handle, device=like.device) if handle else torch.cuda.default_stream(like.device)
+        with torch.cuda.stream(on):
             return _new(None, like, shape, dtype, zero)
     t = like.new_empty(shape, dtype=dtype)
     if zero:
