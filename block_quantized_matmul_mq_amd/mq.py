@@ -247,7 +247,7 @@ def gemm_scratch_bytes(qtype, M, N, K):
 
 
 def quantize_act(X, Xq=None, stream=None):
-    """X: f32 [M, K] CUDA tensor -> Xq: uint8 plane of act_bytes(M, K) bytes."""
+    """X: f32 [M, K] CUDA tensor -> Xq: uint8 plane of act_bytes(M, K) bytes (made on the call's stream)."""
     import torch
     if X.dim() != 2:
         _refuse(-1, "quantize_act", f"X must be 2-D [M, K], not {tuple(X.shape)}")
@@ -257,7 +257,7 @@ def quantize_act(X, Xq=None, stream=None):
     if need == 0:
         _refuse(-2, "quantize_act", f"K={K} is not a positive multiple of 32")
     if Xq is None:
-        Xq = torch.empty(need, dtype=torch.uint8, device=X.device)
+        Xq = _new(stream, X, need, torch.uint8)
     else:
         _buffer(Xq, need, "quantize_act", "Xq")
     _same_device("quantize_act", X, Xq)

@@ -116,3 +116,10 @@ def test_without_a_stream_the_devices_current_one(journal, name):
     FEED_FORWARD[name]()
     assert journal.made and all(where == "current" for where in journal.made)
     assert journal.launches == [("mq_" + name, 1, RAW[1])]
+
+
+@pytest.mark.parametrize("handle", [0, 77])
+def test_quantize_act_makes_its_plane_on_the_given_stream(journal, handle):
+    mq.quantize_act(tensor(M, K), stream=handle)
+    assert journal.made == [("stream", handle)]
+    assert journal.launches == [("mq_quantize_act", 1, handle)]

@@ -36,3 +36,29 @@ def test_the_default_streams_handle(name, M):
         for a, b in zip(ref, out):
             assert torch.equal(a.cpu(), b.cpu()), turn
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("default", [False, True], ids=["side", "default"])
+def test_a_dropped_plane_of_quantize_act(default):
+    """quantize_act and the product on one handle, the plane dropped once both are enqueued: the current stream
+    must not be handed its memory while they run."""
+    import torch
+    from block_quantized_matmul_mq_amd import mq
+    c = Calls(seed=6)
+    ref = c.gemm_ep()[0]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    on, current = (torch.cuda.default_stream(), side) if default else (side, torch.cuda.default_stream())
+    size = c.Xq.numel()
+    for turn in range(10):
+        say(f"quantize_act and gemm_ep on handle {on.cuda_stream}, turn {turn}")
+        with torch.cuda.stream(on):
+            keep_busy(c.X.device)
+        with torch.cuda.stream(current):
+            Xq = mq.quantize_act(c.Xg, stream=on.cuda_stream)
+            out = mq.gemm_ep(c.W, mq.Q4_K, Xq, 40, c.N, c.X.shape[1], act=mq.ACT_SILU, mul=c.mulg, stream=on.cuda_stream)
+            del Xq
+            for _ in range(4):
+                torch.full((size,), 255, dtype=torch.uint8, device=c.X.device)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref), turn
