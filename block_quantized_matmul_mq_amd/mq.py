@@ -191,6 +191,42 @@ def _same_device(fn, *tensors):
         _refuse(-6, fn, f"every tensor must be on one GPU device, got {sorted(map(str, devs))}")
 
 
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn, tensor, stream, *args):
+    """fn(*args, stream) on the device of the (checked) tensors, on `stream` or that device's current one."""
+    import torch
+    device = tensor.get_device()
+    if device == torch._C._cuda_getDevice():
+        code = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream)
+    if code != MQ_OK:
+        _check(code)
+
+
+_GEMM_COUNTER_BYTES, _ROUTE_COUNTER_BYTES = 1024, 256 * 1024    # of the workspaces (include/mq.h)
+
+
+def _new(stream, like, shape, dtype, zero=0):
+    """A tensor on `like`'s device, its first `zero` elements zero, in order on the call's stream: memory that
+    the allocator takes back may otherwise be reused, or be cleared, while the call runs."""
+    if stream is not None and like.is_cuda:
+        import torch
+        handle = stream if isinstance(stream, int) else stream.value or 0
+        # (0 is the default stream's handle; an ExternalStream of 0 would be a new stream, ordered with nothing)
+        on = torch.cuda.ExternalStream(handle, device=like.device) if handle else torch.cuda.default_stream(like.device)
+        with torch.cuda.stream(on):
+            return _new(None, like, shape, dtype, zero)
+    t = like.new_empty(shape, dtype=dtype)
+    if zero:
+        t[:zero].zero_()
+    return t
+
+
 def init(device=0):
     _check(load().mq_init(device))
 
@@ -212,7 +248,7 @@ def repack(W, qtype, N, K, Wr=None, stream=None):
     _weights(W, qtype & ~ROW_TILED, N, K, "repack")
     need = repack_bytes(qtype, N, K)
     if Wr is None:
-        Wr = torch.empty(need, dtype=torch.uint8, device=W.device)
+        Wr = _new(stream, W, need, torch.uint8)
     else:
         _buffer(Wr, need, "repack", "Wr")
     _same_device("repack", W, Wr)
@@ -282,7 +318,7 @@ def gemv(W, qtype, x, N, K, y=None, stream=None):
     _weights(W, qtype, N, K, "gemv")
     _f32(x, K, "gemv", "x")
     if y is None:
-        y = torch.empty(N, dtype=torch.float32, device=x.device)
+        y = _new(stream, x, N, torch.float32)
     else:
         _f32(y, N, "gemv", "y")
     _same_device("gemv", W, x, y)
@@ -304,12 +340,12 @@ def gemm(W, qtype, Xq, M, N, K, Y=None, scratch=None, stream=None):
     _weights(W, qtype, N, K, "gemm")
     _act_plane(Xq, M, K, "gemm")
     if Y is None:
-        Y = torch.empty((M, N), dtype=torch.float32, device=Xq.device)
+        Y = _new(stream, Xq, (M, N), torch.float32)
     else:
         _f32(Y, M * N, "gemm", "Y")
     need = gemm_scratch_bytes(qtype, M, N, K)
     if scratch is None and need:
-        scratch = torch.zeros(need, dtype=torch.uint8, device=Xq.device)
+        scratch = _new(stream, Xq, need, torch.uint8, zero=_GEMM_COUNTER_BYTES)
     tensors = [W, Xq, Y]
     if scratch is not None:
         _buffer(scratch, need, "gemm", "scratch")
@@ -341,7 +377,7 @@ def gemm_blockdots(W, qtype, Xq, M, N, K, D=None, stream=None):
     _act_plane(Xq, M, K, "gemm_blockdots")
     G = K // 16 if (qtype & ~REPACKED) == Q6_K else K // 32
     if D is None:
-        D = torch.empty((M, N, G), dtype=torch.int32, device=Xq.device)
+        D = _new(stream, Xq, (M, N, G), torch.int32)
     else:
         if D.dtype != torch.int32:
             _refuse(-1, "gemm_blockdots", f"D must be int32, not {D.dtype}")
@@ -352,42 +388,6 @@ def gemm_blockdots(W, qtype, Xq, M, N, K, D=None, stream=None):
     _check(load().mq_debug_gemm_blockdots(ctypes.c_void_p(W.data_ptr()), qtype, ctypes.c_void_p(Xq.data_ptr()),
                                           ctypes.c_void_p(D.data_ptr()), M, N, K, _stream(stream)))
     return D
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _call(fn, tensor, stream, *args):
-    """fn(*args, stream) on the device of the (checked) tensors, on `stream` or that device's current one."""
-    import torch
-    device = tensor.get_device()
-    if device == torch._C._cuda_getDevice():
-        code = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream)
-    else:
-        with torch.cuda.device(device):
-            code = fn(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream)
-    if code != MQ_OK:
-        _check(code)
-
-
-_GEMM_COUNTER_BYTES, _ROUTE_COUNTER_BYTES = 1024, 256 * 1024    # of the workspaces (include/mq.h)
-
-
-def _new(stream, like, shape, dtype, zero=0):
-    """A tensor on `like`'s device, its first `zero` elements zero, in order on the call's stream: memory that
-    the allocator takes back may otherwise be reused, or be cleared, while the call runs."""
-    import torch
-    if stream is not None and like.is_cuda:
-        handle = stream if isinstance(stream, int) else stream.value or 0
-        # (0 is the default stream's handle; an ExternalStream of 0 would be a new stream, ordered with nothing)
-        on = torch.cuda.ExternalStream(handle, device=like.device) if handle else torch.cuda.default_stream(like.device)
-        with torch.cuda.stream(on):
-            return _new(None, like, shape, dtype, zero)
-    t = like.new_empty(shape, dtype=dtype)
-    if zero:
-        t[:zero].zero_()
-    return t
 
 
 def _terms(fn, M, N, bias, mul, residual):

@@ -48,7 +48,7 @@ def journal(monkeypatch):
             def launch(*args):
                 stream = args[-1]
                 device = next((c[1] for c in reversed(j.contexts) if c[0] == "device"), 0)
-                j.launches.append((name, device, stream.value if isinstance(stream, mq.ctypes.c_void_p) else stream))
+                j.launches.append((name, device, (stream.value or 0) if isinstance(stream, mq.ctypes.c_void_p) else stream))
                 return 0
             return launch
 
@@ -123,3 +123,21 @@ def test_quantize_act_makes_its_plane_on_the_given_stream(journal, handle):
     mq.quantize_act(tensor(M, K), stream=handle)
     assert journal.made == [("stream", handle)]
     assert journal.launches == [("mq_quantize_act", 1, handle)]
+
+
+PRODUCTS = {
+    "gemv": lambda **k: mq.gemv(payload(mq.Q4_K, N, K), mq.Q4_K, tensor(K), N, K, **k),
+    "gemm": lambda **k: mq.gemm(payload(mq.Q4_K, N, K), mq.Q4_K, plane(), M, N, K, **k),      # (K cut: with a workspace)
+    "repack": lambda **k: mq.repack(payload(mq.Q4_K, N, K), mq.Q4_K, N, K, **k),
+    "gemm_blockdots": lambda **k: mq.gemm_blockdots(payload(mq.Q4_K, N, K), mq.Q4_K, plane(), M, N, K, **k),
+}
+
+
+@pytest.mark.parametrize("handle", [0, 77])
+@pytest.mark.parametrize("name", PRODUCTS)
+def test_buffers_of_the_products_are_made_on_the_given_stream(journal, name, handle):
+    """A workspace cleared on another stream than the product's may be cleared after the product starts."""
+    PRODUCTS[name](stream=handle)
+    assert journal.made and all(where == ("stream", handle) for where in journal.made), journal.made
+    assert len(journal.made) == (2 if name == "gemm" else 1)
+    assert journal.launches[0][2] == handle

@@ -62,3 +62,33 @@ def test_a_dropped_plane_of_quantize_act(default):
                 torch.full((size,), 255, dtype=torch.uint8, device=c.X.device)
         torch.cuda.synchronize()
         assert torch.equal(out, ref), turn
+
+
+@pytest.mark.parametrize("default", [False, True], ids=["side", "default"])
+@pytest.mark.parametrize("name", ["gemv", "gemm", "repack", "gemm_blockdots"])
+def test_products_without_buffers(name, default):
+    """The products' own outputs and workspaces (a K that is cut) on a handle while another stream is busy."""
+    import torch
+    from block_quantized_matmul_mq_amd import mq
+    from gpu_cases import device, to_dev, weights
+    dev = device()
+    M, N, K = 40, 100, 8192
+    W = to_dev(weights(mq.Q4_K, N, K, "random", 41).reshape(-1), dev)
+    X = torch.randn(M, K, device=dev)
+    Xq, x = mq.quantize_act(X), X[0].contiguous()
+    assert mq.gemm_scratch_bytes(mq.Q4_K, M, N, K) > 0
+    call = {"gemv": lambda **k: mq.gemv(W, mq.Q4_K, x, N, K, **k), "gemm": lambda **k: mq.gemm(W, mq.Q4_K, Xq, M, N, K, **k),
+            "repack": lambda **k: mq.repack(W, mq.Q4_K, N, K, **k),
+            "gemm_blockdots": lambda **k: mq.gemm_blockdots(W, mq.Q4_K, Xq, M, N, K, **k)}[name]
+    ref = call()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    on, current = (torch.cuda.default_stream(), side) if default else (side, torch.cuda.default_stream())
+    for turn in range(5):
+        say(f"{name} on handle {on.cuda_stream}, turn {turn}")
+        with torch.cuda.stream(current):
+            keep_busy(dev)
+            out = call(stream=on.cuda_stream)
+        on.synchronize()
+        assert torch.equal(out.cpu(), ref.cpu()), turn
+        torch.cuda.synchronize()
