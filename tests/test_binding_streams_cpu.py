@@ -141,3 +141,14 @@ def test_buffers_of_the_products_are_made_on_the_given_stream(journal, name, han
     assert journal.made and all(where == ("stream", handle) for where in journal.made), journal.made
     assert len(journal.made) == (2 if name == "gemm" else 1)
     assert journal.launches[0][2] == handle
+
+
+@pytest.mark.parametrize("stream", [None, 0, 77])
+@pytest.mark.parametrize("name", [*PRODUCTS, "gemm_noalloc", "quantize_act"])
+def test_products_launch_on_the_tensors_device(journal, name, stream):
+    """With another device current: on the tensors' device, on its current stream where none is given."""
+    call = {**PRODUCTS, "quantize_act": lambda **k: mq.quantize_act(tensor(M, K), **k),
+            "gemm_noalloc": lambda **k: mq.gemm_noalloc(payload(mq.Q4_K, N, K), mq.Q4_K, plane(), M, N, K, tensor(M, N), **k)}[name]
+    call(stream=stream)
+    entry = "mq_debug_gemm_blockdots" if name == "gemm_blockdots" else "mq_" + name
+    assert journal.launches == [(entry, 1, RAW[1] if stream is None else stream)]
