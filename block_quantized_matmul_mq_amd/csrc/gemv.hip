@@ -232,7 +232,7 @@ __device__ __forceinline__ uint32_t digits(float x, int k) {
 template <int QT, int kThreads, int kSlots, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restrict__ W,
                                                         const float* __restrict__ x,
-                                                        float* __restrict__ y, int N, int K,
+                                                        typename Output<EP>::T y, int N, int K,
                                                         int64_t row_bytes, int tile_units, int blk_stride,
                                                         int blk_off, EP ep) {
     using Unit = typename UnitOf<QT>::T;

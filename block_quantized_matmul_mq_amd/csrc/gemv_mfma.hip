@@ -124,7 +124,7 @@ __device__ __forceinline__ float sum_lane_groups(float v) {
 template <int NB, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_mfma_q4k_kernel(const uint8_t* __restrict__ W,
                                                                  const float* __restrict__ x,
-                                                                 float* __restrict__ y, int N, int K,
+                                                                 typename Output<EP>::T y, int N, int K,
                                                                  int row_bytes, EP ep) {
     // One static array per ring slot: with compile-time slot numbers the compiler knows
     // which slot a read touches and waits for that slot's loads only.
@@ -325,7 +325,7 @@ constexpr uint32_t kPastEnd = 0x7FFF0000u;   // a buffer offset past the end of 
 template <int NB, bool TILED, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_mfma_q4k_long_kernel(const uint8_t* __restrict__ W,
                                                                        const float* __restrict__ x,
-                                                                       float* __restrict__ y, int N, int K,
+                                                                       typename Output<EP>::T y, int N, int K,
                                                                        int row_bytes, int TR, int nbytes, EP ep) {
     __shared__ __attribute__((aligned(16))) uint8_t ring0[kWaves * kItemBytes];
     __shared__ __attribute__((aligned(16))) uint8_t ring1[kWaves * kItemBytes];
@@ -645,7 +645,7 @@ constexpr int tiled_slot_bytes() { return kTileRows * kMaxSB * TiledItem<QT>::kS
 template <int QT, int D, int CPL, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_tiled_kernel(const uint8_t* __restrict__ W,
                                                               const float* __restrict__ x,
-                                                              float* __restrict__ y, int N, int K,
+                                                              typename Output<EP>::T y, int N, int K,
                                                               int row_bytes, EP ep) {
     using Item = TiledItem<QT>;
     constexpr int kSlot = tiled_slot_bytes<QT>();
@@ -804,7 +804,7 @@ template <int MR, bool DUMP, int CPL, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_q8_q6k_kernel(const uint8_t* __restrict__ W,
                                                                const int8_t* __restrict__ codes,
                                                                const float* __restrict__ xscale,
-                                                               float* __restrict__ Y, int32_t* __restrict__ dots,
+                                                               typename Output<EP>::T Y, int32_t* __restrict__ dots,
                                                                int M, int N, int K, int row_bytes, EP ep) {
     constexpr int kSlot = tiled_slot_bytes<kQ6_K>();
     constexpr int H = MR / 4;   // MFMAs per quarter
@@ -1035,7 +1035,7 @@ struct WideItem {
 template <int QT, int NB, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_wide_kernel(const uint8_t* __restrict__ W,
                                                              const float* __restrict__ x,
-                                                             float* __restrict__ y, int N, int K,
+                                                             typename Output<EP>::T y, int N, int K,
                                                              int row_bytes, EP ep) {
     using WI = WideItem<QT>;
     constexpr int kIB = WI::kBytes;

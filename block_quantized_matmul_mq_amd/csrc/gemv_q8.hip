@@ -104,7 +104,7 @@ template <int QT, int MR, bool DUMP, class EP>
 __global__ __launch_bounds__(kThreads) void gemv_q8_kernel(const uint8_t* __restrict__ W,
                                                            const int8_t* __restrict__ codes,
                                                            const float* __restrict__ xscale,
-                                                           const int32_t* __restrict__ xsum, float* __restrict__ Y,
+                                                           const int32_t* __restrict__ xsum, typename Output<EP>::T Y,
                                                            int32_t* __restrict__ dots, int M, int N, int K,
                                                            int64_t row_bytes, int tile_units, int blk_stride,
                                                            int blk_off, EP ep) {

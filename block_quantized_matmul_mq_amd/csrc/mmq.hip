@@ -462,7 +462,7 @@ __global__ __launch_bounds__(256, 2) void mmq_kernel(const uint8_t* __restrict__
                                                      const int8_t* __restrict__ codes,
                                                      const float* __restrict__ xscale,
                                                      const int32_t* __restrict__ xsum,
-                                                     float* __restrict__ Y, int32_t* __restrict__ dots,
+                                                     typename Output<EP>::T Y, int32_t* __restrict__ dots,
                                                      float* __restrict__ partial, unsigned* __restrict__ counters,
                                                      int M, int N, int K, int64_t row_bytes, int blk_stride,
                                                      int blk_off, int tiles_m, int full, int split_tiles, int splits,

@@ -124,7 +124,7 @@ __device__ __forceinline__ uint32_t weight_piece(int j, int R, int n0) {
 template <bool DUMP, class EP>
 __global__ __launch_bounds__(kThreads, 2) void mmq_f6_q4k_kernel(const uint8_t* __restrict__ Wp,
                                                                  const uint8_t* __restrict__ Ap,
-                                                                 float* __restrict__ Y, int32_t* __restrict__ dots,
+                                                                 typename Output<EP>::T Y, int32_t* __restrict__ dots,
                                                                  float* __restrict__ partial,
                                                                  unsigned* __restrict__ counters, int M, int N, int K,
                                                                  int Mp, int Np, int tiles_m, int full,

@@ -218,7 +218,7 @@ __global__ __launch_bounds__(64 * kWaves, DUMP ? 1 : 2) void mmq_kw_q4k_kernel(c
                                                                            const int8_t* __restrict__ codes,
                                                                            const float* __restrict__ xscale,
                                                                            const int32_t* __restrict__ xsum,
-                                                                           float* __restrict__ Y,
+                                                                           typename Output<EP>::T Y,
                                                                            int32_t* __restrict__ dots, int M, int N,
                                                                            int K, int64_t row_bytes, int tiles_n,
                                                                            int tiles, EP ep) {

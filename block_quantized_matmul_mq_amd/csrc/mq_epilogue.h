@@ -100,6 +100,11 @@ struct Epilogue {
     }
 };
 
+// The output pointer of a product kernel.  Its epilogue's mul and residual may be the same memory, so only the
+// products without one promise the compiler that nothing else reads it.
+template <class EP> struct Output { using T = float* __restrict__; };
+template <> struct Output<Epilogue> { using T = float*; };
+
 // The epilogue argument of a kernel launched through an argument array (ep null: NoEpilogue's,
 // one byte that nothing reads).
 inline void* epilogue_arg(const Epilogue* ep) {
