@@ -872,9 +872,9 @@ MmqPlan mmq_filled_plan(int type, int64_t M, int64_t N, int64_t K) {
     // many K ranges (of at least kRange steps) as fill both workgroups of every CU, and the tile rows are
     // those of the lower cost in row steps per workgroup: a row step of a 32-row tile costs 1.7 of a
     // 128-row tile's, writing and adding a round of partial tiles as much as 640 row steps (128 rows) or 160 (32).
-    // (us, mmq_plan -> this: Q6_K 333 x 5120 x 13824 248 -> 169, Q8_0 141 -> 109; Q6_K 128 x 8192 x 8192
-    // 105 -> 78, 512 x 8192 x 8192 261 -> 199;
-    // Q5_1 64 x 8192 x 8192 50 -> 36; Q8_0 384 x 2048 x 8192 87 -> 54.)
+    // (us in a captured graph, three weight matrices in turn, mmq_plan -> this: Q6_K 333 x 5120 x 13824
+    // 239 -> 168, Q8_0 174 -> 117; Q6_K 128 x 8192 x 8192 107 -> 73, 512 x 8192 x 8192 259 -> 197;
+    // Q5_1 64 x 8192 x 8192 50 -> 36; Q8_0 384 x 2048 x 8192 88 -> 50.)
     constexpr int kRange = 7;
     const MmqPlan plain = mmq_plan(type, M, N, K);
     auto cut = [&](int bm) {

@@ -659,7 +659,8 @@ __global__ __launch_bounds__(kThreads, 4) void moe_many_kernel(MoeArgs a) {
 
 // ------------------------------------------------------------------ one token
 // (8 of 64 experts of 2048 x 1024, Q4_K: up 7.4 us, down 6.7, 2.5 and 1.4 TB/s: two launches' ramps and
-// round trips, not bytes.  4 of 32 of 4096 x 2048: up Q4_K 10.4 us, down Q6_K 9.8, 3.6 and 2.8 TB/s.)
+// round trips, and a down kernel of K / 16 = 128 workgroups, which leaves half of the 256 CUs idle.
+// 4 of 32 of 4096 x 2048, 256 workgroups in down: up Q4_K 10.6 us, down Q6_K 9.6, 3.6 and 2.9 TB/s.)
 // blockIdx.y: choice; blockIdx.x: kWaves / (2 splits) 16-row tiles of its expert.  Wave w: part w % splits of
 // the groups (part ks: ks, ks + splits, ...) of matrix w / splits % 2 (gate, up), tile w / (2 splits) of
 // the workgroup; the sums meet in LDS, parts in order.
@@ -939,7 +940,8 @@ int pow2_floor(int64_t v) {
 
 template <int QT, bool UP>
 hipError_t launch_many(MoeArgs a, hipStream_t s) {
-    // Tokens of a slot: four.  (The LDS of a CU holds them of rows of up to 38 groups, and one of the longest.)
+    // Tokens of a slot: four, or as many as fit in the LDS of a CU: four of rows of up to 35 (Q8_0) to 41 (Q4_K)
+    // groups, one of the longest.
     constexpr size_t kFixed = kManyFixed + size_t(kWaves) * Tile<QT>::kSlot;
     static_assert(kFixed + 128 * size_t(unit_bytes<QT>()) <= kGfx950LdsBytes, "a token of the longest rows fits");
     const size_t per_token = size_t(a.groups) * unit_bytes<QT>();

@@ -460,7 +460,7 @@ def moe_route(X, Wr, topk, bias=None, score=SCORE_SOFTMAX, norm=True, scale=1.0,
               stream=None):
     """(ids int32 [M, topk], wts f32 [M, topk]) of tokens X (f32 [M, K]) by router weights Wr (f32 [E, K]);
     bias: f32 [E], added to the scores for the choice only.  scratch: moe_route_scratch_bytes(M, K, E) bytes,
-    zero before its first use."""
+    zero before its first use, and for calls of moe_route only."""
     import torch
     M, K = _rows(X, "moe_route")
     E = Wr.shape[0]

@@ -258,8 +258,8 @@ size_t mq_gemm_scratch_bytes(int type, int64_t M, int64_t N, int64_t K);
  * overwritten).  scratch / scratch_bytes: device memory of at least
  * mq_gemm_scratch_bytes(type, M, N, K) bytes, 16-byte aligned (may be NULL/0
  * when that is 0), zeroed before its first use (the counters); its partial
- * tiles are overwritten, and calls that share one scratch buffer must be
- * ordered on one stream.  MQ_ERR_SIZE when it is too small, MQ_ERR_ALIGN when
+ * tiles are overwritten, and calls that share one scratch buffer (of mq_gemm and
+ * mq_gemm_ep only) must be ordered on one stream.  MQ_ERR_SIZE when it is too small, MQ_ERR_ALIGN when
  * misaligned.
  */
 int mq_gemm(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_t N, int64_t K,
@@ -308,7 +308,9 @@ int mq_gemm_ep(const void* W, int type, const void* Xq, float* Y, int64_t M, int
  * <= MQ_MOE_MAX_TOPK.  Every id is in [0, E) and a token's ids differ, whatever X holds.
  * scratch: mq_moe_route_scratch_bytes(M, K, E) bytes (0 for a shape the call refuses), 16-byte
  * aligned; its first 256 KiB are counters that must be zero before the first call and that every
- * call leaves at zero; calls that share one buffer, of any shapes, must be ordered on one stream.
+ * call leaves at zero; mq_moe_route calls that share one buffer, of any shapes, must be ordered on one
+ * stream.  No other call's scratch may be the same memory: mq_gemm's and mq_gemm_ep's partial tiles and all of
+ * mq_moe_ffn's would overwrite the counters.
  * Deterministic.  MQ_ERR_SIZE for a scratch that is too small.
  */
 size_t mq_moe_route_scratch_bytes(int64_t M, int64_t K, int64_t E);
@@ -334,7 +336,8 @@ int mq_moe_route(const float* X, const float* Wr, const float* bias, int32_t* id
  * Deterministic: a token's bits depend on its own row, ids and weights and on which kernels run
  * (one token of at most 64 choices, or more), not on the other tokens.
  * scratch: mq_moe_scratch_bytes(M, topk, F, K) bytes (0 for sizes the call refuses), 16-byte
- * aligned, no initial value; calls that share one buffer must be ordered on one stream.
+ * aligned, no initial value; mq_moe_ffn calls that share one buffer must be ordered on one stream (it overwrites
+ * all of it, so a buffer whose counters another call needs is not for it).
  * Runs two launches for one token (of at most 64 choices), else three.
  */
 size_t mq_moe_scratch_bytes(int64_t M, int64_t topk, int64_t F, int64_t K);
