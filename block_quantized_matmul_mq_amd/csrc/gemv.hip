@@ -318,6 +318,13 @@ __global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restric
     // Then the first tile's weight loads.
     prime(t0);
 
+    // With an epilogue an infinity or a NaN in x (its digits mean nothing) reaches the outputs through the
+    // sums.  Q8_0 has none: there each wave notes in a byte of the planes' unused chunk U whether it staged one.
+    constexpr bool kNote = EP::kIs && QT == kQ8_0;
+    float bad = 0.f;
+    uint8_t* const bad_x = p0 + U * 16;
+    static_assert(kThreads / 64 <= 16, "a byte per wave");
+
     // Stage x: 8 lanes per 32-block, 4 values (one float4) per lane.
     auto stage = [&](int i, const float4 v) {
         float a = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
@@ -343,6 +350,7 @@ __global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restric
         *reinterpret_cast<uint32_t*>(p0 + off) = d0;
         *reinterpret_cast<uint32_t*>(p1 + off) = d1;
         *reinterpret_cast<uint32_t*>(p2 + off) = d2;
+        if constexpr (kNote) bad = not_finite(v, bad);
         float sm = staged_sum<EP>(v, k);
         sm = lanes8_sum<2>(sm);
         if constexpr (QT == kQ6_K) {
@@ -367,6 +375,10 @@ __global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restric
     for (int i = tid + kEarly * kThreads; i < nquads; i += kThreads)
         stage(i, reinterpret_cast<const float4*>(x)[i]);
     __syncthreads();
+    if constexpr (kNote) {   // (read after the next barrier)
+        const bool any = __ballot(!(bad == 0.f)) != 0;
+        if ((tid & 63) == 0) bad_x[tid >> 6] = any;
+    }
 
     const Stage st{p0, p1, p2, S, ex, sums};
 
@@ -402,6 +414,8 @@ __global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restric
         const int groups = kThreads / width;
         const int lane_in = tid & (width - 1);
         const int padded = rows + (groups - rows % groups) % groups;
+        uint4 any = {};
+        if constexpr (kNote) any = *reinterpret_cast<const uint4*>(bad_x);
         for (int r = tid / width; r < padded; r += groups) {
             float s = 0.f;
             if (r < rows) {
@@ -409,6 +423,8 @@ __global__ __launch_bounds__(kThreads) void gemv_kernel(const uint8_t* __restric
                 for (int j = lane_in; j < U; j += width) s += pr[j];
             }
             s = group_sum(s, width);
+            if constexpr (kNote)
+                if ((any.x | any.y | any.z | any.w) != 0) s = __builtin_nanf("");
             if (r < rows && lane_in == 0) y[t0 + r] = ep(s, t0 + r, t0 + r);
         }
         __syncthreads();

@@ -570,8 +570,8 @@ template <> struct TiledItem<kQ6_K> {
 template <> struct TiledItem<kQ8_0> {
     static constexpr int kSBBytes = 8 * 34;
     __device__ static float run(const uint8_t* row, int sc, int q, const v4i (&a)[4], const int (&e)[4],
-                                const float (&)[4]) {
-        float acc = 0.f;
+                                const float (&bad)[4]) {
+        float acc = bad[0];   // (no sum of x is needed: 0, or with an epilogue a NaN for an x that is not finite)
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             const uint8_t* blk = row + (8 * sc + 2 * t + (q >> 1)) * 34;   // block of run 4t + q
@@ -1121,7 +1121,7 @@ __global__ __launch_bounds__(kThreads) void gemv_wide_kernel(const uint8_t* __re
         *reinterpret_cast<uint32_t*>(xp + 4 * tid) = d0;
         *reinterpret_cast<uint32_t*>(xp + K + 4 * tid) = d1;
         *reinterpret_cast<uint32_t*>(xp + 2 * K + 4 * tid) = d2;
-        float sm = staged_sum<EP>(v, k);
+        float sm = QT == kQ8_0 && EP::kIs ? not_finite(v, 0.f) : staged_sum<EP>(v, k);
         sm = lanes8_sum<2>(sm);
         if ((tid & 3) == 0) sums[tid >> 2] = sm;
         if ((tid & 7) == 0) ex[tid >> 3] = -k;
@@ -1141,6 +1141,7 @@ __global__ __launch_bounds__(kThreads) void gemv_wide_kernel(const uint8_t* __re
         e[t] = ex[8 * sc + 2 * t + (q >> 1)];
         sx[t] = sums[16 * sc + 4 * t + q];
     }
+    if constexpr (QT == kQ8_0) sx[0] = EP::kIs ? ((sx[0] + sx[1]) + (sx[2] + sx[3])) + 0.f : 0.f;   // (no -0)
     wait_barrier<(NB - 1) * WI::kLoads>();   // x no longer read: its LDS now takes the partials
 
     auto compute = [&](const uint8_t* it, int k) {

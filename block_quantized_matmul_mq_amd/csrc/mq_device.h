@@ -68,6 +68,11 @@ __device__ __forceinline__ uint32_t load_u32_unaligned(const uint8_t* p) {
     return v;
 }
 
+// `before`, or a NaN where one of the values is an infinity or a NaN.
+__device__ __forceinline__ float not_finite(const float4 v, float before) {
+    return fmaf(0.f, v.x, fmaf(0.f, v.y, fmaf(0.f, v.z, fmaf(0.f, v.w, before))));
+}
+
 __device__ __forceinline__ uint32_t load_u16(const uint8_t* p) {
     return *reinterpret_cast<const uint16_t*>(p);
 }

@@ -7,6 +7,8 @@
 
 #include <type_traits>
 
+#include "mq_device.h"
+
 namespace mq {
 
 constexpr int kActNone = 0;
@@ -115,13 +117,14 @@ inline void* epilogue_arg(const Epilogue* ep) {
 // The sum of four activations of a block staged as integers, x = 2^-k rint(2^k x) with |2^k x| <= 2^21: of
 // the staged x in the kernels with an epilogue (exact), of x itself in those without, whose results are
 // fixed.  A code's offset and a minimum then multiply the same x that the codes meet, so that staging's error of
-// x carries through the weight and not through the code (Q4_0, 9872 x 5408: 9.8e-7 -> 5.1e-7 relative).
+// x carries through the weight and not through the code (Q4_0, 9872 x 5408: 9.8e-7 -> 5.1e-7 relative).  A value
+// that is not finite, whose digits mean nothing, makes the sum a NaN, and so every output.
 template <class EP>
 __device__ __forceinline__ float staged_sum(const float4 v, int k) {
     if constexpr (!EP::kIs) return (v.x + v.y) + (v.z + v.w);
     constexpr float kRound = 12582912.0f;   // 1.5 * 2^23: adding it rounds to whole numbers
     auto rounded = [&](float x) { return (ldexpf(x, k) + kRound) - kRound; };
-    return ldexpf((rounded(v.x) + rounded(v.y)) + (rounded(v.z) + rounded(v.w)), -k);
+    return not_finite(v, ldexpf((rounded(v.x) + rounded(v.y)) + (rounded(v.z) + rounded(v.w)), -k));
 }
 
 // An f32 (its bits) as three bf16 pieces of 8 bits each, high + mid + low exactly; each piece

@@ -215,7 +215,7 @@ int mq_quantize_act(const float* X, void* Xq, int64_t M, int64_t K, void* stream
  * payload (device, 16-byte aligned); x: K f32 (device); y: N f32 (device,
  * overwritten).  K must be a multiple of the block size (32 or 256) [BD4.3].
  * f32 accumulation; the result is within 2e-4 of the exact product relative to
- * ||deq(W)[n]|| * ||x||.
+ * ||deq(W)[n]|| * ||x||.  x must be finite (NaN/Inf are outside the contract).
  */
 int mq_gemv(const void* W, int type, const float* x, float* y, int64_t N, int64_t K, void* stream);
 
@@ -279,6 +279,7 @@ int mq_gemm(const void* W, int type, const void* Xq, float* Y, int64_t M, int64_
  * scratch holds.
  * mul and residual may be the output itself (the residual stream updated in place), or the
  * same buffer; no input may overlap the output otherwise.  MQ_ERR_ARG for an unknown act.
+ * An infinity or a NaN in mq_gemv_ep's x makes every output NaN.  (mq_gemm_ep's Xq comes from a finite X.)
  * So a gated feed-forward layer takes three products and no other launch:
  *   u = mq_gemv(Wup), h = mq_gemv_ep(Wgate, act = MQ_ACT_SILU, mul = u),
  *   y = mq_gemv_ep(Wdown, h, residual = y).
