@@ -21,7 +21,7 @@ MEASURE_SRC = os.path.join(HERE, "measure", "read_ceiling.hip")
 MEASURE_LIB = os.path.join(HERE, "libmq_measure.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["mq_api.hip", "quantize_act.hip", "gemv.hip", "gemv_mfma.hip", "gemv_q8.hip", "mmq.hip", "mmq_kw.hip", "mmq_f6.hip", "repack.hip",
-           "moe.hip", "moe_route.hip"]
+           "moe.hip", "moe_route.hip", "kv_append.hip", "attn.hip", "sample.hip"]
 FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-fno-gpu-rdc",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",

@@ -1,0 +1,268 @@
+// mq_kv_append: the heads' norm, the position rotation and the append of keys and values to the paged
+// cache, in one pass over a decoder layer's q, k and v; mq_kv_read: rows of the cache as f32.
+//
+//   y = x w / sqrt(mean(x^2) + eps)                            (q and k, where a norm is given)
+//   (y1, y2) -> (y1 cos a - y2 sin a, y2 cos a + y1 sin a),  a = pos inv_freq[j]
+//   K, V: blocks of 32, 4 bits: d = f16(m / -8), m the value of largest magnitude with its sign,
+//   code = clamp(rne(x / d) + 8, 0, 15); 8 bits: d = f16(amax / 127), code = clamp(rne(x / d), -127, 127) + 128
+//
+// Norm and rotation are formed in f64 and rounded once to f32: a key's code flips where its last f32 bit
+// does, and a cache should not depend on the order of a sum.  f64 runs at the f32 rate here and the pass is
+// bound by its bytes and its latency.
+#include "kv_layout.h"
+#include "mq_device.h"
+#include "mq_internal.h"
+
+namespace mq {
+
+namespace {
+
+constexpr int kWaves = 4;
+
+struct AppendArgs {
+    KvView c;
+    const float *q, *k, *v, *q_norm, *k_norm, *inv_freq;
+    const int32_t* pos;
+    float* q_out;
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    int q_heads, rot, rope;
+    float eps;
+};
+
+// cos and sin of a >= 0 or < 0 in f64: a - n pi/2 with pi/2 as two doubles (the fma is exact in the first),
+// then both Taylor series on [-pi/4, pi/4] (the first terms left out are below 2^-53).
+__device__ __forceinline__ void sincos64(double a, double& s, double& c) {
+    const double n = rint(a * 0.63661977236758134308);
+    double r = fma(-n, 1.57079632679489655800, a);
+    r = fma(-n, 6.12323399573676603587e-17, r);
+    const double z = r * r;
+    double ps = -1.0 / 1307674368000.0;
+    ps = fma(ps, z, 1.0 / 6227020800.0);
+    ps = fma(ps, z, -1.0 / 39916800.0);
+    ps = fma(ps, z, 1.0 / 362880.0);
+    ps = fma(ps, z, -1.0 / 5040.0);
+    ps = fma(ps, z, 1.0 / 120.0);
+    ps = fma(ps, z, -1.0 / 6.0);
+    ps = fma(ps * z, r, r);
+    double pc = 1.0 / 20922789888000.0;
+    pc = fma(pc, z, -1.0 / 87178291200.0);
+    pc = fma(pc, z, 1.0 / 479001600.0);
+    pc = fma(pc, z, -1.0 / 3628800.0);
+    pc = fma(pc, z, 1.0 / 40320.0);
+    pc = fma(pc, z, -1.0 / 720.0);
+    pc = fma(pc, z, 1.0 / 24.0);
+    pc = fma(pc, z, -0.5);
+    pc = fma(pc, z, 1.0);
+    const int64_t k = int64_t(n);
+    s = k & 1 ? pc : ps;
+    c = k & 1 ? ps : pc;
+    if (k & 2) s = -s;
+    if ((k + 1) & 2) c = -c;
+}
+
+__device__ __forceinline__ double wave_sum64(double v) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+    return v;
+}
+
+// One block per 32 lanes: the scale (f16 bits) and this lane's code of x.
+template <int BITS>
+__device__ __forceinline__ int quantize(float x, uint32_t& d_bits) {
+    const int lane = threadIdx.x & 63;
+    float big = fabsf(x);
+    bool bad = !(big <= 3.4028235e38f);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
+    const unsigned long long half = 0xFFFFFFFFull << (lane & 32);
+    const bool any_bad = (__ballot(bad) & half) != 0;
+    _Float16 d;
+    if constexpr (BITS == 4) {
+        const unsigned long long who = __ballot(fabsf(x) == big) & half;
+        const float m = __shfl(x, who ? __ffsll(who) - 1 : lane, 64);
+        d = static_cast<_Float16>(m / -8.0f);
+    } else {
+        d = static_cast<_Float16>(big / 127.0f);
+    }
+    float df = static_cast<float>(d);
+    // a block with an infinity or a NaN, or past f16's range, reads as NaN
+    if (any_bad || !(fabsf(df) <= 65504.0f)) {
+        d_bits = 0x7E00u;
+        return BITS == 4 ? 8 : 128;
+    }
+    if (df == 0.0f) {
+        d_bits = 0;
+        return BITS == 4 ? 8 : 128;
+    }
+    d_bits = __builtin_bit_cast(uint16_t, d);
+    const float r = rintf(x / df);
+    if constexpr (BITS == 4) return int(fminf(fmaxf(r + 8.0f, 0.0f), 15.0f));
+    return int(fminf(fmaxf(r, -127.0f), 127.0f)) + 128;
+}
+
+// A workgroup per token, a wave per head's row; lane l holds dimensions l + 64 i.
+template <int BITS, int D>
+__global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(AppendArgs a) {
+    using L = KvLayout<BITS, D>;
+    constexpr int R = D / 64;
+    __shared__ double row[kWaves][D];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = blockIdx.x;
+    const KvToken tok = kv_token(a.c, t);
+    if (tok.seq < 0) return;
+    const int page = kv_page(a.c, tok.seq, tok.pos);
+    const int slot = tok.pos & (a.c.page_tokens - 1);
+    double sn[R], cs[R];
+    int partner[R];
+    if (a.rope) {
+        const double pos = a.pos ? double(a.pos[t]) : double(tok.pos);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int d = lane + 64 * i, h = a.rot / 2;
+            sn[i] = 0.0;
+            cs[i] = 1.0;
+            partner[i] = d;
+            if (d < a.rot) {
+                const bool first = a.rope == 1 ? d < h : (d & 1) == 0;
+                partner[i] = a.rope == 1 ? (first ? d + h : d - h) : d ^ 1;
+                sincos64(pos * double(a.inv_freq[a.rope == 1 ? (first ? d : d - h) : d >> 1]), sn[i], cs[i]);
+                if (first) sn[i] = -sn[i];
+            }
+        }
+    }
+    const int q_rows = a.q ? a.q_heads : 0, kv = a.c.heads;
+    for (int r = wave; r < q_rows + 2 * kv; r += kWaves) {
+        const bool is_q = r < q_rows, is_v = r >= q_rows + kv;
+        const int h = is_q ? r : is_v ? r - q_rows - kv : r - q_rows;
+        if (!is_q && page < 0) continue;
+        const float* from = is_q ? a.q + t * a.q_stride : is_v ? a.v + t * a.v_stride : a.k + t * a.k_stride;
+        from += int64_t(h) * D;
+        float x[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) x[i] = from[lane + 64 * i];
+        if (!is_v) {
+            double y[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) y[i] = x[i];
+            const float* w = is_q ? a.q_norm : a.k_norm;
+            if (w) {
+                double s = 0.0;
+#pragma unroll
+                for (int i = 0; i < R; ++i) s = fma(y[i], y[i], s);
+                s = 1.0 / sqrt(wave_sum64(s) / D + double(a.eps));
+#pragma unroll
+                for (int i = 0; i < R; ++i) y[i] = y[i] * s * double(w[lane + 64 * i]);
+            }
+            if (a.rope) {
+#pragma unroll
+                for (int i = 0; i < R; ++i) row[wave][lane + 64 * i] = y[i];
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int i = 0; i < R; ++i)
+                    if (lane + 64 * i < a.rot) y[i] = fma(y[i], cs[i], row[wave][partner[i]] * sn[i]);
+                __builtin_amdgcn_wave_barrier();
+            }
+#pragma unroll
+            for (int i = 0; i < R; ++i) x[i] = float(y[i]);
+        }
+        if (is_q) {
+#pragma unroll
+            for (int i = 0; i < R; ++i) a.q_out[t * a.out_stride + int64_t(h) * D + lane + 64 * i] = x[i];
+            continue;
+        }
+        uint8_t* chunk = a.c.data + (int64_t(page) * kv + h) * a.c.chunk;
+        const int64_t section = int64_t(a.c.page_tokens) * L::kRow;
+        uint8_t* codes = chunk + (is_v ? section : 0);
+        uint16_t* scales = reinterpret_cast<uint16_t*>(chunk + 2 * section) +
+                           (int64_t(is_v) * a.c.page_tokens + slot) * L::kBlocks;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int dim = lane + 64 * i;
+            uint32_t d;
+            const int code = quantize<BITS>(x[i], d);
+            if ((lane & 31) == 0) scales[dim / 32] = uint16_t(d);
+            if (!is_v) {    // 4 or 8 lanes fill a dword
+                constexpr int kPer = 32 / BITS;
+                uint32_t w = uint32_t(code) << (BITS * (lane % kPer));
+#pragma unroll
+                for (int off = 1; off < kPer; off <<= 1) w |= __shfl_xor(w, off, 64);
+                if (lane % kPer == 0) *reinterpret_cast<uint32_t*>(codes + L::k_byte(slot, dim)) = w;
+            } else {        // lanes 16 apart fill two bytes
+                constexpr int kPer = 16 / BITS;
+                uint32_t w = uint32_t(code) << (BITS * (lane / 16 % kPer));
+#pragma unroll
+                for (int off = 16; off < 16 * kPer; off <<= 1) w |= __shfl_xor(w, off, 64);
+                if (lane / 16 % kPer == 0) *reinterpret_cast<uint16_t*>(codes + L::v_byte(slot, dim)) = uint16_t(w);
+            }
+        }
+    }
+}
+
+// A workgroup per token, a wave per head; lane l gives dimensions l + 64 i.
+template <int BITS, int D>
+__global__ __launch_bounds__(64 * kWaves) void kv_read_kernel(KvView c, float* k, float* v) {
+    using L = KvLayout<BITS, D>;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int t = blockIdx.x;
+    const KvToken tok = kv_token(c, t);
+    if (tok.seq < 0) return;
+    const int page = kv_page(c, tok.seq, tok.pos);
+    const int slot = tok.pos & (c.page_tokens - 1);
+    const int64_t section = int64_t(c.page_tokens) * L::kRow;
+    for (int r = wave; r < 2 * c.heads; r += kWaves) {
+        const bool is_v = r >= c.heads;
+        const int h = is_v ? r - c.heads : r;
+        float* out = is_v ? v : k;
+        if (!out) continue;
+        out += (int64_t(t) * c.heads + h) * D;
+        const uint8_t* chunk = c.data + (int64_t(page) * c.heads + h) * c.chunk;
+        const uint16_t* scales = reinterpret_cast<const uint16_t*>(chunk + 2 * section) +
+                                 (int64_t(is_v) * c.page_tokens + slot) * L::kBlocks;
+#pragma unroll
+        for (int dim = lane; dim < D; dim += 64) {
+            float x = 0.0f;
+            if (page >= 0) {
+                int code = chunk[is_v ? section + L::v_byte(slot, dim) : L::k_byte(slot, dim)];
+                if constexpr (BITS == 4) code = (code >> (4 * (is_v ? L::v_nibble(dim) : L::k_nibble(dim)))) & 15;
+                x = float(code - L::kOffset) * half_bits_to_float(scales[dim / 32]);
+            }
+            out[dim] = x;
+        }
+    }
+}
+
+template <class F>
+hipError_t by_kind(int bits, int64_t dim, const F& f) {
+    if (bits == 4) {
+        if (dim == 64) f(std::integral_constant<int, 4>{}, std::integral_constant<int, 64>{});
+        else if (dim == 128) f(std::integral_constant<int, 4>{}, std::integral_constant<int, 128>{});
+        else f(std::integral_constant<int, 4>{}, std::integral_constant<int, 256>{});
+    } else {
+        if (dim == 64) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 64>{});
+        else if (dim == 128) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 128>{});
+        else f(std::integral_constant<int, 8>{}, std::integral_constant<int, 256>{});
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_append(const KvAppend& r, hipStream_t s, const char** name) {
+    *name = "kv_append";
+    const AppendArgs a = {r.cache.view, r.q, r.k, r.v, r.q_norm, r.k_norm, r.inv_freq, r.pos, r.q_out, r.q_stride,
+                          r.k_stride, r.v_stride, r.out_stride, int(r.q_heads), int(r.rot), r.rope, r.eps};
+    return by_kind(r.cache.bits, r.cache.dim, [&](auto bits, auto dim) {
+        hipLaunchKernelGGL((kv_append_kernel<decltype(bits)::value, decltype(dim)::value>), dim3(unsigned(r.T)),
+                           dim3(64 * kWaves), 0, s, a);
+    });
+}
+
+hipError_t launch_kv_read(const KvCache& cache, int64_t T, float* k, float* v, hipStream_t s, const char** name) {
+    *name = "kv_read";
+    return by_kind(cache.bits, cache.dim, [&](auto bits, auto dim) {
+        hipLaunchKernelGGL((kv_read_kernel<decltype(bits)::value, decltype(dim)::value>), dim3(unsigned(T)),
+                           dim3(64 * kWaves), 0, s, cache.view, k, v);
+    });
+}
+
+}  // namespace mq

@@ -584,6 +584,235 @@ int mq_moe_route(const float* X, const float* Wr, const float* bias, int32_t* id
     return launch_status(fn, e, kernel);
 }
 
+static int kv_bits(int type) { return type == MQ_Q4_0 ? 4 : type == MQ_Q8_0 ? 8 : 0; }
+
+size_t mq_kv_cache_bytes(int type, int64_t pages, int64_t page_tokens, int64_t heads, int64_t dim) {
+    if (!kv_bits(type) || pages <= 0 || pages > MQ_KV_MAX_PAGES || heads <= 0 || heads > MQ_KV_MAX_HEADS ||
+        page_tokens < 16 || page_tokens > 256 || (page_tokens & (page_tokens - 1)) != 0 ||
+        (dim != 64 && dim != 128 && dim != 256))
+        return 0;
+    return size_t(pages) * size_t(heads) * size_t(kv_chunk_bytes(kv_bits(type), page_tokens, dim));
+}
+
+// The cache and the sequences of a call, checked; `c` for its kernels.
+static int check_kv(const char* fn, const mq_kv_cache* cache, const mq_kv_seqs* seqs, int64_t T, KvCache& c) {
+    if (!cache || !seqs) return fail(MQ_ERR_ARG, "%s: null pointer (cache=%p seqs=%p)", fn, (const void*)cache, (const void*)seqs);
+    if (!cache->data || !seqs->q_start || !seqs->kv_len || !seqs->table)
+        return fail(MQ_ERR_ARG, "%s: null pointer (data=%p q_start=%p kv_len=%p table=%p)", fn, cache->data,
+                    (const void*)seqs->q_start, (const void*)seqs->kv_len, (const void*)seqs->table);
+    if (!kv_bits(cache->type)) return fail(MQ_ERR_TYPE, "%s: unsupported cache type %d", fn, cache->type);
+    if (cache->pages <= 0 || cache->heads <= 0 || seqs->seqs <= 0 || seqs->table_width <= 0 || T <= 0)
+        return fail(MQ_ERR_ARG, "%s: pages=%lld heads=%lld seqs=%lld table_width=%lld T=%lld must be positive", fn,
+                    (long long)cache->pages, (long long)cache->heads, (long long)seqs->seqs,
+                    (long long)seqs->table_width, (long long)T);
+    if (mq_kv_cache_bytes(cache->type, cache->pages, cache->page_tokens, cache->heads, cache->dim) == 0)
+        return fail(MQ_ERR_SHAPE, "%s: a cache of pages=%lld page_tokens=%lld heads=%lld dim=%lld is not served "
+                    "(pages <= %d, page_tokens 16, 32, 64, 128 or 256, heads <= %d, dim 64, 128 or 256)", fn,
+                    (long long)cache->pages, (long long)cache->page_tokens, (long long)cache->heads,
+                    (long long)cache->dim, MQ_KV_MAX_PAGES, MQ_KV_MAX_HEADS);
+    if (seqs->seqs > MQ_KV_MAX_SEQS || T > MQ_MAX_M || seqs->table_width > MQ_KV_MAX_TOKENS / cache->page_tokens)
+        return fail(MQ_ERR_SHAPE, "%s: seqs=%lld T=%lld table_width=%lld exceed seqs <= %d, T <= %d, "
+                    "table_width * page_tokens <= %d", fn, (long long)seqs->seqs, (long long)T,
+                    (long long)seqs->table_width, MQ_KV_MAX_SEQS, MQ_MAX_M, MQ_KV_MAX_TOKENS);
+    if (!aligned(cache->data, 16) || !aligned(seqs->q_start, 4) || !aligned(seqs->kv_len, 4) || !aligned(seqs->table, 4))
+        return fail(MQ_ERR_ALIGN, "%s: data must be 16-byte, q_start, kv_len and table 4-byte aligned", fn);
+    c.bits = kv_bits(cache->type);
+    c.dim = cache->dim;
+    KvView& v = c.view;
+    v.data = static_cast<uint8_t*>(cache->data);
+    v.q_start = seqs->q_start;
+    v.kv_len = seqs->kv_len;
+    v.table = seqs->table;
+    v.chunk = kv_chunk_bytes(c.bits, cache->page_tokens, cache->dim);
+    v.pages = int(cache->pages);
+    v.page_tokens = int(cache->page_tokens);
+    v.page_shift = __builtin_ctz(unsigned(cache->page_tokens));
+    v.heads = int(cache->heads);
+    v.seqs = int(seqs->seqs);
+    v.width = int(seqs->table_width);
+    return MQ_OK;
+}
+
+// Rows of `heads` heads of dim f32, `stride` floats apart.
+static int check_rows(const char* fn, const char* name, const float* p, int64_t stride, int64_t heads, int64_t dim) {
+    if (!p) return fail(MQ_ERR_ARG, "%s: null %s", fn, name);
+    if (stride < heads * dim || stride % 4 != 0 || stride > (int64_t(1) << 31))
+        return fail(MQ_ERR_SHAPE, "%s: %s rows %lld floats apart: a multiple of 4 from %lld to 2^31 is required", fn,
+                    name, (long long)stride, (long long)(heads * dim));
+    if (!aligned(p, 16)) return fail(MQ_ERR_ALIGN, "%s: %s must be 16-byte aligned (%p)", fn, name, (const void*)p);
+    return MQ_OK;
+}
+
+int mq_kv_append(const mq_kv_cache* cache, const mq_kv_seqs* seqs, const float* q, int64_t q_stride, const float* k,
+                 int64_t k_stride, const float* v, int64_t v_stride, float* q_out, int64_t out_stride, int64_t T,
+                 int64_t q_heads, const float* q_norm, const float* k_norm, float eps, int rope, const float* inv_freq,
+                 int64_t rot, const int32_t* pos, void* stream) {
+    const char* fn = "mq_kv_append";
+    KvAppend r = {};
+    int rc = check_kv(fn, cache, seqs, T, r.cache);
+    if (rc) return rc;
+    const int64_t dim = cache->dim;
+    if ((q == nullptr) != (q_out == nullptr) || (q == nullptr) != (q_heads == 0))
+        return fail(MQ_ERR_ARG, "%s: q, q_out and q_heads go together (q=%p q_out=%p q_heads=%lld)", fn, (const void*)q,
+                    (void*)q_out, (long long)q_heads);
+    if (q_heads < 0) return fail(MQ_ERR_ARG, "%s: q_heads=%lld must not be negative", fn, (long long)q_heads);
+    if (q_heads > MQ_KV_MAX_HEADS)
+        return fail(MQ_ERR_SHAPE, "%s: q_heads=%lld exceeds %d", fn, (long long)q_heads, MQ_KV_MAX_HEADS);
+    if (rope < MQ_ROPE_NONE || rope > MQ_ROPE_INTERLEAVED)
+        return fail(MQ_ERR_ARG, "%s: unknown rotation %d", fn, rope);
+    if (rope == MQ_ROPE_NONE ? inv_freq || pos || rot != 0 : !inv_freq)
+        return fail(MQ_ERR_ARG, "%s: a rotation needs inv_freq, and MQ_ROPE_NONE takes no inv_freq, pos and rot "
+                    "(rope=%d inv_freq=%p pos=%p rot=%lld)", fn, rope, (const void*)inv_freq, (const void*)pos,
+                    (long long)rot);
+    if (rope != MQ_ROPE_NONE && (rot < 2 || rot > dim || rot % 2 != 0))
+        return fail(MQ_ERR_SHAPE, "%s: rot=%lld is not an even number from 2 to dim=%lld", fn, (long long)rot,
+                    (long long)dim);
+    if (!(eps >= 0.0f)) return fail(MQ_ERR_ARG, "%s: eps=%g must not be negative", fn, double(eps));
+    if (q) {
+        rc = check_rows(fn, "q", q, q_stride, q_heads, dim);
+        if (rc == MQ_OK) rc = check_rows(fn, "q_out", q_out, out_stride, q_heads, dim);
+        if (rc) return rc;
+        if (q == q_out && q_stride != out_stride)
+            return fail(MQ_ERR_ARG, "%s: q_out is q with another stride (%lld, %lld)", fn, (long long)q_stride,
+                        (long long)out_stride);
+    }
+    rc = check_rows(fn, "k", k, k_stride, cache->heads, dim);
+    if (rc == MQ_OK) rc = check_rows(fn, "v", v, v_stride, cache->heads, dim);
+    if (rc) return rc;
+    if (!aligned(q_norm, 4) || !aligned(k_norm, 4) || !aligned(inv_freq, 4) || !aligned(pos, 4))
+        return fail(MQ_ERR_ALIGN, "%s: q_norm, k_norm, inv_freq and pos must be 4-byte aligned", fn);
+    rc = check_ready(fn);
+    if (rc) return rc;
+    r.q = q;
+    r.k = k;
+    r.v = v;
+    r.q_norm = q_norm;
+    r.k_norm = k_norm;
+    r.inv_freq = inv_freq;
+    r.pos = pos;
+    r.q_out = q_out;
+    r.T = T;
+    r.q_heads = q_heads;
+    r.q_stride = q_stride;
+    r.k_stride = k_stride;
+    r.v_stride = v_stride;
+    r.out_stride = out_stride;
+    r.rot = rot;
+    r.rope = rope;
+    r.eps = eps;
+    const char* kernel = "kv_append";
+    if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, kernel);
+    hipError_t e = launch_kv_append(r, static_cast<hipStream_t>(stream), &kernel);
+    return launch_status(fn, e, kernel);
+}
+
+int mq_kv_read(const mq_kv_cache* cache, const mq_kv_seqs* seqs, int64_t T, float* k, float* v, void* stream) {
+    const char* fn = "mq_kv_read";
+    KvCache c = {};
+    int rc = check_kv(fn, cache, seqs, T, c);
+    if (rc) return rc;
+    if (!k && !v) return fail(MQ_ERR_ARG, "%s: k and v are both null", fn);
+    if (!aligned(k, 16) || !aligned(v, 16))
+        return fail(MQ_ERR_ALIGN, "%s: k and v must be 16-byte aligned (k=%p v=%p)", fn, (void*)k, (void*)v);
+    rc = check_ready(fn);
+    if (rc) return rc;
+    const char* kernel = "kv_read";
+    if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, kernel);
+    hipError_t e = launch_kv_read(c, T, k, v, static_cast<hipStream_t>(stream), &kernel);
+    return launch_status(fn, e, kernel);
+}
+
+size_t mq_attn_scratch_bytes(int type, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q,
+                             int64_t max_kv) {
+    if (!kv_bits(type) || seqs <= 0 || seqs > MQ_KV_MAX_SEQS || heads <= 0 || heads > MQ_KV_MAX_HEADS || q_heads <= 0 ||
+        q_heads > MQ_KV_MAX_HEADS || q_heads % heads != 0 || (dim != 64 && dim != 128 && dim != 256) || max_q <= 0 ||
+        max_q > MQ_MAX_M || max_kv <= 0 || max_kv > MQ_KV_MAX_TOKENS)
+        return 0;
+    return attn_scratch_bytes(kv_bits(type), seqs, q_heads, heads, dim, max_q, max_kv);
+}
+
+int mq_attn(const mq_kv_cache* cache, const mq_kv_seqs* seqs, const float* q, int64_t q_stride, float* out, int64_t T,
+            int64_t q_heads, float scale, int causal, int64_t window, int64_t max_q, int64_t max_kv, void* scratch,
+            size_t scratch_bytes, void* stream) {
+    const char* fn = "mq_attn";
+    Attn r = {};
+    int rc = check_kv(fn, cache, seqs, T, r.cache);
+    if (rc) return rc;
+    if (!out || !scratch) return fail(MQ_ERR_ARG, "%s: null pointer (out=%p scratch=%p)", fn, (void*)out, scratch);
+    if (q_heads <= 0 || max_q <= 0 || max_kv <= 0)
+        return fail(MQ_ERR_ARG, "%s: q_heads=%lld max_q=%lld max_kv=%lld must be positive", fn, (long long)q_heads,
+                    (long long)max_q, (long long)max_kv);
+    if (q_heads > MQ_KV_MAX_HEADS || q_heads % cache->heads != 0)
+        return fail(MQ_ERR_SHAPE, "%s: q_heads=%lld is not a multiple of the cache's %lld heads up to %d", fn,
+                    (long long)q_heads, (long long)cache->heads, MQ_KV_MAX_HEADS);
+    if (max_q > MQ_MAX_M || max_kv > MQ_KV_MAX_TOKENS)
+        return fail(MQ_ERR_SHAPE, "%s: max_q=%lld max_kv=%lld exceed %d and %d", fn, (long long)max_q, (long long)max_kv,
+                    MQ_MAX_M, MQ_KV_MAX_TOKENS);
+    if (window < 0 || window > MQ_KV_MAX_TOKENS || (window > 0 && !causal))
+        return fail(MQ_ERR_ARG, "%s: window=%lld (0 for none, up to %d, and with causal only)", fn, (long long)window,
+                    MQ_KV_MAX_TOKENS);
+    rc = check_rows(fn, "q", q, q_stride, q_heads, cache->dim);
+    if (rc) return rc;
+    if (!aligned(out, 16) || !aligned(scratch, 16))
+        return fail(MQ_ERR_ALIGN, "%s: out and scratch must be 16-byte aligned (out=%p scratch=%p)", fn, (void*)out,
+                    scratch);
+    const size_t need =
+        attn_scratch_bytes(r.cache.bits, seqs->seqs, q_heads, cache->heads, cache->dim, max_q, max_kv);
+    if (scratch_bytes < need)
+        return fail(MQ_ERR_SIZE, "%s: scratch of %zu bytes, %zu required", fn, scratch_bytes, need);
+    rc = check_ready(fn);
+    if (rc) return rc;
+    r.q = q;
+    r.out = out;
+    r.scratch = scratch;
+    r.T = T;
+    r.q_heads = q_heads;
+    r.q_stride = q_stride;
+    r.window = window;
+    r.max_q = max_q;
+    r.max_kv = max_kv;
+    r.causal = causal != 0;
+    r.scale = scale;
+    const char* kernel = "attn";
+    if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, kernel);
+    hipError_t e = launch_attn(r, static_cast<hipStream_t>(stream), &kernel);
+    return launch_status(fn, e, kernel);
+}
+
+size_t mq_sample_scratch_bytes(int64_t M, int64_t V) {
+    if (M <= 0 || M > MQ_MAX_M || V <= 0 || V > MQ_MAX_VOCAB) return 0;
+    return sample_scratch_bytes(M, V);
+}
+
+int mq_sample(const float* logits, int64_t stride, int64_t M, int64_t V, const float* temperature, const int32_t* top_k,
+              const float* top_p, const float* min_p, const float* u, int32_t* ids, float* probs, void* scratch,
+              size_t scratch_bytes, void* stream) {
+    const char* fn = "mq_sample";
+    if (!logits || !u || !ids || !scratch)
+        return fail(MQ_ERR_ARG, "%s: null pointer (logits=%p u=%p ids=%p scratch=%p)", fn, (const void*)logits,
+                    (const void*)u, (void*)ids, scratch);
+    if (M <= 0 || V <= 0) return fail(MQ_ERR_ARG, "%s: M=%lld V=%lld must be positive", fn, (long long)M, (long long)V);
+    if (M > MQ_MAX_M || V > MQ_MAX_VOCAB)
+        return fail(MQ_ERR_SHAPE, "%s: M=%lld V=%lld exceed %d and %d", fn, (long long)M, (long long)V, MQ_MAX_M,
+                    MQ_MAX_VOCAB);
+    if (stride < V || stride > (int64_t(1) << 31))
+        return fail(MQ_ERR_SHAPE, "%s: rows %lld floats apart: from V=%lld to 2^31 is required", fn, (long long)stride,
+                    (long long)V);
+    if (!aligned(logits, 4) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) ||
+        !aligned(min_p, 4) || !aligned(u, 4) || !aligned(ids, 4) || !aligned(probs, 4) || !aligned(scratch, 16))
+        return fail(MQ_ERR_ALIGN, "%s: arrays must be 4-byte, scratch 16-byte aligned", fn);
+    const size_t need = sample_scratch_bytes(M, V);
+    if (scratch_bytes < need)
+        return fail(MQ_ERR_SIZE, "%s: scratch of %zu bytes, %zu required", fn, scratch_bytes, need);
+    const int rc = check_ready(fn);
+    if (rc) return rc;
+    const Sample r = {logits, temperature, top_p, min_p, u, top_k, ids, probs, scratch, stride, M, V};
+    const char* kernel = "sample";
+    if (refuse_this_launch()) return launch_status(fn, hipErrorLaunchFailure, kernel);
+    hipError_t e = launch_sample(r, static_cast<hipStream_t>(stream), &kernel);
+    return launch_status(fn, e, kernel);
+}
+
 int mq_repack(const void* W, int type, int64_t N, int64_t K, size_t nbytes, void* Wr, size_t wr_bytes,
               void* stream) {
     const char* fn = "mq_repack";

@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "kv_layout.h"
 #include "mq_device.h"
 
 namespace mq {
@@ -212,6 +213,47 @@ struct MoeRoute {
 };
 size_t moe_route_scratch_bytes(int64_t M, int64_t K, int64_t E);
 hipError_t launch_moe_route(const MoeRoute& r, hipStream_t s, const char** kernel_name);
+// mq_kv_append, mq_kv_read (kv_append.hip) and mq_attn (attn.hip) on a paged cache (kv_layout.h)
+struct KvCache {
+    KvView view;
+    int bits;
+    int64_t dim;
+};
+struct KvAppend {
+    KvCache cache;
+    const float *q, *k, *v, *q_norm, *k_norm, *inv_freq;
+    const int32_t* pos;
+    float* q_out;
+    int64_t T, q_heads, q_stride, k_stride, v_stride, out_stride, rot;
+    int rope;
+    float eps;
+};
+hipError_t launch_kv_append(const KvAppend& r, hipStream_t s, const char** kernel_name);
+hipError_t launch_kv_read(const KvCache& cache, int64_t T, float* k, float* v, hipStream_t s,
+                          const char** kernel_name);
+struct Attn {
+    KvCache cache;
+    const float* q;
+    float* out;
+    void* scratch;
+    int64_t T, q_heads, q_stride, window, max_q, max_kv;
+    int causal;
+    float scale;
+};
+size_t attn_scratch_bytes(int bits, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q,
+                          int64_t max_kv);
+hipError_t launch_attn(const Attn& r, hipStream_t s, const char** kernel_name);
+// mq_sample (sample.hip)
+struct Sample {
+    const float *logits, *temperature, *top_p, *min_p, *u;
+    const int32_t* top_k;
+    int32_t* ids;
+    float* probs;
+    void* scratch;
+    int64_t stride, M, V;
+};
+size_t sample_scratch_bytes(int64_t M, int64_t V);
+hipError_t launch_sample(const Sample& r, hipStream_t s, const char** kernel_name);
 // mq_repack: every `in_bytes`-byte block of W into a `slot_bytes`-byte slot of Wr at offset
 // `off`, the rest of the slot zero (repack.hip).
 hipError_t launch_repack(const uint8_t* W, uint8_t* Wr, int64_t blocks, int in_bytes, int slot_bytes, int off,

@@ -25,12 +25,26 @@ ROW_TILED = 0x200  # OR-ed into Q4_K: its row-tiled layout (long-row GEMV), from
 # Activations of gemv_ep / gemm_ep / moe_ffn and router scores of moe_route (include/mq.h)
 ACT_NONE, ACT_SILU, ACT_GELU_TANH, ACT_GELU_ERF, ACT_RELU = range(5)
 SCORE_SOFTMAX, SCORE_SIGMOID = range(2)
+# Position rotations of kv_append
+ROPE_NONE, ROPE_HALF, ROPE_INTERLEAVED = range(3)
 
 MQ_OK = 0
 ERRORS = {
     -1: "MQ_ERR_ARG", -2: "MQ_ERR_SHAPE", -3: "MQ_ERR_TYPE", -4: "MQ_ERR_SIZE",
     -5: "MQ_ERR_ALIGN", -6: "MQ_ERR_DEVICE", -7: "MQ_ERR_LAUNCH", -8: "MQ_ERR_NOINIT",
 }
+
+
+
+class _Cache(ctypes.Structure):     # mq_kv_cache
+    _fields_ = [("data", ctypes.c_void_p), ("type", ctypes.c_int), ("pages", ctypes.c_int64),
+                ("page_tokens", ctypes.c_int64), ("heads", ctypes.c_int64), ("dim", ctypes.c_int64)]
+
+
+class _Seqs(ctypes.Structure):      # mq_kv_seqs
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("seqs", ctypes.c_int64), ("table_width", ctypes.c_int64)]
+
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmq.so")
 
@@ -67,6 +81,21 @@ _SIGNATURES = {
                                   ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                   ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                   ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mq_kv_cache_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                            ctypes.c_int64]),
+    "mq_kv_append": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                    ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                    ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float,
+                                    ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p]),
+    "mq_kv_read": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p,
+                                  ctypes.c_void_p]),
+    "mq_attn_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int] + [ctypes.c_int64] * 6),
+    "mq_attn": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                               ctypes.c_int64, ctypes.c_int64, ctypes.c_float, ctypes.c_int, ctypes.c_int64,
+                               ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "mq_sample_scratch_bytes": (ctypes.c_size_t, [ctypes.c_int64, ctypes.c_int64]),
+    "mq_sample": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64] + [ctypes.c_void_p] * 8
+                  + [ctypes.c_size_t, ctypes.c_void_p]),
     "mq_debug_lds_bytes": (ctypes.c_size_t, [ctypes.c_int, ctypes.c_int, ctypes.c_int64]),
     "mq_gemm_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                                        ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]),
@@ -528,3 +557,192 @@ def moe_ffn(Wg, Wu, gu_type, Wd, d_type, X, ids, wts, E, F, act=ACT_SILU, residu
           ids.data_ptr(), wts.data_ptr(), _ptr(residual), Y.data_ptr(), M, topk, E, F, K, act, scratch.data_ptr(),
           _nbytes(scratch))
     return Y
+
+
+@functools.lru_cache(maxsize=4096)
+def kv_cache_bytes(qtype, pages, page_tokens, heads, dim):
+    return load().mq_kv_cache_bytes(qtype, pages, page_tokens, heads, dim)
+
+
+class KVCache:
+    """A paged cache of keys and values in blocks of Q4_0 or Q8_0: data, a uint8 CUDA tensor of exactly
+    kv_cache_bytes(qtype, pages, page_tokens, heads, dim) bytes (layout in include/mq.h)."""
+
+    def __init__(self, data, qtype, pages, page_tokens, heads, dim):
+        need = kv_cache_bytes(qtype, pages, page_tokens, heads, dim)
+        if need == 0:
+            _refuse(-3 if qtype not in (Q4_0, Q8_0) else -2, "KVCache", f"type {qtype} with pages={pages} page_tokens="
+                    f"{page_tokens} heads={heads} dim={dim} is not served")
+        _contiguous(data, "KVCache", "data")
+        if _nbytes(data) != need:
+            _refuse(-4, "KVCache", f"data holds {_nbytes(data)} bytes, this cache is exactly {need}")
+        self.data, self.qtype, self.pages, self.page_tokens, self.heads, self.dim = data, qtype, pages, page_tokens, heads, dim
+        self._c = _Cache(data.data_ptr(), qtype, pages, page_tokens, heads, dim)
+        self._ref = ctypes.addressof(self._c)
+
+
+class KVSeqs:
+    """The sequences of calls on a paged cache: q_start int32 [B + 1], kv_len int32 [B] and the page table int32
+    [B, width] (CUDA tensors, read when the calls run; include/mq.h)."""
+
+    def __init__(self, q_start, kv_len, table):
+        if table.dim() != 2:
+            _refuse(-1, "KVSeqs", f"table must be 2-D [seqs, width], not {tuple(table.shape)}")
+        B, width = table.shape
+        _i32(table, B * width, "KVSeqs", "table")
+        _i32(kv_len, B, "KVSeqs", "kv_len")
+        _i32(q_start, B + 1, "KVSeqs", "q_start")
+        self.q_start, self.kv_len, self.table = q_start, kv_len, table
+        self._c = _Seqs(q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), B, width)
+        self._ref = ctypes.addressof(self._c)
+
+
+def _heads(t, fn, name, T, heads, dim):
+    """The row stride of f32 [T, heads, dim], whose heads follow one another (rows may be parts of longer ones)."""
+    import torch
+    if t.dtype is not torch.float32:
+        _refuse(-1, fn, f"{name} must be float32, not {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != dim or (T is not None and t.shape[0] != T) or (heads is not None and t.shape[1] != heads):
+        _refuse(-2, fn, f"{name} must be [{'T' if T is None else T}, {'heads' if heads is None else heads}, {dim}], "
+                        f"not {tuple(t.shape)}")
+    rows, per, one = t.stride()
+    if one != 1 or (per != dim and t.shape[1] != 1):
+        _refuse(-1, fn, f"{name}: the heads of a row must follow one another (strides {t.stride()})")
+    return rows if t.shape[0] != 1 else t.shape[1] * dim
+
+
+def kv_append(cache, seqs, k, v, q=None, q_norm=None, k_norm=None, eps=1e-6, rope=ROPE_HALF, inv_freq=None, pos=None,
+              q_out=None, stream=None):
+    """Norm, rotation and append: k, v f32 [T, heads, dim] go to the cache (k normed by k_norm f32 [dim] and
+    rotated), q f32 [T, q_heads, dim] (normed, rotated) to q_out, which is returned.  The rows of q, k and v may be
+    parts of one product's rows.  inv_freq: f32 [rot / 2]; pos: int32 [T] or None (the places in the cache)."""
+    import torch
+    fn = "kv_append"
+    dim, T = cache.dim, k.shape[0]
+    ks, vs = _heads(k, fn, "k", None, cache.heads, dim), _heads(v, fn, "v", T, cache.heads, dim)
+    tensors = [k, v, cache.data, seqs.q_start, seqs.kv_len, seqs.table]
+    qs = outs = q_heads = 0
+    if q is not None:
+        qs, q_heads = _heads(q, fn, "q", T, None, dim), q.shape[1]
+        if q_out is None:
+            q_out = _new(stream, q, (T, q_heads, dim), torch.float32)
+        outs = _heads(q_out, fn, "q_out", T, q_heads, dim)
+        tensors += [q, q_out]
+    elif q_out is not None:
+        _refuse(-1, fn, "q_out without q")
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _f32(t, dim, fn, name)
+            tensors.append(t)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _f32(inv_freq, rot // 2, fn, "inv_freq")
+        tensors.append(inv_freq)
+    if pos is not None:
+        _i32(pos, T, fn, "pos")
+        tensors.append(pos)
+    _same_device(fn, *tensors)
+    _call(load().mq_kv_append, k, stream, cache._ref, seqs._ref, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+          _ptr(q_out), outs, T, q_heads, _ptr(q_norm), _ptr(k_norm), eps, rope, _ptr(inv_freq), rot, _ptr(pos))
+    return q_out
+
+
+def kv_read(cache, seqs, T, k=None, v=None, stream=None):
+    """(k, v): f32 [T, heads, dim], the values that the cache holds at the places of the T rows."""
+    import torch
+    shape = (T, cache.heads, cache.dim)
+    if k is None:
+        k = _new(stream, cache.data, shape, torch.float32)
+    else:
+        _f32(k, T * cache.heads * cache.dim, "kv_read", "k")
+    if v is None:
+        v = _new(stream, cache.data, shape, torch.float32)
+    else:
+        _f32(v, T * cache.heads * cache.dim, "kv_read", "v")
+    _same_device("kv_read", k, v, cache.data, seqs.q_start, seqs.kv_len, seqs.table)
+    _call(load().mq_kv_read, k, stream, cache._ref, seqs._ref, T, k.data_ptr(), v.data_ptr())
+    return k, v
+
+
+_ATTN_COUNTER_BYTES, _SAMPLE_COUNTER_BYTES = 256 * 1024, 4 << 20
+
+
+@functools.lru_cache(maxsize=4096)
+def attn_scratch_bytes(qtype, seqs, q_heads, heads, dim, max_q, max_kv):
+    return load().mq_attn_scratch_bytes(qtype, seqs, q_heads, heads, dim, max_q, max_kv)
+
+
+def attn(cache, seqs, q, scale=None, causal=True, window=0, max_q=None, max_kv=None, out=None, scratch=None,
+         stream=None):
+    """out f32 [T, q_heads, dim]: attention of q f32 [T, q_heads, dim] over the sequences' cached keys and values.
+    scale: 1 / sqrt(dim) where None.  max_q, max_kv: at least the most rows and the largest kv_len of a sequence
+    (T and the table's width where None; tighter ones divide the work better).  scratch: attn_scratch_bytes(..) bytes,
+    its first 256 KiB zero before its first use, and for calls of attn only."""
+    import torch
+    fn = "attn"
+    qs = _heads(q, fn, "q", None, None, cache.dim)
+    T, q_heads, dim = q.shape
+    B, width = seqs.table.shape
+    max_q = T if max_q is None else max_q
+    max_kv = width * cache.page_tokens if max_kv is None else max_kv
+    if out is None:
+        out = _new(stream, q, (T, q_heads, dim), torch.float32)
+    else:
+        _f32(out, T * q_heads * dim, fn, "out")
+    need = attn_scratch_bytes(cache.qtype, B, q_heads, cache.heads, dim, max_q, max_kv)
+    if scratch is None:
+        scratch = _new(stream, q, max(need, 16), torch.uint8, zero=_ATTN_COUNTER_BYTES)
+    else:
+        _buffer(scratch, need, fn, "scratch")
+    _same_device(fn, q, out, scratch, cache.data, seqs.q_start, seqs.kv_len, seqs.table)
+    _call(load().mq_attn, q, stream, cache._ref, seqs._ref, q.data_ptr(), qs, out.data_ptr(), T, q_heads,
+          dim ** -0.5 if scale is None else scale, int(causal), window, max_q, max_kv, scratch.data_ptr(),
+          _nbytes(scratch))
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def sample_scratch_bytes(M, V):
+    return load().mq_sample_scratch_bytes(M, V)
+
+
+def sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, ids=None, probs=None, scratch=None,
+           stream=None):
+    """(ids int32 [M], probs f32 [M]): a token per row of logits (f32 [M, V], rows may be parts of longer ones) by the
+    random numbers u (f32 [M], in [0, 1)) and the rows' settings (f32 [M]; top_k int32 [M]; None for none).
+    scratch: sample_scratch_bytes(M, V) bytes, its first 4 MiB zero before its first use, and for calls of sample only."""
+    import torch
+    fn = "sample"
+    if logits.dim() != 2 or logits.dtype is not torch.float32:
+        _refuse(-1, fn, f"logits must be float32 [M, V], not {logits.dtype} {tuple(logits.shape)}")
+    M, V = logits.shape
+    if logits.stride(1) != 1 and V != 1:
+        _refuse(-1, fn, f"logits: the values of a row must follow one another (strides {logits.stride()})")
+    tensors = [logits, u]
+    _f32(u, M, fn, "u")
+    for t, name in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p")):
+        if t is not None:
+            _f32(t, M, fn, name)
+            tensors.append(t)
+    if top_k is not None:
+        _i32(top_k, M, fn, "top_k")
+        tensors.append(top_k)
+    if ids is None:
+        ids = _new(stream, logits, M, torch.int32)
+    else:
+        _i32(ids, M, fn, "ids")
+    if probs is None:
+        probs = _new(stream, logits, M, torch.float32)
+    else:
+        _f32(probs, M, fn, "probs")
+    need = sample_scratch_bytes(M, V)
+    if scratch is None:
+        scratch = _new(stream, logits, max(need, 16), torch.uint8, zero=_SAMPLE_COUNTER_BYTES)
+    else:
+        _buffer(scratch, need, fn, "scratch")
+    _same_device(fn, ids, probs, scratch, *tensors)
+    _call(load().mq_sample, logits, stream, logits.data_ptr(), logits.stride(0) if M != 1 else V, M, V, _ptr(temperature),
+          _ptr(top_k), _ptr(top_p), _ptr(min_p), u.data_ptr(), ids.data_ptr(), probs.data_ptr(), scratch.data_ptr(),
+          _nbytes(scratch))
+    return ids, probs

@@ -125,6 +125,11 @@ extern "C" {
 #define MQ_SCORE_SOFTMAX 0
 #define MQ_SCORE_SIGMOID 1
 
+/* Position rotations of mq_kv_append: none; pairs of dimensions (j, j + rot / 2); pairs (2 j, 2 j + 1). */
+#define MQ_ROPE_NONE 0
+#define MQ_ROPE_HALF 1
+#define MQ_ROPE_INTERLEAVED 2
+
 /* Upper bounds accepted by the calls (sizes beyond them are MQ_ERR_SHAPE). */
 #define MQ_MAX_K 32768          /* inputs per row                 */
 #define MQ_MAX_N (1 << 24)      /* output rows                    */
@@ -132,6 +137,11 @@ extern "C" {
 #define MQ_MOE_MAX_EXPERTS 512  /* experts of a layer             */
 #define MQ_MOE_MAX_PAIRS 4096   /* M * topk of mq_moe_ffn         */
 #define MQ_MOE_MAX_TOPK 64      /* choices per token of mq_moe_route */
+#define MQ_KV_MAX_SEQS 65536    /* sequences of a call on a paged cache */
+#define MQ_KV_MAX_HEADS 256     /* heads of keys and values, and of queries */
+#define MQ_KV_MAX_PAGES (1 << 28)   /* pages of a cache           */
+#define MQ_KV_MAX_TOKENS (1 << 30)  /* cached tokens of a sequence (table_width * page_tokens) */
+#define MQ_MAX_VOCAB (1 << 20)  /* logits per row of mq_sample      */
 
 /*
  * mq_init -- select `device`, check that it is gfx950, record its compute-unit
@@ -346,6 +356,110 @@ int mq_moe_ffn(const void* Wg, const void* Wu, int gu_type, const void* Wd, int 
                const int32_t* ids, const float* wts, const float* residual, float* Y, int64_t M, int64_t topk,
                int64_t E, int64_t F, int64_t K, int act, void* scratch, size_t scratch_bytes, void* stream);
 
+/*
+ * The paged cache of keys and values that mq_kv_append writes and mq_attn reads.  `data` (device, 16-byte
+ * aligned, exactly mq_kv_cache_bytes(..) bytes) holds `pages` pages of page_tokens tokens (16, 32, 64, 128 or 256) of
+ * `heads` heads of `dim` dimensions (64, 128 or 256), in blocks of 32 dimensions of MQ_Q4_0 or MQ_Q8_0:
+ *   MQ_Q4_0  value d (code - 8),   d = f16(m / -8), m the block's value of largest magnitude (of equal ones the
+ *            first) with its sign, code = clamp(round_half_even(x / d) + 8, 0, 15)
+ *   MQ_Q8_0  value d (code - 128), d = f16(amax / 127), code = clamp(round_half_even(x / d), -127, 127) + 128
+ * (an IEEE f32 division by the f16-rounded d; a block with d = 0, stored as +0, holds zeros; a block with an infinity or a
+ * NaN, or whose d passes f16's range, reads as NaN).  Page p's chunk of head h starts at (p heads + h) chunk
+ * bytes and holds, for P = page_tokens, R = dim bits / 8 and NB = dim / 32, the sections
+ *   K codes [P][R], V codes [P R], K scales f16 [P][NB], V scales f16 [P][NB].
+ * K: dimension 32 b + 8 g + n (g < 4, n < 8) of token t is code n (4 bits: low nibble first) of the unit of
+ * 8 codes at byte t R + (g NB + b) bits.  V: dimension D' i + 16 j + c (D' = 256 / bits, c < 16) of token t is
+ * code j of the two bytes at 16 R (t / 16) + 4 ((((t % 16) / 4 * 16 + c) * 2 + t % 4 / 2) dim / D' + i) + 2 (t % 2).
+ * Pages that no token was appended to may hold anything: what no sequence's length covers is never used.
+ *
+ * mq_kv_seqs describes the sequences of a call (device arrays): sequence b has the rows q_start[b] ..
+ * q_start[b + 1] - 1 of the call (q_start: seqs + 1 numbers that do not fall, the first 0); its cache holds kv_len[b] tokens,
+ * these rows' included and last; its token j stands in page table[b][j / P] (table: [seqs][table_width]) at place
+ * j % P.  Row i of n of sequence b so has the position kv_len[b] - n + i.  A sequence may have no row, or
+ * no token.  A table entry outside [0, pages), and a position outside the table, is a page that is not there:
+ * nothing is written to it and its keys are left out.  Rows behind the last sequence's are not touched.
+ */
+typedef struct mq_kv_cache {
+    void* data;
+    int type;
+    int64_t pages, page_tokens, heads, dim;
+} mq_kv_cache;
+typedef struct mq_kv_seqs {
+    const int32_t *q_start, *kv_len, *table;
+    int64_t seqs, table_width;
+} mq_kv_seqs;
+
+/* Exact bytes of a cache; 0 for a type, page size, head count or dimension that is not served. */
+size_t mq_kv_cache_bytes(int type, int64_t pages, int64_t page_tokens, int64_t heads, int64_t dim);
+
+/*
+ * mq_kv_append -- after a layer's q, k and v products: the heads' norm, the position rotation and the append,
+ * in one launch, for T rows of q_heads, heads and heads heads of dim f32 (rows q_stride, k_stride and
+ * v_stride floats apart, multiples of 4: the three may be parts of one product's rows):
+ *   y = x w / sqrt(mean(x^2) + eps) over a head   (q with q_norm, k with k_norm: f32 [dim]; NULL: y = x)
+ *   (y1, y2) -> (y1 cos a - y2 sin a, y2 cos a + y1 sin a), a = pos * inv_freq[j]   (rope; f32 [rot / 2])
+ * over the first `rot` dimensions in the pairs that `rope` names; pos is the row's position in its cache, or
+ * pos[row] where `pos` (int32 [T]) is given.  Both are formed in f64 and rounded once to f32.  q goes to q_out (out_stride
+ * floats apart; q_out may be q with its stride), k and v (v as it is) to the cache.  q may be NULL with q_out
+ * (and q_heads 0): k and v alone.  rot: even, 2 .. dim (MQ_ROPE_NONE: inv_freq and pos NULL, rot 0).  Two rows that
+ * go to the same place of the cache leave it with codes and scales of either.
+ */
+int mq_kv_append(const mq_kv_cache* cache, const mq_kv_seqs* seqs, const float* q, int64_t q_stride, const float* k,
+                 int64_t k_stride, const float* v, int64_t v_stride, float* q_out, int64_t out_stride, int64_t T,
+                 int64_t q_heads, const float* q_norm, const float* k_norm, float eps, int rope, const float* inv_freq,
+                 int64_t rot, const int32_t* pos, void* stream);
+
+/*
+ * mq_kv_read -- the cached keys and values of T rows (of the places mq_kv_append would write them to) as the
+ * f32 values that their blocks stand for: k, v f32 [T][heads][dim] (either may be NULL); zeros where there is
+ * no page.  With q_start = the sums of kv_len it gives whole sequences.
+ */
+int mq_kv_read(const mq_kv_cache* cache, const mq_kv_seqs* seqs, int64_t T, float* k, float* v, void* stream);
+
+/*
+ * mq_attn -- attention of T rows of queries (f32, q_heads heads of dim, rows q_stride floats apart; q_heads a
+ * multiple of the cache's heads, each of which serves q_heads / heads consecutive ones) over their sequences'
+ * cached keys and values:
+ *   out[t][h] = sum_j softmax_j(scale q[t][h] . K[j]) V[j]          (out f32 [T][q_heads][dim])
+ * j runs over the cached tokens of t's sequence, with causal != 0 up to t's own position, and with window > 0
+ * (causal only) over the last `window` of these.  A row that sees no key gets zeros.  out must not overlap q.
+ * max_q, max_kv: at least the largest number of rows and the largest kv_len of a sequence (they size the grid
+ * and the scratch, so that the call reads nothing back): rows past max_q of a sequence are not computed, and
+ * a kv_len above max_kv counts as max_kv.
+ * f32 accuracy: the factors of both products are held to 22 bits or more, sums and statistics are f32.  An
+ * infinity or a NaN in a row of q, or in a key or value that it sees, makes the outputs that depend on it NaN
+ * and no other.  Deterministic.
+ * scratch: mq_attn_scratch_bytes(..) bytes (0 for sizes the call refuses), 16-byte aligned; its first 256 KiB are
+ * counters that must be zero before the first call and that every call leaves at zero; mq_attn calls that share
+ * one buffer must be ordered on one stream, and no other call's scratch may be the same memory.
+ */
+size_t mq_attn_scratch_bytes(int type, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q,
+                             int64_t max_kv);
+int mq_attn(const mq_kv_cache* cache, const mq_kv_seqs* seqs, const float* q, int64_t q_stride, float* out, int64_t T,
+            int64_t q_heads, float scale, int causal, int64_t window, int64_t max_q, int64_t max_kv, void* scratch,
+            size_t scratch_bytes, void* stream);
+
+/*
+ * mq_sample -- a token for each of M rows of V logits (f32, rows `stride` floats apart), by given random
+ * numbers u (f32 [M], in [0, 1)):
+ *   e_i = exp((l_i - max l) / temperature), the tokens in falling order of l, of equal ones the lower index first
+ *   kept: the shortest of: the first top_k tokens; of these the shortest prefix that holds top_p of their mass (sum of e);
+ *         the tokens with e_i >= min_p -- and always the first one
+ *   ids[m]: the first kept token in index order at which the sum of the kept e passes u times their total
+ *   probs[m] (or NULL): its e over that total
+ * temperature, top_p, min_p f32 [M] and top_k int32 [M], each NULL for none (1, all, 1, 0).  temperature <= 0 takes the
+ * first token (probability 1), as does a NaN; top_k <= 0 or >= V, top_p >= 1, min_p <= 0 and a NaN of these keep all.  A logit of -inf or NaN is never chosen;
+ * a row of only these gets -1 and probability 0.  +inf stands above all, several share.  Sums are 64-bit integers in units of 2^-43:
+ * the result does not depend on the order of the work, and a token with e < 2^-44 is never chosen.
+ * scratch: mq_sample_scratch_bytes(M, V) bytes (0 for sizes the call refuses), 16-byte aligned; its first 4 MiB
+ * must be zero before the first call, and every call leaves them at zero; mq_sample calls that share one
+ * buffer must be ordered on one stream, and no other call's scratch may be the same memory.
+ */
+size_t mq_sample_scratch_bytes(int64_t M, int64_t V);
+int mq_sample(const float* logits, int64_t stride, int64_t M, int64_t V, const float* temperature, const int32_t* top_k,
+              const float* top_p, const float* min_p, const float* u, int32_t* ids, float* probs, void* scratch,
+              size_t scratch_bytes, void* stream);
+
 /* Partial-tile bytes of mq_gemm_noalloc's per-device scratch array. */
 #define MQ_NOALLOC_PARTIAL_BYTES (32u << 20)
 
@@ -439,7 +553,8 @@ int mq_device_lds_bytes(void);
  *     "gemv_q8<type>" (other M <= 8 shapes that fit LDS), "mmq_kw<q4_K>" (Q4_K,
  *     GGUF payload, few output tiles: see mq_gemm_scratch_bytes), else "mmq<type>";
  *   mq_gemv_ep, mq_gemm_ep: the name of the product's kernel; mq_moe_route: "moe_route";
- *   mq_moe_ffn: "moe_one" (one token, topk <= 64) or "moe_many". */
+ *   mq_moe_ffn: "moe_one" (one token, topk <= 64) or "moe_many";
+ *   mq_kv_append: "kv_append"; mq_kv_read: "kv_read"; mq_attn: "attn"; mq_sample: "sample". */
 const char* mq_last_kernel(void);
 
 /* Library version string. */
