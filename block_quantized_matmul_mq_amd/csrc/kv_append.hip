@@ -231,38 +231,26 @@ __global__ __launch_bounds__(64 * kWaves) void kv_read_kernel(KvView c, float* k
     }
 }
 
-template <class F>
-hipError_t by_kind(int bits, int64_t dim, const F& f) {
-    if (bits == 4) {
-        if (dim == 64) f(std::integral_constant<int, 4>{}, std::integral_constant<int, 64>{});
-        else if (dim == 128) f(std::integral_constant<int, 4>{}, std::integral_constant<int, 128>{});
-        else f(std::integral_constant<int, 4>{}, std::integral_constant<int, 256>{});
-    } else {
-        if (dim == 64) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 64>{});
-        else if (dim == 128) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 128>{});
-        else f(std::integral_constant<int, 8>{}, std::integral_constant<int, 256>{});
-    }
-    return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_kv_append(const KvAppend& r, hipStream_t s, const char** name) {
     *name = "kv_append";
     const AppendArgs a = {r.cache.view, r.q, r.k, r.v, r.q_norm, r.k_norm, r.inv_freq, r.pos, r.q_out, r.q_stride,
                           r.k_stride, r.v_stride, r.out_stride, int(r.q_heads), int(r.rot), r.rope, r.eps};
-    return by_kind(r.cache.bits, r.cache.dim, [&](auto bits, auto dim) {
+    kv_kinds(r.cache.bits, r.cache.dim, [&](auto bits, auto dim) {
         hipLaunchKernelGGL((kv_append_kernel<decltype(bits)::value, decltype(dim)::value>), dim3(unsigned(r.T)),
                            dim3(64 * kWaves), 0, s, a);
     });
+    return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const KvCache& cache, int64_t T, float* k, float* v, hipStream_t s, const char** name) {
     *name = "kv_read";
-    return by_kind(cache.bits, cache.dim, [&](auto bits, auto dim) {
+    kv_kinds(cache.bits, cache.dim, [&](auto bits, auto dim) {
         hipLaunchKernelGGL((kv_read_kernel<decltype(bits)::value, decltype(dim)::value>), dim3(unsigned(T)),
                            dim3(64 * kWaves), 0, s, cache.view, k, v);
     });
+    return hipGetLastError();
 }
 
 }  // namespace mq

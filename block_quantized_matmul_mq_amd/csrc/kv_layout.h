@@ -20,6 +20,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace mq {
 
 // Sequences of a call: sequence b's tokens are rows q_start[b] .. q_start[b + 1] - 1 and its cache holds
@@ -53,6 +55,18 @@ struct KvLayout {
 
 inline int64_t kv_chunk_bytes(int bits, int64_t page_tokens, int64_t dim) {
     return 2 * page_tokens * (dim * bits / 8 + dim / 16);
+}
+
+// f(bits, dim) with the cache's kind as compile-time constants.
+template <class F>
+void kv_kinds(int bits, int64_t dim, const F& f) {
+    auto dims = [&](auto b) {
+        if (dim == 64) f(b, std::integral_constant<int, 64>{});
+        else if (dim == 128) f(b, std::integral_constant<int, 128>{});
+        else f(b, std::integral_constant<int, 256>{});
+    };
+    if (bits == 4) dims(std::integral_constant<int, 4>{});
+    else dims(std::integral_constant<int, 8>{});
 }
 
 // The token's sequence and its position in that sequence's cache; seq < 0 for a row of no sequence.
