@@ -19,7 +19,14 @@
 //     2^-E that keep it in f16's upper range (E follows the largest scale so far).
 //
 // Queries: the G = q_heads / heads query heads of a cache head and the tokens of a sequence are one list of rows
-// (token G + head), cut into tiles of 16 RT rows per wave, so that a decoded token uses the cache once for all its heads.
+// (token G + head), so that a decoded token uses the cache once for all its heads.  Two kernels:
+//   attn_few   16 rows to a workgroup, whose four waves divide the keys: bound by the cache's bytes, which go from
+//              memory to the lanes that use them, the next step's in flight.
+//   attn_many  64 or 128 rows to a workgroup, a wave 16 or 32 of them, over the same keys: bound by the vector unit, so the codes
+//              are unpacked once for the workgroup, into LDS as operands; and V with its scale, as two f16 (exact:
+//              f16 times a code), which takes the weights' multiplication and split per block off the waves for a third
+//              matrix instruction.
+// Both cut the keys of a tile into pieces over workgroups where there are few tiles, joined by the last one.
 #include <algorithm>
 
 #include "kv_layout.h"
@@ -43,6 +50,9 @@ constexpr int kCounters = 65536;         // of the scratch; cut tiles are at mos
 constexpr int kTarget = 512;             // workgroups that a call is cut into where it has fewer tiles
 constexpr int kMaxSplits = 128;
 constexpr int kMinSteps = 4;             // steps of a wave at least where a tile's keys are cut
+constexpr int kJoinRows = 4096;          // of attn_many: pieces times rows of a tile at most (LDS of the join)
+constexpr int kMinManySteps = 8;         // steps of a piece at least
+constexpr float kWeightUnit = 4096.0f;   // attn_many's weights are in units of its reciprocal: f16's normal range from 2^-26 on
 
 struct AttnArgs {
     KvView c;
@@ -51,7 +61,7 @@ struct AttnArgs {
     unsigned* counters;
     float* partial;
     int64_t q_stride;
-    int T, q_heads, group, causal, window, max_q, max_kv;
+    int T, q_heads, dim, group, causal, window, max_q, max_kv;
     int tiles, splits, chunk_steps;      // row tiles of a sequence, pieces of a tile's keys, steps of a piece
     float scale;
 };
@@ -120,17 +130,14 @@ struct Step {
     uint32_t k[2][kDwords], v[2][kDwords], ks[2][kScales], vs[2][kScales];
     bool there[2];                                      // (uniform) the tile has a page
 
-    __device__ __forceinline__ void load(const KvView& c, int seq, int head, int key0, int lane) {
+    __device__ __forceinline__ void load(const KvView& c, const int (&pages)[2], int head, int key0, int lane) {
         using L = KvLayout<BITS, D>;
         const int64_t section = int64_t(c.page_tokens) * L::kRow;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int key = key0 + 16 * t;
-            int page = __builtin_amdgcn_readfirstlane(kv_page(c, seq, key));
-            there[t] = page >= 0;
-            page = there[t] ? page : 0;
-            const int slot = key & (c.page_tokens - 1);
-            const uint8_t* p = c.data + (int64_t(page) * c.heads + head) * c.chunk;
+            there[t] = pages[t] >= 0;
+            const int slot = (key0 + 16 * t) & (c.page_tokens - 1);
+            const uint8_t* p = c.data + (int64_t(max(pages[t], 0)) * c.heads + head) * c.chunk;
             load_dwords(p + slot * L::kRow + (lane & 15) * L::kRow + (lane >> 4) * (L::kRow / 4), k[t]);
             load_dwords(p + section + slot * L::kRow + lane * (L::kRow / 4), v[t]);
             const uint8_t* s = p + 2 * section + (slot + 4 * (lane >> 4)) * (2 * L::kBlocks);
@@ -197,6 +204,21 @@ struct Rows {
         m = kNone;
         l = 0.0f;
     }
+    // The running maximum with these scores; what the weights' exponents are relative to: the stored, rounded m f, so
+    // that its rounding drops out.
+    __device__ __forceinline__ float raise(const float (&sc)[8]) {
+        float top = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
+        top = fmaxf(row_max(top), m);
+        const float base = top == kNone ? 0.0f : top * f;
+        if (__ballot(top != m) != 0) {
+            const float keep = m == kNone ? 1.0f : __builtin_amdgcn_exp2f(m * f - base);
+            l *= keep;
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j) o[j] *= keep;
+            m = top;
+        }
+        return base;
+    }
 };
 
 // Two codes from where `mask` finds them in the dword, offset taken off: 1024 + code as f16, less 1024 + offset; of codes
@@ -242,7 +264,7 @@ __device__ __forceinline__ h8 value_codes(const Step<BITS, D>& s, int j) {
 // One step for one set of rows.  MASKED: some row does not see some key.
 template <int BITS, int D, bool MASKED>
 __device__ __forceinline__ void attend(const Step<BITS, D>& s, Rows<BITS, D>& r, int key0, int lane, float unit) {
-    constexpr int kBlocks = D / 32, kTiles = D / 16;
+    constexpr int kBlocks = D / 32;
     float sc[8];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -268,17 +290,7 @@ __device__ __forceinline__ void attend(const Step<BITS, D>& s, Rows<BITS, D>& r,
             sc[i] = ok[i] ? sc[i] : kNone;
         }
     }
-    float top = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
-    top = fmaxf(row_max(top), r.m);
-    // weights relative to the stored (rounded) m f, so that its rounding drops out
-    const float base = top == kNone ? 0.0f : top * r.f;
-    if (__ballot(top != r.m) != 0) {
-        const float keep = r.m == kNone ? 1.0f : __builtin_amdgcn_exp2f(r.m * r.f - base);
-        r.l *= keep;
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) r.o[j] *= keep;
-        r.m = top;
-    }
+    const float base = r.raise(sc);
     float p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -343,240 +355,557 @@ __device__ __forceinline__ int scale_exponent(const Step<BITS, D>& s, int key0, 
     return __builtin_amdgcn_readfirstlane(top);
 }
 
-// KW: waves that share their rows and divide the keys (4: few rows; 1: each wave has rows of its own).
-template <int BITS, int D, int RT, int KW>
-__global__ __launch_bounds__(kThreads) void attn_kernel(AttnArgs a) {
-    constexpr int kTiles = D / 16;
-    constexpr int kRows = 16 * RT;
-    constexpr int kPad = 4;                                  // (rows a bank apart)
-    __shared__ float part[KW > 1 ? 2 : 1][KW > 1 ? kRows : 1][KW > 1 ? D + kPad : 1];
-    __shared__ float stat[KW > 1 ? KW : 1][2][KW > 1 ? kRows : 1];
-    __shared__ float share[KW > 1 ? kMaxSplits : 1][KW > 1 ? kRows : 1];
-    __shared__ unsigned ticket;
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    // heads vary fastest (workgroups are dealt to the XCDs in turn, whose L2 so holds few heads), later rows, which
+// A workgroup's part of the call: a tile of rows of one cache head, and of a piece of its keys.
+struct Work {
+    int head, seq, tile, split, cell;
+    int q0, n, all, rows, row0;      // the sequence's first row, its rows (also those past max_q), rows of the list, this tile's first
+    int real, len;                   // cached tokens, and as far as they count
+};
+__device__ __forceinline__ bool work_of(const AttnArgs& a, int tile_rows, Work& w) {
+    // heads vary fastest (workgroups are dealt to the XCDs in turn, whose L2 so holds few heads); later rows, which
     // see more keys, come first
     int item = blockIdx.x;
-    const int head = item % a.c.heads;
+    w.head = item % a.c.heads;
     item /= a.c.heads;
-    const int split = item % a.splits;
+    w.split = item % a.splits;
     item /= a.splits;
-    const int tile = a.tiles - 1 - item % a.tiles, seq = item / a.tiles;
-    const int q0 = a.c.q_start[seq], all = a.c.q_start[seq + 1] - q0;
-    const int n = q0 < 0 ? 0 : min(all, min(a.max_q, a.T - q0));
-    const int rows = n * a.group;
-    const int row0 = (KW > 1 ? tile : tile * kWaves + wave) * kRows;
-    if (row0 >= rows) return;                                // (KW > 1: the whole workgroup)
-    const int real = a.c.kv_len[seq], len = min(real, a.max_kv);
-    const int tok0 = row0 / a.group, tok1 = (min(row0 + kRows, rows) - 1) / a.group;
-    // keys that some row of the tile sees, and keys that every row sees
-    auto first_of = [&](int tok) { return a.window > 0 ? max(0, real - all + tok + 1 - a.window) : 0; };
-    auto last_of = [&](int tok) { return a.causal ? min(len, real - all + tok + 1) : len; };
-    const int begin = first_of(tok0) / kStep, end = (max(0, last_of(tok1)) + kStep - 1) / kStep;   // steps
-    const int full_begin = first_of(tok1), full_end = last_of(tok0);
-    int from = begin, to = end, pieces = 1;
-    if constexpr (KW > 1) {
-        pieces = max(1, (end - begin + a.chunk_steps - 1) / a.chunk_steps);
-        if (split >= pieces) return;
-        from = begin + split * a.chunk_steps;
-        to = min(end, from + a.chunk_steps);
+    w.tile = a.tiles - 1 - item % a.tiles;
+    w.seq = item / a.tiles;
+    w.cell = (w.seq * a.tiles + w.tile) * a.c.heads + w.head;
+    w.q0 = a.c.q_start[w.seq];
+    w.all = a.c.q_start[w.seq + 1] - w.q0;
+    w.n = w.q0 < 0 ? 0 : min(w.all, min(a.max_q, a.T - w.q0));
+    w.rows = w.n * a.group;
+    w.row0 = w.tile * tile_rows;
+    w.real = a.c.kv_len[w.seq];
+    w.len = min(w.real, a.max_kv);
+    return w.row0 < w.rows;
+}
+// Keys [first, last) that a token of the sequence sees.
+__device__ __forceinline__ int first_key(const AttnArgs& a, const Work& w, int tok) {
+    return a.window > 0 ? max(0, w.real - w.all + tok + 1 - a.window) : 0;
+}
+__device__ __forceinline__ int last_key(const AttnArgs& a, const Work& w, int tok) {
+    return a.causal ? min(w.len, w.real - w.all + tok + 1) : w.len;
+}
+__device__ __forceinline__ const float* query_row(const AttnArgs& a, const Work& w, int row) {
+    const int tok = row / a.group;
+    return a.q + int64_t(w.q0 + tok) * a.q_stride + int64_t(w.head * a.group + row - tok * a.group) * (a.dim);
+}
+__device__ __forceinline__ float* out_row(const AttnArgs& a, const Work& w, int row) {
+    const int tok = row / a.group;
+    return a.out + (int64_t(w.q0 + tok) * a.q_heads + w.head * a.group + row - tok * a.group) * a.dim;
+}
+__device__ __forceinline__ void pages_of(const AttnArgs& a, const Work& w, int step, int (&pages)[2]) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) pages[t] = __builtin_amdgcn_readfirstlane(kv_page(a.c, w.seq, step * kStep + 16 * t));
+}
+
+// A piece's rows to its slot of the scratch (sums, then maxima in log2 units, then sums of weights).
+template <int D, int ROWS>
+struct Slot {
+    static constexpr int kFloats = ROWS * (D + 2);
+    __amdgpu_buffer_rsrc_t rsrc;
+    __device__ __forceinline__ Slot(const AttnArgs& a, int cell) {
+        rsrc = __builtin_amdgcn_make_buffer_rsrc(a.partial + int64_t(cell) * a.splits * kFloats, 0, a.splits * kFloats * 4,
+                                                 0x00020000);
     }
-    Rows<BITS, D> r[RT];
+    __device__ __forceinline__ void put(int split, int row, const f4 (&o)[D / 16], float m, float l, int lane) const {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        const int row = min(row0 + 16 * i + (lane & 15), rows - 1);
-        const int tok = row / a.group, h = head * a.group + row - tok * a.group;
-        r[i].init(a.q + int64_t(q0 + tok) * a.q_stride + int64_t(h) * D, a.scale, lane);
-        r[i].first = first_of(tok);
-        r[i].last = last_of(tok);
-    }
-    // Weights times scales are kept in units of 2^-unit_e: the largest scale seen (2^(x - 14) at most, x its exponent
-    // field) is 2^7 then, so a later one may be 2^8 times as large before the units change.
-    constexpr int kRoom = 21, kLimit = 29, kUnset = 1000;
-    float unit = 1.0f;
-    int unit_e = kUnset;
-    Step<BITS, D> s;
-    for (int step = from + (KW > 1 ? wave : 0); step < to; step += KW) {
-        const int key0 = step * kStep;
-        s.load(a.c, seq, head, key0, lane);
-        if (__ballot(scale_bits(s) > kLimit - unit_e) != 0) {
-            const int x = scale_exponent(s, key0, len, lane);
-            if (x > kLimit - unit_e) {
-                const float by = unit_e == kUnset ? 1.0f : ldexpf(1.0f, kRoom - x - unit_e);
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int j = 0; j < kTiles; ++j) r[i].o[j] *= by;
-                unit_e = kRoom - x;
-                unit = ldexpf(1.0f, unit_e);
-            }
-        }
-        const bool full = key0 >= full_begin && key0 + kStep <= full_end && s.there[0] && s.there[1];
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            if (full) attend<BITS, D, false>(s, r[i], key0, lane, unit);
-            else attend<BITS, D, true>(s, r[i], key0, lane, unit);
+        for (int j = 0; j < D / 16; ++j)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(splitk_u4, o[j]), rsrc,
+                                                   (row * D + 16 * j + 4 * (lane >> 4)) * 4, split * kFloats * 4, kSplitkSc1);
+        if (lane < 16) {
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, m), rsrc, (ROWS * D + row) * 4,
+                                                  split * kFloats * 4, kSplitkSc1);
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, l), rsrc, (ROWS * (D + 1) + row) * 4,
+                                                  split * kFloats * 4, kSplitkSc1);
         }
     }
-    const float back = 1.0f / unit;
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        r[i].l = row_sum(r[i].l);
-        r[i].m = r[i].m == kNone ? kNone : r[i].m * r[i].f;      // log2 units from here on
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) r[i].o[j] *= BITS == 4 && (j & 1) ? back * 0.0625f : back;
-    }
-    auto out_of = [&](int row) {
-        const int tok = row / a.group, h = head * a.group + row - tok * a.group;
-        return a.out + (int64_t(q0 + tok) * a.q_heads + h) * D;
-    };
-    if constexpr (KW == 1) {
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int row = row0 + 16 * i + (lane & 15);
-            if (row >= rows) continue;
-            const float inv = r[i].l == 0.0f ? 0.0f : 1.0f / r[i].l;
-            float* out = out_of(row) + 4 * (lane >> 4);
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j) *reinterpret_cast<f4*>(out + 16 * j) = r[i].o[j] * inv;
-        }
-    } else {
-        // the waves' sums relative to the largest of their maxima, added in pairs through LDS
-#pragma unroll
-        for (int i = 0; i < RT; ++i)
-            if (lane < 16) {
-                stat[wave][0][16 * i + lane] = r[i].m;
-                stat[wave][1][16 * i + lane] = r[i].l;
-            }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            const int row = 16 * i + (lane & 15);
-            float top = kNone, sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < KW; ++w) top = fmaxf(top, stat[w][0][row]);
-#pragma unroll
-            for (int w = 0; w < KW; ++w) {
-                const float m = stat[w][0][row];
-                sum = fmaf(stat[w][1][row], m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - top), sum);
-            }
-            const float keep = r[i].m == kNone ? 0.0f : __builtin_amdgcn_exp2f(r[i].m - top);
-#pragma unroll
-            for (int j = 0; j < kTiles; ++j) r[i].o[j] = r[i].m == kNone ? f4{0, 0, 0, 0} : r[i].o[j] * keep;
-            r[i].m = top;
-            r[i].l = sum;
-        }
-        static_assert(KW == 4, "pairs");
-        for (int stage = 2; stage >= 1; stage >>= 1) {
-            if (wave >= stage && wave < 2 * stage)
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int j = 0; j < kTiles; ++j)
-                        *reinterpret_cast<f4*>(&part[wave - stage][16 * i + (lane & 15)][16 * j + 4 * (lane >> 4)]) = r[i].o[j];
-            __syncthreads();
-            if (wave < stage)
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int j = 0; j < kTiles; ++j)
-                        r[i].o[j] += *reinterpret_cast<const f4*>(&part[wave][16 * i + (lane & 15)][16 * j + 4 * (lane >> 4)]);
-            __syncthreads();
-        }
-        if (pieces == 1) {
-            if (wave == 0)
-#pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    const int row = row0 + 16 * i + (lane & 15);
-                    if (row >= rows) continue;
-                    const float inv = r[i].l == 0.0f ? 0.0f : 1.0f / r[i].l;
-                    float* out = out_of(row) + 4 * (lane >> 4);
-#pragma unroll
-                    for (int j = 0; j < kTiles; ++j) *reinterpret_cast<f4*>(out + 16 * j) = r[i].o[j] * inv;
-                }
-            return;
-        }
-        // a piece of the keys: its sums and statistics to its slot, the last piece joins them (mmq_splitk.h)
-        constexpr int kSlot = kRows * (D + 2);               // floats: sums, then maxima, then sums of weights
-        const int cell = (seq * a.tiles + tile) * a.c.heads + head;
-        float* slots = a.partial + int64_t(cell) * a.splits * kSlot;
-        const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(slots, 0, a.splits * kSlot * 4, 0x00020000);
-        const int live = min(kRows, rows - row0);
-        if (wave == 0)
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const int row = 16 * i + (lane & 15);
-                if (row >= live) continue;
-#pragma unroll
-                for (int j = 0; j < kTiles; ++j)
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(splitk_u4, r[i].o[j]), rsrc,
-                                                           (row * D + 16 * j + 4 * (lane >> 4)) * 4, split * kSlot * 4, kSplitkSc1);
-                if (lane < 16) {
-                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, r[i].m), rsrc, (kRows * D + row) * 4,
-                                                          split * kSlot * 4, kSplitkSc1);
-                    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, r[i].l), rsrc, (kRows * (D + 1) + row) * 4,
-                                                          split * kSlot * 4, kSplitkSc1);
-                }
-            }
-        if (!splitk_arrive(a.counters + cell, pieces, &ticket)) return;
+    // The last piece: every row's sums, in the order of the pieces.  share: LDS of pieces * ROWS * 2 floats.
+    __device__ __forceinline__ void join(const AttnArgs& a, const Work& w, int pieces, float* share) const {
+        const int live = min(ROWS, w.rows - w.row0);
         auto word = [&](int piece, int at) {
-            return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, at * 4, piece * kSlot * 4, kSplitkSc1));
+            return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, at * 4, piece * kFloats * 4, kSplitkSc1));
         };
-        // a piece's share of each row
-        __shared__ float weight[kMaxSplits][kRows];
-        for (int i = threadIdx.x; i < pieces * kRows; i += kThreads) {
-            const int piece = i / kRows, row = i % kRows;
+        float* const weight = share + pieces * ROWS;
+        for (int i = threadIdx.x; i < pieces * ROWS; i += kThreads) {
+            const int piece = i / ROWS, row = i % ROWS;
             if (row < live) {
-                share[piece][row] = word(piece, kRows * D + row);
-                weight[piece][row] = word(piece, kRows * (D + 1) + row);
+                share[i] = word(piece, ROWS * D + row);
+                weight[i] = word(piece, ROWS * (D + 1) + row);
             }
         }
         __syncthreads();
         if (int(threadIdx.x) < live) {
             const int row = threadIdx.x;
             float top = kNone, sum = 0.0f;
-            for (int p = 0; p < pieces; ++p) top = fmaxf(top, share[p][row]);
+            for (int p = 0; p < pieces; ++p) top = fmaxf(top, share[p * ROWS + row]);
             for (int p = 0; p < pieces; ++p) {
-                const float w = share[p][row] == kNone ? 0.0f : __builtin_amdgcn_exp2f(share[p][row] - top);
-                share[p][row] = w;
-                sum = fmaf(weight[p][row], w, sum);
+                float& s = share[p * ROWS + row];
+                s = s == kNone ? 0.0f : __builtin_amdgcn_exp2f(s - top);
+                sum = fmaf(weight[p * ROWS + row], s, sum);
             }
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            for (int p = 0; p < pieces; ++p) share[p][row] *= inv;
+            for (int p = 0; p < pieces; ++p) share[p * ROWS + row] *= inv;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < live * (D / 4); i += kThreads) {
             const int row = i / (D / 4), at = row * D + i % (D / 4) * 4;
             f4 sum = {0, 0, 0, 0};
-            for (int p = 0; p < pieces; ++p) {
-                const f4 v = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at * 4, p * kSlot * 4, kSplitkSc1));
-                const float w = share[p][row];
+            int p = 0;
+            auto batch = [&](auto n_c) {      // that many loads in flight
+                constexpr int kN = decltype(n_c)::value;
+                for (; p + kN <= pieces; p += kN) {
+                    f4 v[kN];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[j], w, sum[j]);
+                    for (int k = 0; k < kN; ++k)
+                        v[k] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at * 4, (p + k) * kFloats * 4, kSplitkSc1));
+#pragma unroll
+                    for (int k = 0; k < kN; ++k) {
+                        const float x = share[(p + k) * ROWS + row];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[k][j], x, sum[j]);
+                    }
+                }
+            };
+            batch(std::integral_constant<int, 8>{});
+            batch(std::integral_constant<int, 1>{});
+            *reinterpret_cast<f4*>(out_row(a, w, w.row0 + row) + i % (D / 4) * 4) = sum;
+        }
+    }
+};
+
+template <int D>
+__device__ __forceinline__ void write_row(float* out, const f4 (&o)[D / 16], float l, int lane) {
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) *reinterpret_cast<f4*>(out + 16 * j + 4 * (lane >> 4)) = o[j] * inv;
+}
+
+// 16 rows; the waves take steps in turn.
+template <int BITS, int D>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(AttnArgs a) {
+    constexpr int kTiles = D / 16, kRows = 16;
+    constexpr int kPad = 4;                                  // (rows a bank apart)
+    __shared__ float part[2][kRows][D + kPad];
+    __shared__ float stat[kWaves][2][kRows];
+    __shared__ float share[2 * kMaxSplits * kRows];
+    __shared__ unsigned ticket;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Work w;
+    if (!work_of(a, kRows, w)) return;
+    const int tok0 = w.row0 / a.group, tok1 = (min(w.row0 + kRows, w.rows) - 1) / a.group;
+    const int begin = first_key(a, w, tok0) / kStep, end = (max(0, last_key(a, w, tok1)) + kStep - 1) / kStep;   // steps
+    const int full_begin = first_key(a, w, tok1), full_end = last_key(a, w, tok0);   // keys that every row sees
+    const int pieces = max(1, (end - begin + a.chunk_steps - 1) / a.chunk_steps);
+    if (w.split >= pieces) return;
+    const int from = begin + w.split * a.chunk_steps, to = min(end, from + a.chunk_steps);
+    Rows<BITS, D> r;
+    const int row = min(w.row0 + (lane & 15), w.rows - 1);
+    r.init(query_row(a, w, row), a.scale, lane);
+    r.first = first_key(a, w, row / a.group);
+    r.last = last_key(a, w, row / a.group);
+    // Weights times scales are kept in units of 2^-unit_e: the largest scale seen (2^(x - 14) at most, x its exponent
+    // field) is 2^7 then, so a later one may be 2^8 times as large before the units change.
+    constexpr int kRoom = 21, kLimit = 29, kUnset = 1000;
+    float unit = 1.0f;
+    int unit_e = kUnset;
+    auto take = [&](const Step<BITS, D>& s, int step) {
+        const int key0 = step * kStep;
+        if (__ballot(scale_bits(s) > kLimit - unit_e) != 0) {
+            const int x = scale_exponent(s, key0, w.len, lane);
+            if (x > kLimit - unit_e) {
+                const float by = unit_e == kUnset ? 1.0f : ldexpf(1.0f, kRoom - x - unit_e);
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) r.o[j] *= by;
+                unit_e = kRoom - x;
+                unit = ldexpf(1.0f, unit_e);
             }
-            *reinterpret_cast<f4*>(out_of(row0 + row) + i % (D / 4) * 4) = sum;
+        }
+        if (key0 >= full_begin && key0 + kStep <= full_end && s.there[0] && s.there[1])
+            attend<BITS, D, false>(s, r, key0, lane, unit);
+        else
+            attend<BITS, D, true>(s, r, key0, lane, unit);
+    };
+    // A step's loads are in flight while the one before is worked on, its page numbers one step earlier.  Behind the
+    // last step the last one is read again: loads without a branch, so that the wait for a step leaves the next one's be.
+    int step = from + wave;
+    if (step < to) {
+        auto at = [&](int n) { return min(step + n * kWaves, to - 1); };
+        Step<BITS, D> s, t;
+        int pages[2];
+        pages_of(a, w, step, pages);
+        s.load(a.c, pages, w.head, step * kStep, lane);
+        pages_of(a, w, at(1), pages);
+        for (;;) {
+            t.load(a.c, pages, w.head, at(1) * kStep, lane);
+            pages_of(a, w, at(2), pages);
+            take(s, step);
+            step += kWaves;
+            if (step >= to) break;
+            s.load(a.c, pages, w.head, at(1) * kStep, lane);
+            pages_of(a, w, at(2), pages);
+            take(t, step);
+            step += kWaves;
+            if (step >= to) break;
+        }
+    }
+    const float back = 1.0f / unit;
+    r.l = row_sum(r.l);
+    r.m = r.m == kNone ? kNone : r.m * r.f;      // log2 units from here on
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) r.o[j] *= BITS == 4 && (j & 1) ? back * 0.0625f : back;
+    // the waves' sums relative to the largest of their maxima, added in pairs through LDS
+    if (lane < 16) {
+        stat[wave][0][lane] = r.m;
+        stat[wave][1][lane] = r.l;
+    }
+    __syncthreads();
+    {
+        const int c = lane & 15;
+        float top = kNone, sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) top = fmaxf(top, stat[v][0][c]);
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            const float m = stat[v][0][c];
+            sum = fmaf(stat[v][1][c], m == kNone ? 0.0f : __builtin_amdgcn_exp2f(m - top), sum);
+        }
+        const float keep = r.m == kNone ? 0.0f : __builtin_amdgcn_exp2f(r.m - top);
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) r.o[j] = r.m == kNone ? f4{0, 0, 0, 0} : r.o[j] * keep;
+        r.m = top;
+        r.l = sum;
+    }
+    static_assert(kWaves == 4, "pairs");
+    for (int stage = 2; stage >= 1; stage >>= 1) {
+        if (wave >= stage && wave < 2 * stage)
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+                *reinterpret_cast<f4*>(&part[wave - stage][lane & 15][16 * j + 4 * (lane >> 4)]) = r.o[j];
+        __syncthreads();
+        if (wave < stage)
+#pragma unroll
+            for (int j = 0; j < kTiles; ++j)
+                r.o[j] += *reinterpret_cast<const f4*>(&part[wave][lane & 15][16 * j + 4 * (lane >> 4)]);
+        __syncthreads();
+    }
+    const bool live = w.row0 + (lane & 15) < w.rows;
+    if (pieces == 1) {
+        if (wave == 0 && live) write_row<D>(out_row(a, w, row), r.o, r.l, lane);
+        return;
+    }
+    const Slot<D, kRows> slot(a, w.cell);
+    if (wave == 0 && live) slot.put(w.split, lane & 15, r.o, r.m, r.l, lane);
+    if (!splitk_arrive(a.counters + w.cell, pieces, &ticket)) return;
+    slot.join(a, w, pieces, share);
+}
+
+// 64 RT rows, a wave 16 RT of them; the workgroup's steps go through LDS as operands, two buffers.
+template <int BITS, int D>
+struct Staged {
+    static constexpr int kBlocks = D / 32, kTiles = D / 16;
+    u4 k[2][kBlocks][64];            // [16 keys][block][lane]
+    u4 v_hi[kTiles][64], v_lo[kTiles][64];
+    uint32_t ks[2][kBlocks * 8], vs[2][kBlocks * 8];   // scales as in the cache: [16 tokens][block]
+    uint32_t bad[kWaves];            // per wave: a value's scale is an infinity or a NaN
+    uint32_t large[kWaves];          // per wave: a scale whose products may pass f16
+};
+
+// What a thread loads of a step: half of a lane's K codes of one 16-token tile; half (two tokens) of a lane's V codes and the
+// scales of these tokens; a dword of both kinds of scales.
+template <int BITS, int D>
+struct Piece {
+    static constexpr int kHalf = D * BITS / 256, kBlocks = D / 32;
+    static constexpr int kScaleDwords = kBlocks * 16;      // of K, or V, of a step
+    uint32_t k[kHalf], v[kHalf], d[kBlocks], ks[(kScaleDwords + kThreads - 1) / kThreads], vs[(kScaleDwords + kThreads - 1) / kThreads];
+    bool there;              // (of the thread's V tokens' tile)
+
+    template <int N>
+    static __device__ __forceinline__ void load_any(const uint8_t* p, uint32_t (&v)[N]) {
+        if constexpr (N == 1) v[0] = *reinterpret_cast<const uint32_t*>(p);
+        else load_dwords(p, v);
+    }
+    __device__ __forceinline__ void load(const KvView& c, const int (&pages)[2], int head, int key0) {
+        using L = KvLayout<BITS, D>;
+        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int64_t section = int64_t(c.page_tokens) * L::kRow;
+        const uint8_t* base[2];
+        int slot[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            base[t] = c.data + (int64_t(max(pages[t], 0)) * c.heads + head) * c.chunk;
+            slot[t] = (key0 + 16 * t) & (c.page_tokens - 1);
+        }
+        {
+            const int t = wave >> 1, h = wave & 1;
+            load_any((t ? base[1] : base[0]) + (t ? slot[1] : slot[0]) * L::kRow + (lane & 15) * L::kRow + (lane >> 4) * (L::kRow / 4) + h * 4 * kHalf, k);
+        }
+        {
+            const int t = (tid >> 1) & 1, pair = tid & 1, ln = tid >> 2;
+            const uint8_t* p = t ? base[1] : base[0];
+            const int s = t ? slot[1] : slot[0];
+            there = (t ? pages[1] : pages[0]) >= 0;
+            load_any(p + section + s * L::kRow + ln * (L::kRow / 4) + pair * 4 * kHalf, v);
+            load_any(p + 2 * section + int64_t(c.page_tokens + s + 4 * (ln >> 4) + 2 * pair) * (2 * kBlocks), d);
+        }
+#pragma unroll
+        for (int i = 0; i < kScaleDwords; i += kThreads) {
+            const int at = min(i + tid, kScaleDwords - 1), t = at / (kBlocks * 8), o = at % (kBlocks * 8);
+            const uint8_t* p = (t ? base[1] : base[0]) + 2 * section + (t ? slot[1] : slot[0]) * (2 * kBlocks) + 4 * o;
+            ks[i / kThreads] = *reinterpret_cast<const uint32_t*>(p);
+            vs[i / kThreads] = *reinterpret_cast<const uint32_t*>(p + int64_t(c.page_tokens) * (2 * kBlocks));
+        }
+    }
+    // V's scale times a code is held as two f16, exactly, as long as the products stay below f16's end: scales under
+    // 2^12 (codes to 8) or 2^8 (codes to 128).  From the first larger one on they are all taken times kSmall.
+    static constexpr int kLarge = BITS == 4 ? 27 : 23;      // exponent field
+    static constexpr float kSmall = BITS == 4 ? 0x1p-4f : 0x1p-8f;
+    __device__ __forceinline__ void stage(Staged<BITS, D>& s, int key0, int len, bool small) const {
+        const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        {
+            const int t = wave >> 1, h = wave & 1;
+#pragma unroll
+            for (int b = 0; b < kBlocks / 2; ++b) s.k[t][h * (kBlocks / 2) + b][lane] = __builtin_bit_cast(u4, key_codes<BITS>(k, b));
+        }
+        const int t = (tid >> 1) & 1, pair = tid & 1, ln = tid >> 2;
+        const int key = key0 + 16 * t + 4 * (ln >> 4) + 2 * pair;
+        const bool ok0 = there && key < len, ok1 = there && key + 1 < len;
+        bool bad = false, large = false;
+        uint32_t* hi = reinterpret_cast<uint32_t*>(s.v_hi);
+        uint32_t* lo = reinterpret_cast<uint32_t*>(s.v_lo);
+        const _Float16 by = static_cast<_Float16>(small ? kSmall : 1.0f);
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            // (scale of the first token, of the second)
+            uint32_t two = __builtin_amdgcn_perm(d[kBlocks / 2 + b / 2], d[b / 2], b & 1 ? 0x07060302u : 0x05040100u);
+            const uint32_t e = two & 0x7C007C00u;
+            const bool nf0 = (e & 0xFFFFu) == 0x7C00u, nf1 = (e >> 16) == 0x7C00u;
+            bad |= (nf0 && ok0) || (nf1 && ok1);
+            two = (ok0 && !nf0 ? two & 0xFFFFu : 0u) | (ok1 && !nf1 ? two & 0xFFFF0000u : 0u);
+            large |= (two & 0x7C00u) >= (kLarge << 10) || (two & 0x7C000000u) >= (uint32_t(kLarge) << 26);
+            const h2 dd = __builtin_bit_cast(h2, two) * h2{by, by};
+#pragma unroll
+            for (int j = 2 * b; j < 2 * b + 2; ++j) {
+                constexpr int kPer = BITS == 4 ? 4 : 2;
+                const int i = j / kPer, n = j % kPer;
+                uint32_t x = v[i];
+                if (BITS == 8 ? n == 1 : n >= 2) x >>= 8;
+                const bool up = BITS == 4 && (n & 1);
+                const h2 code = __builtin_bit_cast(h2, two_codes<BITS>(x, up));
+                const h2 c = up ? code * h2{static_cast<_Float16>(0.0625f), static_cast<_Float16>(0.0625f)} : code;
+                const h2 p = c * dd;
+                const h2 q = __builtin_elementwise_fma(c, dd, -p);
+                hi[(j * 64 + ln) * 4 + (tid & 3)] = __builtin_bit_cast(uint32_t, p);
+                lo[(j * 64 + ln) * 4 + (tid & 3)] = __builtin_bit_cast(uint32_t, q);
+            }
+        }
+        const bool any_bad = __ballot(bad) != 0, any_large = __ballot(large) != 0;
+        if (lane == 0) {
+            s.bad[wave] = any_bad;
+            s.large[wave] = any_large;
+        }
+#pragma unroll
+        for (int i = 0; i < kScaleDwords; i += kThreads)
+            if (i + tid < kScaleDwords) {
+                (&s.ks[0][0])[i + tid] = ks[i / kThreads];
+                (&s.vs[0][0])[i + tid] = vs[i / kThreads];
+            }
+    }
+};
+
+// One staged step for a wave's RT sets of rows.
+template <int BITS, int D, int RT, bool MASKED>
+__device__ __forceinline__ void attend_staged(const Staged<BITS, D>& s, Rows<BITS, D> (&r)[RT], int key0, const bool (&there)[2], int lane) {
+    constexpr int kBlocks = D / 32, kTiles = D / 16;
+    float sc[RT][8];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        uint32_t d[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; i += 4) {
+            const u4 x = *reinterpret_cast<const u4*>(&s.ks[t][(lane >> 4) * (2 * kBlocks) + i]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d[i + j] = x[j];
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[i][4 * t + j] = 0.0f;
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            const h8 k = __builtin_bit_cast(h8, s.k[t][b][lane]);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                f4 acc = {0, 0, 0, 0};
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, r[i].hi[b], acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, r[i].lo[b], acc, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    sc[i][4 * t + j] = fmaf(half_of(d[j * (kBlocks / 2) + b / 2], b & 1), acc[j], sc[i][4 * t + j]);
+            }
+        }
+    }
+    h8 hi[RT], lo[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        bool ok[8];
+        if constexpr (MASKED) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int key = key0 + 16 * (j >> 2) + 4 * (lane >> 4) + (j & 3);
+                ok[j] = key >= r[i].first && key < r[i].last && there[j >> 2];
+                sc[i][j] = ok[j] ? sc[i][j] : kNone;
+            }
+        }
+        const float base = r[i].raise(sc[i]);
+        u4 h, l;
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            f2 p;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                p[k] = __builtin_amdgcn_exp2f(fmaf(sc[i][j + k], r[i].f, -base));
+                if constexpr (MASKED) p[k] = ok[j + k] ? p[k] : 0.0f;
+                r[i].l += p[k];
+            }
+            uint32_t u, w;
+            split(p, f2{kWeightUnit, kWeightUnit}, u, w);
+            h[j / 2] = u;
+            l[j / 2] = w;
+        }
+        hi[i] = __builtin_bit_cast(h8, h);
+        lo[i] = __builtin_bit_cast(h8, l);
+    }
+#pragma unroll
+    for (int j = 0; j < kTiles; ++j) {
+        const h8 vh = __builtin_bit_cast(h8, s.v_hi[j][lane]), vl = __builtin_bit_cast(h8, s.v_lo[j][lane]);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vh, hi[i], r[i].o[j], 0, 0, 0);
+            r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vh, lo[i], r[i].o[j], 0, 0, 0);
+            r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vl, hi[i], r[i].o[j], 0, 0, 0);
         }
     }
 }
 
-// How a call is cut.  Rows enough to fill the card four waves of rows at a time: KW = 1; else the waves of a
-// workgroup divide the keys, and workgroups too where there are few tiles.
+template <int BITS, int D, int RT>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArgs a) {
+    constexpr int kTiles = D / 16, kBlocks = D / 32, kRows = 64 * RT;
+    constexpr size_t kBuffers = 2 * sizeof(Staged<BITS, D>), kJoin = 2 * kJoinRows * sizeof(float);
+    __shared__ __align__(16) uint8_t memory[kBuffers > kJoin ? kBuffers : kJoin];
+    __shared__ unsigned ticket;
+    Staged<BITS, D>* const buf = reinterpret_cast<Staged<BITS, D>*>(memory);
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    Work w;
+    if (!work_of(a, kRows, w)) return;
+    const int tok0 = w.row0 / a.group, tok1 = (min(w.row0 + kRows, w.rows) - 1) / a.group;
+    const int begin = first_key(a, w, tok0) / kStep, end = (max(0, last_key(a, w, tok1)) + kStep - 1) / kStep;   // steps
+    const int pieces = max(1, (end - begin + a.chunk_steps - 1) / a.chunk_steps);
+    if (w.split >= pieces) return;
+    const int from = begin + w.split * a.chunk_steps, to = min(end, from + a.chunk_steps);
+    // the wave's own rows: keys that every one of them sees, and that any does
+    const int mine = w.row0 + wave * 16 * RT;
+    const int t0 = min(mine, w.rows - 1) / a.group, t1 = (min(mine + 16 * RT, w.rows) - 1) / a.group;
+    const int full_begin = first_key(a, w, t1), full_end = last_key(a, w, t0);
+    const int any_begin = first_key(a, w, t0), any_end = mine < w.rows ? last_key(a, w, t1) : 0;
+    Rows<BITS, D> r[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int row = min(mine + 16 * i + (lane & 15), w.rows - 1);
+        r[i].init(query_row(a, w, row), a.scale, lane);
+        r[i].first = first_key(a, w, row / a.group);
+        r[i].last = last_key(a, w, row / a.group);
+    }
+    bool small = false;
+    if (from < to) {
+        using P = Piece<BITS, D>;
+        P piece;
+        int pages[2], next[2];
+        pages_of(a, w, from, pages);
+        piece.load(a.c, pages, w.head, from * kStep);
+        piece.stage(buf[0], from * kStep, w.len, false);
+        pages_of(a, w, min(from + 1, to - 1), next);
+        __syncthreads();
+        for (int step = from; step < to; ++step) {
+            const int key0 = step * kStep;
+            Staged<BITS, D>& s = buf[(step - from) & 1];
+            if (!small && (s.large[0] | s.large[1] | s.large[2] | s.large[3])) {      // (the piece is still this step's)
+                small = true;
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int j = 0; j < kTiles; ++j) r[i].o[j] *= P::kSmall;
+                __syncthreads();
+                piece.stage(s, key0, w.len, true);
+                __syncthreads();
+            }
+            const bool there[2] = {pages[0] >= 0, pages[1] >= 0};
+            const int ahead = min(step + 1, to - 1);
+            pages[0] = next[0];
+            pages[1] = next[1];
+            piece.load(a.c, pages, w.head, ahead * kStep);
+            pages_of(a, w, min(step + 2, to - 1), next);
+            if (key0 < any_end && key0 + kStep > any_begin) {
+                if (key0 >= full_begin && key0 + kStep <= full_end && there[0] && there[1])
+                    attend_staged<BITS, D, RT, false>(s, r, key0, there, lane);
+                else
+                    attend_staged<BITS, D, RT, true>(s, r, key0, there, lane);
+                if (s.bad[0] | s.bad[1] | s.bad[2] | s.bad[3]) {      // (staged as zeros)
+                    for (int i = 0; i < kStep; ++i)
+#pragma unroll
+                        for (int b = 0; b < kBlocks; ++b) {
+                            const uint32_t d = s.vs[i >> 4][(i & 15) * (kBlocks / 2) + b / 2] >> (16 * (b & 1));
+                            if ((d & 0x7C00u) != 0x7C00u) continue;
+#pragma unroll
+                            for (int k = 0; k < RT; ++k)
+                                if (key0 + i >= r[k].first && key0 + i < r[k].last && there[i >> 4]) {
+                                    const float nan = __builtin_nanf("");
+                                    r[k].o[2 * b] = r[k].o[2 * b + 1] = f4{nan, nan, nan, nan};
+                                }
+                        }
+                }
+            }
+            piece.stage(buf[(step + 1 - from) & 1], ahead * kStep, w.len, small);
+            __syncthreads();
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        r[i].l = row_sum(r[i].l);
+        r[i].m = r[i].m == kNone ? kNone : r[i].m * r[i].f;      // log2 units from here on
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) r[i].o[j] *= small ? 1.0f / (kWeightUnit * Piece<BITS, D>::kSmall) : 1.0f / kWeightUnit;
+    }
+    const Slot<D, kRows> slot(a, w.cell);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int row = mine + 16 * i + (lane & 15);
+        if (row >= w.rows) continue;
+        if (pieces == 1) write_row<D>(out_row(a, w, row), r[i].o, r[i].l, lane);
+        else slot.put(w.split, row - w.row0, r[i].o, r[i].m, r[i].l, lane);
+    }
+    if (pieces == 1 || !splitk_arrive(a.counters + w.cell, pieces, &ticket)) return;
+    slot.join(a, w, pieces, reinterpret_cast<float*>(memory));
+}
+
+// How a call is cut: tiles of 16 rows, or of 64 or 128 where a sequence has more than 32; and the keys of a tile into pieces where
+// there are few tiles.
 struct Plan {
-    int rt, kw, tiles, splits, chunk_steps;
+    int tile_rows, tiles, splits, chunk_steps;
     int64_t blocks;
 };
-Plan plan(int64_t seqs, int64_t q_heads, int64_t heads, int64_t max_q, int64_t max_kv) {
+Plan plan(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q, int64_t max_kv) {
     Plan p;
     const int64_t rows = max_q * (q_heads / heads), steps = (max_kv + kStep - 1) / kStep + 1;
-    p.rt = rows <= 16 ? 1 : 2;
-    const int64_t wide = (rows + 16 * p.rt * kWaves - 1) / (16 * p.rt * kWaves);
-    p.kw = rows >= 16 * p.rt * kWaves && seqs * heads * wide >= kTarget ? 1 : kWaves;
-    const int64_t tiles = p.kw == 1 ? wide : (rows + 16 * p.rt - 1) / (16 * p.rt);
-    const int64_t items = seqs * heads * tiles;
-    int64_t splits = 1;
-    if (p.kw > 1 && items < kTarget)
-        splits = std::max<int64_t>(1, std::min<int64_t>({int64_t(kMaxSplits), kTarget / items, steps / (kMinSteps * kWaves)}));
+    p.tile_rows = rows <= 32 ? 16 : rows <= 64 ? 64 : 128;
+    const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows, items = seqs * heads * tiles;
+    const int64_t most = p.tile_rows == 16 ? kMaxSplits : kJoinRows / p.tile_rows;
+    const int64_t least = p.tile_rows == 16 ? kMinSteps * kWaves : kMinManySteps;
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({most, kTarget / items, steps / least}));
     p.chunk_steps = int((steps + splits - 1) / splits);
     p.splits = int((steps + p.chunk_steps - 1) / p.chunk_steps);
     p.tiles = int(tiles);
@@ -584,22 +913,22 @@ Plan plan(int64_t seqs, int64_t q_heads, int64_t heads, int64_t max_q, int64_t m
     return p;
 }
 
-size_t slot_floats(const Plan& p, int64_t dim) { return size_t(16 * p.rt) * size_t(dim + 2); }
+size_t slot_floats(const Plan& p, int64_t dim) { return size_t(p.tile_rows) * size_t(dim + 2); }
 
 }  // namespace
 
 size_t attn_scratch_bytes(int, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q, int64_t max_kv) {
-    const Plan p = plan(seqs, q_heads, heads, max_q, max_kv);
+    const Plan p = plan(seqs, q_heads, heads, dim, max_q, max_kv);
     return size_t(kCounters) * 4 + (p.splits > 1 ? size_t(p.blocks) * slot_floats(p, dim) * 4 : 0);
 }
 
 bool attn_fits(int64_t seqs, int64_t q_heads, int64_t heads, int64_t max_q, int64_t max_kv) {
-    return plan(seqs, q_heads, heads, max_q, max_kv).blocks < (int64_t(1) << 31);
+    return plan(seqs, q_heads, heads, 64, max_q, max_kv).blocks < (int64_t(1) << 31);
 }
 
 hipError_t launch_attn(const Attn& r, hipStream_t s, const char** name) {
-    const Plan p = plan(r.cache.view.seqs, r.q_heads, r.cache.view.heads, r.max_q, r.max_kv);
-    *name = p.kw == 1 ? "attn_rows" : p.splits > 1 ? "attn_split" : "attn_keys";
+    const Plan p = plan(r.cache.view.seqs, r.q_heads, r.cache.view.heads, r.cache.dim, r.max_q, r.max_kv);
+    *name = p.tile_rows == 16 ? "attn_few" : "attn_many";
     AttnArgs a;
     a.c = r.cache.view;
     a.q = r.q;
@@ -609,6 +938,7 @@ hipError_t launch_attn(const Attn& r, hipStream_t s, const char** name) {
     a.q_stride = r.q_stride;
     a.T = int(r.T);
     a.q_heads = int(r.q_heads);
+    a.dim = int(r.cache.dim);
     a.group = int(r.q_heads / r.cache.view.heads);
     a.causal = r.causal;
     a.window = int(r.window);
@@ -619,12 +949,12 @@ hipError_t launch_attn(const Attn& r, hipStream_t s, const char** name) {
     a.chunk_steps = p.chunk_steps;
     a.scale = r.scale;
     auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(unsigned(p.blocks)), dim3(kThreads), 0, s, a); };
-    auto shape = [&](auto bits, auto dim) {
+    kv_kinds(r.cache.bits, r.cache.dim, [&](auto bits, auto dim) {
         constexpr int kB = decltype(bits)::value, kD = decltype(dim)::value;
-        if (p.kw == 1) p.rt == 1 ? run(attn_kernel<kB, kD, 1, 1>) : run(attn_kernel<kB, kD, 2, 1>);
-        else p.rt == 1 ? run(attn_kernel<kB, kD, 1, kWaves>) : run(attn_kernel<kB, kD, 2, kWaves>);
-    };
-    kv_kinds(r.cache.bits, r.cache.dim, shape);
+        if (p.tile_rows == 16) run(attn_few_kernel<kB, kD>);
+        else if (p.tile_rows == 64) run(attn_many_kernel<kB, kD, 1>);
+        else run(attn_many_kernel<kB, kD, 2>);
+    });
     return hipGetLastError();
 }
 
