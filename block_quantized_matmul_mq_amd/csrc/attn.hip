@@ -47,12 +47,14 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 32;                // keys of a step
 constexpr int kCounters = 65536;         // of the scratch; cut tiles are at most kTarget
-constexpr int kTarget = 512;             // workgroups that a call is cut into where it has fewer tiles
+constexpr int kTarget = 512;             // workgroups that a call is cut into where it has fewer tiles (half of it: of 512 threads)
 constexpr int kMaxSplits = 128;
 constexpr int kMinSteps = 4;             // steps of a wave at least where a tile's keys are cut
 constexpr int kJoinRows = 4096;          // of attn_many: pieces times rows of a tile at most (LDS of the join)
 constexpr int kMinManySteps = 8;         // steps of a piece at least
-constexpr float kWeightUnit = 4096.0f;   // attn_many's weights are in units of its reciprocal: f16's normal range from 2^-26 on
+// attn_many's weights are in units of 2^-kManyUnit, f16's normal range from 2^-20 on, and up to 2^kManySlack
+constexpr float kManyUnit = 6.0f;
+constexpr int kManySlack = 8;
 
 struct AttnArgs {
     KvView c;
@@ -110,17 +112,27 @@ constexpr float kNone = -__builtin_inff();
 
 typedef float f2 __attribute__((ext_vector_type(2)));
 
-// Two values as f16 pairs, hi + lo to 22 bits: hi rounded from the f32 values w, lo from the exact rest p d - hi (w = p d
-// rounded).  The empty asm keeps hi one value: formed a second time for the rest, by a fused instruction from the
-// exact product, it would round the other way once in some thousand values and the sum miss by 2^-11.
+// Two values p d as f16 pairs, hi + lo to 22 bits: hi rounded from the f32 products, lo from the exact rest p d - hi.  The
+// empty asm keeps hi one value: formed a second time for the rest, by a fused instruction from the exact product,
+// it would round the other way once in some thousand values and the sum miss by 2^-11.
 __device__ __forceinline__ void split(f2 p, f2 d, uint32_t& hi, uint32_t& lo) {
-    const f2 w = p * d;
-    hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(w, h2));
+    hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{p[0] * d[0], p[1] * d[1]}, h2));
     asm("" : "+v"(hi));
     const h2 h = __builtin_bit_cast(h2, hi);
     const f2 rest = {fmaf(p[0], d[0], -static_cast<float>(h[0])), fmaf(p[1], d[1], -static_cast<float>(h[1]))};
     lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, h2));
 }
+
+// The bits of two codes in a dword, in registers of the vector unit: its AND-OR takes one scalar operand only.
+struct Masks {
+    uint32_t low, up;
+    template <int BITS>
+    static __device__ __forceinline__ Masks make() {
+        Masks m = {BITS == 8 ? 0x00FF00FFu : 0x000F000Fu, 0x00F000F0u};
+        asm("" : "+v"(m.low), "+v"(m.up));
+        return m;
+    }
+};
 
 // The keys and values of one step as they lie in the cache: two tiles of 16 tokens.
 template <int BITS, int D>
@@ -155,7 +167,7 @@ struct Rows {
     h8 hi[kBlocks], lo[kBlocks];
     f4 o[kTiles];
     float f;                        // score in log2 units per unit of the accumulated sums
-    float m, l;                     // the largest sum so far (or none), this lane's part of the sum of weights
+    float m, l;                     // the score (log2 units) that weights are relative to, or none; this lane's part of the sum of weights
     int first, last;                // keys first .. last - 1 are seen
 
     // q: the row's f32 values, of which this lane has 8 in each block
@@ -180,7 +192,7 @@ struct Rows {
         // then 2^-28 of the largest)
         int e = 0;
         if (top > 0.0f && top <= 3.4028235e38f) e = 14 - (ilogbf(top) + 1);
-        f = ldexpf(fabsf(scale) * 1.44269504088896341f, -e);
+        f = fmaxf(ldexpf(fabsf(scale) * 1.44269504088896341f, -e), 0x1p-126f);     // (not 0: a masked score times f stays -inf)
         constexpr int kOrder4[8] = {0, 4, 1, 5, 2, 6, 3, 7}, kOrder8[8] = {0, 2, 1, 3, 4, 6, 5, 7};
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
@@ -204,42 +216,44 @@ struct Rows {
         m = kNone;
         l = 0.0f;
     }
-    // The running maximum with these scores; what the weights' exponents are relative to: the stored, rounded m f, so
-    // that its rounding drops out.
+    // The score that weights are relative to follows these scores' maximum where that passes it by more than SLACK (a weight
+    // may so be up to 2^SLACK, and the sums are rescaled in few steps only).  It is a rounded product, but the same in every
+    // weight's exponent, so that its rounding drops out.
+    template <int SLACK>
     __device__ __forceinline__ float raise(const float (&sc)[8]) {
         float top = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
-        top = fmaxf(row_max(top), m);
-        const float base = top == kNone ? 0.0f : top * f;
-        if (__ballot(top != m) != 0) {
-            const float keep = m == kNone ? 1.0f : __builtin_amdgcn_exp2f(m * f - base);
+        top = row_max(top);
+        const bool up = fmaf(top, f, -m) > float(SLACK);      // (no score seen, none before: NaN, no)
+        if (__ballot(up) != 0) {
+            const float to = up ? top * f : m;
+            const float keep = !up || m == kNone ? 1.0f : __builtin_amdgcn_exp2f(m - to);
             l *= keep;
 #pragma unroll
             for (int j = 0; j < kTiles; ++j) o[j] *= keep;
-            m = top;
+            m = to;
         }
-        return base;
+        return m == kNone ? 0.0f : m;
     }
 };
 
-// Two codes from where `mask` finds them in the dword, offset taken off: 1024 + code as f16, less 1024 + offset; of codes
+// Two codes from where the mask finds them in the dword, offset taken off: 1024 + code as f16, less 1024 + offset; of codes
 // that lie four bits up, 16 times the code less 16 times the offset.
 template <int BITS>
-__device__ __forceinline__ uint32_t two_codes(uint32_t w, bool up) {
-    const uint32_t mask = BITS == 8 ? 0x00FF00FFu : up ? 0x00F000F0u : 0x000F000Fu;
+__device__ __forceinline__ uint32_t two_codes(const Masks& m, uint32_t w, bool up) {
     const _Float16 off = static_cast<_Float16>(BITS == 8 || up ? -1152.0f : -1032.0f);
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (w & mask) | 0x64006400u) + h2{off, off});
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, (w & (up ? m.up : m.low)) | 0x64006400u) + h2{off, off});
 }
 
 // The codes of K's block b as a matrix operand.
 template <int BITS, int N>
-__device__ __forceinline__ h8 key_codes(const uint32_t (&k)[N], int b) {
+__device__ __forceinline__ h8 key_codes(const Masks& m, const uint32_t (&k)[N], int b) {
     u4 a;
     if constexpr (BITS == 4) {
         const uint32_t w = k[b], x = w >> 8;
-        a = u4{two_codes<4>(w, false), two_codes<4>(w, true), two_codes<4>(x, false), two_codes<4>(x, true)};
+        a = u4{two_codes<4>(m, w, false), two_codes<4>(m, w, true), two_codes<4>(m, x, false), two_codes<4>(m, x, true)};
     } else {
         const uint32_t w = k[2 * b], x = k[2 * b + 1];
-        a = u4{two_codes<8>(w, false), two_codes<8>(w >> 8, false), two_codes<8>(x, false), two_codes<8>(x >> 8, false)};
+        a = u4{two_codes<8>(m, w, false), two_codes<8>(m, w >> 8, false), two_codes<8>(m, x, false), two_codes<8>(m, x >> 8, false)};
     }
     return __builtin_bit_cast(h8, a);
 }
@@ -247,7 +261,7 @@ __device__ __forceinline__ h8 key_codes(const uint32_t (&k)[N], int b) {
 // Codes of V's dimensions 16 j .. 16 j + 15 (of which this lane supplies one) for the step's 32 keys; for 4 bits and odd
 // j, 16 times the codes.
 template <int BITS, int D>
-__device__ __forceinline__ h8 value_codes(const Step<BITS, D>& s, int j) {
+__device__ __forceinline__ h8 value_codes(const Masks& m, const Step<BITS, D>& s, int j) {
     constexpr int kPer = BITS == 4 ? 4 : 2;                 // 16s of dimensions in a unit
     constexpr int kUnits = KvLayout<BITS, D>::kUnits;
     const int i = j / kPer, n = j % kPer;
@@ -256,14 +270,14 @@ __device__ __forceinline__ h8 value_codes(const Step<BITS, D>& s, int j) {
     for (int p = 0; p < 4; ++p) {
         uint32_t w = s.v[p >> 1][(p & 1) * kUnits + i];
         if (BITS == 8 ? n == 1 : n >= 2) w >>= 8;
-        a[p] = two_codes<BITS>(w, BITS == 4 && (n & 1));
+        a[p] = two_codes<BITS>(m, w, BITS == 4 && (n & 1));
     }
     return __builtin_bit_cast(h8, a);
 }
 
-// One step for one set of rows.  MASKED: some row does not see some key.
-template <int BITS, int D, bool MASKED>
-__device__ __forceinline__ void attend(const Step<BITS, D>& s, Rows<BITS, D>& r, int key0, int lane, float unit) {
+// One step for one set of rows.  full: every row sees every key.
+template <int BITS, int D>
+__device__ __forceinline__ void attend(const Masks& masks, const Step<BITS, D>& s, Rows<BITS, D>& r, int key0, bool full, int lane, float unit_e) {
     constexpr int kBlocks = D / 32;
     float sc[8];
 #pragma unroll
@@ -272,7 +286,7 @@ __device__ __forceinline__ void attend(const Step<BITS, D>& s, Rows<BITS, D>& r,
         for (int i = 0; i < 4; ++i) sc[4 * t + i] = 0.0f;
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
-            const h8 a = key_codes<BITS>(s.k[t], b);
+            const h8 a = key_codes<BITS>(masks, s.k[t], b);
             f4 acc = {0, 0, 0, 0};
             acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, r.hi[b], acc, 0, 0, 0);
             acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, r.lo[b], acc, 0, 0, 0);
@@ -281,23 +295,35 @@ __device__ __forceinline__ void attend(const Step<BITS, D>& s, Rows<BITS, D>& r,
                 sc[4 * t + i] = fmaf(half_of(s.ks[t][i * (kBlocks / 2) + b / 2], b & 1), acc[i], sc[4 * t + i]);
         }
     }
-    bool ok[8];
-    if constexpr (MASKED) {
+    uint32_t seen = 0xFF;
+    if (!full) {
+        seen = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int key = key0 + 16 * (i >> 2) + 4 * (lane >> 4) + (i & 3);
-            ok[i] = key >= r.first && key < r.last && s.there[i >> 2];
-            sc[i] = ok[i] ? sc[i] : kNone;
+            const bool ok = key >= r.first && key < r.last && s.there[i >> 2];
+            sc[i] = ok ? sc[i] : kNone;
+            seen |= uint32_t(ok) << i;
         }
     }
-    const float base = r.raise(sc);
+    const float base = r.template raise<4>(sc) - unit_e;
     float p[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], r.f, -base));
-        if constexpr (MASKED) p[i] = ok[i] ? p[i] : 0.0f;
         r.l += p[i];
-        p[i] *= unit;
+    }
+    // V's scales, 0 of keys that the row does not see (whose bits may be anything)
+    uint32_t vs[8][kBlocks / 2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int b = 0; b < kBlocks / 2; ++b) vs[i][b] = s.vs[i >> 2][(i & 3) * (kBlocks / 2) + b];
+    if (!full) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int b = 0; b < kBlocks / 2; ++b) vs[i][b] = seen >> i & 1 ? vs[i][b] : 0;
     }
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b) {
@@ -307,9 +333,7 @@ __device__ __forceinline__ void attend(const Step<BITS, D>& s, Rows<BITS, D>& r,
             f2 d;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                uint32_t v = s.vs[i >> 2][((i + j) & 3) * (kBlocks / 2) + b / 2];
-                if constexpr (MASKED) v = ok[i + j] ? v : 0;
-                d[j] = half_of(v, b & 1);
+                d[j] = half_of(vs[i + j][b / 2], b & 1);
             }
             uint32_t u, w;
             split(f2{p[i], p[i + 1]}, d, u, w);
@@ -319,24 +343,27 @@ __device__ __forceinline__ void attend(const Step<BITS, D>& s, Rows<BITS, D>& r,
         const h8 hi = __builtin_bit_cast(h8, h), lo = __builtin_bit_cast(h8, l);
 #pragma unroll
         for (int j = 2 * b; j < 2 * b + 2; ++j) {
-            const h8 a = value_codes<BITS, D>(s, j);
+            const h8 a = value_codes<BITS, D>(masks, s, j);
             r.o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, hi, r.o[j], 0, 0, 0);
             r.o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, lo, r.o[j], 0, 0, 0);
         }
     }
 }
 
-// A bound on the exponent field (f16) of V's scales of the step, the bits of all of them together: quick, and
-// at most one less than a power of two.
+// The largest magnitude of V's scales in this lane, a NaN where one is.
 template <int BITS, int D>
-__device__ __forceinline__ int scale_bits(const Step<BITS, D>& s) {
-    uint32_t all = 0;
+__device__ __forceinline__ float scale_top(const Step<BITS, D>& s) {
+    auto at = [&](int i) { return __builtin_bit_cast(h2, s.vs[i / Step<BITS, D>::kScales][i % Step<BITS, D>::kScales]); };
+    h2 hi = at(0), lo = hi;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < Step<BITS, D>::kScales; ++i) all |= s.vs[t][i];
-    all |= all >> 16;
-    return (all >> 10) & 31;
+    for (int i = 1; i + 1 < 2 * Step<BITS, D>::kScales; i += 2) {      // (two a time: v_pk_maximum3_f16)
+        hi = __builtin_elementwise_maximum(__builtin_elementwise_maximum(hi, at(i)), at(i + 1));
+        lo = __builtin_elementwise_minimum(__builtin_elementwise_minimum(lo, at(i)), at(i + 1));
+    }
+    hi = __builtin_elementwise_maximum(hi, at(2 * Step<BITS, D>::kScales - 1));
+    lo = __builtin_elementwise_minimum(lo, at(2 * Step<BITS, D>::kScales - 1));
+    hi = __builtin_elementwise_maximum(hi, -lo);
+    return __builtin_elementwise_maximum(static_cast<float>(hi[0]), static_cast<float>(hi[1]));
 }
 // The largest exponent field of the finite scales of the sequence's tokens in the step; uniform.
 template <int BITS, int D>
@@ -402,7 +429,7 @@ __device__ __forceinline__ void pages_of(const AttnArgs& a, const Work& w, int s
 }
 
 // A piece's rows to its slot of the scratch (sums, then maxima in log2 units, then sums of weights).
-template <int D, int ROWS>
+template <int D, int ROWS, int NT>
 struct Slot {
     static constexpr int kFloats = ROWS * (D + 2);
     __amdgpu_buffer_rsrc_t rsrc;
@@ -429,7 +456,7 @@ struct Slot {
             return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, at * 4, piece * kFloats * 4, kSplitkSc1));
         };
         float* const weight = share + pieces * ROWS;
-        for (int i = threadIdx.x; i < pieces * ROWS; i += kThreads) {
+        for (int i = threadIdx.x; i < pieces * ROWS; i += NT) {
             const int piece = i / ROWS, row = i % ROWS;
             if (row < live) {
                 share[i] = word(piece, ROWS * D + row);
@@ -450,7 +477,7 @@ struct Slot {
             for (int p = 0; p < pieces; ++p) share[p * ROWS + row] *= inv;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < live * (D / 4); i += kThreads) {
+        for (int i = threadIdx.x; i < live * (D / 4); i += NT) {
             const int row = i / (D / 4), at = row * D + i % (D / 4) * 4;
             f4 sum = {0, 0, 0, 0};
             int p = 0;
@@ -507,27 +534,28 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
     r.init(query_row(a, w, row), a.scale, lane);
     r.first = first_key(a, w, row / a.group);
     r.last = last_key(a, w, row / a.group);
-    // Weights times scales are kept in units of 2^-unit_e: the largest scale seen (2^(x - 14) at most, x its exponent
-    // field) is 2^7 then, so a later one may be 2^8 times as large before the units change.
-    constexpr int kRoom = 21, kLimit = 29, kUnset = 1000;
-    float unit = 1.0f;
-    int unit_e = kUnset;
+    // Weights are kept in units of 2^-unit_e, so that they stay in f16's upper range times V's scales: the largest scale
+    // seen (2^(x - 14) at most, x its exponent field) is 2^7 then; a weight to 2^4 and a scale 2^4 times as large fit
+    // before the units change.
+    constexpr int kRoom = 21;
+    int unit_e = 0;
+    float unit_top = -1.0f;          // scales to this fit
+    const Masks masks = Masks::make<BITS>();
     auto take = [&](const Step<BITS, D>& s, int step) {
         const int key0 = step * kStep;
-        if (__ballot(scale_bits(s) > kLimit - unit_e) != 0) {
+        if (__ballot(!(scale_top(s) <= unit_top)) != 0) {
             const int x = scale_exponent(s, key0, w.len, lane);
-            if (x > kLimit - unit_e) {
-                const float by = unit_e == kUnset ? 1.0f : ldexpf(1.0f, kRoom - x - unit_e);
+            if (unit_top < 0.0f || x > kRoom - unit_e + 4) {
+                const float by = ldexpf(1.0f, kRoom - x - unit_e);
+                r.l *= by;
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j) r.o[j] *= by;
                 unit_e = kRoom - x;
-                unit = ldexpf(1.0f, unit_e);
+                unit_top = ldexpf(1.0f, x - 14 + 4);
             }
         }
-        if (key0 >= full_begin && key0 + kStep <= full_end && s.there[0] && s.there[1])
-            attend<BITS, D, false>(s, r, key0, lane, unit);
-        else
-            attend<BITS, D, true>(s, r, key0, lane, unit);
+        const bool full = key0 >= full_begin && key0 + kStep <= full_end && s.there[0] && s.there[1];
+        attend<BITS, D>(masks, s, r, key0, full, lane, float(unit_e));
     };
     // A step's loads are in flight while the one before is worked on, its page numbers one step earlier.  Behind the
     // last step the last one is read again: loads without a branch, so that the wait for a step leaves the next one's be.
@@ -552,9 +580,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
             if (step >= to) break;
         }
     }
-    const float back = 1.0f / unit;
-    r.l = row_sum(r.l);
-    r.m = r.m == kNone ? kNone : r.m * r.f;      // log2 units from here on
+    const float back = ldexpf(1.0f, -unit_e);
+    r.l = row_sum(r.l) * back;
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) r.o[j] *= BITS == 4 && (j & 1) ? back * 0.0625f : back;
     // the waves' sums relative to the largest of their maxima, added in pairs through LDS
@@ -597,41 +624,50 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
         if (wave == 0 && live) write_row<D>(out_row(a, w, row), r.o, r.l, lane);
         return;
     }
-    const Slot<D, kRows> slot(a, w.cell);
+    const Slot<D, kRows, kThreads> slot(a, w.cell);
     if (wave == 0 && live) slot.put(w.split, lane & 15, r.o, r.m, r.l, lane);
     if (!splitk_arrive(a.counters + w.cell, pieces, &ticket)) return;
     slot.join(a, w, pieces, share);
 }
 
-// 64 RT rows, a wave 16 RT of them; the workgroup's steps go through LDS as operands, two buffers.
-template <int BITS, int D>
+// NT / 64 waves, each with 16 RT rows; the workgroup's steps go through LDS as operands, two buffers.
+template <int BITS, int D, int NT>
 struct Staged {
     static constexpr int kBlocks = D / 32, kTiles = D / 16;
     u4 k[2][kBlocks][64];            // [16 keys][block][lane]
     u4 v_hi[kTiles][64], v_lo[kTiles][64];
-    uint32_t ks[2][kBlocks * 8], vs[2][kBlocks * 8];   // scales as in the cache: [16 tokens][block]
-    uint32_t bad[kWaves];            // per wave: a value's scale is an infinity or a NaN
-    uint32_t large[kWaves];          // per wave: a scale whose products may pass f16
+    float ks[2][kBlocks][16];        // K's scales
+    uint32_t vs[2][kBlocks * 8];     // V's, as in the cache: [16 tokens][block]
+    uint32_t special[NT / 64], bad[NT / 64], large[NT / 64];   // per wave, of V's scales: see Piece::stage
 };
 
-// What a thread loads of a step: half of a lane's K codes of one 16-token tile; half (two tokens) of a lane's V codes and the
-// scales of these tokens; a dword of both kinds of scales.
-template <int BITS, int D>
+// What a thread loads of a step and lays into LDS: K's codes of some blocks of a lane; V's of some units of a lane and of two tokens,
+// with these tokens' scales; a dword of both kinds of scales.  (Where a step has less than that for every thread, the first ones.)
+template <int BITS, int D, int NT>
 struct Piece {
-    static constexpr int kHalf = D * BITS / 256, kBlocks = D / 32;
+    using L = KvLayout<BITS, D>;
+    static constexpr int kBlocks = D / 32, kUnits = L::kUnits;
+    static constexpr int kOps = 128 * kBlocks > NT ? 128 * kBlocks / NT : 1, kKThreads = 128 * kBlocks / kOps;
+    static constexpr int kVs = 256 * kUnits > NT ? 256 * kUnits / NT : 1, kVThreads = 256 * kUnits / kVs;
+    static constexpr int kDs = BITS == 4 ? kVs : (kVs + 1) / 2;
     static constexpr int kScaleDwords = kBlocks * 16;      // of K, or V, of a step
-    uint32_t k[kHalf], v[kHalf], d[kBlocks], ks[(kScaleDwords + kThreads - 1) / kThreads], vs[(kScaleDwords + kThreads - 1) / kThreads];
-    bool there;              // (of the thread's V tokens' tile)
+    static_assert(kScaleDwords <= NT && kKThreads <= NT && kVThreads <= NT, "one piece a thread");
+    uint32_t k[kOps * BITS / 4], v[kVs], d[2 * kDs], ks, vs;
 
     template <int N>
-    static __device__ __forceinline__ void load_any(const uint8_t* p, uint32_t (&v)[N]) {
-        if constexpr (N == 1) v[0] = *reinterpret_cast<const uint32_t*>(p);
-        else load_dwords(p, v);
+    static __device__ __forceinline__ void load_any(const uint8_t* p, uint32_t* v) {
+        if constexpr (N >= 4) {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) *reinterpret_cast<u4*>(v + i) = *reinterpret_cast<const u4*>(p + 4 * i);
+        } else if constexpr (N == 2) {
+            *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+        } else {
+            *v = *reinterpret_cast<const uint32_t*>(p);
+        }
     }
     __device__ __forceinline__ void load(const KvView& c, const int (&pages)[2], int head, int key0) {
-        using L = KvLayout<BITS, D>;
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        const int64_t section = int64_t(c.page_tokens) * L::kRow;
+        const int section = c.page_tokens * L::kRow;
         const uint8_t* base[2];
         int slot[2];
 #pragma unroll
@@ -639,128 +675,176 @@ struct Piece {
             base[t] = c.data + (int64_t(max(pages[t], 0)) * c.heads + head) * c.chunk;
             slot[t] = (key0 + 16 * t) & (c.page_tokens - 1);
         }
-        {
-            const int t = wave >> 1, h = wave & 1;
-            load_any((t ? base[1] : base[0]) + (t ? slot[1] : slot[0]) * L::kRow + (lane & 15) * L::kRow + (lane >> 4) * (L::kRow / 4) + h * 4 * kHalf, k);
+        if (kKThreads == NT || tid < kKThreads) {
+            constexpr int kPer = kBlocks / kOps;
+            const int t = wave / kPer, h = wave % kPer;
+            load_any<kOps * BITS / 4>((t ? base[1] : base[0]) + (t ? slot[1] : slot[0]) * L::kRow + (lane & 15) * L::kRow +
+                                          (lane >> 4) * (L::kRow / 4) + h * (kOps * BITS), k);
         }
-        {
-            const int t = (tid >> 1) & 1, pair = tid & 1, ln = tid >> 2;
-            const uint8_t* p = t ? base[1] : base[0];
+        if (kVThreads == NT || tid < kVThreads) {
+            const int t = (tid >> 1) & 1, pair = tid & 1, ln = (tid >> 2) & 63, i0 = (tid >> 8) * kVs;
+            const uint8_t* p = (t ? base[1] : base[0]) + section;
             const int s = t ? slot[1] : slot[0];
-            there = (t ? pages[1] : pages[0]) >= 0;
-            load_any(p + section + s * L::kRow + ln * (L::kRow / 4) + pair * 4 * kHalf, v);
-            load_any(p + 2 * section + int64_t(c.page_tokens + s + 4 * (ln >> 4) + 2 * pair) * (2 * kBlocks), d);
+            load_any<kVs>(p + s * L::kRow + ln * (L::kRow / 4) + (pair * kUnits + i0) * 4, v);
+            const uint8_t* q = p + section + (c.page_tokens + s + 4 * (ln >> 4) + 2 * pair) * (2 * kBlocks) + (BITS == 4 ? i0 : i0 / 2) * 4;
+            load_any<kDs>(q, d);
+            load_any<kDs>(q + 2 * kBlocks, d + kDs);
         }
-#pragma unroll
-        for (int i = 0; i < kScaleDwords; i += kThreads) {
-            const int at = min(i + tid, kScaleDwords - 1), t = at / (kBlocks * 8), o = at % (kBlocks * 8);
+        if (tid < kScaleDwords) {
+            const int t = tid / (kBlocks * 8), o = tid % (kBlocks * 8);
             const uint8_t* p = (t ? base[1] : base[0]) + 2 * section + (t ? slot[1] : slot[0]) * (2 * kBlocks) + 4 * o;
-            ks[i / kThreads] = *reinterpret_cast<const uint32_t*>(p);
-            vs[i / kThreads] = *reinterpret_cast<const uint32_t*>(p + int64_t(c.page_tokens) * (2 * kBlocks));
+            ks = *reinterpret_cast<const uint32_t*>(p);
+            vs = *reinterpret_cast<const uint32_t*>(p + c.page_tokens * (2 * kBlocks));
         }
     }
-    // V's scale times a code is held as two f16, exactly, as long as the products stay below f16's end: scales under
-    // 2^12 (codes to 8) or 2^8 (codes to 128).  From the first larger one on they are all taken times kSmall.
-    static constexpr int kLarge = BITS == 4 ? 27 : 23;      // exponent field
-    static constexpr float kSmall = BITS == 4 ? 0x1p-4f : 0x1p-8f;
-    __device__ __forceinline__ void stage(Staged<BITS, D>& s, int key0, int len, bool small) const {
+    // V's scale times a code (for 4 bits and odd 16s of dimensions 16 times the code) is held as two f16, exactly, as long as the
+    // products stay below f16's end: scales under 2^8 (times 128).  The quick form (PRECISE false) says in `special` where a
+    // scale is an infinity, a NaN or larger; its products of that step are then made again by the other form, which takes what is not
+    // finite as 0 (in `bad`) and says in `large` where a finite one is larger; from the first of those on
+    // (`small`) all products are taken times kSmall, to 2^-24 of f16's range (2^-27 of the scale that asked for it).
+    static constexpr int kLarge = 23;                       // exponent field
+    static constexpr float kSmall = 0x1p-8f;
+    template <bool PRECISE>
+    __device__ __forceinline__ void stage(const Masks& masks, Staged<BITS, D, NT>& s, const int (&pages)[2], int key0, int len, bool small) const {
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        {
-            const int t = wave >> 1, h = wave & 1;
+        if (kKThreads == NT || tid < kKThreads) {
+            constexpr int kPer = kBlocks / kOps;
+            const int t = wave / kPer, h = wave % kPer;
 #pragma unroll
-            for (int b = 0; b < kBlocks / 2; ++b) s.k[t][h * (kBlocks / 2) + b][lane] = __builtin_bit_cast(u4, key_codes<BITS>(k, b));
+            for (int b = 0; b < kOps; ++b) s.k[t][h * kOps + b][lane] = __builtin_bit_cast(u4, key_codes<BITS>(masks, k, b));
         }
-        const int t = (tid >> 1) & 1, pair = tid & 1, ln = tid >> 2;
-        const int key = key0 + 16 * t + 4 * (ln >> 4) + 2 * pair;
-        const bool ok0 = there && key < len, ok1 = there && key + 1 < len;
-        bool bad = false, large = false;
-        uint32_t* hi = reinterpret_cast<uint32_t*>(s.v_hi);
-        uint32_t* lo = reinterpret_cast<uint32_t*>(s.v_lo);
-        const _Float16 by = static_cast<_Float16>(small ? kSmall : 1.0f);
+        bool special = false, bad = false, large = false;
+        if (kVThreads == NT || tid < kVThreads) {
+            const int t = (tid >> 1) & 1, pair = tid & 1, ln = (tid >> 2) & 63, i0 = (tid >> 8) * kVs;
+            uint32_t e[2 * kDs];             // the scales, 0 behind the sequence's end
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            // (scale of the first token, of the second)
-            uint32_t two = __builtin_amdgcn_perm(d[kBlocks / 2 + b / 2], d[b / 2], b & 1 ? 0x07060302u : 0x05040100u);
-            const uint32_t e = two & 0x7C007C00u;
-            const bool nf0 = (e & 0xFFFFu) == 0x7C00u, nf1 = (e >> 16) == 0x7C00u;
-            bad |= (nf0 && ok0) || (nf1 && ok1);
-            two = (ok0 && !nf0 ? two & 0xFFFFu : 0u) | (ok1 && !nf1 ? two & 0xFFFF0000u : 0u);
-            large |= (two & 0x7C00u) >= (kLarge << 10) || (two & 0x7C000000u) >= (uint32_t(kLarge) << 26);
-            const h2 dd = __builtin_bit_cast(h2, two) * h2{by, by};
+            for (int i = 0; i < 2 * kDs; ++i) e[i] = d[i];
+            if (key0 + kStep > len || pages[0] < 0 || pages[1] < 0) {
+                const int key = key0 + 16 * t + 4 * (ln >> 4) + 2 * pair;
+                const bool there = (t ? pages[1] : pages[0]) >= 0;
 #pragma unroll
-            for (int j = 2 * b; j < 2 * b + 2; ++j) {
-                constexpr int kPer = BITS == 4 ? 4 : 2;
-                const int i = j / kPer, n = j % kPer;
-                uint32_t x = v[i];
-                if (BITS == 8 ? n == 1 : n >= 2) x >>= 8;
-                const bool up = BITS == 4 && (n & 1);
-                const h2 code = __builtin_bit_cast(h2, two_codes<BITS>(x, up));
-                const h2 c = up ? code * h2{static_cast<_Float16>(0.0625f), static_cast<_Float16>(0.0625f)} : code;
-                const h2 p = c * dd;
-                const h2 q = __builtin_elementwise_fma(c, dd, -p);
-                hi[(j * 64 + ln) * 4 + (tid & 3)] = __builtin_bit_cast(uint32_t, p);
-                lo[(j * 64 + ln) * 4 + (tid & 3)] = __builtin_bit_cast(uint32_t, q);
+                for (int i = 0; i < 2 * kDs; ++i) e[i] = there && key + i / kDs < len ? e[i] : 0;
             }
+            if constexpr (!PRECISE) {
+                typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+                us2 top = {0, 0};
+#pragma unroll
+                for (int i = 0; i < 2 * kDs; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(us2, e[i] & 0x7FFF7FFFu));
+                special = top[0] >= (kLarge << 10) || top[1] >= (kLarge << 10);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2 * kDs; ++i)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t x = (e[i] >> (16 * h + 10)) & 31;
+                        bad |= x == 31;
+                        large |= x >= kLarge && x < 31;
+                        if (x == 31) e[i] &= h ? 0x0000FFFFu : 0xFFFF0000u;
+                    }
+            }
+            uint32_t* hi = reinterpret_cast<uint32_t*>(s.v_hi);
+            uint32_t* lo = reinterpret_cast<uint32_t*>(s.v_lo);
+            constexpr int kPer = BITS == 4 ? 4 : 2;         // 16s of dimensions in a unit
+#pragma unroll
+            for (int i = 0; i < kVs; ++i)
+#pragma unroll
+                for (int n = 0; n < kPer; ++n) {
+                    // the two tokens' scales of the unit's block
+                    const int word = BITS == 4 ? i : i / 2;
+                    const bool second = BITS == 4 ? n >= 2 : ((kVs == 1 ? i0 : i) & 1) != 0;
+                    const h2 dd = __builtin_bit_cast(h2, __builtin_amdgcn_perm(e[kDs + word], e[word], second ? 0x07060302u : 0x05040100u));
+                    uint32_t x = v[i];
+                    if (BITS == 8 ? n == 1 : n >= 2) x >>= 8;
+                    const h2 c = __builtin_bit_cast(h2, two_codes<BITS>(masks, x, BITS == 4 && (n & 1)));
+                    uint32_t h, l;
+                    if constexpr (!PRECISE) {
+                        const h2 p = c * dd;
+                        h = __builtin_bit_cast(uint32_t, p);
+                        l = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, dd, -p));
+                    } else {
+                        const float by = small ? kSmall : 1.0f;
+                        split(f2{static_cast<float>(c[0]), static_cast<float>(c[1])},
+                              f2{static_cast<float>(dd[0]) * by, static_cast<float>(dd[1]) * by}, h, l);
+                    }
+                    const int at = (((i0 + i) * kPer + n) * 64 + ln) * 4 + (tid & 3);
+                    hi[at] = h;
+                    lo[at] = l;
+                }
         }
-        const bool any_bad = __ballot(bad) != 0, any_large = __ballot(large) != 0;
+        const bool any_special = __ballot(special) != 0, any_bad = __ballot(bad) != 0, any_large = __ballot(large) != 0;
         if (lane == 0) {
+            s.special[wave] = any_special;
             s.bad[wave] = any_bad;
             s.large[wave] = any_large;
         }
-#pragma unroll
-        for (int i = 0; i < kScaleDwords; i += kThreads)
-            if (i + tid < kScaleDwords) {
-                (&s.ks[0][0])[i + tid] = ks[i / kThreads];
-                (&s.vs[0][0])[i + tid] = vs[i / kThreads];
-            }
+        if (tid < kScaleDwords) {
+            const int tt = tid / (kBlocks * 8), o = tid % (kBlocks * 8), token = o / (kBlocks / 2), b = 2 * (o % (kBlocks / 2));
+            s.ks[tt][b][token] = half_of(ks, 0);
+            s.ks[tt][b + 1][token] = half_of(ks, 1);
+            s.vs[tt][o] = vs;
+        }
     }
 };
 
+template <int N>
+__device__ __forceinline__ bool any_of(const uint32_t (&v)[N]) {
+    uint32_t all = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) all |= v[i];
+    return __builtin_amdgcn_readfirstlane(all) != 0;
+}
+
 // One staged step for a wave's RT sets of rows.
-template <int BITS, int D, int RT, bool MASKED>
-__device__ __forceinline__ void attend_staged(const Staged<BITS, D>& s, Rows<BITS, D> (&r)[RT], int key0, const bool (&there)[2], int lane) {
+template <int BITS, int D, int NT, int RT>
+__device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, Rows<BITS, D> (&r)[RT], int key0, bool full, bool there0, bool there1, int lane) {
     constexpr int kBlocks = D / 32, kTiles = D / 16;
+    // Operands are read from LDS one product ahead; the scheduling barriers keep it at that (all of them at once take more
+    // registers than there are).
     float sc[RT][8];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        uint32_t d[D / 16];
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int i = 0; i < D / 16; i += 4) {
-            const u4 x = *reinterpret_cast<const u4*>(&s.ks[t][(lane >> 4) * (2 * kBlocks) + i]);
+        for (int j = 0; j < 8; ++j) sc[i][j] = 0.0f;
+    u4 k = s.k[0][0][lane];
+    f4 d = *reinterpret_cast<const f4*>(&s.ks[0][0][4 * (lane >> 4)]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) d[i + j] = x[j];
+    for (int n = 0; n < 2 * kBlocks; ++n) {
+        const int t = n / kBlocks, b = n % kBlocks, t1 = (n + 1) / kBlocks % 2, b1 = (n + 1) % kBlocks;
+        const h8 k0 = __builtin_bit_cast(h8, k);
+        const f4 d0 = d;
+        if (n + 1 < 2 * kBlocks) {
+            k = s.k[t1][b1][lane];
+            d = *reinterpret_cast<const f4*>(&s.ks[t1][b1][4 * (lane >> 4)]);
         }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            f4 acc = {0, 0, 0, 0};
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, r[i].hi[b], acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, r[i].lo[b], acc, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sc[i][4 * t + j] = fmaf(d0[j], acc[j], sc[i][4 * t + j]);
+        }
+        if (n & 1) __builtin_amdgcn_sched_barrier(0);
+    }
+    // (One code path with the masks as a branch over a few selects; the asm keeps the scores here, whose sums the compiler
+    // otherwise moves behind the branches of another row set, holding every operand until then.)
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(sc[i][j]));
+    if (!full) {
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sc[i][4 * t + j] = 0.0f;
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            const h8 k = __builtin_bit_cast(h8, s.k[t][b][lane]);
-#pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                f4 acc = {0, 0, 0, 0};
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, r[i].hi[b], acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, r[i].lo[b], acc, 0, 0, 0);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    sc[i][4 * t + j] = fmaf(half_of(d[j * (kBlocks / 2) + b / 2], b & 1), acc[j], sc[i][4 * t + j]);
+            for (int j = 0; j < 8; ++j) {
+                const int key = key0 + 16 * (j >> 2) + 4 * (lane >> 4) + (j & 3);
+                sc[i][j] = key >= r[i].first && key < r[i].last && (j < 4 ? there0 : there1) ? sc[i][j] : kNone;
             }
-        }
     }
     h8 hi[RT], lo[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        bool ok[8];
-        if constexpr (MASKED) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int key = key0 + 16 * (j >> 2) + 4 * (lane >> 4) + (j & 3);
-                ok[j] = key >= r[i].first && key < r[i].last && there[j >> 2];
-                sc[i][j] = ok[j] ? sc[i][j] : kNone;
-            }
-        }
-        const float base = r[i].raise(sc[i]);
+        const float base = r[i].template raise<kManySlack>(sc[i]) - kManyUnit;
         u4 h, l;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
@@ -768,36 +852,41 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D>& s, Rows<BIT
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 p[k] = __builtin_amdgcn_exp2f(fmaf(sc[i][j + k], r[i].f, -base));
-                if constexpr (MASKED) p[k] = ok[j + k] ? p[k] : 0.0f;
                 r[i].l += p[k];
             }
             uint32_t u, w;
-            split(p, f2{kWeightUnit, kWeightUnit}, u, w);
+            split(p, f2{1.0f, 1.0f}, u, w);
             h[j / 2] = u;
             l[j / 2] = w;
         }
         hi[i] = __builtin_bit_cast(h8, h);
         lo[i] = __builtin_bit_cast(h8, l);
     }
+    u4 vh = s.v_hi[0][lane], vl = s.v_lo[0][lane];
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
-        const h8 vh = __builtin_bit_cast(h8, s.v_hi[j][lane]), vl = __builtin_bit_cast(h8, s.v_lo[j][lane]);
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vh, hi[i], r[i].o[j], 0, 0, 0);
-            r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vh, lo[i], r[i].o[j], 0, 0, 0);
-            r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vl, hi[i], r[i].o[j], 0, 0, 0);
+        const h8 h = __builtin_bit_cast(h8, vh), l = __builtin_bit_cast(h8, vl);
+        if (j + 1 < kTiles) {
+            vh = s.v_hi[j + 1][lane];
+            vl = s.v_lo[j + 1][lane];
         }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h, hi[i], r[i].o[j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h, lo[i], r[i].o[j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(l, hi[i], r[i].o[j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
-template <int BITS, int D, int RT>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArgs a) {
-    constexpr int kTiles = D / 16, kBlocks = D / 32, kRows = 64 * RT;
-    constexpr size_t kBuffers = 2 * sizeof(Staged<BITS, D>), kJoin = 2 * kJoinRows * sizeof(float);
+template <int BITS, int D, int NT, int RT>
+__global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArgs a) {
+    constexpr int kTiles = D / 16, kBlocks = D / 32, kRows = NT / 4 * RT;
+    constexpr size_t kBuffers = 2 * sizeof(Staged<BITS, D, NT>), kJoin = 2 * kJoinRows * sizeof(float);
     __shared__ __align__(16) uint8_t memory[kBuffers > kJoin ? kBuffers : kJoin];
     __shared__ unsigned ticket;
-    Staged<BITS, D>* const buf = reinterpret_cast<Staged<BITS, D>*>(memory);
+    Staged<BITS, D, NT>* const buf = reinterpret_cast<Staged<BITS, D, NT>*>(memory);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Work w;
@@ -807,11 +896,10 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_many_kernel(A
     const int pieces = max(1, (end - begin + a.chunk_steps - 1) / a.chunk_steps);
     if (w.split >= pieces) return;
     const int from = begin + w.split * a.chunk_steps, to = min(end, from + a.chunk_steps);
-    // the wave's own rows: keys that every one of them sees, and that any does
+    // the wave's own rows, and the keys that every one of them sees
     const int mine = w.row0 + wave * 16 * RT;
     const int t0 = min(mine, w.rows - 1) / a.group, t1 = (min(mine + 16 * RT, w.rows) - 1) / a.group;
     const int full_begin = first_key(a, w, t1), full_end = last_key(a, w, t0);
-    const int any_begin = first_key(a, w, t0), any_end = mine < w.rows ? last_key(a, w, t1) : 0;
     Rows<BITS, D> r[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -821,66 +909,70 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_many_kernel(A
         r[i].last = last_key(a, w, row / a.group);
     }
     bool small = false;
+    using P = Piece<BITS, D, NT>;
     if (from < to) {
-        using P = Piece<BITS, D>;
+        const Masks masks = Masks::make<BITS>();
         P piece;
         int pages[2], next[2];
         pages_of(a, w, from, pages);
         piece.load(a.c, pages, w.head, from * kStep);
-        piece.stage(buf[0], from * kStep, w.len, false);
+        piece.template stage<false>(masks, buf[0], pages, from * kStep, w.len, false);
         pages_of(a, w, min(from + 1, to - 1), next);
         __syncthreads();
         for (int step = from; step < to; ++step) {
             const int key0 = step * kStep;
-            Staged<BITS, D>& s = buf[(step - from) & 1];
-            if (!small && (s.large[0] | s.large[1] | s.large[2] | s.large[3])) {      // (the piece is still this step's)
-                small = true;
-#pragma unroll
-                for (int i = 0; i < RT; ++i)
-#pragma unroll
-                    for (int j = 0; j < kTiles; ++j) r[i].o[j] *= P::kSmall;
+            Staged<BITS, D, NT>& s = buf[(step - from) & 1];
+            if (any_of(s.special)) {         // (the piece is still this step's)
                 __syncthreads();
-                piece.stage(s, key0, w.len, true);
+                piece.template stage<true>(masks, s, pages, key0, w.len, false);
                 __syncthreads();
+                if (any_of(s.large)) {
+                    small = true;
+#pragma unroll
+                    for (int i = 0; i < RT; ++i)
+#pragma unroll
+                        for (int j = 0; j < kTiles; ++j) r[i].o[j] *= P::kSmall;
+                    __syncthreads();
+                    piece.template stage<true>(masks, s, pages, key0, w.len, true);
+                    __syncthreads();
+                }
             }
-            const bool there[2] = {pages[0] >= 0, pages[1] >= 0};
+            const bool there0 = pages[0] >= 0, there1 = pages[1] >= 0;
             const int ahead = min(step + 1, to - 1);
             pages[0] = next[0];
             pages[1] = next[1];
             piece.load(a.c, pages, w.head, ahead * kStep);
             pages_of(a, w, min(step + 2, to - 1), next);
-            if (key0 < any_end && key0 + kStep > any_begin) {
-                if (key0 >= full_begin && key0 + kStep <= full_end && there[0] && there[1])
-                    attend_staged<BITS, D, RT, false>(s, r, key0, there, lane);
-                else
-                    attend_staged<BITS, D, RT, true>(s, r, key0, there, lane);
-                if (s.bad[0] | s.bad[1] | s.bad[2] | s.bad[3]) {      // (staged as zeros)
-                    for (int i = 0; i < kStep; ++i)
+            const bool full = key0 >= full_begin && key0 + kStep <= full_end && there0 && there1;
+            attend_staged<BITS, D, NT, RT>(s, r, key0, full, there0, there1, lane);
+            if (any_of(s.bad)) {      // (staged as zeros)
+                for (int i = 0; i < kStep; ++i)
 #pragma unroll
-                        for (int b = 0; b < kBlocks; ++b) {
-                            const uint32_t d = s.vs[i >> 4][(i & 15) * (kBlocks / 2) + b / 2] >> (16 * (b & 1));
-                            if ((d & 0x7C00u) != 0x7C00u) continue;
+                    for (int b = 0; b < kBlocks; ++b) {
+                        const uint32_t d = s.vs[i >> 4][(i & 15) * (kBlocks / 2) + b / 2] >> (16 * (b & 1));
+                        if ((d & 0x7C00u) != 0x7C00u) continue;
 #pragma unroll
-                            for (int k = 0; k < RT; ++k)
-                                if (key0 + i >= r[k].first && key0 + i < r[k].last && there[i >> 4]) {
-                                    const float nan = __builtin_nanf("");
-                                    r[k].o[2 * b] = r[k].o[2 * b + 1] = f4{nan, nan, nan, nan};
-                                }
-                        }
-                }
+                        for (int k = 0; k < RT; ++k)
+                            if (key0 + i >= r[k].first && key0 + i < r[k].last && (i < 16 ? there0 : there1)) {
+                                const float nan = __builtin_nanf("");
+                                r[k].o[2 * b] = r[k].o[2 * b + 1] = f4{nan, nan, nan, nan};
+                            }
+                    }
             }
-            piece.stage(buf[(step + 1 - from) & 1], ahead * kStep, w.len, small);
+            Staged<BITS, D, NT>& t = buf[(step + 1 - from) & 1];
+            if (!small) piece.template stage<false>(masks, t, pages, ahead * kStep, w.len, false);
+            else piece.template stage<true>(masks, t, pages, ahead * kStep, w.len, true);
             __syncthreads();
         }
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         r[i].l = row_sum(r[i].l);
-        r[i].m = r[i].m == kNone ? kNone : r[i].m * r[i].f;      // log2 units from here on
+        const float even = small ? 1.0f / P::kSmall : 1.0f;
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) r[i].o[j] *= small ? 1.0f / (kWeightUnit * Piece<BITS, D>::kSmall) : 1.0f / kWeightUnit;
+        for (int j = 0; j < kTiles; ++j) r[i].o[j] *= BITS == 4 && (j & 1) ? even * 0.0625f : even;
     }
-    const Slot<D, kRows> slot(a, w.cell);
+    const Slot<D, kRows, NT> slot(a, w.cell);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int row = mine + 16 * i + (lane & 15);
@@ -901,11 +993,11 @@ struct Plan {
 Plan plan(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q, int64_t max_kv) {
     Plan p;
     const int64_t rows = max_q * (q_heads / heads), steps = (max_kv + kStep - 1) / kStep + 1;
-    p.tile_rows = rows <= 32 ? 16 : rows <= 64 ? 64 : 128;
+    p.tile_rows = rows <= 32 ? 16 : rows <= 128 || dim > 128 ? 64 : 256;
     const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows, items = seqs * heads * tiles;
     const int64_t most = p.tile_rows == 16 ? kMaxSplits : kJoinRows / p.tile_rows;
     const int64_t least = p.tile_rows == 16 ? kMinSteps * kWaves : kMinManySteps;
-    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({most, kTarget / items, steps / least}));
+    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({most, (p.tile_rows == 256 ? kTarget / 2 : kTarget) / items, steps / least}));
     p.chunk_steps = int((steps + splits - 1) / splits);
     p.splits = int((steps + p.chunk_steps - 1) / p.chunk_steps);
     p.tiles = int(tiles);
@@ -923,7 +1015,7 @@ size_t attn_scratch_bytes(int, int64_t seqs, int64_t q_heads, int64_t heads, int
 }
 
 bool attn_fits(int64_t seqs, int64_t q_heads, int64_t heads, int64_t max_q, int64_t max_kv) {
-    return plan(seqs, q_heads, heads, 64, max_q, max_kv).blocks < (int64_t(1) << 31);
+    return plan(seqs, q_heads, heads, 256, max_q, max_kv).blocks < (int64_t(1) << 31);
 }
 
 hipError_t launch_attn(const Attn& r, hipStream_t s, const char** name) {
@@ -948,12 +1040,12 @@ hipError_t launch_attn(const Attn& r, hipStream_t s, const char** name) {
     a.splits = p.splits;
     a.chunk_steps = p.chunk_steps;
     a.scale = r.scale;
-    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(unsigned(p.blocks)), dim3(kThreads), 0, s, a); };
+    auto run = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3(unsigned(p.blocks)), dim3(threads), 0, s, a); };
     kv_kinds(r.cache.bits, r.cache.dim, [&](auto bits, auto dim) {
         constexpr int kB = decltype(bits)::value, kD = decltype(dim)::value;
-        if (p.tile_rows == 16) run(attn_few_kernel<kB, kD>);
-        else if (p.tile_rows == 64) run(attn_many_kernel<kB, kD, 1>);
-        else run(attn_many_kernel<kB, kD, 2>);
+        if (p.tile_rows == 16) run(attn_few_kernel<kB, kD>, kThreads);
+        else if (p.tile_rows == 64) run(attn_many_kernel<kB, kD, 256, 1>, 256);
+        else if constexpr (kD <= 128) run(attn_many_kernel<kB, kD, 512, 2>, 512);
     });
     return hipGetLastError();
 }
