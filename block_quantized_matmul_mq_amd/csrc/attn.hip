@@ -51,7 +51,8 @@ constexpr int kTarget = 512;             // workgroups that a call is cut into w
 constexpr int kMaxSplits = 128;
 constexpr int kMinSteps = 4;             // steps of a wave at least where a tile's keys are cut
 constexpr int kJoinRows = 4096;          // of attn_many: pieces times rows of a tile at most (LDS of the join)
-constexpr int kMinManySteps = 8;         // steps of a piece at least
+constexpr int kMinManySteps = 8, kPieceSteps = 2;   // steps of a piece at least, and what its start and end cost
+constexpr size_t kMaxSlots = 60 << 20;   // bytes of all pieces at most
 // attn_many's weights are in units of 2^-kManyUnit, f16's normal range from 2^-20 on, and up to 2^kManySlack
 constexpr float kManyUnit = 6.0f;
 constexpr int kManySlack = 8;
@@ -798,34 +799,47 @@ __device__ __forceinline__ bool any_of(const uint32_t (&v)[N]) {
 template <int BITS, int D, int NT, int RT>
 __device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, Rows<BITS, D> (&r)[RT], int key0, bool full, bool there0, bool there1, int lane) {
     constexpr int kBlocks = D / 32, kTiles = D / 16;
-    // Operands are read from LDS one product ahead; the scheduling barriers keep it at that (all of them at once take more
-    // registers than there are).
+    // Operands are read from LDS one product ahead (the scheduling barriers keep it at that: all of them at once take more
+    // registers than there are), and a block's sums are used while the next block's products run.
     float sc[RT][8];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sc[i][j] = 0.0f;
     u4 k = s.k[0][0][lane];
-    f4 d = *reinterpret_cast<const f4*>(&s.ks[0][0][4 * (lane >> 4)]);
+    f4 d = *reinterpret_cast<const f4*>(&s.ks[0][0][4 * (lane >> 4)]), d1;
+    f4 acc[RT], acc1[RT];
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-    for (int n = 0; n < 2 * kBlocks; ++n) {
-        const int t = n / kBlocks, b = n % kBlocks, t1 = (n + 1) / kBlocks % 2, b1 = (n + 1) % kBlocks;
+    for (int n = 0; n <= 2 * kBlocks; ++n) {
+        const int b = n % kBlocks, tn = (n + 1) / kBlocks % 2, bn = (n + 1) % kBlocks;
         const h8 k0 = __builtin_bit_cast(h8, k);
         const f4 d0 = d;
         if (n + 1 < 2 * kBlocks) {
-            k = s.k[t1][b1][lane];
-            d = *reinterpret_cast<const f4*>(&s.ks[t1][b1][4 * (lane >> 4)]);
+            k = s.k[tn][bn][lane];
+            d = *reinterpret_cast<const f4*>(&s.ks[tn][bn][4 * (lane >> 4)]);
+        }
+        if (n < 2 * kBlocks) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, r[i].hi[b], f4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, r[i].lo[b], acc[i], 0, 0, 0);
+        }
+        if (n > 0) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float& x = sc[i][4 * ((n - 1) / kBlocks) + j];
+                    x = (n - 1) % kBlocks == 0 ? d1[j] * acc1[i][j] : fmaf(d1[j], acc1[i][j], x);
+                }
         }
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            f4 acc = {0, 0, 0, 0};
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, r[i].hi[b], acc, 0, 0, 0);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(k0, r[i].lo[b], acc, 0, 0, 0);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sc[i][4 * t + j] = fmaf(d0[j], acc[j], sc[i][4 * t + j]);
-        }
-        if (n & 1) __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < RT; ++i) acc1[i] = acc[i];
+        d1 = d0;
+        __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
     // (One code path with the masks as a branch over a few selects; the asm keeps the scores here, whose sums the compiler
     // otherwise moves behind the branches of another row set, holding every operand until then.)
 #pragma unroll
@@ -862,22 +876,35 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, Rows
         hi[i] = __builtin_bit_cast(h8, h);
         lo[i] = __builtin_bit_cast(h8, l);
     }
-    u4 vh = s.v_hi[0][lane], vl = s.v_lo[0][lane];
+    __builtin_amdgcn_s_setprio(1);
+    u4 vh[2], vl[2];
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-        const h8 h = __builtin_bit_cast(h8, vh), l = __builtin_bit_cast(h8, vl);
-        if (j + 1 < kTiles) {
-            vh = s.v_hi[j + 1][lane];
-            vl = s.v_lo[j + 1][lane];
+    for (int k = 0; k < 2; ++k) {
+        vh[k] = s.v_hi[k][lane];
+        vl[k] = s.v_lo[k][lane];
+    }
+#pragma unroll
+    for (int j = 0; j < kTiles; j += 2) {
+        h8 h[2], l[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            h[k] = __builtin_bit_cast(h8, vh[k]);
+            l[k] = __builtin_bit_cast(h8, vl[k]);
+            if (j + 2 < kTiles) {
+                vh[k] = s.v_hi[j + 2 + k][lane];
+                vl[k] = s.v_lo[j + 2 + k][lane];
+            }
         }
 #pragma unroll
-        for (int i = 0; i < RT; ++i) r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h, hi[i], r[i].o[j], 0, 0, 0);
+        for (int m = 0; m < 3; ++m)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(h, lo[i], r[i].o[j], 0, 0, 0);
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) r[i].o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(l, hi[i], r[i].o[j], 0, 0, 0);
+                for (int i = 0; i < RT; ++i)
+                    r[i].o[j + k] = __builtin_amdgcn_mfma_f32_16x16x32_f16(m < 2 ? h[k] : l[k], m == 1 ? lo[i] : hi[i], r[i].o[j + k], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
 }
 
 template <int BITS, int D, int NT, int RT>
@@ -990,14 +1017,28 @@ struct Plan {
     int tile_rows, tiles, splits, chunk_steps;
     int64_t blocks;
 };
+size_t slot_bytes(int rows, int64_t dim) { return size_t(rows) * size_t(dim + 2) * 4; }
 Plan plan(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q, int64_t max_kv) {
     Plan p;
     const int64_t rows = max_q * (q_heads / heads), steps = (max_kv + kStep - 1) / kStep + 1;
-    p.tile_rows = rows <= 32 ? 16 : rows <= 128 || dim > 128 ? 64 : 256;
+    p.tile_rows = rows <= 32 ? 16 : rows <= 128 || dim > 128 ? 64 : 128;
     const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows, items = seqs * heads * tiles;
     const int64_t most = p.tile_rows == 16 ? kMaxSplits : kJoinRows / p.tile_rows;
     const int64_t least = p.tile_rows == 16 ? kMinSteps * kWaves : kMinManySteps;
-    const int64_t splits = std::max<int64_t>(1, std::min<int64_t>({most, (p.tile_rows == 256 ? kTarget / 2 : kTarget) / items, steps / least}));
+    int64_t splits = std::max<int64_t>(1, std::min<int64_t>({most, kTarget / items, steps / least}));
+    if (p.tile_rows > 16) {
+        // the number of pieces that keeps rounds of kTarget workgroups fullest, a piece's start and end at the price of kPieceSteps
+        double best = 0.0;
+        for (int64_t n = 1; n <= std::min<int64_t>(most, std::max<int64_t>(1, steps / least)) && (n == 1 || size_t(n * items) * slot_bytes(p.tile_rows, dim) <= kMaxSlots); ++n) {
+            const int64_t chunk = (steps + n - 1) / n, blocks = items * n;
+            const double full = double(blocks) / double((blocks + kTarget - 1) / kTarget * kTarget);
+            const double rate = full * double(chunk) / double(chunk + kPieceSteps + (n > 1 ? 1 : 0));
+            if (rate > best) {
+                best = rate;
+                splits = n;
+            }
+        }
+    }
     p.chunk_steps = int((steps + splits - 1) / splits);
     p.splits = int((steps + p.chunk_steps - 1) / p.chunk_steps);
     p.tiles = int(tiles);
@@ -1005,13 +1046,11 @@ Plan plan(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max
     return p;
 }
 
-size_t slot_floats(const Plan& p, int64_t dim) { return size_t(p.tile_rows) * size_t(dim + 2); }
-
 }  // namespace
 
 size_t attn_scratch_bytes(int, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q, int64_t max_kv) {
     const Plan p = plan(seqs, q_heads, heads, dim, max_q, max_kv);
-    return size_t(kCounters) * 4 + (p.splits > 1 ? size_t(p.blocks) * slot_floats(p, dim) * 4 : 0);
+    return size_t(kCounters) * 4 + (p.splits > 1 ? size_t(p.blocks) * slot_bytes(p.tile_rows, dim) : 0);
 }
 
 bool attn_fits(int64_t seqs, int64_t q_heads, int64_t heads, int64_t max_q, int64_t max_kv) {
@@ -1045,7 +1084,7 @@ hipError_t launch_attn(const Attn& r, hipStream_t s, const char** name) {
         constexpr int kB = decltype(bits)::value, kD = decltype(dim)::value;
         if (p.tile_rows == 16) run(attn_few_kernel<kB, kD>, kThreads);
         else if (p.tile_rows == 64) run(attn_many_kernel<kB, kD, 256, 1>, 256);
-        else if constexpr (kD <= 128) run(attn_many_kernel<kB, kD, 512, 2>, 512);
+        else if constexpr (kD <= 128) run(attn_many_kernel<kB, kD, 256, 2>, 256);
     });
     return hipGetLastError();
 }
