@@ -48,8 +48,7 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 32;                // keys of a step
 constexpr int kCounters = 65536;         // of the scratch; cut tiles are at most kTarget
 constexpr int kTarget = 512;             // workgroups that a call is cut into where it has fewer tiles (half of it: of 512 threads)
-constexpr int kMaxSplits = 128;
-constexpr int kMinSteps = 4;             // steps of a wave at least where a tile's keys are cut
+constexpr int kMaxSplits = 64;
 constexpr int kJoinRows = 4096;          // of attn_many: pieces times rows of a tile at most (LDS of the join)
 constexpr int kMinManySteps = 8, kPieceSteps = 2;   // steps of a piece at least, and what its start and end cost
 constexpr size_t kMaxSlots = 60 << 20;   // bytes of all pieces at most
@@ -391,14 +390,14 @@ struct Work {
 };
 __device__ __forceinline__ bool work_of(const AttnArgs& a, int tile_rows, Work& w) {
     // heads vary fastest (workgroups are dealt to the XCDs in turn, whose L2 so holds few heads); later rows, which
-    // see more keys, come first
+    // see more keys, come first, and a tile's last piece, which is rarely a whole one, comes last
     int item = blockIdx.x;
     w.head = item % a.c.heads;
     item /= a.c.heads;
-    w.split = item % a.splits;
-    item /= a.splits;
+    w.seq = item % a.c.seqs;
+    item /= a.c.seqs;
     w.tile = a.tiles - 1 - item % a.tiles;
-    w.seq = item / a.tiles;
+    w.split = item / a.tiles;
     w.cell = (w.seq * a.tiles + w.tile) * a.c.heads + w.head;
     w.q0 = a.c.q_start[w.seq];
     w.all = a.c.q_start[w.seq + 1] - w.q0;
@@ -497,7 +496,8 @@ struct Slot {
                     }
                 }
             };
-            batch(std::integral_constant<int, 8>{});
+            batch(std::integral_constant<int, 16>{});
+            batch(std::integral_constant<int, 4>{});
             batch(std::integral_constant<int, 1>{});
             *reinterpret_cast<f4*>(out_row(a, w, w.row0 + row) + i % (D / 4) * 4) = sum;
         }
@@ -1024,8 +1024,9 @@ Plan plan(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max
     p.tile_rows = rows <= 32 ? 16 : rows <= 128 || dim > 128 ? 64 : 128;
     const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows, items = seqs * heads * tiles;
     const int64_t most = p.tile_rows == 16 ? kMaxSplits : kJoinRows / p.tile_rows;
-    const int64_t least = p.tile_rows == 16 ? kMinSteps * kWaves : kMinManySteps;
-    int64_t splits = std::max<int64_t>(1, std::min<int64_t>({most, kTarget / items, steps / least}));
+    const int64_t least = kMinManySteps;
+    // attn_few: pieces of 8 steps for a workgroup per CU, of 64 steps for four (lengths differ: pieces even them out)
+    int64_t splits = std::max<int64_t>(1, std::min(most, std::max(std::min(kTarget / 2 / items, steps / 8), std::min(2 * kTarget / items, steps / 64))));
     if (p.tile_rows > 16) {
         // the number of pieces that keeps rounds of kTarget workgroups fullest, a piece's start and end at the price of kPieceSteps
         double best = 0.0;
