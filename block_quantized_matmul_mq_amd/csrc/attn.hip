@@ -112,15 +112,33 @@ constexpr float kNone = -__builtin_inff();
 
 typedef float f2 __attribute__((ext_vector_type(2)));
 
-// Two values p d as f16 pairs, hi + lo to 22 bits: hi rounded from the f32 products, lo from the exact rest p d - hi.  The
-// empty asm keeps hi one value: formed a second time for the rest, by a fused instruction from the exact product,
-// it would round the other way once in some thousand values and the sum miss by 2^-11.
-__device__ __forceinline__ void split(f2 p, f2 d, uint32_t& hi, uint32_t& lo) {
-    hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{p[0] * d[0], p[1] * d[1]}, h2));
+// Two products p d (d f16) as f16 pairs, hi + lo to 22 bits: hi the rounded product, lo the rounded rest of the exact one.  Each is
+// one instruction a value (v_fma_mixlo_f16, v_fma_mixhi_f16), as long as hi's sum with 0 is not taken away.  The empty asm
+// keeps hi one value: formed a second time for the rest, in another way, it would round differently once in some
+// thousand values and the sum miss by 2^-11.
+__device__ __forceinline__ void split(f2 p, _Float16 d0, _Float16 d1, uint32_t& hi, uint32_t& lo) {
+    const h2 a = {static_cast<_Float16>(fmaf(p[0], static_cast<float>(d0), 0.0f)),
+                  static_cast<_Float16>(fmaf(p[1], static_cast<float>(d1), 0.0f))};
+    hi = __builtin_bit_cast(uint32_t, a);
     asm("" : "+v"(hi));
     const h2 h = __builtin_bit_cast(h2, hi);
-    const f2 rest = {fmaf(p[0], d[0], -static_cast<float>(h[0])), fmaf(p[1], d[1], -static_cast<float>(h[1]))};
-    lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, h2));
+    const h2 b = {static_cast<_Float16>(fmaf(p[0], static_cast<float>(d0), -static_cast<float>(h[0]))),
+                  static_cast<_Float16>(fmaf(p[1], static_cast<float>(d1), -static_cast<float>(h[1])))};
+    lo = __builtin_bit_cast(uint32_t, b);
+}
+// The same of two f32 values.  one: 1, in a register (as a constant it would cost the rest a conversion more).
+__device__ __forceinline__ void split(f2 w, float one, uint32_t& hi, uint32_t& lo) {
+    hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(w, h2));
+    asm("" : "+v"(hi));
+    const h2 h = __builtin_bit_cast(h2, hi);
+    const h2 b = {static_cast<_Float16>(fmaf(w[0], one, -static_cast<float>(h[0]))),
+                  static_cast<_Float16>(fmaf(w[1], one, -static_cast<float>(h[1])))};
+    lo = __builtin_bit_cast(uint32_t, b);
+}
+__device__ __forceinline__ float opaque_one() {
+    float one = 1.0f;
+    asm("" : "+v"(one));
+    return one;
 }
 
 // The bits of two codes in a dword, in registers of the vector unit: its AND-OR takes one scalar operand only.
@@ -204,7 +222,7 @@ struct Rows {
                 for (int j = 0; j < 2; ++j)
                     v[j] = ldexpf(x[b][BITS == 4 ? kOrder4[i + j] : kOrder8[i + j]], BITS == 4 && (i & 2) ? e - 4 : e);   // (codes 16 times as large)
                 uint32_t u, w;
-                split(v, f2{1.0f, 1.0f}, u, w);
+                split(v, 1.0f, u, w);
                 h[i / 2] = u;
                 l[i / 2] = w;
             }
@@ -330,13 +348,8 @@ __device__ __forceinline__ void attend(const Masks& masks, const Step<BITS, D>& 
         u4 h, l;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            f2 d;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                d[j] = half_of(vs[i + j][b / 2], b & 1);
-            }
             uint32_t u, w;
-            split(f2{p[i], p[i + 1]}, d, u, w);
+            split(f2{p[i], p[i + 1]}, __builtin_bit_cast(h2, vs[i][b / 2])[b & 1], __builtin_bit_cast(h2, vs[i + 1][b / 2])[b & 1], u, w);
             h[i / 2] = u;
             l[i / 2] = w;
         }
@@ -764,8 +777,8 @@ struct Piece {
                         l = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, dd, -p));
                     } else {
                         const float by = small ? kSmall : 1.0f;
-                        split(f2{static_cast<float>(c[0]), static_cast<float>(c[1])},
-                              f2{static_cast<float>(dd[0]) * by, static_cast<float>(dd[1]) * by}, h, l);
+                        split(f2{static_cast<float>(c[0]) * (static_cast<float>(dd[0]) * by),
+                                 static_cast<float>(c[1]) * (static_cast<float>(dd[1]) * by)}, 1.0f, h, l);
                     }
                     const int at = (((i0 + i) * kPer + n) * 64 + ln) * 4 + (tid & 3);
                     hi[at] = h;
@@ -855,6 +868,7 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, Rows
                 sc[i][j] = key >= r[i].first && key < r[i].last && (j < 4 ? there0 : there1) ? sc[i][j] : kNone;
             }
     }
+    const float one = opaque_one();
     h8 hi[RT], lo[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
@@ -869,7 +883,7 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, Rows
                 r[i].l += p[k];
             }
             uint32_t u, w;
-            split(p, f2{1.0f, 1.0f}, u, w);
+            split(p, one, u, w);
             h[j / 2] = u;
             l[j / 2] = w;
         }
