@@ -93,9 +93,9 @@ struct Smem {
         u64 list[kCap];
     };
     u64 block[kMaxBlocks];
-    u64 wave_a[kWaves], wave_b[kWaves];
+    u64 wave[2][2][kWaves];
     Cuts cuts;
-    u64 cut, total, found;
+    u64 cut, found, k_mass;
     uint32_t count, ticket;
     uint32_t key, above_n;
     u64 above_w;
@@ -146,46 +146,77 @@ __device__ __forceinline__ u64 wave_scan(u64 v) {    // inclusive
     }
     return v;
 }
-// Inclusive sums over the workgroup's threads; every thread calls, red is free again afterwards.
-__device__ u64 block_scan(u64 v, u64* red) {
+// Sums of two numbers over the workgroup: inclusive up to each thread, and the totals.  Every thread calls; one barrier: calls
+// that follow one another take turns with the two halves of sm.wave.
+struct Sums {
+    u64 a, b, all_a, all_b;
+};
+__device__ __forceinline__ Sums block_sums(Smem& sm, int turn, u64 a, u64 b = 0) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    v = wave_scan(v);
-    if (lane == 63) red[wave] = v;
+    a = wave_scan(a);
+    b = wave_scan(b);
+    if (lane == 63) {
+        sm.wave[turn][0][wave] = a;
+        sm.wave[turn][1][wave] = b;
+    }
     __syncthreads();
-    for (int w = 0; w < wave; ++w) v += red[w];
-    __syncthreads();
-    return v;
-}
-__device__ u64 block_sum(u64 v, u64* red) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    v = wave_sum(v);
-    if (lane == 0) red[wave] = v;
-    __syncthreads();
-    v = 0;
-    for (int w = 0; w < kWaves; ++w) v += red[w];
-    __syncthreads();
-    return v;
+    Sums s = {a, b, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const u64 x = sm.wave[turn][0][w], y = sm.wave[turn][1][w];
+        s.all_a += x;
+        s.all_b += y;
+        s.a += w < wave ? x : 0;
+        s.b += w < wave ? y : 0;
+    }
+    return s;
 }
 
-// f(i, l) for the row's tokens of blocks [b0, b1), every thread of the workgroup in step (i >= V: l is a NaN).
+// f(block, i, l) for the row's tokens of blocks [b0, b1), every thread of the workgroup in step (i >= V: l is a NaN); the
+// loads of kAhead blocks are in flight together.
+constexpr int kAhead = 4;
 template <class F>
 __device__ __forceinline__ void each(const Row& r, int b0, int b1, const F& f) {
-    for (int b = b0; b < b1; ++b) {
-        float l[kPer];
+    for (int b = b0; b < b1; b += kAhead) {
+        float l[kAhead][kPer];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const int i = b * kBlock + j * kThreads + threadIdx.x;
-            l[j] = i < r.V ? r.l[i] : __builtin_nanf("");
-        }
+        for (int n = 0; n < kAhead; ++n)
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) f(b * kBlock + j * kThreads + int(threadIdx.x), l[j]);
+            for (int j = 0; j < kPer; ++j) {
+                const int i = (b + n) * kBlock + j * kThreads + threadIdx.x;
+                l[n][j] = b + n < b1 && i < r.V ? r.l[i] : __builtin_nanf("");
+            }
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) f(b + n, (b + n) * kBlock + j * kThreads + int(threadIdx.x), l[n][j]);
     }
+}
+// Masses by block: f(block, i, l) is the token's; sums to sm.block[block].
+template <class F>
+__device__ __forceinline__ void sum_blocks(const Row& r, Smem& sm, int b0, int b1, const F& f) {
+    for (int b = b0 + threadIdx.x; b < b1; b += kThreads) sm.block[b] = 0;
+    __syncthreads();
+    for (int b = b0; b < b1; b += kAhead) {
+        u64 w[kAhead] = {};
+        each(r, b, min(b + kAhead, b1), [&](int block, int i, float l) {
+            const u64 v = f(block, i, l);
+#pragma unroll
+            for (int n = 0; n < kAhead; ++n) w[n] += block == b + n ? v : 0;
+        });
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+            w[n] = wave_sum(w[n]);
+            if ((threadIdx.x & 63) == 0 && w[n]) atomicAdd(&sm.block[b + n], w[n]);
+        }
+    }
+    __syncthreads();
 }
 
 __device__ u64 pass_top(const Row& r, Smem& sm, int b0, int b1) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     u64 best = 0;
-    each(r, b0, b1, [&](int i, float l) {
+    each(r, b0, b1, [&](int, int i, float l) {
         const u64 n = number(l, i);
         best = n > best ? n : best;
     });
@@ -194,26 +225,32 @@ __device__ u64 pass_top(const Row& r, Smem& sm, int b0, int b1) {
         const u64 o = __shfl_xor(best, off, 64);
         best = o > best ? o : best;
     }
-    if (lane == 0) sm.wave_a[wave] = best;
+    if (lane == 0) sm.wave[0][0][wave] = best;
     __syncthreads();
-    for (int w = 0; w < kWaves; ++w) best = sm.wave_a[w] > best ? sm.wave_a[w] : best;
-    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) best = sm.wave[0][0][w] > best ? sm.wave[0][0][w] : best;
     return best;
 }
 
-// The row's settings.  True where there is a choice to make: else (greedy, or no token at all) `best` is the answer.
-__device__ __forceinline__ bool settings(const Args& a, int m, u64 best, Row& r, int& k, float& p) {
-    const float T = a.s.temperature ? a.s.temperature[m] : 1.0f;
+// The row's settings, and whether there is a choice to make: else (greedy, or no token at all) `best` is the answer.
+struct Settings {
+    float T, p, low, u;
+    int k;
+    __device__ __forceinline__ Settings(const Args& a, int m)
+        : T(a.s.temperature ? a.s.temperature[m] : 1.0f), p(a.s.top_p ? a.s.top_p[m] : 1.0f),
+          low(a.s.min_p ? a.s.min_p[m] : 0.0f), u(a.s.u[m]), k(a.s.top_k ? a.s.top_k[m] : 0) {
+        if (k < 0 || k >= a.s.V) k = 0;
+        low = low < 1.0f ? low : low >= 1.0f ? 1.0f : 0.0f;   // (a NaN: none)
+    }
+    __device__ __forceinline__ bool chosen(u64 best) const { return best != 0 && T > 0.0f; }
+    __device__ __forceinline__ bool cut() const { return k > 0 || p < 1.0f; }
+};
+__device__ __forceinline__ Row row_of(const Args& a, int m) { return {a.s.logits + m * a.s.stride, int(a.s.V)}; }
+__device__ __forceinline__ void set_row(Row& r, const Settings& t, u64 best) {
     r.best = best;
-    if (best == 0 || !(T > 0.0f)) return false;
     r.top = double(logit_of(uint32_t(best >> 32)));
-    r.inv = 1.0 / double(T);
-    k = a.s.top_k ? a.s.top_k[m] : 0;
-    k = k > 0 && k < r.V ? k : 0;
-    p = a.s.top_p ? a.s.top_p[m] : 1.0f;
-    const float mp = a.s.min_p ? a.s.min_p[m] : 0.0f;
-    r.low = mp < 1.0f ? double(mp) : mp >= 1.0f ? 1.0 : 0.0;   // (a NaN: none)
-    return true;
+    r.inv = 1.0 / double(t.T);
+    r.low = double(t.low);
 }
 __device__ __forceinline__ void write_only(const Args& a, int m, u64 best) {
     if (threadIdx.x == 0) {
@@ -233,7 +270,7 @@ __device__ void pass_bins(const Row& r, Smem& sm, bool masses, int b0, int b1) {
         sm.bins.w[b] = 0;
     }
     __syncthreads();
-    each(r, b0, b1, [&](int, float l) {
+    each(r, b0, b1, [&](int, int, float l) {
         const double x = distance(r, l);
         if (!(x <= kLast)) return;
         const int b = bin_of(x);
@@ -250,74 +287,97 @@ __device__ void pass_bins(const Row& r, Smem& sm, bool masses, int b0, int b1) {
 __device__ void find_bins(Smem& sm, int k, float p) {
     constexpr int kEach = kBins / kThreads;
     const int b0 = threadIdx.x * kEach;
-    u64 n = 0, w = 0;
+    u64 n[kEach], w[kEach], n_sum = 0, w_sum = 0;
+#pragma unroll
     for (int j = 0; j < kEach; ++j) {
-        n += sm.bins.n[b0 + j];
-        w += sm.bins.w[b0 + j];
+        n[j] = sm.bins.n[b0 + j];
+        w[j] = sm.bins.w[b0 + j];
+        n_sum += n[j];
+        w_sum += w[j];
     }
-    u64 n_before = block_scan(n, sm.wave_a) - n, w_before = block_scan(w, sm.wave_b) - w;
-    const u64 all_n = block_sum(n, sm.wave_a), all_w = block_sum(w, sm.wave_b);
-    if (threadIdx.x == 0) sm.cuts = {kBins, kBins, -1, -1, 0, all_w, 0};
-    __syncthreads();
+    if (threadIdx.x == 0) {
+        sm.cuts = {kBins, kBins, -1, -1, 0, 0, 0};
+        sm.k_mass = 0;
+    }
+    const Sums s = block_sums(sm, 0, n_sum, w_sum);
     // top-k's: the first bin at which the count reaches k
-    if (k > 0 && u64(k) < all_n) {
-        u64 nb = n_before, wb = w_before;
+    const bool has_k = k > 0 && u64(k) < s.all_a;
+    u64 nb = s.a - n_sum, wb = s.b - w_sum;
+    if (has_k) {
+#pragma unroll
         for (int j = 0; j < kEach; ++j) {
-            if (nb < u64(k) && nb + sm.bins.n[b0 + j] >= u64(k)) {
+            if (nb < u64(k) && nb + n[j] >= u64(k)) {
                 sm.cuts.kbin = sm.cuts.sure = b0 + j;
                 sm.cuts.k_left = uint32_t(u64(k) - nb);
                 sm.cuts.k_before = wb;
+                sm.k_mass = w[j];
             }
-            nb += sm.bins.n[b0 + j];
-            wb += sm.bins.w[b0 + j];
+            nb += n[j];
+            wb += w[j];
         }
+    } else if (threadIdx.x == 0) {
+        sm.cuts.k_before = s.all_b;
     }
     __syncthreads();
     if (p < 1.0f) {
-        // top-p's: its goal lies between those of the masses without and with all of kbin
-        const u64 most = sm.cuts.kbin < 0 ? all_w : sm.cuts.k_before + sm.bins.w[sm.cuts.kbin];
-        const double lo = double(p) * double(sm.cuts.k_before), hi = double(p) * double(most);
-        // (the first bin whose sum reaches a goal; at least the first that has a token: what is kept is never empty)
-        u64 wb = w_before;
+        // top-p's: its goal lies between those of the masses without and with all of kbin; the first bin whose sum reaches
+        // it, at least the first that has a token: what is kept is never empty
+        const u64 least = sm.cuts.k_before, most = least + sm.k_mass;
+        const double lo = double(p) * double(least), hi = double(p) * double(most);
+        wb = s.b - w_sum;
+#pragma unroll
         for (int j = 0; j < kEach; ++j) {
-            const u64 we = wb + sm.bins.w[b0 + j];
+            const u64 we = wb + w[j];
             if (we > 0 && double(we) >= lo && (wb == 0 || double(wb) < lo)) {
-                sm.cuts.first = b0 + j;
+                sm.cuts.first = sm.cuts.sure = b0 + j;
                 sm.cuts.p_before = wb;
             }
             if (we > 0 && double(we) >= hi && (wb == 0 || double(wb) < hi)) sm.cuts.last = b0 + j;
             wb = we;
         }
         __syncthreads();
-        if (threadIdx.x == 0) sm.cuts.sure = sm.cuts.first;
     }
-    __syncthreads();
 }
 
-// Pass 3: masses of the part's blocks (sure tokens) and the tokens of the cuts' bins.
-template <class Put, class Block>
-__device__ __forceinline__ void pass_masses(const Row& r, Smem& sm, const Cuts& c, int b0, int b1, const Put& put, const Block& block) {
-    for (int b = b0; b < b1; ++b) {
+// Pass 3: masses of the part's blocks (sure tokens), and the tokens of the cuts' bins to sm.list, counted in sm.count (past
+// kCap counted only).
+__device__ void pass_masses(const Row& r, Smem& sm, const Cuts& c, int b0, int b1) {
+    sum_blocks(r, sm, b0, b1, [&](int, int i, float l) {
         u64 w = 0;
-        each(r, b, b + 1, [&](int i, float l) {
-            const double x = distance(r, l);
-            if (!(x <= kLast)) return;
+        const double x = distance(r, l);
+        if (x <= kLast) {
             const int bin = bin_of(x);
             if (bin < c.sure) {
                 double e;
                 const u64 m = weigh(sm, x, e);
-                w += x == 0.0 || e >= r.low ? m : 0;
+                w = x == 0.0 || e >= r.low ? m : 0;
             }
-            if ((bin >= c.first && bin <= c.last) || bin == c.kbin) put(number(l, i));
-        });
-        w = block_sum(w, sm.wave_a);
-        if (threadIdx.x == 0) block(b, w);
-    }
+            if ((bin >= c.first && bin <= c.last) || bin == c.kbin) {
+                const uint32_t at = atomicAdd(&sm.count, 1u);
+                if (at < kCap) sm.list[at] = number(l, i);
+            }
+        }
+        return w;
+    });
 }
 
-// The collected numbers (n, in LDS) in falling order.
+// The collected numbers (n, in LDS) in falling order: each to its rank where a thread has one (the numbers differ), else sorted
+// in a network.
 __device__ void sort_list(Smem& sm, int n) {
-    int size = 64;
+    if (n <= kThreads) {
+        const int i = threadIdx.x;
+        const u64 mine = i < n ? sm.list[i] : 0;
+        int rank = 0;
+        if (i < ((n + 63) & ~63)) {
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) rank += sm.list[j] > mine;
+        }
+        __syncthreads();
+        if (i < n) sm.list[rank] = mine;
+        __syncthreads();
+        return;
+    }
+    int size = kThreads;
     while (size < n) size <<= 1;
     for (int i = n + threadIdx.x; i < size; i += kThreads) sm.list[i] = 0;
     __syncthreads();
@@ -335,66 +395,67 @@ __device__ void sort_list(Smem& sm, int n) {
         }
 }
 
-__device__ __forceinline__ u64 weigh_number(const Row& r, const Smem& sm, u64 number, double& e) {
-    const double x = distance(r, logit_of(uint32_t(number >> 32)));
-    return weigh(sm, x, e);
-}
-
 // The cut from the sorted list; the kept tokens' masses go to their blocks.
 __device__ void resolve_list(const Row& r, Smem& sm, int n, float p) {
     const Cuts c = sm.cuts;
     constexpr int kEach = kCap / kThreads;
     const int i0 = threadIdx.x * kEach;
-    // tokens of kbin are the last of the list where there is one; `head` of the list are before them
-    u64 in_head = 0;
-    for (int j = 0; j < kEach; ++j)
-        if (i0 + j < n && c.kbin >= 0) in_head += bin_of(distance(r, logit_of(uint32_t(sm.list[i0 + j] >> 32)))) < c.kbin;
-    const int head = c.kbin >= 0 ? int(block_sum(in_head, sm.wave_a)) : n;
-    const int limit = c.kbin >= 0 ? min(n, head + int(c.k_left)) : n;      // of the list, by top-k
+    u64 number[kEach], w[kEach];
+    double e[kEach];
+    u64 ahead = 0, mass = 0;       // tokens before kbin (those of kbin are the list's last), masses of all
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        number[j] = i0 + j < n ? sm.list[i0 + j] : 0;
+        w[j] = 0;
+        if (number[j]) {
+            const double x = distance(r, logit_of(uint32_t(number[j] >> 32)));
+            w[j] = weigh(sm, x, e[j]);
+            ahead += c.kbin < 0 || bin_of(x) < c.kbin;
+        }
+        mass += w[j];
+    }
+    if (threadIdx.x == 0) {
+        sm.cut = ~u64(0);                             // (where the list keeps none: the sure ones alone)
+        sm.k_mass = 0;
+    }
+    const Sums s = block_sums(sm, 0, mass, ahead);
+    const int head = int(s.all_b), limit = c.kbin >= 0 ? min(n, head + int(c.k_left)) : n;      // of the list, by top-k
+    u64 before = c.p_before + s.a - mass;
     if (p < 1.0f) {
-        u64 w[kEach], mine = 0, mine_k = 0;
+        // mass of the first top_k: up to `limit`
+        u64 at = s.a - mass, head_mass = 0, limit_mass = 0;
+#pragma unroll
         for (int j = 0; j < kEach; ++j) {
-            double e;
-            w[j] = i0 + j < limit ? weigh_number(r, sm, sm.list[i0 + j], e) : 0;
-            mine += w[j];
-            if (i0 + j >= head) mine_k += w[j];
+            if (i0 + j == head) head_mass = at;
+            if (i0 + j == limit) limit_mass = at;
+            at += w[j];
         }
-        const u64 whole = c.k_before + block_sum(mine_k, sm.wave_a);       // mass of the first top_k
-        const double goal = double(p) * double(whole);
-        u64 before = c.p_before + block_scan(mine, sm.wave_b) - mine;
-        if (threadIdx.x == 0) sm.cut = c.p_before == 0 ? r.best : 0;       // (at least the first token)
+        // (each of one thread; a border at the list's end, or at the capacity's, is the sum of all)
+        if (i0 <= head && head < i0 + kEach) sm.wave[1][0][0] = head_mass;
+        if (i0 <= limit && limit < i0 + kEach) sm.wave[1][0][1] = limit_mass;
         __syncthreads();
-        // kept: those before which the sum has not reached the goal.  (Between `last` and kbin the list leaves tokens out: the
-        // sum has reached the goal there.)
-        u64 last = 0;
+        const u64 to_head = head < kCap ? sm.wave[1][0][0] : s.all_a, to_limit = limit < kCap ? sm.wave[1][0][1] : s.all_a;
+        const double goal = double(p) * double(c.k_before + to_limit - to_head);
+        // kept: those before which the sum has not reached the goal, and the first token.  (Between `last` and kbin the list
+        // leaves tokens out: the sum has reached the goal there.)
+#pragma unroll
         for (int j = 0; j < kEach; ++j) {
-            if (i0 + j < limit && double(before) < goal) last = sm.list[i0 + j];
-            before += w[j];
+            const u64 after = before + w[j];
+            const bool in = i0 + j < limit && (before == 0 || double(before) < goal);
+            if (in && (i0 + j + 1 >= limit || !(double(after) < goal))) sm.cut = number[j];
+            before = after;
         }
-        const u64 who = __ballot(last != 0);
-        // the smallest number kept: of the last wave that has one (numbers fall along the list)
-        if (who) {
-            const u64 v = __shfl(last, 63 - __clzll(who), 64);
-            if ((threadIdx.x & 63) == 0) sm.wave_a[threadIdx.x >> 6] = v;
-        } else if ((threadIdx.x & 63) == 0) {
-            sm.wave_a[threadIdx.x >> 6] = 0;
-        }
-        __syncthreads();
-        if (threadIdx.x == 0)
-            for (int v = 0; v < kWaves; ++v)
-                if (sm.wave_a[v]) sm.cut = sm.wave_a[v];
-        __syncthreads();
-        if (threadIdx.x == 0 && sm.cut == 0) sm.cut = ~u64(0);             // (none of the list: the sure ones alone)
-    } else if (threadIdx.x == 0) {
-        sm.cut = limit > 0 ? sm.list[limit - 1] : 0;
+    } else {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+            if (i0 + j + 1 == limit) sm.cut = number[j];
     }
     __syncthreads();
-    for (int j = 0; j < kEach; ++j) {
-        if (i0 + j >= n || sm.list[i0 + j] < sm.cut) continue;
-        double e;
-        const u64 m = weigh_number(r, sm, sm.list[i0 + j], e);
-        if (sm.list[i0 + j] >> 32 == r.best >> 32 || e >= r.low) atomicAdd(&sm.block[(~uint32_t(sm.list[i0 + j])) / kBlock], m);
-    }
+    const u64 cut = sm.cut;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+        if (number[j] && number[j] >= cut && (number[j] >> 32 == r.best >> 32 || e[j] >= r.low))
+            atomicAdd(&sm.block[(~uint32_t(number[j])) / kBlock], w[j]);
     __syncthreads();
 }
 
@@ -416,7 +477,7 @@ __device__ void radix(const Row& r, Smem& sm, bool by_mass, double goal, u64 lim
         }
         __syncthreads();
         const uint32_t prefix = sm.key;
-        each(r, 0, blocks, [&](int i, float l) {
+        each(r, 0, blocks, [&](int, int i, float l) {
             const double x = distance(r, l);
             const u64 n = number(l, i);
             const uint32_t key = uint32_t(n >> 32);
@@ -452,22 +513,20 @@ __device__ void radix(const Row& r, Smem& sm, bool by_mass, double goal, u64 lim
 __device__ u64 nth(const Row& r, Smem& sm, uint32_t key, u64 count) {
     const int blocks = (r.V + kBlock - 1) / kBlock;
     if (threadIdx.x == 0) sm.found = 0;
-    __syncthreads();
     u64 seen = 0;
-    for (int b = 0; b < blocks; ++b) {
+    for (int b = 0; b < blocks && seen < count; ++b) {
         // (kPer consecutive tokens a thread: index order)
         const int i0 = b * kBlock + threadIdx.x * kPer;
         u64 n = 0;
         for (int j = 0; j < kPer; ++j) n += i0 + j < r.V && key_of(r.l[i0 + j]) == key;
-        const u64 upto = seen + block_scan(n, sm.wave_a);
-        u64 at = upto - n;
+        const Sums s = block_sums(sm, b & 1, n);
+        u64 at = seen + s.a - n;
         for (int j = 0; j < kPer; ++j)
             if (i0 + j < r.V && key_of(r.l[i0 + j]) == key) {
                 ++at;
-                if (at <= count) atomicMax(reinterpret_cast<unsigned long long*>(&sm.found), u64(i0 + j) + 1);
+                if (at <= count) atomicMax(&sm.found, u64(i0 + j) + 1);
             }
-        seen += block_sum(n, sm.wave_b);
-        if (seen >= count) break;
+        seen += s.all_a;
     }
     __syncthreads();
     const u64 i = sm.found;
@@ -485,70 +544,64 @@ __device__ void resolve_row(const Row& r, Smem& sm, int k, float p) {
     const int blocks = (r.V + kBlock - 1) / kBlock;
     if (p < 1.0f) {
         u64 w = 0;
-        each(r, 0, blocks, [&](int i, float l) {
+        each(r, 0, blocks, [&](int, int i, float l) {
             const double x = distance(r, l);
             double e;
             if (x <= kLast && number(l, i) >= cut) w += weigh(sm, x, e);
         });
-        const double goal = double(p) * double(block_sum(w, sm.wave_a));
+        const double goal = double(p) * double(block_sums(sm, 0, w).all_a);
         radix(r, sm, true, goal, 0, cut);
         const uint32_t key = sm.key;
         double e;
-        const double each_w = double(weigh_number(r, sm, u64(key) << 32, e)), lack = goal - double(sm.above_w);
+        const double each_w = double(weigh(sm, distance(r, logit_of(key)), e)), lack = goal - double(sm.above_w);
         const u64 n = lack > 0.0 && each_w > 0.0 ? u64(ceil(lack / each_w)) : 1;
         const u64 by_p = nth(r, sm, key, n);
         cut = by_p > cut ? by_p : cut;
     }
     __syncthreads();
     if (threadIdx.x == 0) sm.cut = cut;
-    for (int b = 0; b < blocks; ++b) {
-        u64 w = 0;
-        each(r, b, b + 1, [&](int i, float l) {
-            const double x = distance(r, l);
-            if (!(x <= kLast) || number(l, i) < cut) return;
-            double e;
-            const u64 m = weigh(sm, x, e);
-            w += x == 0.0 || e >= r.low ? m : 0;
-        });
-        w = block_sum(w, sm.wave_a);
-        if (threadIdx.x == 0) sm.block[b] = w;
-    }
-    __syncthreads();
+    sum_blocks(r, sm, 0, blocks, [&](int, int i, float l) {
+        const double x = distance(r, l);
+        if (!(x <= kLast) || number(l, i) < cut) return u64(0);
+        double e;
+        const u64 m = weigh(sm, x, e);
+        return x == 0.0 || e >= r.low ? m : u64(0);
+    });
 }
 
 // The choice: masses of the blocks in sm.block, kept are numbers from sm.cut on and those of bins below cuts.sure.
-__device__ void choose(const Args& a, int m, const Row& r, Smem& sm, bool by_bins) {
+__device__ void choose(const Args& a, int m, const Row& r, Smem& sm, float u_row, bool by_bins) {
     const int blocks = (r.V + kBlock - 1) / kBlock;
     const u64 mine = int(threadIdx.x) < blocks ? sm.block[threadIdx.x] : 0;
     static_assert(kMaxBlocks <= kThreads, "a block a thread");
-    const u64 upto = block_scan(mine, sm.wave_a);
-    const u64 total = block_sum(mine, sm.wave_b);
-    double u = double(a.s.u[m]);
-    u = u > 0.0 ? u : 0.0;
+    const Sums s = block_sums(sm, 0, mine);
+    const u64 total = s.all_a;
+    const double u = u_row > 0.0f ? double(u_row) : 0.0;
     const u64 goal = u < 1.0 ? u64(floor(u * double(total))) : ~u64(0);
     const u64 need = goal < total - 1 ? goal : total - 1;   // the first token whose sum passes this
-    if (mine != 0 && need < upto && need >= upto - mine) {
-        sm.found = upto - mine;
+    if (mine != 0 && need < s.a && need >= s.a - mine) {
+        sm.found = s.a - mine;
         sm.count = threadIdx.x;
     }
     __syncthreads();
     const int i0 = int(sm.count) * kBlock + threadIdx.x * kPer;
+    float l[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) l[j] = i0 + j < r.V ? r.l[i0 + j] : __builtin_nanf("");
     u64 w[kPer], sum = 0;
     double e[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-        const int i = i0 + j;
-        const float l = i < r.V ? r.l[i] : __builtin_nanf("");
-        const double x = distance(r, l);
+        const double x = distance(r, l[j]);
         w[j] = 0;
         e[j] = 0.0;
-        if (x <= kLast && ((by_bins && bin_of(x) < sm.cuts.sure) || number(l, i) >= sm.cut)) {
+        if (x <= kLast && ((by_bins && bin_of(x) < sm.cuts.sure) || number(l[j], i0 + j) >= sm.cut)) {
             const u64 v = weigh(sm, x, e[j]);
             w[j] = x == 0.0 || e[j] >= r.low ? v : 0;
         }
         sum += w[j];
     }
-    u64 at = sm.found + block_scan(sum, sm.wave_a) - sum;
+    u64 at = sm.found + block_sums(sm, 1, sum).a - sum;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         if (w[j] != 0 && at <= need && at + w[j] > need) {
@@ -559,55 +612,47 @@ __device__ void choose(const Args& a, int m, const Row& r, Smem& sm, bool by_bin
     }
 }
 
-__device__ void finish(const Args& a, int m, const Row& r, Smem& sm, int k, float p, uint32_t collected) {
+__device__ void finish(const Args& a, int m, const Row& r, Smem& sm, const Settings& t, uint32_t collected) {
     if (collected > kCap) {
-        resolve_row(r, sm, k, p);
-        choose(a, m, r, sm, false);
+        resolve_row(r, sm, t.k, t.p);
+        choose(a, m, r, sm, t.u, false);
         return;
     }
-    if (sm.cuts.kbin >= 0 || p < 1.0f) {
+    if (sm.cuts.kbin >= 0 || t.p < 1.0f) {
         sort_list(sm, int(collected));
-        resolve_list(r, sm, int(collected), p);
-    } else if (threadIdx.x == 0) {
-        sm.cut = ~u64(0);
+        resolve_list(r, sm, int(collected), t.p);
+    } else {
+        if (threadIdx.x == 0) sm.cut = ~u64(0);
+        __syncthreads();
     }
-    __syncthreads();
-    choose(a, m, r, sm, true);
+    choose(a, m, r, sm, t.u, true);
 }
 
 // A workgroup per row, all passes.
 __global__ __launch_bounds__(kThreads) void sample_row_kernel(Args a) {
     __shared__ Smem sm;
     const int m = a.row0 + blockIdx.x, blocks = int((a.s.V + kBlock - 1) / kBlock);
-    Row r = {a.s.logits + m * a.s.stride, int(a.s.V)};
+    const Settings t(a, m);
+    Row r = row_of(a, m);
     make_table(sm);
     const u64 best = pass_top(r, sm, 0, blocks);
-    int k;
-    float p;
-    if (!settings(a, m, best, r, k, p)) {
+    if (!t.chosen(best)) {
         write_only(a, m, best);
         return;
     }
+    set_row(r, t, best);
     if (threadIdx.x == 0) {
         sm.cuts = {kBins, kBins, -1, -1, 0, 0, 0};
         sm.count = 0;
     }
     __syncthreads();
-    if (k > 0 || p < 1.0f) {
-        pass_bins(r, sm, p < 1.0f, 0, blocks);
-        find_bins(sm, k, p);
+    if (t.cut()) {
+        pass_bins(r, sm, t.p < 1.0f, 0, blocks);
+        find_bins(sm, t.k, t.p);
     }
     const Cuts c = sm.cuts;
-    pass_masses(r, sm, c, 0, blocks,
-                [&](u64 n) {
-                    const uint32_t at = atomicAdd(&sm.count, 1u);
-                    if (at < kCap) sm.list[at] = n;
-                },
-                [&](int b, u64 w) { sm.block[b] = w; });
-    __syncthreads();
-    const uint32_t collected = sm.count;
-    __syncthreads();
-    finish(a, m, r, sm, k, p, collected);
+    pass_masses(r, sm, c, 0, blocks);
+    finish(a, m, r, sm, t, sm.count);
 }
 
 // The passes as launches, a row over a.parts workgroups.
@@ -615,11 +660,10 @@ __global__ __launch_bounds__(kThreads) void sample_top_kernel(Args a) {
     __shared__ Smem sm;
     const int row = blockIdx.x / a.parts, part = blockIdx.x % a.parts, m = a.row0 + row;
     const int blocks = int((a.s.V + kBlock - 1) / kBlock);
-    const Row r = {a.s.logits + m * a.s.stride, int(a.s.V)};
-    const u64 best = pass_top(r, sm, part * a.part_blocks, min(blocks, (part + 1) * a.part_blocks));
+    const u64 best = pass_top(row_of(a, m), sm, part * a.part_blocks, min(blocks, (part + 1) * a.part_blocks));
     if (threadIdx.x == 0) a.f->top[row][part] = best;
 }
-__device__ u64 row_top(const Args& a, Smem& sm, int row) {
+__device__ u64 row_top(const Args& a, int row) {
     const int lane = threadIdx.x & 63;
     u64 best = 0;
     for (int i = lane; i < a.parts; i += 64) {
@@ -637,17 +681,17 @@ __global__ __launch_bounds__(kThreads) void sample_bins_kernel(Args a) {
     __shared__ Smem sm;
     const int row = blockIdx.x / a.parts, part = blockIdx.x % a.parts, m = a.row0 + row;
     const int blocks = int((a.s.V + kBlock - 1) / kBlock);
-    Row r = {a.s.logits + m * a.s.stride, int(a.s.V)};
-    int k;
-    float p;
-    if (!settings(a, m, row_top(a, sm, row), r, k, p) || (k == 0 && !(p < 1.0f))) return;
+    const Settings t(a, m);
+    const u64 best = row_top(a, row);
+    if (!t.chosen(best) || !t.cut()) return;
+    Row r = row_of(a, m);
+    set_row(r, t, best);
     make_table(sm);
-    __syncthreads();
-    pass_bins(r, sm, p < 1.0f, part * a.part_blocks, min(blocks, (part + 1) * a.part_blocks));
+    pass_bins(r, sm, t.p < 1.0f, part * a.part_blocks, min(blocks, (part + 1) * a.part_blocks));
     for (int b = threadIdx.x; b < kBins; b += kThreads)
         if (sm.bins.n[b]) {
             __hip_atomic_fetch_add(&a.z->count[row][b], sm.bins.n[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            if (p < 1.0f) __hip_atomic_fetch_add(&a.z->mass[row][b], sm.bins.w[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            if (t.p < 1.0f) __hip_atomic_fetch_add(&a.z->mass[row][b], sm.bins.w[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
         }
     if (!splitk_arrive(&a.z->arrived[0][row], a.parts, &sm.ticket)) return;
     for (int b = threadIdx.x; b < kBins; b += kThreads) {
@@ -657,43 +701,56 @@ __global__ __launch_bounds__(kThreads) void sample_bins_kernel(Args a) {
         __hip_atomic_store(&a.z->mass[row][b], u64(0), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
-    find_bins(sm, k, p);
+    find_bins(sm, t.k, t.p);
+    __syncthreads();
     if (threadIdx.x == 0) a.f->cuts[row] = sm.cuts;
 }
 __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Args a) {
     __shared__ Smem sm;
     const int row = blockIdx.x / a.parts, part = blockIdx.x % a.parts, m = a.row0 + row;
     const int blocks = int((a.s.V + kBlock - 1) / kBlock);
-    Row r = {a.s.logits + m * a.s.stride, int(a.s.V)};
-    int k;
-    float p;
-    const u64 best = row_top(a, sm, row);
-    if (!settings(a, m, best, r, k, p)) {
+    const Settings t(a, m);
+    const Cuts found = a.f->cuts[row];         // (not set where the row is not cut)
+    const u64 best = row_top(a, row);
+    if (!t.chosen(best)) {
         if (part == 0) write_only(a, m, best);
         return;
     }
+    Row r = row_of(a, m);
+    set_row(r, t, best);
     make_table(sm);
+    const Cuts c = t.cut() ? found : Cuts{kBins, kBins, -1, -1, 0, 0, 0};
     if (threadIdx.x == 0) {
-        sm.cuts = {kBins, kBins, -1, -1, 0, 0, 0};
-        if (k > 0 || p < 1.0f) sm.cuts = a.f->cuts[row];
+        sm.cuts = c;
+        sm.count = 0;
     }
-    __syncthreads();
-    const Cuts c = sm.cuts;
-    pass_masses(r, sm, c, part * a.part_blocks, min(blocks, (part + 1) * a.part_blocks),
-                [&](u64 n) {
-                    const uint32_t at = __hip_atomic_fetch_add(&a.z->collected[row], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    if (at < kCap) __hip_atomic_store(&a.f->list[row][at], n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                },
-                [&](int b, u64 w) { __hip_atomic_store(&a.f->block[row][b], w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); });
+    const int b0 = part * a.part_blocks, b1 = min(blocks, (part + 1) * a.part_blocks);
+    pass_masses(r, sm, c, b0, b1);
+    for (int b = b0 + threadIdx.x; b < b1; b += kThreads)
+        __hip_atomic_store(&a.f->block[row][b], sm.block[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t mine = sm.count;
+    if (mine) {       // (the same on every thread)
+        if (threadIdx.x == 0)
+            sm.ticket = __hip_atomic_fetch_add(&a.z->collected[row], mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        const uint32_t at = sm.ticket;
+        for (uint32_t i = threadIdx.x; i < min(mine, uint32_t(kCap)) && at + i < kCap; i += kThreads)
+            __hip_atomic_store(&a.f->list[row][at + i], sm.list[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
     if (!splitk_arrive(&a.z->arrived[1][row], a.parts, &sm.ticket)) return;
+    // (the whole list's places are loaded: how many count is known no earlier)
     const uint32_t collected = __hip_atomic_load(&a.z->collected[row], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int i = threadIdx.x; i < int(min(collected, uint32_t(kCap))); i += kThreads)
-        sm.list[i] = __hip_atomic_load(&a.f->list[row][i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    for (int i = threadIdx.x; i < blocks; i += kThreads)
-        sm.block[i] = __hip_atomic_load(&a.f->block[row][i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    u64 part_list[kCap / kThreads];
+#pragma unroll
+    for (int j = 0; j < kCap / kThreads; ++j)
+        part_list[j] = __hip_atomic_load(&a.f->list[row][j * kThreads + threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (int(threadIdx.x) < blocks)
+        sm.block[threadIdx.x] = __hip_atomic_load(&a.f->block[row][threadIdx.x], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int j = 0; j < kCap / kThreads; ++j) sm.list[j * kThreads + threadIdx.x] = part_list[j];
     __syncthreads();
     if (threadIdx.x == 0) __hip_atomic_store(&a.z->collected[row], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    finish(a, m, r, sm, k, p, collected);
+    finish(a, m, r, sm, t, collected);
 }
 
 }  // namespace
@@ -709,9 +766,9 @@ hipError_t launch_sample(const Sample& r, hipStream_t s, const char** name) {
     for (int64_t m = 0; m < r.M; m += kBatch) {
         const int rows = int(std::min<int64_t>(kBatch, r.M - m));
         a.row0 = int(m);
-        // about two workgroups a CU; rows enough for that, or short ones, are left whole
-        a.parts = std::min(blocks, std::max(1, 512 / rows));
-        if (a.parts <= 2) a.parts = rows >= 128 ? a.parts : 1;
+        // about four workgroups a CU; short rows, and rows enough for that, are left whole
+        a.parts = std::min(blocks, std::max(1, 1024 / rows));
+        if (blocks <= 2) a.parts = 1;
         a.part_blocks = (blocks + a.parts - 1) / a.parts;
         a.parts = (blocks + a.part_blocks - 1) / a.part_blocks;
         if (a.parts == 1) {
