@@ -172,8 +172,8 @@ __device__ __forceinline__ Sums block_sums(Smem& sm, int turn, u64 a, u64 b = 0)
     return s;
 }
 
-// f(block, i, l) for the row's tokens of blocks [b0, b1), every thread of the workgroup in step (i >= V: l is a NaN); the
-// loads of kAhead blocks are in flight together.
+// f(block, i, l) for the row's tokens of blocks [b0, b1), kPer of a thread at a time (token j at i + j kThreads; behind the row's
+// end l is a NaN), every thread of the workgroup in step; the loads of kAhead blocks are in flight together.
 constexpr int kAhead = 4;
 template <class F>
 __device__ __forceinline__ void each(const Row& r, int b0, int b1, const F& f) {
@@ -188,37 +188,48 @@ __device__ __forceinline__ void each(const Row& r, int b0, int b1, const F& f) {
             }
 #pragma unroll
         for (int n = 0; n < kAhead; ++n)
-#pragma unroll
-            for (int j = 0; j < kPer; ++j) f(b + n, (b + n) * kBlock + j * kThreads + int(threadIdx.x), l[n][j]);
+            if (b + n < b1) f(b + n, (b + n) * kBlock + int(threadIdx.x), l[n]);
     }
 }
-// Masses by block: f(block, i, l) is the token's; sums to sm.block[block].
+// True where none of the wave's tokens reaches `floor`: nothing to do for them.
+__device__ __forceinline__ bool all_below(const float (&l)[kPer], float floor) {
+    bool any = false;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) any |= l[j] >= floor;
+    return __ballot(any) == 0;
+}
+// A logit that no token of distance up to x falls below.
+__device__ __forceinline__ float floor_of(const Row& r, double T, double x) {
+    const double f = r.top - x * T;
+    const float low = float(f) - (fabsf(float(f)) + fabsf(float(r.top))) * 1e-6f;      // (more than the roundings of the terms)
+    return low == low ? low : -__builtin_inff();                                     // (an infinite l_max)
+}
+// Masses by block: f(i, l, w) gives the tokens'; sums to sm.block[block].
 template <class F>
-__device__ __forceinline__ void sum_blocks(const Row& r, Smem& sm, int b0, int b1, const F& f) {
+__device__ __forceinline__ void sum_blocks(const Row& r, Smem& sm, int b0, int b1, float floor, const F& f) {
     for (int b = b0 + threadIdx.x; b < b1; b += kThreads) sm.block[b] = 0;
     __syncthreads();
-    for (int b = b0; b < b1; b += kAhead) {
-        u64 w[kAhead] = {};
-        each(r, b, min(b + kAhead, b1), [&](int block, int i, float l) {
-            const u64 v = f(block, i, l);
+    each(r, b0, b1, [&](int block, int i, const float (&l)[kPer]) {
+        if (all_below(l, floor)) return;
+        u64 w[kPer], sum = 0;
+        f(i, l, w);
 #pragma unroll
-            for (int n = 0; n < kAhead; ++n) w[n] += block == b + n ? v : 0;
-        });
-#pragma unroll
-        for (int n = 0; n < kAhead; ++n) {
-            w[n] = wave_sum(w[n]);
-            if ((threadIdx.x & 63) == 0 && w[n]) atomicAdd(&sm.block[b + n], w[n]);
-        }
-    }
+        for (int j = 0; j < kPer; ++j) sum += w[j];
+        sum = wave_sum(sum);
+        if ((threadIdx.x & 63) == 0 && sum) atomicAdd(&sm.block[block], sum);
+    });
     __syncthreads();
 }
 
 __device__ u64 pass_top(const Row& r, Smem& sm, int b0, int b1) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     u64 best = 0;
-    each(r, b0, b1, [&](int, int i, float l) {
-        const u64 n = number(l, i);
-        best = n > best ? n : best;
+    each(r, b0, b1, [&](int, int i, const float (&l)[kPer]) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const u64 n = number(l[j], i + j * kThreads);
+            best = n > best ? n : best;
+        }
     });
 #pragma unroll
     for (int off = 32; off; off >>= 1) {
@@ -270,15 +281,23 @@ __device__ void pass_bins(const Row& r, Smem& sm, bool masses, int b0, int b1) {
         sm.bins.w[b] = 0;
     }
     __syncthreads();
-    each(r, b0, b1, [&](int, int, float l) {
-        const double x = distance(r, l);
-        if (!(x <= kLast)) return;
-        const int b = bin_of(x);
-        atomicAdd(&sm.bins.n[b], 1u);
-        if (masses) {
-            double e;
-            atomicAdd(&sm.bins.w[b], weigh(sm, x, e));
-        }
+    const float floor = floor_of(r, 1.0 / r.inv, kLast);
+    each(r, b0, b1, [&](int, int, const float (&l)[kPer]) {
+        if (all_below(l, floor)) return;
+        double x[kPer], e;
+        u64 w[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) x[j] = distance(r, l[j]);
+        if (masses)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) w[j] = weigh(sm, x[j] <= kLast ? x[j] : kLast, e);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if (x[j] <= kLast) {
+                const int b = bin_of(x[j]);
+                atomicAdd(&sm.bins.n[b], 1u);
+                if (masses) atomicAdd(&sm.bins.w[b], w[j]);
+            }
     });
     __syncthreads();
 }
@@ -342,22 +361,31 @@ __device__ void find_bins(Smem& sm, int k, float p) {
 // Pass 3: masses of the part's blocks (sure tokens), and the tokens of the cuts' bins to sm.list, counted in sm.count (past
 // kCap counted only).
 __device__ void pass_masses(const Row& r, Smem& sm, const Cuts& c, int b0, int b1) {
-    sum_blocks(r, sm, b0, b1, [&](int, int i, float l) {
-        u64 w = 0;
-        const double x = distance(r, l);
-        if (x <= kLast) {
-            const int bin = bin_of(x);
-            if (bin < c.sure) {
-                double e;
-                const u64 m = weigh(sm, x, e);
-                w = x == 0.0 || e >= r.low ? m : 0;
-            }
-            if ((bin >= c.first && bin <= c.last) || bin == c.kbin) {
-                const uint32_t at = atomicAdd(&sm.count, 1u);
-                if (at < kCap) sm.list[at] = number(l, i);
-            }
+    const int low_bin = max(max(c.sure - 1, c.last), c.kbin);          // (kBins - 1: all)
+    sum_blocks(r, sm, b0, b1, floor_of(r, 1.0 / r.inv, min(kLast, (low_bin + 1) / kBinsPerX)), [&](int i, const float (&l)[kPer], u64 (&w)[kPer]) {
+        double x[kPer];
+        int bin[kPer];
+        bool sure = false;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            x[j] = distance(r, l[j]);
+            bin[j] = x[j] <= kLast ? bin_of(x[j]) : kBins;
+            sure |= bin[j] < c.sure;
+            w[j] = 0;
         }
-        return w;
+        if (__ballot(sure) != 0)
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                double e;
+                const u64 m = weigh(sm, bin[j] < kBins ? x[j] : kLast, e);
+                w[j] = bin[j] < c.sure && (x[j] == 0.0 || e >= r.low) ? m : 0;
+            }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+            if ((bin[j] >= c.first && bin[j] <= c.last) || bin[j] == c.kbin) {
+                const uint32_t at = atomicAdd(&sm.count, 1u);
+                if (at < kCap) sm.list[at] = number(l[j], i + j * kThreads);
+            }
     });
 }
 
@@ -477,14 +505,17 @@ __device__ void radix(const Row& r, Smem& sm, bool by_mass, double goal, u64 lim
         }
         __syncthreads();
         const uint32_t prefix = sm.key;
-        each(r, 0, blocks, [&](int, int i, float l) {
-            const double x = distance(r, l);
-            const u64 n = number(l, i);
-            const uint32_t key = uint32_t(n >> 32);
-            if (!(x <= kLast) || n < floor || (shift + width < 32 && key >> (shift + width) != prefix >> (shift + width))) return;
-            double e;
-            atomicAdd(&sm.bins.n[(key >> shift) & (bins - 1)], 1u);
-            atomicAdd(&sm.bins.w[(key >> shift) & (bins - 1)], weigh(sm, x, e));
+        each(r, 0, blocks, [&](int, int i, const float (&l)[kPer]) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const double x = distance(r, l[j]);
+                const u64 n = number(l[j], i + j * kThreads);
+                const uint32_t key = uint32_t(n >> 32);
+                if (!(x <= kLast) || n < floor || (shift + width < 32 && key >> (shift + width) != prefix >> (shift + width))) continue;
+                double e;
+                atomicAdd(&sm.bins.n[(key >> shift) & (bins - 1)], 1u);
+                atomicAdd(&sm.bins.w[(key >> shift) & (bins - 1)], weigh(sm, x, e));
+            }
         });
         __syncthreads();
         if (threadIdx.x == 0) {
@@ -544,10 +575,13 @@ __device__ void resolve_row(const Row& r, Smem& sm, int k, float p) {
     const int blocks = (r.V + kBlock - 1) / kBlock;
     if (p < 1.0f) {
         u64 w = 0;
-        each(r, 0, blocks, [&](int, int i, float l) {
-            const double x = distance(r, l);
-            double e;
-            if (x <= kLast && number(l, i) >= cut) w += weigh(sm, x, e);
+        each(r, 0, blocks, [&](int, int i, const float (&l)[kPer]) {
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const double x = distance(r, l[j]);
+                double e;
+                if (x <= kLast && number(l[j], i + j * kThreads) >= cut) w += weigh(sm, x, e);
+            }
         });
         const double goal = double(p) * double(block_sums(sm, 0, w).all_a);
         radix(r, sm, true, goal, 0, cut);
@@ -560,12 +594,16 @@ __device__ void resolve_row(const Row& r, Smem& sm, int k, float p) {
     }
     __syncthreads();
     if (threadIdx.x == 0) sm.cut = cut;
-    sum_blocks(r, sm, 0, blocks, [&](int, int i, float l) {
-        const double x = distance(r, l);
-        if (!(x <= kLast) || number(l, i) < cut) return u64(0);
-        double e;
-        const u64 m = weigh(sm, x, e);
-        return x == 0.0 || e >= r.low ? m : u64(0);
+    sum_blocks(r, sm, 0, blocks, -__builtin_inff(), [&](int i, const float (&l)[kPer], u64 (&w)[kPer]) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const double x = distance(r, l[j]);
+            double e;
+            w[j] = 0;
+            if (!(x <= kLast) || number(l[j], i + j * kThreads) < cut) continue;
+            const u64 m = weigh(sm, x, e);
+            w[j] = x == 0.0 || e >= r.low ? m : 0;
+        }
     });
 }
 
