@@ -70,21 +70,23 @@ void kv_kinds(int bits, int64_t dim, const F& f) {
 }
 
 // The token's sequence and its position in that sequence's cache; seq < 0 for a row of no sequence.
-// Every lane of the wave is active; the starts are read 64 at a time.
+// Every lane of the wave is active; starts and lengths are read together, 64 sequences at a time.
 struct KvToken {
     int seq, pos;
 };
 __device__ __forceinline__ KvToken kv_token(const KvView& c, int t) {
     const int lane = threadIdx.x & 63;
-    int b = 0;
+    if (t < c.q_start[0]) return {-1, 0};
     for (int i0 = 0; i0 < c.seqs; i0 += 64) {
-        const int i = i0 + lane;
-        const bool past = i < c.seqs && c.q_start[i + 1] <= t;
-        b += __popcll(__ballot(past));
+        const int i = min(i0 + lane, c.seqs - 1);
+        const int end = c.q_start[i + 1], len = c.kv_len[i];
+        const int past = __popcll(__ballot(end <= t));
+        if (past < 64) {     // (starts do not fall: the first sequence that ends behind the token; lanes behind the last repeat it)
+            const int b = __builtin_amdgcn_readfirstlane(past);
+            return {i0 + b, __builtin_amdgcn_readlane(len, b) - (__builtin_amdgcn_readlane(end, b) - t)};
+        }
     }
-    b = __builtin_amdgcn_readfirstlane(b);
-    if (b >= c.seqs || t < c.q_start[0]) return {-1, 0};
-    return {b, c.kv_len[b] - (c.q_start[b + 1] - t)};
+    return {-1, 0};
 }
 
 // Page of position `pos` of sequence b, or -1 where the table has none (also a page outside the cache).

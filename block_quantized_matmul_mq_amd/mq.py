@@ -577,6 +577,7 @@ class KVCache:
         if _nbytes(data) != need:
             _refuse(-4, "KVCache", f"data holds {_nbytes(data)} bytes, this cache is exactly {need}")
         self.data, self.qtype, self.pages, self.page_tokens, self.heads, self.dim = data, qtype, pages, page_tokens, heads, dim
+        self._device = data.get_device()
         self._c = _Cache(data.data_ptr(), qtype, pages, page_tokens, heads, dim)
         self._ref = ctypes.addressof(self._c)
 
@@ -593,6 +594,8 @@ class KVSeqs:
         _i32(kv_len, B, "KVSeqs", "kv_len")
         _i32(q_start, B + 1, "KVSeqs", "q_start")
         self.q_start, self.kv_len, self.table = q_start, kv_len, table
+        self._device = table.get_device() if table.get_device() == kv_len.get_device() == q_start.get_device() else -1
+        self._seqs, self._width = B, width
         self._c = _Seqs(q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), B, width)
         self._ref = ctypes.addressof(self._c)
 
@@ -600,15 +603,29 @@ class KVSeqs:
 def _heads(t, fn, name, T, heads, dim):
     """The row stride of f32 [T, heads, dim], whose heads follow one another (rows may be parts of longer ones)."""
     import torch
+    if t.dtype is torch.float32 and t.dim() == 3:
+        n, h, d = t.shape
+        rows, per, one = t.stride()
+        if d == dim and (T is None or n == T) and (heads is None or h == heads) and one == 1 and (per == dim or h == 1):
+            return rows if n != 1 else h * dim
     if t.dtype is not torch.float32:
         _refuse(-1, fn, f"{name} must be float32, not {t.dtype}")
     if t.dim() != 3 or t.shape[2] != dim or (T is not None and t.shape[0] != T) or (heads is not None and t.shape[1] != heads):
         _refuse(-2, fn, f"{name} must be [{'T' if T is None else T}, {'heads' if heads is None else heads}, {dim}], "
                         f"not {tuple(t.shape)}")
-    rows, per, one = t.stride()
-    if one != 1 or (per != dim and t.shape[1] != 1):
-        _refuse(-1, fn, f"{name}: the heads of a row must follow one another (strides {t.stride()})")
-    return rows if t.shape[0] != 1 else t.shape[1] * dim
+    _refuse(-1, fn, f"{name}: the heads of a row must follow one another (strides {t.stride()})")
+
+
+def _same_cache_device(fn, cache, seqs, *tensors):
+    """Every tensor on the cache's GPU, and the sequences' arrays (their devices were read when they were made)."""
+    d = cache._device
+    if d >= 0 and seqs._device == d:
+        for t in tensors:
+            if t.get_device() != d:
+                break
+        else:
+            return
+    _same_device(fn, cache.data, seqs.q_start, seqs.kv_len, seqs.table, *tensors)
 
 
 def kv_append(cache, seqs, k, v, q=None, q_norm=None, k_norm=None, eps=1e-6, rope=ROPE_HALF, inv_freq=None, pos=None,
@@ -620,29 +637,33 @@ def kv_append(cache, seqs, k, v, q=None, q_norm=None, k_norm=None, eps=1e-6, rop
     fn = "kv_append"
     dim, T = cache.dim, k.shape[0]
     ks, vs = _heads(k, fn, "k", None, cache.heads, dim), _heads(v, fn, "v", T, cache.heads, dim)
-    tensors = [k, v, cache.data, seqs.q_start, seqs.kv_len, seqs.table]
+    given = [k, v]
     qs = outs = q_heads = 0
     if q is not None:
         qs, q_heads = _heads(q, fn, "q", T, None, dim), q.shape[1]
+        given.append(q)
         if q_out is None:
-            q_out = _new(stream, q, (T, q_heads, dim), torch.float32)
-        outs = _heads(q_out, fn, "q_out", T, q_heads, dim)
-        tensors += [q, q_out]
+            q_out, outs = _new(stream, q, (T, q_heads, dim), torch.float32), q_heads * dim
+        else:
+            outs = _heads(q_out, fn, "q_out", T, q_heads, dim)
+            given.append(q_out)
     elif q_out is not None:
         _refuse(-1, fn, "q_out without q")
-    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None:
-            _f32(t, dim, fn, name)
-            tensors.append(t)
+    if q_norm is not None:
+        _f32(q_norm, dim, fn, "q_norm")
+        given.append(q_norm)
+    if k_norm is not None:
+        _f32(k_norm, dim, fn, "k_norm")
+        given.append(k_norm)
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         _f32(inv_freq, rot // 2, fn, "inv_freq")
-        tensors.append(inv_freq)
+        given.append(inv_freq)
     if pos is not None:
         _i32(pos, T, fn, "pos")
-        tensors.append(pos)
-    _same_device(fn, *tensors)
+        given.append(pos)
+    _same_cache_device(fn, cache, seqs, *given)
     _call(load().mq_kv_append, k, stream, cache._ref, seqs._ref, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs,
           _ptr(q_out), outs, T, q_heads, _ptr(q_norm), _ptr(k_norm), eps, rope, _ptr(inv_freq), rot, _ptr(pos))
     return q_out
@@ -652,15 +673,18 @@ def kv_read(cache, seqs, T, k=None, v=None, stream=None):
     """(k, v): f32 [T, heads, dim], the values that the cache holds at the places of the T rows."""
     import torch
     shape = (T, cache.heads, cache.dim)
+    given = []
     if k is None:
         k = _new(stream, cache.data, shape, torch.float32)
     else:
         _f32(k, T * cache.heads * cache.dim, "kv_read", "k")
+        given.append(k)
     if v is None:
         v = _new(stream, cache.data, shape, torch.float32)
     else:
         _f32(v, T * cache.heads * cache.dim, "kv_read", "v")
-    _same_device("kv_read", k, v, cache.data, seqs.q_start, seqs.kv_len, seqs.table)
+        given.append(v)
+    _same_cache_device("kv_read", cache, seqs, *given)
     _call(load().mq_kv_read, k, stream, cache._ref, seqs._ref, T, k.data_ptr(), v.data_ptr())
     return k, v
 
@@ -683,19 +707,18 @@ def attn(cache, seqs, q, scale=None, causal=True, window=0, max_q=None, max_kv=N
     fn = "attn"
     qs = _heads(q, fn, "q", None, None, cache.dim)
     T, q_heads, dim = q.shape
-    B, width = seqs.table.shape
     max_q = T if max_q is None else max_q
-    max_kv = width * cache.page_tokens if max_kv is None else max_kv
+    max_kv = seqs._width * cache.page_tokens if max_kv is None else max_kv
     if out is None:
         out = _new(stream, q, (T, q_heads, dim), torch.float32)
     else:
         _f32(out, T * q_heads * dim, fn, "out")
-    need = attn_scratch_bytes(cache.qtype, B, q_heads, cache.heads, dim, max_q, max_kv)
+    need = attn_scratch_bytes(cache.qtype, seqs._seqs, q_heads, cache.heads, dim, max_q, max_kv)
     if scratch is None:
         scratch = _new(stream, q, max(need, 16), torch.uint8, zero=_ATTN_COUNTER_BYTES)
     else:
         _buffer(scratch, need, fn, "scratch")
-    _same_device(fn, q, out, scratch, cache.data, seqs.q_start, seqs.kv_len, seqs.table)
+    _same_cache_device(fn, cache, seqs, q, out, scratch)
     _call(load().mq_attn, q, stream, cache._ref, seqs._ref, q.data_ptr(), qs, out.data_ptr(), T, q_heads,
           dim ** -0.5 if scale is None else scale, int(causal), window, max_q, max_kv, scratch.data_ptr(),
           _nbytes(scratch))
