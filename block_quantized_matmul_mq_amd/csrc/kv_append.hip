@@ -60,6 +60,14 @@ __device__ __forceinline__ void sincos64(double a, double& s, double& c) {
     if ((k + 1) & 2) c = -c;
 }
 
+// 1 / sqrt(v) of a normal v > 0: the instruction's 2^-26 or so and two Newton steps, each of which squares that.
+__device__ __forceinline__ double inverse_sqrt(double v) {
+    double y = __builtin_amdgcn_rsq(v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) y = fma(fma(-v * y, y, 1.0), 0.5 * y, y);
+    return y;
+}
+
 // Lanes l and l ^ 1, 2 and the other quad of eight, the other eight of sixteen: DPP moves; 16 and 32 apart: swaps.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp(uint32_t v) {
@@ -177,6 +185,14 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(AppendArgs a) {
             }
         }
     }
+    float wq[R], wk[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+        wq[i] = a.q_norm ? a.q_norm[lane + 64 * i] : 1.0f;
+        wk[i] = a.k_norm ? a.k_norm[lane + 64 * i] : 1.0f;
+    }
+    // pairs of halves that lie in one lane need no exchange
+    const bool own = R > 1 && a.rope == 1 && a.rot == D;
     for (int r = first; r < rows; r += step) {
         const bool is_q = r < q_rows, is_v = r >= q_rows + kv;
         const int h = is_q ? r : is_v ? r - q_rows - kv : r - q_rows;
@@ -194,11 +210,18 @@ __global__ __launch_bounds__(64 * kWaves) void kv_append_kernel(AppendArgs a) {
                 double s = 0.0;
 #pragma unroll
                 for (int i = 0; i < R; ++i) s = fma(y[i], y[i], s);
-                s = 1.0 / sqrt(wave_sum64(s) / D + double(a.eps));
+                s = fma(wave_sum64(s), 1.0 / D, double(a.eps));
+                s = s >= 0x1p-1000 && s <= 0x1p1000 ? inverse_sqrt(s) : 1.0 / sqrt(s);
 #pragma unroll
-                for (int i = 0; i < R; ++i) y[i] = y[i] * s * double(w[lane + 64 * i]);
+                for (int i = 0; i < R; ++i) y[i] = y[i] * s * double(is_q ? wq[i] : wk[i]);
             }
-            if (a.rope) {
+            if (own) {
+                double z[R];
+#pragma unroll
+                for (int i = 0; i < R; ++i) z[i] = fma(y[i], cs[i], y[(i + R / 2) % R] * sn[i]);
+#pragma unroll
+                for (int i = 0; i < R; ++i) y[i] = z[i];
+            } else if (a.rope) {
 #pragma unroll
                 for (int i = 0; i < R; ++i) row[wave][lane + 64 * i] = y[i];
                 __builtin_amdgcn_wave_barrier();
