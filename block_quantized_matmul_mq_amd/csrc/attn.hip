@@ -462,32 +462,34 @@ struct Slot {
                                                   split * kFloats * 4, kSplitkSc1);
         }
     }
-    // The last piece: every row's sums, in the order of the pieces.  share: LDS of pieces * ROWS * 2 floats.
+    // The last piece: every row's sums, in the order of the pieces.  share: LDS of pieces * ROWS floats.
     __device__ __forceinline__ void join(const AttnArgs& a, const Work& w, int pieces, float* share) const {
         const int live = min(ROWS, w.rows - w.row0);
         auto word = [&](int piece, int at) {
             return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, at * 4, piece * kFloats * 4, kSplitkSc1));
         };
-        float* const weight = share + pieces * ROWS;
-        for (int i = threadIdx.x; i < pieces * ROWS; i += NT) {
-            const int piece = i / ROWS, row = i % ROWS;
-            if (row < live) {
-                share[i] = word(piece, ROWS * D + row);
-                weight[i] = word(piece, ROWS * (D + 1) + row);
-            }
-        }
-        __syncthreads();
-        if (int(threadIdx.x) < live) {
-            const int row = threadIdx.x;
+        // kTeam threads a row, each some of its pieces
+        constexpr int kTeam = NT / ROWS < 16 ? NT / ROWS : 16;
+        const int row_of = threadIdx.x / kTeam, sub = threadIdx.x % kTeam;
+        if (row_of < live) {
             float top = kNone, sum = 0.0f;
-            for (int p = 0; p < pieces; ++p) top = fmaxf(top, share[p * ROWS + row]);
-            for (int p = 0; p < pieces; ++p) {
-                float& s = share[p * ROWS + row];
-                s = s == kNone ? 0.0f : __builtin_amdgcn_exp2f(s - top);
-                sum = fmaf(weight[p * ROWS + row], s, sum);
+            for (int p = sub; p < pieces; p += kTeam) {
+                const float m = word(p, ROWS * D + row_of);
+                share[p * ROWS + row_of] = m;
+                top = fmaxf(top, m);
             }
+#pragma unroll
+            for (int off = kTeam / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
+            for (int p = sub; p < pieces; p += kTeam) {
+                float& s = share[p * ROWS + row_of];
+                s = s == kNone ? 0.0f : __builtin_amdgcn_exp2f(s - top);
+                sum = fmaf(word(p, ROWS * (D + 1) + row_of), s, sum);
+            }
+            // (the team's sums in a fixed order: the result is the same every time)
+#pragma unroll
+            for (int off = kTeam / 2; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            for (int p = 0; p < pieces; ++p) share[p * ROWS + row] *= inv;
+            for (int p = sub; p < pieces; p += kTeam) share[p * ROWS + row_of] *= inv;
         }
         __syncthreads();
         for (int i = threadIdx.x; i < live * (D / 4); i += NT) {
@@ -509,6 +511,7 @@ struct Slot {
                     }
                 }
             };
+            if constexpr (D <= 128) batch(std::integral_constant<int, 32>{});
             batch(std::integral_constant<int, 16>{});
             batch(std::integral_constant<int, 4>{});
             batch(std::integral_constant<int, 1>{});
@@ -531,7 +534,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
     constexpr int kPad = 4;                                  // (rows a bank apart)
     __shared__ float part[2][kRows][D + kPad];
     __shared__ float stat[kWaves][2][kRows];
-    __shared__ float share[2 * kMaxSplits * kRows];
+    __shared__ float share[kMaxSplits * kRows];
     __shared__ unsigned ticket;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -924,7 +927,7 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, Rows
 template <int BITS, int D, int NT, int RT>
 __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArgs a) {
     constexpr int kTiles = D / 16, kBlocks = D / 32, kRows = NT / 4 * RT;
-    constexpr size_t kBuffers = 2 * sizeof(Staged<BITS, D, NT>), kJoin = 2 * kJoinRows * sizeof(float);
+    constexpr size_t kBuffers = 2 * sizeof(Staged<BITS, D, NT>), kJoin = kJoinRows * sizeof(float);
     __shared__ __align__(16) uint8_t memory[kBuffers > kJoin ? kBuffers : kJoin];
     __shared__ unsigned ticket;
     Staged<BITS, D, NT>* const buf = reinterpret_cast<Staged<BITS, D, NT>*>(memory);
