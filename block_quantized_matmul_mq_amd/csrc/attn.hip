@@ -297,21 +297,26 @@ __device__ __forceinline__ h8 value_codes(const Masks& m, const Step<BITS, D>& s
 template <int BITS, int D>
 __device__ __forceinline__ void attend(const Masks& masks, const Step<BITS, D>& s, Rows<BITS, D>& r, int key0, bool full, int lane, float unit_e) {
     constexpr int kBlocks = D / 32;
+    // (all blocks' first products, then their second ones: neither waits for another)
     float sc[8];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
+        f4 acc[kBlocks];
+        h8 k[kBlocks];
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) {
+            k[b] = key_codes<BITS>(masks, s.k[t], b);
+            acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[b], r.hi[b], f4{0, 0, 0, 0}, 0, 0, 0);
+        }
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b) acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[b], r.lo[b], acc[b], 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[4 * t + i] = 0.0f;
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b) {
-            const h8 a = key_codes<BITS>(masks, s.k[t], b);
-            f4 acc = {0, 0, 0, 0};
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, r.hi[b], acc, 0, 0, 0);
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, r.lo[b], acc, 0, 0, 0);
+        for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                sc[4 * t + i] = fmaf(half_of(s.ks[t][i * (kBlocks / 2) + b / 2], b & 1), acc[i], sc[4 * t + i]);
-        }
+                sc[4 * t + i] = fmaf(half_of(s.ks[t][i * (kBlocks / 2) + b / 2], b & 1), acc[b][i], sc[4 * t + i]);
     }
     uint32_t seen = 0xFF;
     if (!full) {
@@ -354,12 +359,11 @@ __device__ __forceinline__ void attend(const Masks& masks, const Step<BITS, D>& 
             l[i / 2] = w;
         }
         const h8 hi = __builtin_bit_cast(h8, h), lo = __builtin_bit_cast(h8, l);
-#pragma unroll
-        for (int j = 2 * b; j < 2 * b + 2; ++j) {
-            const h8 a = value_codes<BITS, D>(masks, s, j);
-            r.o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, hi, r.o[j], 0, 0, 0);
-            r.o[j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a, lo, r.o[j], 0, 0, 0);
-        }
+        const h8 a0 = value_codes<BITS, D>(masks, s, 2 * b), a1 = value_codes<BITS, D>(masks, s, 2 * b + 1);
+        r.o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, hi, r.o[2 * b], 0, 0, 0);
+        r.o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, hi, r.o[2 * b + 1], 0, 0, 0);
+        r.o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a0, lo, r.o[2 * b], 0, 0, 0);
+        r.o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a1, lo, r.o[2 * b + 1], 0, 0, 0);
     }
 }
 
@@ -468,54 +472,74 @@ struct Slot {
         auto word = [&](int piece, int at) {
             return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rsrc, at * 4, piece * kFloats * 4, kSplitkSc1));
         };
-        // kTeam threads a row, each some of its pieces
+        // A thread's first sums, and kTeam threads a row, each the statistics of some of its pieces: all of these loads in flight
+        // together (a trip to the device-coherent level is more than a microsecond).
+        constexpr int kFirst = ROWS == 16 && D <= 128 ? 16 : 8, kItems = D / 4;
         constexpr int kTeam = NT / ROWS < 16 ? NT / ROWS : 16;
+        auto sums = [&](int piece, int item) {
+            return __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, item * 16, piece * kFloats * 4, kSplitkSc1));
+        };
+        f4 ahead[kFirst];
+        const int mine = min(int(threadIdx.x), live * kItems - 1);
+#pragma unroll
+        for (int p = 0; p < kFirst; ++p) ahead[p] = sums(min(p, pieces - 1), mine);
         const int row_of = threadIdx.x / kTeam, sub = threadIdx.x % kTeam;
         if (row_of < live) {
             float top = kNone, sum = 0.0f;
             for (int p = sub; p < pieces; p += kTeam) {
-                const float m = word(p, ROWS * D + row_of);
+                const float m = word(p, ROWS * D + row_of), l = word(p, ROWS * (D + 1) + row_of);
                 share[p * ROWS + row_of] = m;
-                top = fmaxf(top, m);
+                // (sums so far follow a larger maximum)
+                const float to = fmaxf(top, m);
+                sum = fmaf(sum, top == kNone ? 0.0f : __builtin_amdgcn_exp2f(top - to), m == kNone ? 0.0f : l * __builtin_amdgcn_exp2f(m - to));
+                top = to;
             }
+            float all = top;
 #pragma unroll
-            for (int off = kTeam / 2; off; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
-            for (int p = sub; p < pieces; p += kTeam) {
-                float& s = share[p * ROWS + row_of];
-                s = s == kNone ? 0.0f : __builtin_amdgcn_exp2f(s - top);
-                sum = fmaf(word(p, ROWS * (D + 1) + row_of), s, sum);
-            }
+            for (int off = kTeam / 2; off; off >>= 1) all = fmaxf(all, __shfl_xor(all, off, 64));
+            sum = top == kNone ? 0.0f : sum * __builtin_amdgcn_exp2f(top - all);
             // (the team's sums in a fixed order: the result is the same every time)
 #pragma unroll
             for (int off = kTeam / 2; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            for (int p = sub; p < pieces; p += kTeam) share[p * ROWS + row_of] *= inv;
+            for (int p = sub; p < pieces; p += kTeam) {
+                float& s = share[p * ROWS + row_of];
+                s = s == kNone ? 0.0f : __builtin_amdgcn_exp2f(s - all) * inv;
+            }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < live * (D / 4); i += NT) {
-            const int row = i / (D / 4), at = row * D + i % (D / 4) * 4;
+        for (int i = threadIdx.x; i < live * kItems; i += NT) {
+            const int row = i / kItems;
             f4 sum = {0, 0, 0, 0};
             int p = 0;
+            auto add = [&](const f4& v, int piece) {
+                const float x = share[piece * ROWS + row];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[j], x, sum[j]);
+            };
+            if (i == int(threadIdx.x)) {
+#pragma unroll
+                for (int k = 0; k < kFirst; ++k)
+                    if (k < pieces) add(ahead[k], k);
+                p = min(kFirst, pieces);
+            }
             auto batch = [&](auto n_c) {      // that many loads in flight
                 constexpr int kN = decltype(n_c)::value;
                 for (; p + kN <= pieces; p += kN) {
                     f4 v[kN];
 #pragma unroll
-                    for (int k = 0; k < kN; ++k)
-                        v[k] = __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at * 4, (p + k) * kFloats * 4, kSplitkSc1));
+                    for (int k = 0; k < kN; ++k) v[k] = sums(p + k, i);
 #pragma unroll
-                    for (int k = 0; k < kN; ++k) {
-                        const float x = share[(p + k) * ROWS + row];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) sum[j] = fmaf(v[k][j], x, sum[j]);
-                    }
+                    for (int k = 0; k < kN; ++k) add(v[k], p + k);
                 }
             };
-            if constexpr (D <= 128) batch(std::integral_constant<int, 32>{});
+            if constexpr (ROWS == 16 && D <= 128) batch(std::integral_constant<int, 24>{});
             batch(std::integral_constant<int, 16>{});
+            batch(std::integral_constant<int, 8>{});
             batch(std::integral_constant<int, 4>{});
+            batch(std::integral_constant<int, 2>{});
             batch(std::integral_constant<int, 1>{});
-            *reinterpret_cast<f4*>(out_row(a, w, w.row0 + row) + i % (D / 4) * 4) = sum;
+            *reinterpret_cast<f4*>(out_row(a, w, w.row0 + row) + i % kItems * 4) = sum;
         }
     }
 };
@@ -579,12 +603,20 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
     int step = from + wave;
     if (step < to) {
         auto at = [&](int n) { return min(step + n * kWaves, to - 1); };
-        Step<BITS, D> s, t;
+        Step<BITS, D> s;
         int pages[2];
         pages_of(a, w, step, pages);
         s.load(a.c, pages, w.head, step * kStep, lane);
         pages_of(a, w, at(1), pages);
-        for (;;) {
+        if constexpr (D > 128) {      // (heads of 256: two steps' loads do not fit the registers)
+            for (;;) {
+                take(s, step);
+                step += kWaves;
+                if (step >= to) break;
+                s.load(a.c, pages, w.head, step * kStep, lane);
+                pages_of(a, w, at(1), pages);
+            }
+        } else for (Step<BITS, D> t;;) {
             t.load(a.c, pages, w.head, at(1) * kStep, lane);
             pages_of(a, w, at(2), pages);
             take(s, step);
