@@ -426,7 +426,8 @@ int mq_kv_read(const mq_kv_cache* cache, const mq_kv_seqs* seqs, int64_t T, floa
  * max_q, max_kv: at least the largest number of rows and the largest kv_len of a sequence (they size the grid
  * and the scratch, so that the call reads nothing back): rows past max_q of a sequence are not computed, and
  * a kv_len above max_kv counts as max_kv.
- * f32 accuracy: the factors of both products are held to 22 bits or more, sums and statistics are f32.  An
+ * f32 accuracy: the factors of both products are held to 21 bits or more, sums and statistics are f32.  (Beside a value of
+ * 2^11 or more in the same head and sequence, smaller ones are held to 2^-17.)  Scores past f32's range give NaN.  An
  * infinity or a NaN in a row of q, or in a key or value that it sees, makes the outputs that depend on it NaN
  * and no other.  Deterministic.
  * scratch: mq_attn_scratch_bytes(..) bytes (0 for sizes the call refuses), 16-byte aligned; its first 256 KiB are
@@ -554,7 +555,9 @@ int mq_device_lds_bytes(void);
  *     GGUF payload, few output tiles: see mq_gemm_scratch_bytes), else "mmq<type>";
  *   mq_gemv_ep, mq_gemm_ep: the name of the product's kernel; mq_moe_route: "moe_route";
  *   mq_moe_ffn: "moe_one" (one token, topk <= 64) or "moe_many";
- *   mq_kv_append: "kv_append"; mq_kv_read: "kv_read"; mq_attn: "attn"; mq_sample: "sample". */
+ *   mq_kv_append: "kv_append"; mq_kv_read: "kv_read"; mq_attn: "attn_few" (at most 32 rows of a sequence
+ *   and cache head: max_q * q_heads / heads) or "attn_many"; mq_sample: "sample_row" (a workgroup per row: short rows,
+ *   or rows enough for every CU) or "sample" (three launches, or two without top_k and top_p). */
 const char* mq_last_kernel(void);
 
 /* Library version string. */

@@ -259,3 +259,56 @@ def test_the_same_bits_every_time():
             first = out if first is None else first
             assert torch.equal(first, out)
         assert int(scratch[:1 << 18].sum()) == 0
+
+
+@pytest.mark.parametrize("qtype", TYPES, ids=NAME.get)
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("large", [200.0, 300.0, 5000.0, 60000.0, -60000.0])
+def test_values_of_all_sizes(qtype, n, large):
+    """Scales of single blocks far above and below the others', in the middle of a context and at its end: f16's whole range.
+    Errors to 2^-16 beside those of the largest values (which are held to 22 bits, as the small ones are without them)."""
+    rng = np.random.default_rng([qtype, n])
+    heads, dim = 2, 128
+    plan = Plan([n, n], [n + 260, n + 40], 32, rng)
+    data = random_cache(qtype, plan, heads, dim, rng)
+    raw = data.reshape(plan.pages, heads, -1)
+    at = ko.places(qtype, plan.page, dim)[5]
+
+    def put(b, pos, block, value):
+        page, slot = ko.place(plan.table, plan.pages, plan.page, b, pos)
+        s = at[slot, 32 * block]
+        raw[page, :, s:s + 2] = np.frombuffer(np.float16(value).tobytes(), np.uint8)
+
+    put(0, 100, 1, large)
+    put(0, n + 259, 3, large / 7)
+    put(0, 0, 0, 1e-6)
+    put(1, 3, 2, 6e-8)
+    put(1, n + 39, 0, large)         # seen by the last row alone
+    q = rng.standard_normal((plan.T, 6, dim)).astype(np.float32)
+    dev = device()
+    out = mq.attn(cache_on(dev, data, qtype, plan, heads, dim), plan.seqs(dev), to_dev(q, dev), max_q=n, max_kv=plan.max_kv).cpu().numpy()
+    ref = ko.attn(data, qtype, plan.pages, plan.page, heads, dim, plan.q_start, plan.kv_len, plan.table, q, dim ** -0.5)
+    err = np.abs(out - ref)
+    # by rows: those that see a large value, and those of the second sequence that do not
+    big = np.abs(ref).max((1, 2))[:, None, None]
+    assert (err <= 2.0 ** -16 + 2.0 ** -18 * big).all(), float((err / (2.0 ** -16 + 2.0 ** -18 * big)).max())
+    assert np.linalg.norm(err[:n]) <= 2e-6 * np.linalg.norm(ref[:n])
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("unit", [1e-5, 1e-3, 50.0])
+def test_values_all_small_or_large(n, unit):
+    """Relative accuracy does not depend on the values' size (scales in f16's subnormal range are exact, too)."""
+    rng = np.random.default_rng(n)
+    plan = Plan([n, n], [n + 200, n], 16, rng)
+    data = random_cache(mq.Q4_0, plan, 1, 64, rng)
+    raw = data.reshape(plan.pages, 1, -1)
+    vs = ko.places(mq.Q4_0, plan.page, 64)[5]
+    for s in np.unique(vs):
+        d = raw[:, :, s:s + 2].copy().view(np.float16).astype(np.float32) * (unit / 0.22)
+        raw[:, :, s:s + 2] = d.astype(np.float16).view(np.uint8)
+    q = rng.standard_normal((plan.T, 7, 64)).astype(np.float32)
+    dev = device()
+    out = mq.attn(cache_on(dev, data, mq.Q4_0, plan, 1, 64), plan.seqs(dev), to_dev(q, dev), max_q=n, max_kv=n + 200).cpu().numpy()
+    ref = ko.attn(data, mq.Q4_0, plan.pages, 16, 1, 64, plan.q_start, plan.kv_len, plan.table, q, 0.125)
+    assert np.linalg.norm(out - ref) <= 1e-6 * np.linalg.norm(ref)
