@@ -22,7 +22,7 @@
 // (token G + head), so that a decoded token uses the cache once for all its heads.  Two kernels:
 //   attn_few   16 rows to a workgroup, whose four waves divide the keys: bound by the cache's bytes, which go from
 //              memory to the lanes that use them, the next step's in flight.
-//   attn_many  64 or 128 rows to a workgroup, a wave 16 or 32 of them, over the same keys: bound by the vector unit, so the codes
+//   attn_many  128 rows to a workgroup (64 in dimensions above 128), a wave 32 (16) of them, over the same keys: bound by the vector unit, so the codes
 //              are unpacked once for the workgroup, into LDS as operands; and V with its scale, as two f16 (exact:
 //              f16 times a code), which takes the weights' multiplication and split per block off the waves for a third
 //              matrix instruction.
@@ -48,6 +48,7 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 32;                // keys of a step
 constexpr int kCounters = 65536;         // of the scratch; cut tiles are at most kTarget
 constexpr int kTarget = 512;             // workgroups that a call is cut into where it has fewer tiles (half of it: of 512 threads)
+constexpr int kFewTiles = 768;           // tiles of 16 rows up to which attn_few takes sequences of any number of rows
 constexpr int kMaxSplits = 64;
 constexpr int kJoinRows = 4096;          // of attn_many: pieces times rows of a tile at most (LDS of the join)
 constexpr int kMinManySteps = 8, kPieceSteps = 2;   // steps of a piece at least, and what its start and end cost
@@ -382,9 +383,9 @@ __device__ __forceinline__ float scale_top(const Step<BITS, D>& s) {
     hi = __builtin_elementwise_maximum(hi, -lo);
     return __builtin_elementwise_maximum(static_cast<float>(hi[0]), static_cast<float>(hi[1]));
 }
-// The largest exponent field of the finite scales of the sequence's tokens in the step; uniform.
+// The largest exponent field of the finite scales of the keys that the lane's row sees in the step.
 template <int BITS, int D>
-__device__ __forceinline__ int scale_exponent(const Step<BITS, D>& s, int key0, int len, int lane) {
+__device__ __forceinline__ int scale_exponent(const Step<BITS, D>& s, int key0, int first, int last, int lane) {
     int top = 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
@@ -392,11 +393,11 @@ __device__ __forceinline__ int scale_exponent(const Step<BITS, D>& s, int key0, 
         for (int i = 0; i < Step<BITS, D>::kScales; ++i) {
             const int key = key0 + 16 * t + 4 * (lane >> 4) + i / (D / 64);
             const int a = (s.vs[t][i] >> 10) & 31, b = (s.vs[t][i] >> 26) & 31;
-            if (key < len && s.there[t]) top = max(top, max(a == 31 ? 0 : a, b == 31 ? 0 : b));
+            if (key >= first && key < last && s.there[t]) top = max(top, max(a == 31 ? 0 : a, b == 31 ? 0 : b));
         }
 #pragma unroll
     for (int off = 32; off >= 16; off >>= 1) top = max(top, __shfl_xor(top, off, 64));
-    return __builtin_amdgcn_readfirstlane(top);
+    return top;
 }
 
 // A workgroup's part of the call: a tile of rows of one cache head, and of a piece of its keys.
@@ -577,7 +578,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
     r.last = last_key(a, w, row / a.group);
     // Weights are kept in units of 2^-unit_e, so that they stay in f16's upper range times V's scales: the largest scale
     // seen (2^(x - 14) at most, x its exponent field) is 2^7 then; a weight to 2^4 and a scale 2^4 times as large fit
-    // before the units change.
+    // before the units change.  A row has its own: what it does not see may not take bits from what it sees.
     constexpr int kRoom = 21;
     int unit_e = 0;
     float unit_top = -1.0f;          // scales to this fit
@@ -585,7 +586,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
     auto take = [&](const Step<BITS, D>& s, int step) {
         const int key0 = step * kStep;
         if (__ballot(!(scale_top(s) <= unit_top)) != 0) {
-            const int x = scale_exponent(s, key0, w.len, lane);
+            const int x = scale_exponent(s, key0, r.first, r.last, lane);
             if (unit_top < 0.0f || x > kRoom - unit_e + 4) {
                 const float by = ldexpf(1.0f, kRoom - x - unit_e);
                 r.l *= by;
@@ -1060,8 +1061,19 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
     slot.join(a, w, pieces, reinterpret_cast<float*>(memory));
 }
 
-// How a call is cut: tiles of 16 rows, or of 64 or 128 where a sequence has more than 32; and the keys of a tile into pieces where
-// there are few tiles.
+// How a call is cut: into tiles of 16 rows, or of 128 (64 in dimensions above 128) where a sequence has more than 256 and tiles of 16
+// would be more than kFewTiles; and the keys of a tile into pieces where there are few tiles.  Both sides, in us, 4-bit caches:
+//   rows x sequences and heads, keys, dimension    attn_few  attn_many
+//     84 x  4,  4096, 128                            17.5      52.5
+//    259 x 24,  4096, 128                            81        93
+//    511 x  4,  4096, 128                            33        66
+//   1029 x  4,  4096, 128                            63        72
+//    511 x 24,  4096, 128 (768 tiles of 16)         107       108
+//   1029 x 24,  4096, 128                           224       199
+//   2100 x 24,   600, 128                            80        59
+//    511 x 96,   600, 128                            84        66
+//    259 x 96,   600, 256                           136       123     (the rule's loss there)
+//   2100 x  4,  4096, 128                           103        93     (the same)
 struct Plan {
     int tile_rows, tiles, splits, chunk_steps;
     int64_t blocks;
@@ -1070,7 +1082,7 @@ size_t slot_bytes(int rows, int64_t dim) { return size_t(rows) * size_t(dim + 2)
 Plan plan(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q, int64_t max_kv) {
     Plan p;
     const int64_t rows = max_q * (q_heads / heads), steps = (max_kv + kStep - 1) / kStep + 1;
-    p.tile_rows = rows <= 32 ? 16 : rows <= 128 || dim > 128 ? 64 : 128;
+    p.tile_rows = rows <= 256 || seqs * heads * ((rows + 15) / 16) <= kFewTiles ? 16 : dim > 128 ? 64 : 128;
     const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows, items = seqs * heads * tiles;
     const int64_t most = p.tile_rows == 16 ? kMaxSplits : kJoinRows / p.tile_rows;
     const int64_t least = kMinManySteps;
@@ -1133,8 +1145,7 @@ hipError_t launch_attn(const Attn& r, hipStream_t s, const char** name) {
     kv_kinds(r.cache.bits, r.cache.dim, [&](auto bits, auto dim) {
         constexpr int kB = decltype(bits)::value, kD = decltype(dim)::value;
         if (p.tile_rows == 16) run(attn_few_kernel<kB, kD>, kThreads);
-        else if (p.tile_rows == 64) run(attn_many_kernel<kB, kD, 256, 1>, 256);
-        else if constexpr (kD <= 128) run(attn_many_kernel<kB, kD, 256, 2>, 256);
+        else run(attn_many_kernel<kB, kD, 256, kD <= 128 ? 2 : 1>, 256);
     });
     return hipGetLastError();
 }

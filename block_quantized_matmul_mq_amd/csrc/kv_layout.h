@@ -11,8 +11,8 @@
 //   K  token t's row of D bits / 8 bytes: dimension 32 b + 8 g + n (g = 0..3, n = 0..7) is the n-th code
 //      of the (bits)-byte unit g NB + b (low nibble first).
 //   V  16-token tile t / 16, then lane (t % 16 / 4, c = dim % 16), token pair t % 4 / 2, unit i, token
-//      parity t % 2, two bytes: the 64 bits / 16 ... codes of dimensions c + 16 j of the i-th run of
-//      64 (4 bits, j = 0..3, low nibble first) or 32 dimensions (8 bits, j = 0..1).
+//      parity t % 2: two bytes, the codes of dimensions c + 16 j of the i-th run of 64 dimensions
+//      (4 bits: j = 0..3, low nibble first) or of 32 (8 bits: j = 0, 1).
 // Two tokens never share a byte, so tokens are appended without reading their neighbours.
 #pragma once
 

@@ -41,6 +41,16 @@ class Plan:
         return max(max(self.kv), 1)
 
 
+def bound_for(kernel, plan, hq, heads):
+    """The bound max_q with which mq_attn takes the kernel: the lengths themselves, or the first bound above 256 rows and
+    768 tiles of 16 (of the call's sequences and heads) that the kernel of many rows serves."""
+    if kernel == "attn_few":
+        return plan.max_q
+    group = hq // heads
+    tiles = 768 // (len(plan.n) * heads) + 1
+    return max(16 * (tiles - 1) // group + 1, 256 // group + 1)
+
+
 def random_cache(qtype, plan, heads, dim, rng, unit=None):
     """Bytes of a cache whose values have a deviation of about 1 (scales of both signs for 4 bits)."""
     chunk = ko.chunk_bytes(qtype, plan.page, dim)

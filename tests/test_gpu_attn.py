@@ -6,9 +6,10 @@ import pytest
 from block_quantized_matmul_mq_amd import mq
 from oracle import kv_oracle as ko
 
-from kv_cases import NAME, TYPES, Plan, attn_bound, cache_on, check_attn, device, random_cache, to_dev
+from kv_cases import NAME, TYPES, Plan, attn_bound, bound_for, cache_on, check_attn, device, random_cache, to_dev
 
 pytestmark = pytest.mark.gpu
+KERNELS = ["attn_few", "attn_many"]
 
 # f32 sums of codes with their offset: errors of a few half steps of 2^-24 beside values that the offset makes twice
 # (8 bits: three times) as large, random over the 64 to 256 products and the 4 score blocks of a dimension of 128
@@ -16,17 +17,17 @@ NORM = {mq.Q4_0: 1e-6, mq.Q8_0: 1.5e-6}
 
 
 def run(qtype, plan, hq, heads, dim, rng, causal=True, window=0, data=None, q=None, scale=None, what="", norm=True, scratch=None,
-        **kw):
+        kernel="attn_few", **kw):
     import torch
     dev = device()
     data = random_cache(qtype, plan, heads, dim, rng) if data is None else data
     q = rng.standard_normal((plan.T, hq, dim)).astype(np.float32) if q is None else q
     cache, seqs = cache_on(dev, data, qtype, plan, heads, dim), plan.seqs(dev)
     out = torch.full((plan.T, hq, dim), 777.0, device=dev)
-    args = dict(causal=causal, window=window, max_q=plan.max_q, max_kv=plan.max_kv, scale=scale)
+    args = dict(causal=causal, window=window, max_q=bound_for(kernel, plan, hq, heads), max_kv=plan.max_kv, scale=scale)
     args.update(kw)
     got = mq.attn(cache, seqs, to_dev(q, dev), out=out, scratch=scratch, **args)
-    assert got is out and mq.last_kernel().startswith("attn")
+    assert got is out and mq.last_kernel() == kernel
     out = out.cpu().numpy()
     scale = dim ** -0.5 if scale is None else scale
     ref = ko.attn(data, qtype, plan.pages, plan.page, heads, dim, plan.q_start, plan.kv_len, plan.table, q, scale, causal, window)
@@ -48,37 +49,41 @@ def test_one_row_of_each_sequence(qtype, hq, heads, dim, page, causal, window):
 @pytest.mark.parametrize("qtype", TYPES, ids=NAME.get)
 @pytest.mark.parametrize("hq,heads,dim,page", [(14, 2, 64, 16), (7, 1, 128, 64), (4, 2, 256, 128), (3, 3, 128, 32)])
 @pytest.mark.parametrize("causal,window", [(True, 0), (True, 20), (False, 0)])
-def test_many_rows(qtype, hq, heads, dim, page, causal, window):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_many_rows(qtype, hq, heads, dim, page, causal, window, kernel):
     rng = np.random.default_rng([qtype, hq, dim, page, window, causal, 1])
     plan = Plan([2, 0, 33, 5, 71], [9, 50, 33, 130, 171], page, rng, behind=3)
-    run(qtype, plan, hq, heads, dim, rng, causal, window)
+    run(qtype, plan, hq, heads, dim, rng, causal, window, kernel=kernel)
 
 
 @pytest.mark.parametrize("window", [0, 1, 2, 16, 31, 1000])
-@pytest.mark.parametrize("n", [1, 9])
-def test_windows(n, window):
+@pytest.mark.parametrize("n", [1, 9, 40])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_windows(n, window, kernel):
     rng = np.random.default_rng([window, n])
-    run(mq.Q4_0, Plan([n, n], [n, 999], 16, rng), 4, 1, 128, rng, True, window)
+    run(mq.Q4_0, Plan([n, n], [n, 999], 16, rng), 4, 1, 128, rng, True, window, kernel=kernel)
 
 
 @pytest.mark.parametrize("qtype", TYPES, ids=NAME.get)
-@pytest.mark.parametrize("hq,heads,dim,n,kv", [(28, 4, 128, 1, 5000), (14, 2, 64, 1, 9001), (8, 1, 256, 2, 3333), (16, 1, 128, 40, 2600)])
-def test_long_contexts(qtype, hq, heads, dim, n, kv):
+@pytest.mark.parametrize("hq,heads,dim,n,kv", [(28, 4, 128, 1, 5000), (14, 2, 64, 1, 9001), (8, 1, 256, 2, 3333), (16, 1, 128, 40, 2600), (2, 2, 256, 33, 1500)])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_long_contexts(qtype, hq, heads, dim, n, kv, kernel):
     """Contexts that are cut over workgroups, beside a short sequence."""
     rng = np.random.default_rng([qtype, kv])
-    run(qtype, Plan([n, 1], [kv, 3], 64, rng), hq, heads, dim, rng)
+    run(qtype, Plan([n, 1], [kv, 3], 64, rng), hq, heads, dim, rng, kernel=kernel)
 
 
-def test_rows_that_see_nothing():
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_rows_that_see_nothing(kernel):
     """Lengths of zero, lengths below the number of rows, pages that are not there."""
     rng = np.random.default_rng(1)
     plan = Plan([1, 6, 3, 4, 2], [0, 2, 40, 64, 20], 16, rng)
     plan.table[2] = -1                             # no page of the sequence is there
     plan.table[3, 1], plan.table[3, 3] = plan.pages, -2147483648
-    out = run(mq.Q4_0, plan, 4, 2, 128, rng, what="empty rows")
+    out = run(mq.Q4_0, plan, 4, 2, 128, rng, what="empty rows", kernel=kernel)
     assert (out[:5] == 0).all() and (out[7:10] == 0).all()
-    run(mq.Q8_0, plan, 4, 2, 64, rng, window=8, what="empty rows, window")
-    run(mq.Q4_0, plan, 4, 2, 64, rng, causal=False, what="empty rows, not causal")
+    run(mq.Q8_0, plan, 4, 2, 64, rng, window=8, what="empty rows, window", kernel=kernel)
+    run(mq.Q4_0, plan, 4, 2, 64, rng, causal=False, what="empty rows, not causal", kernel=kernel)
 
 
 @pytest.mark.parametrize("n", [1, 20])
@@ -100,7 +105,8 @@ def test_lengths_past_the_bounds(n):
 
 @pytest.mark.parametrize("qtype", TYPES, ids=NAME.get)
 @pytest.mark.parametrize("n", [1, 5, 40])
-def test_what_no_length_covers_is_never_used(qtype, n):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_what_no_length_covers_is_never_used(qtype, n, kernel):
     """NaN scales in every place behind a sequence's end, in unused pages and in masked keys."""
     rng = np.random.default_rng([qtype, n])
     heads, dim = 2, 128
@@ -123,28 +129,31 @@ def test_what_no_length_covers_is_never_used(qtype, n):
             for s in np.unique(at[which][t]):
                 clean[p, :, s:s + 2] = 0
     q = rng.standard_normal((plan.T, 6, dim)).astype(np.float32)
-    a = run(qtype, plan, 6, heads, dim, rng, data=clean.reshape(-1), q=q)
+    a = run(qtype, plan, 6, heads, dim, rng, data=clean.reshape(-1), q=q, kernel=kernel)
     dev = device()
-    b = mq.attn(cache_on(dev, data, qtype, plan, heads, dim), plan.seqs(dev), to_dev(q, dev), max_q=n, max_kv=plan.max_kv)
+    b = mq.attn(cache_on(dev, data, qtype, plan, heads, dim), plan.seqs(dev), to_dev(q, dev),
+                max_q=bound_for(kernel, plan, 6, heads), max_kv=plan.max_kv)
+    assert mq.last_kernel() == kernel
     assert np.array_equal(a, b.cpu().numpy())
 
 
 @pytest.mark.parametrize("n", [1, 24])
 @pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
-def test_a_bad_query_or_key_spoils_its_own_rows_only(n, bad):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_bad_query_or_key_spoils_its_own_rows_only(n, bad, kernel):
     rng = np.random.default_rng(n)
     heads, dim, hq = 2, 64, 6
     plan = Plan([n, n], [n + 40, n + 3], 16, rng)
     data = random_cache(mq.Q4_0, plan, heads, dim, rng)
     q = rng.standard_normal((plan.T, hq, dim)).astype(np.float32)
-    clean = run(mq.Q4_0, plan, hq, heads, dim, rng, data=data, q=q)
+    clean = run(mq.Q4_0, plan, hq, heads, dim, rng, data=data, q=q, kernel=kernel)
     qb = q.copy()
     qb[0, 1, 5] = bad
     dev = device()
 
     def call(data, q):
-        return mq.attn(cache_on(dev, data, mq.Q4_0, plan, heads, dim), plan.seqs(dev), to_dev(q, dev), max_q=n,
-                       max_kv=plan.max_kv).cpu().numpy()
+        return mq.attn(cache_on(dev, data, mq.Q4_0, plan, heads, dim), plan.seqs(dev), to_dev(q, dev),
+                       max_q=bound_for(kernel, plan, hq, heads), max_kv=plan.max_kv).cpu().numpy()
 
     got = call(data, qb)
     assert np.isnan(got[0, 1]).all()
@@ -165,7 +174,8 @@ def test_a_bad_query_or_key_spoils_its_own_rows_only(n, bad):
 
 @pytest.mark.parametrize("size", [1e-30, 1e-6, 1.0, 30.0, 1e4])
 @pytest.mark.parametrize("scale", [0.125, -0.2, 0.0, 1e-3])
-def test_ranges_of_queries(size, scale):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_ranges_of_queries(size, scale, kernel):
     """Scores from nothing to one key taking all, a negative scale, and zero: the mean."""
     rng = np.random.default_rng(11)
     plan = Plan([3, 18], [70, 200], 32, rng)
@@ -177,13 +187,13 @@ def test_ranges_of_queries(size, scale):
     if big:       # one key takes all where the others are exp(-bound) behind: compared where the gap is clear
         dev = device()
         data = random_cache(mq.Q4_0, plan, 2, 64, rng)
-        out = mq.attn(cache_on(dev, data, mq.Q4_0, plan, 2, 64), plan.seqs(dev), to_dev(q, dev), scale=scale, max_q=18,
-                      max_kv=200).cpu().numpy()
+        out = mq.attn(cache_on(dev, data, mq.Q4_0, plan, 2, 64), plan.seqs(dev), to_dev(q, dev), scale=scale,
+                      max_q=bound_for(kernel, plan, 4, 2), max_kv=200).cpu().numpy()
         ref = ko.attn(data, mq.Q4_0, plan.pages, 32, 2, 64, plan.q_start, plan.kv_len, plan.table, q, scale)
         assert torch.isfinite(torch.from_numpy(out)).all()
         assert np.mean(np.abs(out - ref).max(-1) < 1e-2) > 0.9
     else:
-        run(mq.Q4_0, plan, 4, 2, 64, rng, q=q, scale=scale, norm=False)
+        run(mq.Q4_0, plan, 4, 2, 64, rng, q=q, scale=scale, norm=False, kernel=kernel)
 
 
 @pytest.mark.parametrize("n", [1, 17])
@@ -199,7 +209,7 @@ def test_strided_queries_and_large_bounds(n):
     cache, seqs = cache_on(dev, data, mq.Q4_0, plan, 2, 128), plan.seqs(dev)
     ref = ko.attn(data, mq.Q4_0, plan.pages, 16, 2, 128, plan.q_start, plan.kv_len, plan.table, x[:, 2:8], 128 ** -0.5)
     bound = attn_bound(data, mq.Q4_0, plan, 2, 128, x, 128 ** -0.5)
-    for max_q, max_kv in ((2 * n, 300), (500, 1 << 17), (None, None)):
+    for max_q, max_kv in ((2 * n, 300), (500, 1 << 17), (5000, 400), (None, None)):
         got = mq.attn(cache, seqs, xd[:, 2:8], max_q=max_q, max_kv=max_kv)
         torch.cuda.synchronize()
         check_attn(got.cpu().numpy(), ref, bound, f"max_q={max_q} max_kv={max_kv}", 1e-6)
@@ -240,7 +250,8 @@ def test_a_cache_of_more_than_four_gib():
     assert torch.equal(ref, got)
 
 
-def test_the_same_bits_every_time():
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_the_same_bits_every_time(kernel):
     """Results do not depend on which workgroup ends last, nor on what a workspace held (its counters aside)."""
     import torch
     dev = device()
@@ -249,22 +260,25 @@ def test_the_same_bits_every_time():
     data = random_cache(mq.Q4_0, plan, 4, 128, rng)
     q = to_dev(rng.standard_normal((plan.T, 28, 128)).astype(np.float32), dev)
     cache, seqs = cache_on(dev, data, mq.Q4_0, plan, 4, 128), plan.seqs(dev)
-    need = max(mq.attn_scratch_bytes(mq.Q4_0, 3, 28, 4, 128, 2, 4000), 1 << 18)
+    max_q = bound_for(kernel, plan, 28, 4)
+    need = mq.attn_scratch_bytes(mq.Q4_0, 3, 28, 4, 128, max_q, 4000)
+    assert need > 1 << 18        # joined pieces
     first = None
     for fill in (0, 255, 17):
         scratch = torch.full((need,), fill, dtype=torch.uint8, device=dev)
         scratch[:1 << 18] = 0
         for _ in range(5):
-            out = mq.attn(cache, seqs, q, max_q=2, max_kv=4000, scratch=scratch)
+            out = mq.attn(cache, seqs, q, max_q=max_q, max_kv=4000, scratch=scratch)
             first = out if first is None else first
             assert torch.equal(first, out)
         assert int(scratch[:1 << 18].sum()) == 0
 
 
 @pytest.mark.parametrize("qtype", TYPES, ids=NAME.get)
-@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("n", [1, 9, 40])
 @pytest.mark.parametrize("large", [200.0, 300.0, 5000.0, 60000.0, -60000.0])
-def test_values_of_all_sizes(qtype, n, large):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_values_of_all_sizes(qtype, n, large, kernel):
     """Scales of single blocks far above and below the others', in the middle of a context and at its end: f16's whole range.
     Errors to 2^-16 beside those of the largest values (which are held to 22 bits, as the small ones are without them)."""
     rng = np.random.default_rng([qtype, n])
@@ -286,7 +300,9 @@ def test_values_of_all_sizes(qtype, n, large):
     put(1, n + 39, 0, large)         # seen by the last row alone
     q = rng.standard_normal((plan.T, 6, dim)).astype(np.float32)
     dev = device()
-    out = mq.attn(cache_on(dev, data, qtype, plan, heads, dim), plan.seqs(dev), to_dev(q, dev), max_q=n, max_kv=plan.max_kv).cpu().numpy()
+    out = mq.attn(cache_on(dev, data, qtype, plan, heads, dim), plan.seqs(dev), to_dev(q, dev),
+                  max_q=bound_for(kernel, plan, 6, heads), max_kv=plan.max_kv).cpu().numpy()
+    assert mq.last_kernel() == kernel
     ref = ko.attn(data, qtype, plan.pages, plan.page, heads, dim, plan.q_start, plan.kv_len, plan.table, q, dim ** -0.5)
     err = np.abs(out - ref)
     # by rows: those that see a large value, and those of the second sequence that do not
@@ -297,7 +313,8 @@ def test_values_of_all_sizes(qtype, n, large):
 
 @pytest.mark.parametrize("n", [1, 40])
 @pytest.mark.parametrize("unit", [1e-5, 1e-3, 50.0])
-def test_values_all_small_or_large(n, unit):
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_values_all_small_or_large(n, unit, kernel):
     """Relative accuracy does not depend on the values' size (scales in f16's subnormal range are exact, too)."""
     rng = np.random.default_rng(n)
     plan = Plan([n, n], [n + 200, n], 16, rng)
@@ -309,6 +326,7 @@ def test_values_all_small_or_large(n, unit):
         raw[:, :, s:s + 2] = d.astype(np.float16).view(np.uint8)
     q = rng.standard_normal((plan.T, 7, 64)).astype(np.float32)
     dev = device()
-    out = mq.attn(cache_on(dev, data, mq.Q4_0, plan, 1, 64), plan.seqs(dev), to_dev(q, dev), max_q=n, max_kv=n + 200).cpu().numpy()
+    out = mq.attn(cache_on(dev, data, mq.Q4_0, plan, 1, 64), plan.seqs(dev), to_dev(q, dev),
+                  max_q=bound_for(kernel, plan, 7, 1), max_kv=n + 200).cpu().numpy()
     ref = ko.attn(data, mq.Q4_0, plan.pages, 16, 1, 64, plan.q_start, plan.kv_len, plan.table, q, 0.125)
     assert np.linalg.norm(out - ref) <= 1e-6 * np.linalg.norm(ref)

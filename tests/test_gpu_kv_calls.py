@@ -50,7 +50,7 @@ class Calls:
         return (mq.attn(self.cache, self.seqs, self.q, max_q=2, max_kv=1300, **kw),)
 
     def attn_many(self, **kw):
-        return (mq.attn(self.many_cache, self.many_seqs, self.many_q, max_q=50, max_kv=800, **kw),)
+        return (mq.attn(self.many_cache, self.many_seqs, self.many_q, max_q=1100, max_kv=800, **kw),)
 
     def sample(self, **kw):
         return mq.sample(self.logits, self.u[:3], top_p=self.p[:3], top_k=self.top_k[:3], **kw)
@@ -61,7 +61,7 @@ class Calls:
     def scratch(self, name):
         import torch
         size = {"attn": lambda: mq.attn_scratch_bytes(mq.Q4_0, 3, 6, 2, 64, 2, 1300),
-                "attn_many": lambda: mq.attn_scratch_bytes(mq.Q4_0, 2, 6, 2, 64, 50, 800),
+                "attn_many": lambda: mq.attn_scratch_bytes(mq.Q4_0, 2, 6, 2, 64, 1100, 800),
                 "sample": lambda: mq.sample_scratch_bytes(3, 20000), "sample_row": lambda: mq.sample_scratch_bytes(5, 3000)}
         return torch.zeros(max(size[name](), 16), dtype=torch.uint8, device=self.dev)
 
