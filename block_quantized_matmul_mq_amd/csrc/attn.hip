@@ -21,12 +21,17 @@
 // Queries: the G = q_heads / heads query heads of a cache head and the tokens of a sequence are one list of rows
 // (token G + head), so that a decoded token uses the cache once for all its heads.  Two kernels:
 //   attn_few   16 rows to a workgroup, whose four waves divide the keys: bound by the cache's bytes, which go from
-//              memory to the lanes that use them, the next step's in flight.
+//              memory to the lanes that use them, the next step's in flight; or, few workgroups, by one step's latency.
 //   attn_many  128 rows to a workgroup (64 in dimensions above 128), a wave 32 (16) of them, over the same keys: bound by the vector unit, so the codes
 //              are unpacked once for the workgroup, into LDS as operands; and V with its scale, as two f16 (exact:
 //              f16 times a code), which takes the weights' multiplication and split per block off the waves for a third
 //              matrix instruction.
 // Both cut the keys of a tile into pieces over workgroups where there are few tiles, joined by the last one.
+//
+// Measured, 4 bits, heads of 128: one sequence of 32768 keys, 28 heads on 4, 24 us (0.8 TB/s; its pieces alone 15, the join of
+// 64 pieces the rest); 64 sequences of up to 8192 keys, 40 heads on 8, 109 us (2.8 TB/s; of 8192 each 3.9 TB/s, a copy here
+// reads and writes 4.7).  512 tokens over 8192 keys, 28 heads on 4: 201 us, 290 TF of the formula's operations, 2.5 times as many
+// on the matrix units for f32 accuracy; these are busy 27 % of the time, the vector ALU 30 %.
 #include <algorithm>
 
 #include "kv_layout.h"

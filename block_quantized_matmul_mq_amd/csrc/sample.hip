@@ -18,6 +18,8 @@
 //      blocks, the block that the random number falls in, and the token in it.
 // A row is divided over workgroups and the passes over launches (the last workgroup of a row does a pass's single
 // part, mmq_splitk.h's exchange) where that is faster than a workgroup that makes all passes of a row by itself.
+// Measured: one row of 152064 25 us (launches of 3.6, 11.3 and 11.3: latency of their dependent rounds), nine of 32003 31 us,
+// 128 of 152064 98 us (0.8 TB/s; 16.5, 29.5 and 58: f64 exponentials of every token in the last two).
 // More collected tokens than fit (as where most logits are equal) are resolved by a radix selection over the row.
 #include <algorithm>
 

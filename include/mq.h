@@ -1,7 +1,8 @@
 /*
  * mq.h -- C ABI of libmq: matrix products of GGUF block-quantized weights
  * (Q4_0, Q4_1, Q5_0, Q5_1, Q8_0, Q4_K, Q5_K, Q6_K) with f32 activations on AMD
- * Instinct MI355X (gfx950).
+ * Instinct MI355X (gfx950), and the operators of a decoder around them: epilogues, mixtures of
+ * experts, a paged cache of keys and values with the attention over it, and sampling.
  *
  * Sources (page title, section):
  *   [BD2.3] "minfer CUDA Backend Design", 2.3 Weight residency and registry:

@@ -17,6 +17,8 @@ What is here:
                        ``q4_k_row_tiled`` Q4_K's row-tiled layout for the
                        long-row GEMV; ``epilogue``, ``moe_route`` and ``moe_ffn``
                        the feed-forward operators around the products.
+* ``kv_oracle``     -- the paged cache of keys and values (bytes, append), the
+                       attention over it and the sampling of a token, in f64.
 * ``bitwise_decode`` -- a second, independently written per-block decoder that
                        assembles every field bit by bit; it exists only to
                        cross-check ``mq_oracle``'s vectorised decoders.
