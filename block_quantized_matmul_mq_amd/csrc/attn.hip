@@ -1120,8 +1120,9 @@ size_t attn_scratch_bytes(int, int64_t seqs, int64_t q_heads, int64_t heads, int
     return size_t(kCounters) * 4 + (p.splits > 1 ? size_t(p.blocks) * slot_bytes(p.tile_rows, dim) : 0);
 }
 
-bool attn_fits(int64_t seqs, int64_t q_heads, int64_t heads, int64_t max_q, int64_t max_kv) {
-    return plan(seqs, q_heads, heads, 256, max_q, max_kv).blocks < (int64_t(1) << 31);
+// (a grid's threads are counted in 32 bits)
+bool attn_fits(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q, int64_t max_kv) {
+    return plan(seqs, q_heads, heads, dim, max_q, max_kv).blocks * kThreads < (int64_t(1) << 32);
 }
 
 hipError_t launch_attn(const Attn& r, hipStream_t s, const char** name) {

@@ -728,7 +728,7 @@ size_t mq_attn_scratch_bytes(int type, int64_t seqs, int64_t q_heads, int64_t he
         q_heads > MQ_KV_MAX_HEADS || q_heads % heads != 0 || (dim != 64 && dim != 128 && dim != 256) || max_q <= 0 ||
         max_q > MQ_MAX_M || max_kv <= 0 || max_kv > MQ_KV_MAX_TOKENS)
         return 0;
-    if (!attn_fits(seqs, q_heads, heads, max_q, max_kv)) return 0;
+    if (!attn_fits(seqs, q_heads, heads, dim, max_q, max_kv)) return 0;
     return attn_scratch_bytes(kv_bits(type), seqs, q_heads, heads, dim, max_q, max_kv);
 }
 
@@ -749,7 +749,7 @@ int mq_attn(const mq_kv_cache* cache, const mq_kv_seqs* seqs, const float* q, in
     if (max_q > MQ_MAX_M || max_kv > MQ_KV_MAX_TOKENS)
         return fail(MQ_ERR_SHAPE, "%s: max_q=%lld max_kv=%lld exceed %d and %d", fn, (long long)max_q, (long long)max_kv,
                     MQ_MAX_M, MQ_KV_MAX_TOKENS);
-    if (!attn_fits(seqs->seqs, q_heads, cache->heads, max_q, max_kv))
+    if (!attn_fits(seqs->seqs, q_heads, cache->heads, cache->dim, max_q, max_kv))
         return fail(MQ_ERR_SHAPE, "%s: seqs=%lld times max_q=%lld with %lld heads are more than a grid holds", fn,
                     (long long)seqs->seqs, (long long)max_q, (long long)q_heads);
     if (window < 0 || window > MQ_KV_MAX_TOKENS || (window > 0 && !causal))

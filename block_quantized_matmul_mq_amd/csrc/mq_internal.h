@@ -242,7 +242,7 @@ struct Attn {
 };
 size_t attn_scratch_bytes(int bits, int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q,
                           int64_t max_kv);
-bool attn_fits(int64_t seqs, int64_t q_heads, int64_t heads, int64_t max_q, int64_t max_kv);   // in a grid
+bool attn_fits(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max_q, int64_t max_kv);   // in a grid
 hipError_t launch_attn(const Attn& r, hipStream_t s, const char** kernel_name);
 // mq_sample (sample.hip)
 struct Sample {

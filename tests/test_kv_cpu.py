@@ -111,6 +111,10 @@ def test_attn_sizes_and_refusals():
     assert attn(hq=6) == -2 and attn(hq=512, qs=1 << 20) == -2 and attn(mq_=(1 << 20) + 1) == -2 and attn(mkv=(1 << 30) + 1) == -2
     assert attn(qs=1020) == -2 and attn(qs=1025) == -2
     assert attn(q=FAKE + 4) == -5 and attn(out=FAKE + 4) == -5 and attn(scr=FAKE + 8) == -5
+    # workgroups of 256 threads, at most 2^32 of them: 65535 sequences of 256 heads fit, 65536 do not
+    assert size(mq.Q4_0, 65536, 256, 256, 64, 1, 100) == 0 and size(mq.Q4_0, 65535, 256, 256, 64, 1, 100) > 0
+    assert size(mq.Q4_0, 64, 64, 8, 128, 1 << 20, 100) == 0 and size(mq.Q4_0, 31, 64, 8, 128, 1 << 20, 100) > 0
+    assert size(mq.Q4_0, 31, 64, 8, 256, 1 << 20, 100) == 0 and size(mq.Q4_0, 15, 64, 8, 256, 1 << 20, 100) > 0
     need = size(mq.Q4_0, 3, 8, 4, 128, 5, 1 << 20)
     if need:
         assert attn(mkv=1 << 20, sb=need - 1) == -4 and "scratch" in mq.last_error()
