@@ -1089,14 +1089,16 @@ Plan plan(int64_t seqs, int64_t q_heads, int64_t heads, int64_t dim, int64_t max
     const int64_t rows = max_q * (q_heads / heads), steps = (max_kv + kStep - 1) / kStep + 1;
     p.tile_rows = rows <= 256 || seqs * heads * ((rows + 15) / 16) <= kFewTiles ? 16 : dim > 128 ? 64 : 128;
     const int64_t tiles = (rows + p.tile_rows - 1) / p.tile_rows, items = seqs * heads * tiles;
-    const int64_t most = p.tile_rows == 16 ? kMaxSplits : kJoinRows / p.tile_rows;
-    const int64_t least = kMinManySteps;
-    // attn_few: pieces of 8 steps for a workgroup per CU, of 64 steps for four (lengths differ: pieces even them out)
-    int64_t splits = std::max<int64_t>(1, std::min(most, std::max(std::min(kTarget / 2 / items, steps / 8), std::min(2 * kTarget / items, steps / 64))));
-    if (p.tile_rows > 16) {
+    int64_t splits = 1;
+    if (p.tile_rows == 16) {
+        // pieces of 8 steps for a workgroup per CU, of 64 steps for four (lengths differ: pieces even them out)
+        const int64_t n = std::max(std::min(kTarget / 2 / items, steps / 8), std::min(2 * kTarget / items, steps / 64));
+        splits = std::max<int64_t>(1, std::min<int64_t>(kMaxSplits, n));
+    } else {
         // the number of pieces that keeps rounds of kTarget workgroups fullest, a piece's start and end at the price of kPieceSteps
+        const int64_t most = std::min<int64_t>(kJoinRows / p.tile_rows, steps / kMinManySteps);
         double best = 0.0;
-        for (int64_t n = 1; n <= std::min<int64_t>(most, std::max<int64_t>(1, steps / least)) && (n == 1 || size_t(n * items) * slot_bytes(p.tile_rows, dim) <= kMaxSlots); ++n) {
+        for (int64_t n = 1; n == 1 || (n <= most && size_t(n * items) * slot_bytes(p.tile_rows, dim) <= kMaxSlots); ++n) {
             const int64_t chunk = (steps + n - 1) / n, blocks = items * n;
             const double full = double(blocks) / double((blocks + kTarget - 1) / kTarget * kTarget);
             const double rate = full * double(chunk) / double(chunk + kPieceSteps + (n > 1 ? 1 : 0));
