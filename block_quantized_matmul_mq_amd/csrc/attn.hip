@@ -495,22 +495,22 @@ struct Slot {
             for (int p = sub; p < pieces; p += kTeam) {
                 const float m = word(p, ROWS * D + row_of), l = word(p, ROWS * (D + 1) + row_of);
                 share[p * ROWS + row_of] = m;
-                // (sums so far follow a larger maximum)
+                // (sums so far follow a larger maximum; a piece without one has a sum of 0, or of NaN where its scores are NaN)
                 const float to = fmaxf(top, m);
-                sum = fmaf(sum, top == kNone ? 0.0f : __builtin_amdgcn_exp2f(top - to), m == kNone ? 0.0f : l * __builtin_amdgcn_exp2f(m - to));
+                sum = fmaf(sum, top == kNone ? 1.0f : __builtin_amdgcn_exp2f(top - to), m == kNone ? l : l * __builtin_amdgcn_exp2f(m - to));
                 top = to;
             }
             float all = top;
 #pragma unroll
             for (int off = kTeam / 2; off; off >>= 1) all = fmaxf(all, __shfl_xor(all, off, 64));
-            sum = top == kNone ? 0.0f : sum * __builtin_amdgcn_exp2f(top - all);
+            sum = top == kNone ? sum : sum * __builtin_amdgcn_exp2f(top - all);
             // (the team's sums in a fixed order: the result is the same every time)
 #pragma unroll
             for (int off = kTeam / 2; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
             for (int p = sub; p < pieces; p += kTeam) {
                 float& s = share[p * ROWS + row_of];
-                s = s == kNone ? 0.0f : __builtin_amdgcn_exp2f(s - all) * inv;
+                s = s == kNone ? (inv == inv ? 0.0f : inv) : __builtin_amdgcn_exp2f(s - all) * inv;
             }
         }
         __syncthreads();
