@@ -242,14 +242,16 @@ struct Rows {
     }
     // The score that weights are relative to follows these scores' maximum where that passes it by more than SLACK (a weight
     // may so be up to 2^SLACK, and the sums are rescaled in few steps only).  It is a rounded product, but the same in every
-    // weight's exponent, so that its rounding drops out.
+    // weight's exponent, so that its rounding drops out as long as it is small beside the weights' range (see exponents).
     template <int SLACK>
     __device__ __forceinline__ float raise(const float (&sc)[8]) {
+#pragma clang fp contract(off)
         float top = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
         top = row_max(top);
-        const bool up = fmaf(top, f, -m) > float(SLACK);      // (no score seen, none before: NaN, no)
+        const float score = top * f;
+        const bool up = score - m > float(SLACK);             // (no score seen, none before: NaN, no)
         if (__ballot(up) != 0) {
-            const float to = up ? top * f : m;
+            const float to = up ? score : m;
             const float keep = !up || m == kNone ? 1.0f : __builtin_amdgcn_exp2f(m - to);
             l *= keep;
 #pragma unroll
@@ -257,6 +259,24 @@ struct Rows {
             m = to;
         }
         return m == kNone ? 0.0f : m;
+    }
+    // Weight i is exp2(sc[i] by - base), 2^unit for a score of top (raise's).  Usually by = f, in one fma.  From 2^20 on, where the
+    // rounding of top would shift all weights by 2^(1/16) (from 2^27 on by 2^8 or more, out of f16's range), scores are rounded to
+    // f32 before top is taken off; they are not known to that anyway.
+    __device__ __forceinline__ void exponents(float (&sc)[8], float top, float unit, float& by, float& base) const {
+#pragma clang fp contract(off)
+        by = f;
+        base = top - unit;
+        const bool far = fabsf(top) >= 0x1p20f;
+        if (__ballot(far) != 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = sc[i] * f - top;
+                sc[i] = far ? d : sc[i];
+            }
+            by = far ? 1.0f : f;
+            base = far ? -unit : base;
+        }
     }
 };
 
@@ -335,11 +355,11 @@ __device__ __forceinline__ void attend(const Masks& masks, const Step<BITS, D>& 
             seen |= uint32_t(ok) << i;
         }
     }
-    const float base = r.template raise<4>(sc) - unit_e;
-    float p[8];
+    float by, base, p[8];
+    r.exponents(sc, r.template raise<4>(sc), unit_e, by, base);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], r.f, -base));
+        p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], by, -base));
         r.l += p[i];
     }
     // V's scales, 0 of keys that the row does not see (whose bits may be anything)
@@ -913,14 +933,15 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, Rows
     h8 hi[RT], lo[RT];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        const float base = r[i].template raise<kManySlack>(sc[i]) - kManyUnit;
+        float by, base;
+        r[i].exponents(sc[i], r[i].template raise<kManySlack>(sc[i]), kManyUnit, by, base);
         u4 h, l;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
             f2 p;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                p[k] = __builtin_amdgcn_exp2f(fmaf(sc[i][j + k], r[i].f, -base));
+                p[k] = __builtin_amdgcn_exp2f(fmaf(sc[i][j + k], by, -base));
                 r[i].l += p[k];
             }
             uint32_t u, w;

@@ -1,0 +1,102 @@
+"""mq_attn where scores are large: one key takes nearly all of a row, up to f32's range.
+
+A score is known to E: the roundings of q (2^-22), of the sums of codes with their offset (attn_bound), and of the score itself
+and of the scale's product with log2 e (2^-22 of the row's largest score together).  Where E is small the bound is attn_bound's.
+Elsewhere a key that is 2 E + 40 behind the largest score weighs less than e^-40: the row lies, in every dimension, between the
+least and the largest value of the keys that are nearer (one key: it is that key's value), to 2^-20 of the largest value that
+blocks of these scales hold."""
+
+import numpy as np
+import pytest
+
+from block_quantized_matmul_mq_amd import mq
+from oracle import kv_oracle as ko
+
+from kv_cases import NAME, TYPES, Plan, bound_for, cache_on, device, random_cache, to_dev
+
+pytestmark = pytest.mark.gpu
+
+KERNELS = ["attn_few", "attn_many"]
+SIZES = [0.1, 3.0, 30.0, 1e3, 1e5, 1e6, 3e6, 1e7, 2e7, 5e7, 1e8, 1e9, 1e12, 1e20, 1e30, 5e35]
+
+
+def steps_of(data, qtype, plan, dim):
+    raw = data.reshape(-1, ko.chunk_bytes(qtype, plan.page, dim))
+    at = ko.places(qtype, plan.page, dim)
+    s = np.unique(np.concatenate([at[4].ravel(), at[5].ravel()]))
+    bits = raw[:, s].astype(np.uint16) | raw[:, s + 1].astype(np.uint16) << 8
+    return float(np.abs(bits.view(np.float16).astype(np.float64)).max())
+
+
+def check(out, data, qtype, plan, heads, dim, q, scale):
+    C = 15 if qtype == mq.Q4_0 else 255
+    step = steps_of(data, qtype, plan, dim)
+    K, V = ko.get(data, qtype, plan.page, heads, dim)
+    G = q.shape[1] // heads
+    near_rows = 0
+    for t, (b, pos) in enumerate(ko.rows_of(plan.q_start, plan.kv_len, plan.T)):
+        spots = [ko.place(plan.table, plan.pages, plan.page, b, j) for j in range(pos + 1)]
+        p, s = (np.array(a) for a in zip(*spots))
+        for h in range(q.shape[1]):
+            k, v = K[p, h // G, s], V[p, h // G, s]
+            score = scale * (k @ q[t, h].astype(np.float64))
+            E = abs(scale) * np.abs(q[t, h].astype(np.float64)).sum() * step * C * (2.0 ** -22 + (dim + 8) * 2.0 ** -24)
+            E += 2.0 ** -22 * np.abs(score).max()
+            got = out[t, h].astype(np.float64)
+            if E < 0.05:
+                e = np.exp(score - score.max())
+                ref = (e / e.sum()) @ v
+                limit = C / 2 * step * (np.expm1(2 * E) + 2.0 ** -21) + C * step * (2.0 ** -22 + (len(k) + 8) * 2.0 ** -24)
+                assert np.abs(got - ref).max() <= limit, (t, h, np.abs(got - ref).max(), limit)
+                continue
+            near = score >= score.max() - 2 * E - 40
+            near_rows += near.sum() == 1
+            lo, hi = v[near].min(0), v[near].max(0)
+            tol = 2.0 ** -20 * C * step
+            assert (got >= lo - tol).all() and (got <= hi + tol).all(), (t, h, near.sum(), np.maximum(lo - got, got - hi).max(), tol)
+    return near_rows
+
+
+@pytest.mark.parametrize("qtype", TYPES, ids=NAME.get)
+@pytest.mark.parametrize("kv", [40, 2700])
+@pytest.mark.parametrize("scale", [0.125, -1.0])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_scores_of_all_sizes(qtype, kv, scale, kernel):
+    rng = np.random.default_rng([qtype, kv, int(scale > 0)])
+    heads, dim, hq, n = 2, 64, 4, len(SIZES)
+    plan = Plan([n, n], [kv, n + 3], 32, rng)
+    data = random_cache(qtype, plan, heads, dim, rng)
+    q = (np.tile(np.array(SIZES), 2)[:, None, None] * rng.standard_normal((plan.T, hq, dim))).astype(np.float32)
+    q[:, 1] = q[::-1, 1]           # (rows of a tile with other sizes in another order)
+    dev = device()
+    out = mq.attn(cache_on(dev, data, qtype, plan, heads, dim), plan.seqs(dev), to_dev(q, dev), scale=scale,
+                  max_q=bound_for(kernel, plan, hq, heads), max_kv=kv).cpu().numpy()
+    assert mq.last_kernel() == kernel
+    near = check(out, data, qtype, plan, heads, dim, q, scale)
+    assert near >= 8       # rows that are one key's value
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_rising_and_falling_scores(kernel):
+    """Keys in order of their scores, rising and falling over several pieces: the running maximum moves at every step, or never."""
+    rng = np.random.default_rng(5)
+    dim, n = 64, 2
+    plan = Plan([n, n], [2000, 2000], 32, rng)
+    data = random_cache(mq.Q8_0, plan, 1, dim, rng)
+    raw = data.reshape(plan.pages, 1, -1)
+    at = ko.places(mq.Q8_0, 32, dim)
+    for b in range(2):
+        for j in range(2000):
+            page, slot = ko.place(plan.table, plan.pages, 32, b, j)
+            raw[page, 0, at[0][slot]] = 255                          # code 127
+            s = np.unique(at[4][slot])
+            size = 1e-5 * (1 + (j if b == 0 else 1999 - j))
+            for i in s:
+                raw[page, 0, i:i + 2] = np.frombuffer(np.float16(size).tobytes(), np.uint8)
+    dev = device()
+    for size in (1.0, 100.0, 1e4, 1e9, 1e30):
+        q = np.full((plan.T, 3, dim), size, np.float32)
+        out = mq.attn(cache_on(dev, data, mq.Q8_0, plan, 1, dim), plan.seqs(dev), to_dev(q, dev), scale=1.0,
+                      max_q=bound_for(kernel, plan, 3, 1), max_kv=2000).cpu().numpy()
+        assert mq.last_kernel() == kernel
+        check(out, data, mq.Q8_0, plan, 1, dim, q, 1.0)
