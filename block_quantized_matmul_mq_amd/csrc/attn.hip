@@ -114,7 +114,11 @@ __device__ __forceinline__ float row_sum(float v) {
     return row_all(v, [](float a, float b) { return a + b; });
 }
 
-constexpr float kNone = -__builtin_inff();
+// The maximum of a row that has seen no key; of one whose scores all lie below f32's range it is kLowest.
+constexpr float kNone = -__builtin_inff(), kLowest = -3.4028234663852886e38f;
+// A row whose largest score passes f32's range, to either side: its weights are not known.  (Beside a score in range one
+// below it weighs nothing.)
+__device__ __forceinline__ bool out_of_range(float m) { return m != kNone && !(fabsf(m) < -kLowest); }
 
 typedef float f2 __attribute__((ext_vector_type(2)));
 
@@ -248,7 +252,7 @@ struct Rows {
 #pragma clang fp contract(off)
         float top = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
         top = row_max(top);
-        const float score = top * f;
+        const float score = top == kNone ? kNone : fmaxf(top * f, kLowest);
         const bool up = score - m > float(SLACK);             // (no score seen, none before: NaN, no)
         if (__ballot(up) != 0) {
             const float to = up ? score : m;
@@ -527,7 +531,7 @@ struct Slot {
             // (the team's sums in a fixed order: the result is the same every time)
 #pragma unroll
             for (int off = kTeam / 2; off; off >>= 1) sum += __shfl_xor(sum, off, 64);
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = out_of_range(all) ? __builtin_nanf("") : sum == 0.0f ? 0.0f : 1.0f / sum;
             for (int p = sub; p < pieces; p += kTeam) {
                 float& s = share[p * ROWS + row_of];
                 s = s == kNone ? (inv == inv ? 0.0f : inv) : __builtin_amdgcn_exp2f(s - all) * inv;
@@ -571,8 +575,8 @@ struct Slot {
 };
 
 template <int D>
-__device__ __forceinline__ void write_row(float* out, const f4 (&o)[D / 16], float l, int lane) {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+__device__ __forceinline__ void write_row(float* out, const f4 (&o)[D / 16], float m, float l, int lane) {
+    const float inv = out_of_range(m) ? __builtin_nanf("") : l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) *reinterpret_cast<f4*>(out + 16 * j + 4 * (lane >> 4)) = o[j] * inv;
 }
@@ -696,7 +700,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
     }
     const bool live = w.row0 + (lane & 15) < w.rows;
     if (pieces == 1) {
-        if (wave == 0 && live) write_row<D>(out_row(a, w, row), r.o, r.l, lane);
+        if (wave == 0 && live) write_row<D>(out_row(a, w, row), r.o, r.m, r.l, lane);
         return;
     }
     const Slot<D, kRows, kThreads> slot(a, w.cell);
@@ -1080,7 +1084,7 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
     for (int i = 0; i < RT; ++i) {
         const int row = mine + 16 * i + (lane & 15);
         if (row >= w.rows) continue;
-        if (pieces == 1) write_row<D>(out_row(a, w, row), r[i].o, r[i].l, lane);
+        if (pieces == 1) write_row<D>(out_row(a, w, row), r[i].o, r[i].m, r[i].l, lane);
         else slot.put(w.split, row - w.row0, r[i].o, r[i].m, r[i].l, lane);
     }
     if (pieces == 1 || !splitk_arrive(a.counters + w.cell, pieces, &ticket)) return;

@@ -100,3 +100,64 @@ def test_rising_and_falling_scores(kernel):
                       max_q=bound_for(kernel, plan, 3, 1), max_kv=2000).cpu().numpy()
         assert mq.last_kernel() == kernel
         check(out, data, mq.Q8_0, plan, 1, dim, q, 1.0)
+
+
+def one_sided(plan, heads, dim, rng):
+    """A cache of 8 bits whose keys have no value below 1/8 (so that a query's sign is its scores' sign)."""
+    data = random_cache(mq.Q8_0, plan, heads, dim, rng)
+    raw = data.reshape(plan.pages, heads, -1)
+    at = ko.places(mq.Q8_0, plan.page, dim)
+    size = plan.page * dim
+    raw[:, :, :size] = rng.integers(144, 256, raw[:, :, :size].shape)           # codes 16 to 127
+    for s in np.unique(at[4]):
+        raw[:, :, s:s + 2] = np.frombuffer(np.float16(2.0 ** -7).tobytes(), np.uint8)
+    return data
+
+
+@pytest.mark.parametrize("kv", [40, 2700])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_scores_past_the_range(kernel, kv):
+    """Rows whose largest score passes f32's range, to either side, are NaN; beside a larger score that does not, one below the
+    range weighs nothing; and other rows keep their bits."""
+    rng = np.random.default_rng(kv)
+    heads, dim, hq, n = 1, 64, 3, 6
+    plan = Plan([n, n], [kv, n + 3], 32, rng)
+    data = one_sided(plan, heads, dim, rng)
+    raw = data.reshape(plan.pages, heads, -1)
+    at = ko.places(mq.Q8_0, 32, dim)
+    # the second sequence's third key is small: a thousandth of the least of the others
+    page, slot = ko.place(plan.table, plan.pages, 32, 1, 2)
+    raw[page, 0, at[0][slot]] = 129
+    for s in np.unique(at[4][slot]):
+        raw[page, 0, s:s + 2] = np.frombuffer(np.float16(2.0 ** -14).tobytes(), np.uint8)
+    dev = device()
+
+    def call(q, scale):
+        out = mq.attn(cache_on(dev, data, mq.Q8_0, plan, heads, dim), plan.seqs(dev), to_dev(q, dev), scale=scale,
+                      max_q=bound_for(kernel, plan, hq, heads), max_kv=kv).cpu().numpy()
+        assert mq.last_kernel() == kernel
+        return out
+
+    base = np.abs(rng.standard_normal((plan.T, hq, dim))).astype(np.float32) + 0.5
+    clean = call(base, 1.0)
+    V = ko.get(data, mq.Q8_0, plan.page, heads, dim)[1]
+    small = V[page, 0, slot]
+    for sign in (1.0, -1.0):
+        # a score is at least 64 * 0.5 * 2^38 * 2^-3 * 2^100 = 2^140 in magnitude, of the small key at most 64 * 8 * 2^138 * 2^-14 = 2^133
+        q = base.copy()
+        rows = np.zeros((plan.T, hq), bool)
+        rows[1, 0] = rows[n - 1, 2] = rows[n, 1] = rows[n + 4, 0] = True
+        q[rows] *= np.float32(sign * 2.0 ** 38)
+        got = call(q, 2.0 ** 100)
+        want = call(base, 2.0 ** 100)          # (scores of 2^102 and more: in range)
+        assert np.isfinite(want).all()
+        assert np.isnan(got[rows]).all(), (sign, np.argwhere(~np.isnan(got)).shape)
+        assert np.array_equal(got[~rows], want[~rows])
+    # the small key's score is in range, at least 2^20 above the others', which are below it
+    q = base.copy()
+    q[n:] *= np.float32(-2.0 ** 26)
+    got = call(q, 2.0 ** 100)
+    assert np.array_equal(got[:n], want[:n])
+    tol = 2.0 ** -20 * np.abs(V).max()
+    assert np.abs(got[n:] - small).max() <= tol
+    assert np.array_equal(call(base, 1.0), clean)
