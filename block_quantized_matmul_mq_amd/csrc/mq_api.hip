@@ -755,6 +755,7 @@ int mq_attn(const mq_kv_cache* cache, const mq_kv_seqs* seqs, const float* q, in
     if (window < 0 || window > MQ_KV_MAX_TOKENS || (window > 0 && !causal))
         return fail(MQ_ERR_ARG, "%s: window=%lld (0 for none, up to %d, and with causal only)", fn, (long long)window,
                     MQ_KV_MAX_TOKENS);
+    if (!(__builtin_fabsf(scale) <= 3.4028235e38f)) return fail(MQ_ERR_ARG, "%s: scale=%g must be finite", fn, double(scale));
     rc = check_rows(fn, "q", q, q_stride, q_heads, cache->dim);
     if (rc) return rc;
     if (!aligned(out, 16) || !aligned(scratch, 16))

@@ -428,8 +428,9 @@ int mq_kv_read(const mq_kv_cache* cache, const mq_kv_seqs* seqs, int64_t T, floa
  * and the scratch, so that the call reads nothing back): rows past max_q of a sequence are not computed, and
  * a kv_len above max_kv counts as max_kv.
  * f32 accuracy: the factors of both products are held to 21 bits or more, sums and statistics are f32.  (Beside a value of
- * 2^11 or more in the same head and sequence, smaller ones are held to 2^-17.)  A row whose largest score times log2 e passes
- * f32's range, to either side, gets NaN (beside a larger one, a score below the range weighs nothing).  An infinity or a NaN in a row of q, or in a key or value that it sees, makes the outputs that depend on it NaN
+ * 2^11 or more in the same head and sequence, smaller ones are held to 2^-17.)  scale must be finite.  A row whose largest score
+ * times log2 e passes f32's range, to either side, gets NaN (beside a larger one, a score below the range weighs nothing).  An
+ * infinity or a NaN in a row of q, or in a key or value that it sees, makes the outputs that depend on it NaN
  * and no other.  Deterministic.
  * scratch: mq_attn_scratch_bytes(..) bytes (0 for sizes the call refuses), 16-byte aligned; its first 256 KiB are
  * counters that must be zero before the first call and that every call leaves at zero; mq_attn calls that share

@@ -120,6 +120,13 @@ def test_attn_sizes_and_refusals():
         assert attn(mkv=1 << 20, sb=need - 1) == -4 and "scratch" in mq.last_error()
 
 
+def test_attn_scale_that_is_not_finite_is_refused():
+    for bad in (float("nan"), float("inf"), -float("inf"), 1e39):        # (1e39 is an infinity in f32)
+        assert attn(scale=bad) == -1 and "mq_attn: scale=" in mq.last_error()
+    for good in (0.0, -0.0, -2.5, 3.4e38, 1e-45):
+        assert attn(scale=good, sb=0) == -4                              # (the next check: no scratch)
+
+
 def test_sample_sizes_and_refusals():
     size = mq.sample_scratch_bytes
     assert size(0, 100) == size(1, 0) == size(1, (1 << 20) + 1) == size((1 << 20) + 1, 8) == 0
