@@ -220,7 +220,8 @@ struct Rows {
         // then 2^-28 of the largest)
         int e = 0;
         if (top > 0.0f && top <= 3.4028235e38f) e = 14 - (ilogbf(top) + 1);
-        f = fmaxf(ldexpf(fabsf(scale) * 1.44269504088896341f, -e), 0x1p-126f);     // (not 0: a masked score times f stays -inf)
+        // (half of log2 e, so that the product holds for every scale; not 0: a masked score times f stays -inf)
+        f = fmaxf(ldexpf(fabsf(scale) * 0.721347520444481703f, 1 - e), 0x1p-126f);
         constexpr int kOrder4[8] = {0, 4, 1, 5, 2, 6, 3, 7}, kOrder8[8] = {0, 2, 1, 3, 4, 6, 5, 7};
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {

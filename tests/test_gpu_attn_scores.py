@@ -161,3 +161,20 @@ def test_scores_past_the_range(kernel, kv):
     tol = 2.0 ** -20 * np.abs(V).max()
     assert np.abs(got[n:] - small).max() <= tol
     assert np.array_equal(call(base, 1.0), clean)
+
+
+@pytest.mark.parametrize("size,scale", [(1e-38, 3e38), (1e-38, 2e37), (3e-42, -3.4e38), (1e38, 1e-38), (1e37, 2e-38), (1e30, -1e-30)])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_scales_over_their_range(size, scale, kernel):
+    """Ordinary scores of tiny queries by large scales, and the other way round.  (A scale below f32's normal range: its own
+    rounding, 2^-126 / 2^-149 at 1e-38, is in the f32 number that the oracle is given, too.)"""
+    rng = np.random.default_rng(3)
+    plan = Plan([2, 5], [300, 40], 32, rng)
+    data = random_cache(mq.Q4_0, plan, 2, 64, rng)
+    q = (size * 0.125 * rng.standard_normal((plan.T, 4, 64))).astype(np.float32)
+    scale = float(np.float32(scale))
+    dev = device()
+    out = mq.attn(cache_on(dev, data, mq.Q4_0, plan, 2, 64), plan.seqs(dev), to_dev(q, dev), scale=scale,
+                  max_q=bound_for(kernel, plan, 4, 2), max_kv=300).cpu().numpy()
+    assert mq.last_kernel() == kernel
+    check(out, data, mq.Q4_0, plan, 2, 64, q, scale)
