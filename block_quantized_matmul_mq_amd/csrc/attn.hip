@@ -349,17 +349,24 @@ __device__ __forceinline__ void attend(const Masks& masks, const Step<BITS, D>& 
             for (int i = 0; i < 4; ++i)
                 sc[4 * t + i] = fmaf(half_of(s.ks[t][i * (kBlocks / 2) + b / 2], b & 1), acc[b][i], sc[4 * t + i]);
     }
+    // (The sums of finite operands stay below 2^48: a score of -inf comes from a scale that is an infinity, and would pass for a key
+    // that is not seen.)
     uint32_t seen = 0xFF;
+    float least = 0.0f;
     if (!full) {
         seen = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int key = key0 + 16 * (i >> 2) + 4 * (lane >> 4) + (i & 3);
             const bool ok = key >= r.first && key < r.last && s.there[i >> 2];
+            least = ok ? fminf(least, sc[i]) : least;
             sc[i] = ok ? sc[i] : kNone;
             seen |= uint32_t(ok) << i;
         }
+    } else {
+        least = fminf(fminf(fminf(sc[0], sc[1]), fminf(sc[2], sc[3])), fminf(fminf(sc[4], sc[5]), fminf(sc[6], sc[7])));
     }
+    if (least == kNone) r.l = __builtin_nanf("");
     float by, base, p[8];
     r.exponents(sc, r.template raise<4>(sc), unit_e, by, base);
 #pragma unroll
@@ -859,8 +866,9 @@ struct Piece {
         }
         if (tid < kScaleDwords) {
             const int tt = tid / (kBlocks * 8), o = tid % (kBlocks * 8), token = o / (kBlocks / 2), b = 2 * (o % (kBlocks / 2));
-            s.ks[tt][b][token] = half_of(ks, 0);
-            s.ks[tt][b + 1][token] = half_of(ks, 1);
+            // (an infinity as a NaN: a score of -inf would pass for a key that is not seen)
+            s.ks[tt][b][token] = fmaf(half_of(ks, 0), 0.0f, half_of(ks, 0));
+            s.ks[tt][b + 1][token] = fmaf(half_of(ks, 1), 0.0f, half_of(ks, 1));
             s.vs[tt][o] = vs;
         }
     }

@@ -95,3 +95,41 @@ def test_nothing_but_nan_keys(kernel):
     want = c.clean.copy()
     want[c.row(1, 0):c.row(1, 2), :3] = np.nan
     assert np.array_equal(c.call(raw.reshape(-1), c.q), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("qtype", TYPES, ids=NAME.get)
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("bad", [np.inf, -np.inf])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_an_infinite_key_or_value(qtype, n, bad, kernel):
+    """A block whose scale is an infinity (no append makes one; a cache may be filled otherwise): codes of both signs times it are
+    infinities of both signs, whatever the sign of the score that they would give."""
+    c = Case(qtype, kernel, n, 4)
+    for b, l in enumerate(LENGTHS):
+        for pos in (l - 1, l // 2, 0):
+            for which in (4, 5):
+                say(f"sequence {b}, position {pos}, {'key' if which == 4 else 'value'}")
+                got = c.call(c.with_scale(which, b, pos, 1, 33, bad), c.q)
+                want = c.clean.copy()
+                for i in range(n):
+                    if l - n + i >= pos:
+                        want[c.row(b, i), 3:, 0 if which == 4 else 32:] = np.nan
+                assert np.array_equal(got, want, equal_nan=True)
+
+
+@pytest.mark.parametrize("window", [8, 40])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_infinite_keys_out_of_sight(window, kernel):
+    """Infinite scales just outside a window and behind a row's own position."""
+    c = Case(mq.Q4_0, kernel, 2, 5)
+    raw = c.data.copy().reshape(c.plan.pages, HEADS, -1)
+    inf = np.frombuffer(np.float16(-np.inf).tobytes(), np.uint8)
+    clean = c.call(c.data, c.q, window=window)
+    for b, l in enumerate(LENGTHS):
+        if l - 2 - window < 0:       # the window covers the sequence
+            continue
+        page, slot = ko.place(c.plan.table, c.plan.pages, PAGE, b, l - 2 - window)      # the first row's first key is one further
+        for which in (4, 5):
+            for s in np.unique(ko.places(c.qtype, PAGE, DIM)[which][slot]):
+                raw[page, :, s:s + 2] = inf
+    assert np.array_equal(c.call(raw.reshape(-1), c.q, window=window), clean)
