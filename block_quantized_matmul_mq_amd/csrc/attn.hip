@@ -785,16 +785,17 @@ struct Piece {
         }
     }
     // V's scale times a code (for 4 bits and odd 16s of dimensions 16 times the code) is held as two f16, exactly, as long as the
-    // products stay below f16's end: scales under 2^8 (times 128).  The quick form (PRECISE false) says in `special` where a
-    // scale is an infinity, a NaN or larger; its products of that step are then made again by the other form, which takes what is not
-    // finite as 0 (in `bad`) and says in `large` where a finite one is larger; from the first of those on
-    // (`small`) all products are taken times kSmall, to 2^-24 of f16's range (2^-27 of the scale that asked for it).
+    // products stay below f16's end: scales under 2^8 (times 128).  The quick form says in `special` where a scale is an infinity, a
+    // NaN or larger; its products of that step are then made again in the ordinary form, which takes those as 0 and says in `bad`
+    // where one is not finite, in `large` where a finite one is larger.  The products of large ones alone, times kSmall, are the
+    // third form, for a product of their own: rows that do not see them, and smaller values beside them, lose nothing.
+    enum Form { kQuick, kOrdinary, kLargeOnes };
     static constexpr int kLarge = 23;                       // exponent field
     static constexpr float kSmall = 0x1p-8f;
-    template <bool PRECISE>
-    __device__ __forceinline__ void stage(const Masks& masks, Staged<BITS, D, NT>& s, const int (&pages)[2], int key0, int len, bool small) const {
+    template <Form FORM>
+    __device__ __forceinline__ void stage(const Masks& masks, Staged<BITS, D, NT>& s, const int (&pages)[2], int key0, int len) const {
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        if (kKThreads == NT || tid < kKThreads) {
+        if (FORM != kLargeOnes && (kKThreads == NT || tid < kKThreads)) {
             constexpr int kPer = kBlocks / kOps;
             const int t = wave / kPer, h = wave % kPer;
 #pragma unroll
@@ -812,7 +813,7 @@ struct Piece {
 #pragma unroll
                 for (int i = 0; i < 2 * kDs; ++i) e[i] = there && key + i / kDs < len ? e[i] : 0;
             }
-            if constexpr (!PRECISE) {
+            if constexpr (FORM == kQuick) {
                 typedef unsigned short us2 __attribute__((ext_vector_type(2)));
                 us2 top = {0, 0};
 #pragma unroll
@@ -824,9 +825,10 @@ struct Piece {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t x = (e[i] >> (16 * h + 10)) & 31;
+                        const bool is_large = x >= kLarge && x < 31;
                         bad |= x == 31;
-                        large |= x >= kLarge && x < 31;
-                        if (x == 31) e[i] &= h ? 0x0000FFFFu : 0xFFFF0000u;
+                        large |= is_large;
+                        if (FORM == kOrdinary ? x >= kLarge : !is_large) e[i] &= h ? 0x0000FFFFu : 0xFFFF0000u;
                     }
             }
             uint32_t* hi = reinterpret_cast<uint32_t*>(s.v_hi);
@@ -844,12 +846,12 @@ struct Piece {
                     if (BITS == 8 ? n == 1 : n >= 2) x >>= 8;
                     const h2 c = __builtin_bit_cast(h2, two_codes<BITS>(masks, x, BITS == 4 && (n & 1)));
                     uint32_t h, l;
-                    if constexpr (!PRECISE) {
+                    if constexpr (FORM == kQuick) {
                         const h2 p = c * dd;
                         h = __builtin_bit_cast(uint32_t, p);
                         l = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, dd, -p));
                     } else {
-                        const float by = small ? kSmall : 1.0f;
+                        const float by = FORM == kLargeOnes ? kSmall : 1.0f;
                         split(f2{static_cast<float>(c[0]) * (static_cast<float>(dd[0]) * by),
                                  static_cast<float>(c[1]) * (static_cast<float>(dd[1]) * by)}, 1.0f, h, l);
                     }
@@ -858,6 +860,7 @@ struct Piece {
                     lo[at] = l;
                 }
         }
+        if constexpr (FORM == kLargeOnes) return;
         const bool any_special = __ballot(special) != 0, any_bad = __ballot(bad) != 0, any_large = __ballot(large) != 0;
         if (lane == 0) {
             s.special[wave] = any_special;
@@ -882,9 +885,10 @@ __device__ __forceinline__ bool any_of(const uint32_t (&v)[N]) {
     return __builtin_amdgcn_readfirstlane(all) != 0;
 }
 
-// One staged step for a wave's RT sets of rows.
+// One staged step for a wave's RT sets of rows.  large: V's products of large scales (Piece::stage), or null.
 template <int BITS, int D, int NT, int RT>
-__device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, Rows<BITS, D> (&r)[RT], int key0, bool full, bool there0, bool there1, int lane) {
+__device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, const Staged<BITS, D, NT>* large, Rows<BITS, D> (&r)[RT], int key0,
+                                              bool full, bool there0, bool there1, int lane) {
     constexpr int kBlocks = D / 32, kTiles = D / 16;
     // Operands are read from LDS one product ahead (the scheduling barriers keep it at that: all of them at once take more
     // registers than there are), and a block's sums are used while the next block's products run.
@@ -994,6 +998,20 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, Rows
         __builtin_amdgcn_sched_barrier(0);
     }
     __builtin_amdgcn_s_setprio(0);
+    if (large) {
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+            const h8 h = __builtin_bit_cast(h8, large->v_hi[j][lane]), l = __builtin_bit_cast(h8, large->v_lo[j][lane]);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                f4 sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(h, hi[i], f4{0, 0, 0, 0}, 0, 0, 0);
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(h, lo[i], sum, 0, 0, 0);
+                sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(l, hi[i], sum, 0, 0, 0);
+                r[i].o[j] += sum * (1.0f / Piece<BITS, D, NT>::kSmall);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
 }
 
 template <int BITS, int D, int NT, int RT>
@@ -1024,7 +1042,6 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
         r[i].first = first_key(a, w, row / a.group);
         r[i].last = last_key(a, w, row / a.group);
     }
-    bool small = false;
     using P = Piece<BITS, D, NT>;
     if (from < to) {
         const Masks masks = Masks::make<BITS>();
@@ -1032,24 +1049,20 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
         int pages[2], next[2];
         pages_of(a, w, from, pages);
         piece.load(a.c, pages, w.head, from * kStep);
-        piece.template stage<false>(masks, buf[0], pages, from * kStep, w.len, false);
+        piece.template stage<P::kQuick>(masks, buf[0], pages, from * kStep, w.len);
         pages_of(a, w, min(from + 1, to - 1), next);
         __syncthreads();
         for (int step = from; step < to; ++step) {
             const int key0 = step * kStep;
-            Staged<BITS, D, NT>& s = buf[(step - from) & 1];
-            if (any_of(s.special)) {         // (the piece is still this step's)
+            Staged<BITS, D, NT>&s = buf[(step - from) & 1], &t = buf[(step + 1 - from) & 1];
+            bool large = false;
+            if (any_of(s.special)) {         // (the piece is still this step's, and the other buffer free)
                 __syncthreads();
-                piece.template stage<true>(masks, s, pages, key0, w.len, false);
+                piece.template stage<P::kOrdinary>(masks, s, pages, key0, w.len);
                 __syncthreads();
-                if (any_of(s.large)) {
-                    small = true;
-#pragma unroll
-                    for (int i = 0; i < RT; ++i)
-#pragma unroll
-                        for (int j = 0; j < kTiles; ++j) r[i].o[j] *= P::kSmall;
-                    __syncthreads();
-                    piece.template stage<true>(masks, s, pages, key0, w.len, true);
+                large = any_of(s.large);
+                if (large) {
+                    piece.template stage<P::kLargeOnes>(masks, t, pages, key0, w.len);
                     __syncthreads();
                 }
             }
@@ -1060,7 +1073,7 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
             piece.load(a.c, pages, w.head, ahead * kStep);
             pages_of(a, w, min(step + 2, to - 1), next);
             const bool full = key0 >= full_begin && key0 + kStep <= full_end && there0 && there1;
-            attend_staged<BITS, D, NT, RT>(s, r, key0, full, there0, there1, lane);
+            attend_staged<BITS, D, NT, RT>(s, large ? &t : nullptr, r, key0, full, there0, there1, lane);
             if (any_of(s.bad)) {      // (staged as zeros)
                 for (int i = 0; i < kStep; ++i)
 #pragma unroll
@@ -1075,18 +1088,17 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
                             }
                     }
             }
-            Staged<BITS, D, NT>& t = buf[(step + 1 - from) & 1];
-            if (!small) piece.template stage<false>(masks, t, pages, ahead * kStep, w.len, false);
-            else piece.template stage<true>(masks, t, pages, ahead * kStep, w.len, true);
+            if (large) __syncthreads();      // (every wave is through with the other buffer)
+            piece.template stage<P::kQuick>(masks, t, pages, ahead * kStep, w.len);
             __syncthreads();
         }
     }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         r[i].l = row_sum(r[i].l);
-        const float even = small ? 1.0f / P::kSmall : 1.0f;
+        if constexpr (BITS == 4)
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) r[i].o[j] *= BITS == 4 && (j & 1) ? even * 0.0625f : even;
+            for (int j = 1; j < kTiles; j += 2) r[i].o[j] *= 0.0625f;
     }
     const Slot<D, kRows, NT> slot(a, w.cell);
 #pragma unroll

@@ -427,8 +427,8 @@ int mq_kv_read(const mq_kv_cache* cache, const mq_kv_seqs* seqs, int64_t T, floa
  * max_q, max_kv: at least the largest number of rows and the largest kv_len of a sequence (they size the grid
  * and the scratch, so that the call reads nothing back): rows past max_q of a sequence are not computed, and
  * a kv_len above max_kv counts as max_kv.
- * f32 accuracy: the factors of both products are held to 21 bits or more, sums and statistics are f32.  (Beside a value of
- * 2^11 or more in the same head and sequence, smaller ones are held to 2^-17.)  scale must be finite.  A row whose largest score
+ * f32 accuracy: q is held to 21 bits or more, a weight times a value to 21 bits or to 2^-30 of the row's largest weight times the
+ * largest value that it sees; sums and statistics are f32.  scale must be finite.  A row whose largest score
  * times log2 e passes f32's range, to either side, gets NaN (beside a larger one, a score below the range weighs nothing).  An
  * infinity or a NaN in a row of q, or in a key or value that it sees, makes the outputs that depend on it NaN
  * and no other.  Deterministic.
