@@ -196,6 +196,7 @@ struct Rows {
     f4 o[kTiles];
     float f;                        // score in log2 units per unit of the accumulated sums
     float m, l;                     // the score (log2 units) that weights are relative to, or none; this lane's part of the sum of weights
+    float least;                    // attn_few: the least score seen (unscaled, or 0)
     int first, last;                // keys first .. last - 1 are seen
 
     // q: the row's f32 values, of which this lane has 8 in each block
@@ -220,8 +221,8 @@ struct Rows {
         // then 2^-28 of the largest)
         int e = 0;
         if (top > 0.0f && top <= 3.4028235e38f) e = 14 - (ilogbf(top) + 1);
-        // (half of log2 e, so that the product holds for every scale; not 0: a masked score times f stays -inf)
-        f = fmaxf(ldexpf(fabsf(scale) * 0.721347520444481703f, 1 - e), 0x1p-126f);
+        // (half of log2 e, so that the product holds for every scale; not 0: a masked score times f stays -inf; and finite)
+        f = fminf(fmaxf(ldexpf(fabsf(scale) * 0.721347520444481703f, 1 - e), 0x1p-126f), -kLowest);
         constexpr int kOrder4[8] = {0, 4, 1, 5, 2, 6, 3, 7}, kOrder8[8] = {0, 2, 1, 3, 4, 6, 5, 7};
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b) {
@@ -243,20 +244,18 @@ struct Rows {
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) o[j] = f4{0, 0, 0, 0};
         m = kNone;
-        l = 0.0f;
+        l = least = 0.0f;
     }
     // The score that weights are relative to follows these scores' maximum where that passes it by more than SLACK (a weight
     // may so be up to 2^SLACK, and the sums are rescaled in few steps only).  It is a rounded product, but the same in every
     // weight's exponent, so that its rounding drops out as long as it is small beside the weights' range (see exponents).
     template <int SLACK>
     __device__ __forceinline__ float raise(const float (&sc)[8]) {
-#pragma clang fp contract(off)
         float top = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
         top = row_max(top);
-        const float score = top == kNone ? kNone : fmaxf(top * f, kLowest);
-        const bool up = score - m > float(SLACK);             // (no score seen, none before: NaN, no)
+        const bool up = fmaf(top, f, -m) > float(SLACK);      // (no score seen, none before: NaN, no)
         if (__ballot(up) != 0) {
-            const float to = up ? score : m;
+            const float to = up ? fmaxf(top * f, kLowest) : m;
             const float keep = !up || m == kNone ? 1.0f : __builtin_amdgcn_exp2f(m - to);
             l *= keep;
 #pragma unroll
@@ -268,6 +267,7 @@ struct Rows {
     // Weight i is exp2(sc[i] by - base), 2^unit for a score of top (raise's).  Usually by = f, in one fma.  From 2^20 on, where the
     // rounding of top would shift all weights by 2^(1/16) (from 2^27 on by 2^8 or more, out of f16's range), scores are rounded to
     // f32 before top is taken off; they are not known to that anyway.
+    template <int SLACK>
     __device__ __forceinline__ void exponents(float (&sc)[8], float top, float unit, float& by, float& base) const {
 #pragma clang fp contract(off)
         by = f;
@@ -276,8 +276,8 @@ struct Rows {
         if (__ballot(far) != 0) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float d = sc[i] * f - top;
-                sc[i] = far ? d : sc[i];
+                const float d = sc[i] * f - top;          // (the exact difference is SLACK at most)
+                sc[i] = far ? (d > float(SLACK) ? float(SLACK) : d) : sc[i];
             }
             by = far ? 1.0f : f;
             base = far ? -unit : base;
@@ -350,25 +350,24 @@ __device__ __forceinline__ void attend(const Masks& masks, const Step<BITS, D>& 
                 sc[4 * t + i] = fmaf(half_of(s.ks[t][i * (kBlocks / 2) + b / 2], b & 1), acc[b][i], sc[4 * t + i]);
     }
     // (The sums of finite operands stay below 2^48: a score of -inf comes from a scale that is an infinity, and would pass for a key
-    // that is not seen.)
+    // that is not seen.  The kernel's end makes the row NaN.  Four v_min3 a step: 64 sequences of up to 8192 keys 110.2 -> 111.6 us.)
     uint32_t seen = 0xFF;
-    float least = 0.0f;
     if (!full) {
         seen = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int key = key0 + 16 * (i >> 2) + 4 * (lane >> 4) + (i & 3);
             const bool ok = key >= r.first && key < r.last && s.there[i >> 2];
-            least = ok ? fminf(least, sc[i]) : least;
+            r.least = ok ? fminf(r.least, sc[i]) : r.least;
             sc[i] = ok ? sc[i] : kNone;
             seen |= uint32_t(ok) << i;
         }
     } else {
-        least = fminf(fminf(fminf(sc[0], sc[1]), fminf(sc[2], sc[3])), fminf(fminf(sc[4], sc[5]), fminf(sc[6], sc[7])));
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) r.least = fminf(fminf(r.least, sc[i]), sc[i + 1]);
     }
-    if (least == kNone) r.l = __builtin_nanf("");
     float by, base, p[8];
-    r.exponents(sc, r.template raise<4>(sc), unit_e, by, base);
+    r.template exponents<4>(sc, r.template raise<4>(sc), unit_e, by, base);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], by, -base));
@@ -668,6 +667,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
         }
     }
     const float back = ldexpf(1.0f, -unit_e);
+    if (r.least == kNone) r.l = __builtin_nanf("");
     r.l = row_sum(r.l) * back;
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) r.o[j] *= BITS == 4 && (j & 1) ? back * 0.0625f : back;
@@ -951,7 +951,7 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, cons
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         float by, base;
-        r[i].exponents(sc[i], r[i].template raise<kManySlack>(sc[i]), kManyUnit, by, base);
+        r[i].template exponents<kManySlack>(sc[i], r[i].template raise<kManySlack>(sc[i]), kManyUnit, by, base);
         u4 h, l;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {

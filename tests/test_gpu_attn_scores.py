@@ -178,3 +178,21 @@ def test_scales_over_their_range(size, scale, kernel):
                   max_q=bound_for(kernel, plan, 4, 2), max_kv=300).cpu().numpy()
     assert mq.last_kernel() == kernel
     check(out, data, mq.Q4_0, plan, 2, 64, q, scale)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_a_query_and_a_scale_at_their_ends(kernel):
+    """|scale| times the row's largest value past f32's range: NaN either side; a row of zeros is the mean of its values."""
+    rng = np.random.default_rng(9)
+    plan = Plan([3, 3], [300, 40], 32, rng)
+    data = one_sided(plan, 1, 64, rng)
+    q = np.full((plan.T, 3, 64), 1e38, np.float32)
+    q[:, 1] *= -1
+    q[:, 2] = 0
+    dev = device()
+    for scale in (3e38, -3e38):
+        out = mq.attn(cache_on(dev, data, mq.Q8_0, plan, 1, 64), plan.seqs(dev), to_dev(q, dev), scale=scale,
+                      max_q=bound_for(kernel, plan, 3, 1), max_kv=300).cpu().numpy()
+        assert mq.last_kernel() == kernel
+        assert np.isnan(out[:, :2]).all()
+        check(out[:, 2:], data, mq.Q8_0, plan, 1, 64, q[:, 2:], scale)
