@@ -83,7 +83,9 @@ __device__ __forceinline__ KvToken kv_token(const KvView& c, int t) {
         const int past = __popcll(__ballot(end <= t));
         if (past < 64) {     // (starts do not fall: the first sequence that ends behind the token; lanes behind the last repeat it)
             const int b = __builtin_amdgcn_readfirstlane(past);
-            return {i0 + b, __builtin_amdgcn_readlane(len, b) - (__builtin_amdgcn_readlane(end, b) - t)};
+            if (i0 + b >= c.seqs) return {-1, 0};     // (starts that fall: no such sequence, and no read behind the table)
+            const unsigned behind = unsigned(__builtin_amdgcn_readlane(end, b)) - unsigned(t);
+            return {i0 + b, int(unsigned(__builtin_amdgcn_readlane(len, b)) - behind)};
         }
     }
     return {-1, 0};
