@@ -439,9 +439,10 @@ __device__ __forceinline__ int scale_exponent(const Step<BITS, D>& s, int key0, 
 // A workgroup's part of the call: a tile of rows of one cache head, and of a piece of its keys.
 struct Work {
     int head, seq, tile, split, cell;
-    int q0, n, all, rows, row0;      // the sequence's first row, its rows (also those past max_q), rows of the list, this tile's first
-    int real, len;                   // cached tokens, and as far as they count
+    int q0, n, rows, row0;           // the sequence's first row, its rows, rows of the list, this tile's first
+    int past, len;                   // the first row's position in the cache; cached tokens as far as they count
 };
+__device__ __forceinline__ int wrapping(unsigned a, unsigned b) { return int(a + b); }
 __device__ __forceinline__ bool work_of(const AttnArgs& a, int tile_rows, Work& w) {
     // heads vary fastest (workgroups are dealt to the XCDs in turn, whose L2 so holds few heads); later rows, which
     // see more keys, come first, and a tile's last piece, which is rarely a whole one, comes last
@@ -454,20 +455,23 @@ __device__ __forceinline__ bool work_of(const AttnArgs& a, int tile_rows, Work& 
     w.split = item / a.tiles;
     w.cell = (w.seq * a.tiles + w.tile) * a.c.heads + w.head;
     w.q0 = a.c.q_start[w.seq];
-    w.all = a.c.q_start[w.seq + 1] - w.q0;
-    w.n = w.q0 < 0 ? 0 : min(w.all, min(a.max_q, a.T - w.q0));
+    // (rows inside the call's whatever the arrays hold, and sums that may wrap without a sign: starts of any value make a product
+    // n group that wraps to rows that are not there)
+    const int all = wrapping(a.c.q_start[w.seq + 1], -unsigned(w.q0));
+    w.n = w.q0 < 0 || w.q0 >= a.T ? 0 : max(0, min(all, min(a.max_q, a.T - w.q0)));
     w.rows = w.n * a.group;
     w.row0 = w.tile * tile_rows;
-    w.real = a.c.kv_len[w.seq];
-    w.len = min(w.real, a.max_kv);
+    const int real = a.c.kv_len[w.seq];
+    w.past = wrapping(real, -unsigned(all));
+    w.len = min(real, a.max_kv);
     return w.row0 < w.rows;
 }
 // Keys [first, last) that a token of the sequence sees.
 __device__ __forceinline__ int first_key(const AttnArgs& a, const Work& w, int tok) {
-    return a.window > 0 ? max(0, w.real - w.all + tok + 1 - a.window) : 0;
+    return a.window > 0 ? max(0, wrapping(w.past, tok + 1 - a.window)) : 0;
 }
 __device__ __forceinline__ int last_key(const AttnArgs& a, const Work& w, int tok) {
-    return a.causal ? min(w.len, w.real - w.all + tok + 1) : w.len;
+    return a.causal ? min(w.len, wrapping(w.past, tok + 1)) : w.len;
 }
 __device__ __forceinline__ const float* query_row(const AttnArgs& a, const Work& w, int row) {
     const int tok = row / a.group;

@@ -7,7 +7,7 @@ from block_quantized_matmul_mq_amd import mq
 from oracle import kv_oracle as ko
 
 from gpu_cases import say
-from kv_cases import Plan, device, random_cache, to_dev
+from kv_cases import Plan, bound_for, cache_on, device, random_cache, to_dev
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +92,32 @@ def test_append_and_read(name):
     assert torch.equal(before, c.data[spare])
     if name == "falling starts":        # rows 0 and 1 are the first sequence's; row 4 is none's
         assert (q_out[0] != 777.0).any() and (q_out[4] == 777.0).all() and (kr[4] == 777.0).all()
+
+
+@pytest.mark.parametrize("name", PLANS)
+@pytest.mark.parametrize("window", [0, 3])
+@pytest.mark.parametrize("kernel", ["attn_few", "attn_many"])
+def test_attention(name, window, kernel):
+    import torch
+    c = Call(name, 23)
+    q, out = c.guard(c.x[:, :HQ].cpu().numpy(), 0.5), c.rows(HQ)
+    say(f"{kernel}: {name}, window {window}")
+    mq.attn(c.cache, c.seqs, q, window=window, max_q=bound_for(kernel, c.plan, HQ, HEADS), max_kv=40, out=out)
+    torch.cuda.synchronize()
+    assert mq.last_kernel() == kernel
+    c.check()
+
+
+def test_a_valid_plan_beside_them():
+    """The guard's own arrays with a valid plan: every row is served."""
+    import torch
+    dev = device()
+    rng = np.random.default_rng(22)
+    plan = Plan([2, 2, 2], [20, 20, 20], PAGE, rng)
+    data = random_cache(mq.Q4_0, plan, HEADS, DIM, rng)
+    q = rng.standard_normal((T, HQ, DIM)).astype(np.float32)
+    table, c = guarded(plan.table, dev, 1)
+    seqs = mq.KVSeqs(to_dev(plan.q_start, dev), to_dev(plan.kv_len, dev), table)
+    one = mq.attn(cache_on(dev, data, mq.Q4_0, plan, HEADS, DIM), seqs, to_dev(q, dev), max_q=2, max_kv=20)
+    two = mq.attn(cache_on(dev, data, mq.Q4_0, plan, HEADS, DIM), plan.seqs(dev), to_dev(q, dev), max_q=2, max_kv=20)
+    assert torch.equal(one, two) and c()
