@@ -16,8 +16,8 @@
 //   3  the tokens of these bins, a few hundred, collected; and the masses of 2048-token blocks of the tokens that are in whatever
 //      the cuts are.  Then, once a row: the collected tokens sorted, both cuts, the kept ones' masses added to their
 //      blocks, the block that the random number falls in, and the token in it.
-// A row is divided over workgroups and the passes over launches (the last workgroup of a row does a pass's single
-// part, mmq_splitk.h's exchange) where that is faster than a workgroup that makes all passes of a row by itself.
+// A row of more than two blocks is divided over workgroups and the passes over launches (the last workgroup of a row does a
+// pass's single part, mmq_splitk.h's exchange); a shorter one is a workgroup's, which makes all passes by itself.
 // Measured: one row of 152064 25 us (launches of 3.6, 11.3 and 11.3: latency of their dependent rounds), nine of 32003 31 us,
 // 128 of 152064 98 us (0.8 TB/s; 16.5, 29.5 and 58: f64 exponentials of every token in the last two).
 // More collected tokens than fit (as where most logits are equal) are resolved by a radix selection over the row.
@@ -40,7 +40,7 @@ constexpr int kBlock = 2048;                       // tokens whose masses are su
 constexpr int kPer = kBlock / kThreads;
 constexpr int kMaxBlocks = (1 << 20) / kBlock;
 constexpr int kCap = 2048;                         // collected tokens
-constexpr int kBatch = 256;                        // rows of a launch
+constexpr int kBatch = 256;                        // rows of a launch (at most 1024: a workgroup each)
 constexpr double kLast = 30.498475;                // x beyond which rne(2^43 exp(-x)) is 0 (44 ln 2)
 constexpr double kBinsPerX = 33.0;
 static_assert(kLast * kBinsPerX < kBins, "bins");
@@ -795,6 +795,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Args a) {
 
 }  // namespace
 
+// (the same for every size: one buffer serves calls of any)
 size_t sample_scratch_bytes(int64_t, int64_t) { return (size_t(4) << 20) + sizeof(Free); }
 
 hipError_t launch_sample(const Sample& r, hipStream_t s, const char** name) {
@@ -806,9 +807,10 @@ hipError_t launch_sample(const Sample& r, hipStream_t s, const char** name) {
     for (int64_t m = 0; m < r.M; m += kBatch) {
         const int rows = int(std::min<int64_t>(kBatch, r.M - m));
         a.row0 = int(m);
-        // about four workgroups a CU; short rows, and rows enough for that, are left whole
-        a.parts = std::min(blocks, std::max(1, 1024 / rows));
-        if (blocks <= 2) a.parts = 1;
+        // about four workgroups a CU; rows of one or two blocks are left whole.  One row, and 256, with top-k and top-p, in us, whole
+        // and in launches: 4096 tokens 15 and 16, 21 and 29; 8192 17 and 19, 21 and 52 (the rule's loss, as for 128 rows
+        // to about 32000: 38, 53); 16384 25 and 26, 22 and 55; 152064 111 and 129, 25 and 127
+        a.parts = blocks <= 2 ? 1 : std::min(blocks, 1024 / rows);
         a.part_blocks = (blocks + a.parts - 1) / a.parts;
         a.parts = (blocks + a.part_blocks - 1) / a.part_blocks;
         if (a.parts == 1) {

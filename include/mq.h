@@ -560,8 +560,8 @@ int mq_device_lds_bytes(void);
  *   mq_gemv_ep, mq_gemm_ep: the name of the product's kernel; mq_moe_route: "moe_route";
  *   mq_moe_ffn: "moe_one" (one token, topk <= 64) or "moe_many";
  *   mq_kv_append: "kv_append"; mq_kv_read: "kv_read"; mq_attn: "attn_few" (at most 256 rows of a sequence
- *   and cache head, max_q * q_heads / heads, or few sequences and heads) or "attn_many"; mq_sample: "sample_row" (a workgroup per row: short rows,
- *   or rows enough for every CU) or "sample" (three launches, or two without top_k and top_p). */
+ *   and cache head, max_q * q_heads / heads, or few sequences and heads) or "attn_many"; mq_sample: "sample_row" (a
+ *   workgroup per row and one launch: V <= 4096) or "sample" (three launches, or two without top_k and top_p). */
 const char* mq_last_kernel(void);
 
 /* Library version string. */
