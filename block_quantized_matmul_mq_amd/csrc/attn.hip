@@ -458,7 +458,7 @@ __device__ __forceinline__ bool work_of(const AttnArgs& a, int tile_rows, Work& 
     // (rows inside the call's whatever the arrays hold, and sums that may wrap without a sign: starts of any value make a product
     // n group that wraps to rows that are not there)
     const int all = wrapping(a.c.q_start[w.seq + 1], -unsigned(w.q0));
-    w.n = w.q0 < 0 || w.q0 >= a.T ? 0 : max(0, min(all, min(a.max_q, a.T - w.q0)));
+    w.n = w.q0 < 0 ? 0 : max(0, min(all, min(a.max_q, a.T - w.q0)));
     w.rows = w.n * a.group;
     w.row0 = w.tile * tile_rows;
     const int real = a.c.kv_len[w.seq];
