@@ -52,7 +52,7 @@ constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 32;                // keys of a step
 constexpr int kCounters = 65536;         // of the scratch; cut tiles are at most kTarget
-constexpr int kTarget = 512;             // workgroups that a call is cut into where it has fewer tiles (half of it: of 512 threads)
+constexpr int kTarget = 512;             // workgroups that a call is cut into where it has fewer tiles (attn_few: half of it, or twice, see plan)
 constexpr int kFewTiles = 768;           // tiles of 16 rows up to which attn_few takes sequences of any number of rows
 constexpr int kMaxSplits = 64;
 constexpr int kJoinRows = 4096;          // of attn_many: pieces times rows of a tile at most (LDS of the join)
@@ -487,7 +487,7 @@ __device__ __forceinline__ void pages_of(const AttnArgs& a, const Work& w, int s
 }
 
 // A piece's rows to its slot of the scratch (sums, then maxima in log2 units, then sums of weights).
-template <int D, int ROWS, int NT>
+template <int D, int ROWS>
 struct Slot {
     static constexpr int kFloats = ROWS * (D + 2);
     __amdgpu_buffer_rsrc_t rsrc;
@@ -516,7 +516,7 @@ struct Slot {
         // A thread's first sums, and kTeam threads a row, each the statistics of some of its pieces: all of these loads in flight
         // together (a trip to the device-coherent level is more than a microsecond).
         constexpr int kFirst = ROWS == 16 && D <= 128 ? 16 : 8, kItems = D / 4;
-        constexpr int kTeam = NT / ROWS < 16 ? NT / ROWS : 16;
+        constexpr int kTeam = kThreads / ROWS;
         auto sums = [&](int piece, int item) {
             return __builtin_bit_cast(f4, __builtin_amdgcn_raw_buffer_load_b128(rsrc, item * 16, piece * kFloats * 4, kSplitkSc1));
         };
@@ -549,7 +549,7 @@ struct Slot {
             }
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < live * kItems; i += NT) {
+        for (int i = threadIdx.x; i < live * kItems; i += kThreads) {
             const int row = i / kItems;
             f4 sum = {0, 0, 0, 0};
             int p = 0;
@@ -715,35 +715,34 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_few_kernel(At
         if (wave == 0 && live) write_row<D>(out_row(a, w, row), r.o, r.m, r.l, lane);
         return;
     }
-    const Slot<D, kRows, kThreads> slot(a, w.cell);
+    const Slot<D, kRows> slot(a, w.cell);
     if (wave == 0 && live) slot.put(w.split, lane & 15, r.o, r.m, r.l, lane);
     if (!splitk_arrive(a.counters + w.cell, pieces, &ticket)) return;
     slot.join(a, w, pieces, share);
 }
 
-// NT / 64 waves, each with 16 RT rows; the workgroup's steps go through LDS as operands, two buffers.
-template <int BITS, int D, int NT>
+// Four waves, each with 16 RT rows; the workgroup's steps go through LDS as operands, two buffers.
+template <int BITS, int D>
 struct Staged {
     static constexpr int kBlocks = D / 32, kTiles = D / 16;
     u4 k[2][kBlocks][64];            // [16 keys][block][lane]
     u4 v_hi[kTiles][64], v_lo[kTiles][64];
     float ks[2][kBlocks][16];        // K's scales
     uint32_t vs[2][kBlocks * 8];     // V's, as in the cache: [16 tokens][block]
-    uint32_t special[NT / 64], bad[NT / 64], large[NT / 64];   // per wave, of V's scales: see Piece::stage
+    uint32_t special[kWaves], bad[kWaves], large[kWaves];   // per wave, of V's scales: see Piece::stage
 };
 
-// What a thread loads of a step and lays into LDS: K's codes of some blocks of a lane; V's of some units of a lane and of two tokens,
-// with these tokens' scales; a dword of both kinds of scales.  (Where a step has less than that for every thread, the first ones.)
-template <int BITS, int D, int NT>
+// What a thread loads of a step and lays into LDS: K's codes of some blocks of a lane; V's units of a lane and of two tokens,
+// with these tokens' scales; the first threads a dword of both kinds of scales.
+template <int BITS, int D>
 struct Piece {
     using L = KvLayout<BITS, D>;
     static constexpr int kBlocks = D / 32, kUnits = L::kUnits;
-    static constexpr int kOps = 128 * kBlocks > NT ? 128 * kBlocks / NT : 1, kKThreads = 128 * kBlocks / kOps;
-    static constexpr int kVs = 256 * kUnits > NT ? 256 * kUnits / NT : 1, kVThreads = 256 * kUnits / kVs;
-    static constexpr int kDs = BITS == 4 ? kVs : (kVs + 1) / 2;
+    static constexpr int kOps = kBlocks / 2;               // of K's 128 (lane, tile) times kBlocks operands
+    static constexpr int kDs = BITS == 4 ? kUnits : kUnits / 2;
     static constexpr int kScaleDwords = kBlocks * 16;      // of K, or V, of a step
-    static_assert(kScaleDwords <= NT && kKThreads <= NT && kVThreads <= NT, "one piece a thread");
-    uint32_t k[kOps * BITS / 4], v[kVs], d[2 * kDs], ks, vs;
+    static_assert(kThreads == 256 && kScaleDwords <= kThreads, "one piece a thread");
+    uint32_t k[kOps * BITS / 4], v[kUnits], d[2 * kDs], ks, vs;
 
     template <int N>
     static __device__ __forceinline__ void load_any(const uint8_t* p, uint32_t* v) {
@@ -766,21 +765,16 @@ struct Piece {
             base[t] = c.data + (int64_t(max(pages[t], 0)) * c.heads + head) * c.chunk;
             slot[t] = (key0 + 16 * t) & (c.page_tokens - 1);
         }
-        if (kKThreads == NT || tid < kKThreads) {
-            constexpr int kPer = kBlocks / kOps;
-            const int t = wave / kPer, h = wave % kPer;
-            load_any<kOps * BITS / 4>((t ? base[1] : base[0]) + (t ? slot[1] : slot[0]) * L::kRow + (lane & 15) * L::kRow +
-                                          (lane >> 4) * (L::kRow / 4) + h * (kOps * BITS), k);
-        }
-        if (kVThreads == NT || tid < kVThreads) {
-            const int t = (tid >> 1) & 1, pair = tid & 1, ln = (tid >> 2) & 63, i0 = (tid >> 8) * kVs;
-            const uint8_t* p = (t ? base[1] : base[0]) + section;
-            const int s = t ? slot[1] : slot[0];
-            load_any<kVs>(p + s * L::kRow + ln * (L::kRow / 4) + (pair * kUnits + i0) * 4, v);
-            const uint8_t* q = p + section + (c.page_tokens + s + 4 * (ln >> 4) + 2 * pair) * (2 * kBlocks) + (BITS == 4 ? i0 : i0 / 2) * 4;
-            load_any<kDs>(q, d);
-            load_any<kDs>(q + 2 * kBlocks, d + kDs);
-        }
+        const int kt = wave / 2, h = wave % 2;
+        load_any<kOps * BITS / 4>((kt ? base[1] : base[0]) + (kt ? slot[1] : slot[0]) * L::kRow + (lane & 15) * L::kRow +
+                                      (lane >> 4) * (L::kRow / 4) + h * (kOps * BITS), k);
+        const int vt = (tid >> 1) & 1, pair = tid & 1, ln = tid >> 2;
+        const uint8_t* p = (vt ? base[1] : base[0]) + section;
+        const int s = vt ? slot[1] : slot[0];
+        load_any<kUnits>(p + s * L::kRow + ln * (L::kRow / 4) + pair * kUnits * 4, v);
+        const uint8_t* q = p + section + (c.page_tokens + s + 4 * (ln >> 4) + 2 * pair) * (2 * kBlocks);
+        load_any<kDs>(q, d);
+        load_any<kDs>(q + 2 * kBlocks, d + kDs);
         if (tid < kScaleDwords) {
             const int t = tid / (kBlocks * 8), o = tid % (kBlocks * 8);
             const uint8_t* p = (t ? base[1] : base[0]) + 2 * section + (t ? slot[1] : slot[0]) * (2 * kBlocks) + 4 * o;
@@ -797,73 +791,68 @@ struct Piece {
     static constexpr int kLarge = 23;                       // exponent field
     static constexpr float kSmall = 0x1p-8f;
     template <Form FORM>
-    __device__ __forceinline__ void stage(const Masks& masks, Staged<BITS, D, NT>& s, const int (&pages)[2], int key0, int len) const {
+    __device__ __forceinline__ void stage(const Masks& masks, Staged<BITS, D>& s, const int (&pages)[2], int key0, int len) const {
         const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-        if (FORM != kLargeOnes && (kKThreads == NT || tid < kKThreads)) {
-            constexpr int kPer = kBlocks / kOps;
-            const int t = wave / kPer, h = wave % kPer;
+        if constexpr (FORM != kLargeOnes)
 #pragma unroll
-            for (int b = 0; b < kOps; ++b) s.k[t][h * kOps + b][lane] = __builtin_bit_cast(u4, key_codes<BITS>(masks, k, b));
-        }
+            for (int b = 0; b < kOps; ++b) s.k[wave / 2][wave % 2 * kOps + b][lane] = __builtin_bit_cast(u4, key_codes<BITS>(masks, k, b));
         bool special = false, bad = false, large = false;
-        if (kVThreads == NT || tid < kVThreads) {
-            const int t = (tid >> 1) & 1, pair = tid & 1, ln = (tid >> 2) & 63, i0 = (tid >> 8) * kVs;
-            uint32_t e[2 * kDs];             // the scales, 0 behind the sequence's end
+        const int t = (tid >> 1) & 1, pair = tid & 1, ln = tid >> 2;
+        uint32_t e[2 * kDs];             // the scales, 0 behind the sequence's end
 #pragma unroll
-            for (int i = 0; i < 2 * kDs; ++i) e[i] = d[i];
-            if (key0 + kStep > len || pages[0] < 0 || pages[1] < 0) {
-                const int key = key0 + 16 * t + 4 * (ln >> 4) + 2 * pair;
-                const bool there = (t ? pages[1] : pages[0]) >= 0;
+        for (int i = 0; i < 2 * kDs; ++i) e[i] = d[i];
+        if (key0 + kStep > len || pages[0] < 0 || pages[1] < 0) {
+            const int key = key0 + 16 * t + 4 * (ln >> 4) + 2 * pair;
+            const bool there = (t ? pages[1] : pages[0]) >= 0;
 #pragma unroll
-                for (int i = 0; i < 2 * kDs; ++i) e[i] = there && key + i / kDs < len ? e[i] : 0;
-            }
-            if constexpr (FORM == kQuick) {
-                typedef unsigned short us2 __attribute__((ext_vector_type(2)));
-                us2 top = {0, 0};
+            for (int i = 0; i < 2 * kDs; ++i) e[i] = there && key + i / kDs < len ? e[i] : 0;
+        }
+        if constexpr (FORM == kQuick) {
+            typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+            us2 top = {0, 0};
 #pragma unroll
-                for (int i = 0; i < 2 * kDs; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(us2, e[i] & 0x7FFF7FFFu));
-                special = top[0] >= (kLarge << 10) || top[1] >= (kLarge << 10);
-            } else {
+            for (int i = 0; i < 2 * kDs; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(us2, e[i] & 0x7FFF7FFFu));
+            special = top[0] >= (kLarge << 10) || top[1] >= (kLarge << 10);
+        } else {
 #pragma unroll
-                for (int i = 0; i < 2 * kDs; ++i)
+            for (int i = 0; i < 2 * kDs; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t x = (e[i] >> (16 * h + 10)) & 31;
-                        const bool is_large = x >= kLarge && x < 31;
-                        bad |= x == 31;
-                        large |= is_large;
-                        if (FORM == kOrdinary ? x >= kLarge : !is_large) e[i] &= h ? 0x0000FFFFu : 0xFFFF0000u;
-                    }
-            }
-            uint32_t* hi = reinterpret_cast<uint32_t*>(s.v_hi);
-            uint32_t* lo = reinterpret_cast<uint32_t*>(s.v_lo);
-            constexpr int kPer = BITS == 4 ? 4 : 2;         // 16s of dimensions in a unit
-#pragma unroll
-            for (int i = 0; i < kVs; ++i)
-#pragma unroll
-                for (int n = 0; n < kPer; ++n) {
-                    // the two tokens' scales of the unit's block
-                    const int word = BITS == 4 ? i : i / 2;
-                    const bool second = BITS == 4 ? n >= 2 : ((kVs == 1 ? i0 : i) & 1) != 0;
-                    const h2 dd = __builtin_bit_cast(h2, __builtin_amdgcn_perm(e[kDs + word], e[word], second ? 0x07060302u : 0x05040100u));
-                    uint32_t x = v[i];
-                    if (BITS == 8 ? n == 1 : n >= 2) x >>= 8;
-                    const h2 c = __builtin_bit_cast(h2, two_codes<BITS>(masks, x, BITS == 4 && (n & 1)));
-                    uint32_t h, l;
-                    if constexpr (FORM == kQuick) {
-                        const h2 p = c * dd;
-                        h = __builtin_bit_cast(uint32_t, p);
-                        l = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, dd, -p));
-                    } else {
-                        const float by = FORM == kLargeOnes ? kSmall : 1.0f;
-                        split(f2{static_cast<float>(c[0]) * (static_cast<float>(dd[0]) * by),
-                                 static_cast<float>(c[1]) * (static_cast<float>(dd[1]) * by)}, 1.0f, h, l);
-                    }
-                    const int at = (((i0 + i) * kPer + n) * 64 + ln) * 4 + (tid & 3);
-                    hi[at] = h;
-                    lo[at] = l;
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t x = (e[i] >> (16 * h + 10)) & 31;
+                    const bool is_large = x >= kLarge && x < 31;
+                    bad |= x == 31;
+                    large |= is_large;
+                    if (FORM == kOrdinary ? x >= kLarge : !is_large) e[i] &= h ? 0x0000FFFFu : 0xFFFF0000u;
                 }
         }
+        uint32_t* hi = reinterpret_cast<uint32_t*>(s.v_hi);
+        uint32_t* lo = reinterpret_cast<uint32_t*>(s.v_lo);
+        constexpr int kPer = BITS == 4 ? 4 : 2;         // 16s of dimensions in a unit
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i)
+#pragma unroll
+            for (int n = 0; n < kPer; ++n) {
+                // the two tokens' scales of the unit's block
+                const int word = BITS == 4 ? i : i / 2;
+                const bool second = BITS == 4 ? n >= 2 : (i & 1) != 0;
+                const h2 dd = __builtin_bit_cast(h2, __builtin_amdgcn_perm(e[kDs + word], e[word], second ? 0x07060302u : 0x05040100u));
+                uint32_t x = v[i];
+                if (BITS == 8 ? n == 1 : n >= 2) x >>= 8;
+                const h2 c = __builtin_bit_cast(h2, two_codes<BITS>(masks, x, BITS == 4 && (n & 1)));
+                uint32_t h, l;
+                if constexpr (FORM == kQuick) {
+                    const h2 p = c * dd;
+                    h = __builtin_bit_cast(uint32_t, p);
+                    l = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(c, dd, -p));
+                } else {
+                    const float by = FORM == kLargeOnes ? kSmall : 1.0f;
+                    split(f2{static_cast<float>(c[0]) * (static_cast<float>(dd[0]) * by),
+                             static_cast<float>(c[1]) * (static_cast<float>(dd[1]) * by)}, 1.0f, h, l);
+                }
+                const int at = ((i * kPer + n) * 64 + ln) * 4 + (tid & 3);
+                hi[at] = h;
+                lo[at] = l;
+            }
         if constexpr (FORM == kLargeOnes) return;
         const bool any_special = __ballot(special) != 0, any_bad = __ballot(bad) != 0, any_large = __ballot(large) != 0;
         if (lane == 0) {
@@ -890,8 +879,8 @@ __device__ __forceinline__ bool any_of(const uint32_t (&v)[N]) {
 }
 
 // One staged step for a wave's RT sets of rows.  large: V's products of large scales (Piece::stage), or null.
-template <int BITS, int D, int NT, int RT>
-__device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, const Staged<BITS, D, NT>* large, Rows<BITS, D> (&r)[RT], int key0,
+template <int BITS, int D, int RT>
+__device__ __forceinline__ void attend_staged(const Staged<BITS, D>& s, const Staged<BITS, D>* large, Rows<BITS, D> (&r)[RT], int key0,
                                               bool full, bool there0, bool there1, int lane) {
     constexpr int kBlocks = D / 32, kTiles = D / 16;
     // Operands are read from LDS one product ahead (the scheduling barriers keep it at that: all of them at once take more
@@ -1011,20 +1000,20 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D, NT>& s, cons
                 f4 sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(h, hi[i], f4{0, 0, 0, 0}, 0, 0, 0);
                 sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(h, lo[i], sum, 0, 0, 0);
                 sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(l, hi[i], sum, 0, 0, 0);
-                r[i].o[j] += sum * (1.0f / Piece<BITS, D, NT>::kSmall);
+                r[i].o[j] += sum * (1.0f / Piece<BITS, D>::kSmall);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
 
-template <int BITS, int D, int NT, int RT>
-__global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArgs a) {
-    constexpr int kTiles = D / 16, kBlocks = D / 32, kRows = NT / 4 * RT;
-    constexpr size_t kBuffers = 2 * sizeof(Staged<BITS, D, NT>), kJoin = kJoinRows * sizeof(float);
+template <int BITS, int D>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArgs a) {
+    constexpr int RT = D <= 128 ? 2 : 1, kTiles = D / 16, kBlocks = D / 32, kRows = 16 * kWaves * RT;
+    constexpr size_t kBuffers = 2 * sizeof(Staged<BITS, D>), kJoin = kJoinRows * sizeof(float);
     __shared__ __align__(16) uint8_t memory[kBuffers > kJoin ? kBuffers : kJoin];
     __shared__ unsigned ticket;
-    Staged<BITS, D, NT>* const buf = reinterpret_cast<Staged<BITS, D, NT>*>(memory);
+    Staged<BITS, D>* const buf = reinterpret_cast<Staged<BITS, D>*>(memory);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     Work w;
@@ -1046,7 +1035,7 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
         r[i].first = first_key(a, w, row / a.group);
         r[i].last = last_key(a, w, row / a.group);
     }
-    using P = Piece<BITS, D, NT>;
+    using P = Piece<BITS, D>;
     if (from < to) {
         const Masks masks = Masks::make<BITS>();
         P piece;
@@ -1058,7 +1047,7 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
         __syncthreads();
         for (int step = from; step < to; ++step) {
             const int key0 = step * kStep;
-            Staged<BITS, D, NT>&s = buf[(step - from) & 1], &t = buf[(step + 1 - from) & 1];
+            Staged<BITS, D>&s = buf[(step - from) & 1], &t = buf[(step + 1 - from) & 1];
             bool large = false;
             if (any_of(s.special)) {         // (the piece is still this step's, and the other buffer free)
                 __syncthreads();
@@ -1077,7 +1066,7 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
             piece.load(a.c, pages, w.head, ahead * kStep);
             pages_of(a, w, min(step + 2, to - 1), next);
             const bool full = key0 >= full_begin && key0 + kStep <= full_end && there0 && there1;
-            attend_staged<BITS, D, NT, RT>(s, large ? &t : nullptr, r, key0, full, there0, there1, lane);
+            attend_staged<BITS, D, RT>(s, large ? &t : nullptr, r, key0, full, there0, there1, lane);
             if (any_of(s.bad)) {      // (staged as zeros)
                 for (int i = 0; i < kStep; ++i)
 #pragma unroll
@@ -1104,7 +1093,7 @@ __global__ __launch_bounds__(NT, D <= 128 ? 2 : 1) void attn_many_kernel(AttnArg
 #pragma unroll
             for (int j = 1; j < kTiles; j += 2) r[i].o[j] *= 0.0625f;
     }
-    const Slot<D, kRows, NT> slot(a, w.cell);
+    const Slot<D, kRows> slot(a, w.cell);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         const int row = mine + 16 * i + (lane & 15);
@@ -1199,11 +1188,11 @@ hipError_t launch_attn(const Attn& r, hipStream_t s, const char** name) {
     a.splits = p.splits;
     a.chunk_steps = p.chunk_steps;
     a.scale = r.scale;
-    auto run = [&](auto kernel, int threads) { hipLaunchKernelGGL(kernel, dim3(unsigned(p.blocks)), dim3(threads), 0, s, a); };
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, dim3(unsigned(p.blocks)), dim3(kThreads), 0, s, a); };
     kv_kinds(r.cache.bits, r.cache.dim, [&](auto bits, auto dim) {
         constexpr int kB = decltype(bits)::value, kD = decltype(dim)::value;
-        if (p.tile_rows == 16) run(attn_few_kernel<kB, kD>, kThreads);
-        else run(attn_many_kernel<kB, kD, 256, kD <= 128 ? 2 : 1>, 256);
+        if (p.tile_rows == 16) run(attn_few_kernel<kB, kD>);
+        else run(attn_many_kernel<kB, kD>);
     });
     return hipGetLastError();
 }
