@@ -197,6 +197,7 @@ struct Rows {
     float f;                        // score in log2 units per unit of the accumulated sums
     float m, l;                     // the score (log2 units) that weights are relative to, or none; this lane's part of the sum of weights
     float least;                    // attn_few: the least score seen (unscaled, or 0)
+    bool far;                       // (uniform) a row's m is far (see exponents)
     int first, last;                // keys first .. last - 1 are seen
 
     // q: the row's f32 values, of which this lane has 8 in each block
@@ -244,6 +245,7 @@ struct Rows {
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) o[j] = f4{0, 0, 0, 0};
         m = kNone;
+        far = false;
         l = least = 0.0f;
     }
     // The score that weights are relative to follows these scores' maximum where that passes it by more than SLACK (a weight
@@ -261,26 +263,28 @@ struct Rows {
 #pragma unroll
             for (int j = 0; j < kTiles; ++j) o[j] *= keep;
             m = to;
+            far = __ballot(m != kNone && is_far(m)) != 0;
         }
         return m == kNone ? 0.0f : m;
     }
     // Weight i is exp2(sc[i] by - base), 2^unit for a score of top (raise's).  Usually by = f, in one fma.  From 2^20 on, where the
     // rounding of top would shift all weights by 2^(1/16) (from 2^27 on by 2^8 or more, out of f16's range), scores are rounded to
-    // f32 before top is taken off; they are not known to that anyway.
+    // f32 before top is taken off; they are not known to that anyway.  any_far: a row of the wave is there.
+    static __device__ __forceinline__ bool is_far(float top) { return fabsf(top) >= 0x1p20f; }
     template <int SLACK>
-    __device__ __forceinline__ void exponents(float (&sc)[8], float top, float unit, float& by, float& base) const {
+    __device__ __forceinline__ void exponents(float (&sc)[8], float top, float unit, bool any_far, float& by, float& base) const {
 #pragma clang fp contract(off)
         by = f;
         base = top - unit;
-        const bool far = fabsf(top) >= 0x1p20f;
-        if (__ballot(far) != 0) {
+        if (any_far) {
+            const bool mine = is_far(top);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float d = sc[i] * f - top;          // (the exact difference is SLACK at most)
-                sc[i] = far ? (d > float(SLACK) ? float(SLACK) : d) : sc[i];
+                sc[i] = mine ? (d > float(SLACK) ? float(SLACK) : d) : sc[i];
             }
-            by = far ? 1.0f : f;
-            base = far ? -unit : base;
+            by = mine ? 1.0f : f;
+            base = mine ? -unit : base;
         }
     }
 };
@@ -367,7 +371,8 @@ __device__ __forceinline__ void attend(const Masks& masks, const Step<BITS, D>& 
         for (int i = 0; i < 8; i += 2) r.least = fminf(fminf(r.least, sc[i]), sc[i + 1]);
     }
     float by, base, p[8];
-    r.template exponents<4>(sc, r.template raise<4>(sc), unit_e, by, base);
+    const float top = r.template raise<4>(sc);
+    r.template exponents<4>(sc, top, unit_e, r.far, by, base);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         p[i] = __builtin_amdgcn_exp2f(fmaf(sc[i], by, -base));
@@ -944,7 +949,9 @@ __device__ __forceinline__ void attend_staged(const Staged<BITS, D>& s, const St
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
         float by, base;
-        r[i].template exponents<kManySlack>(sc[i], r[i].template raise<kManySlack>(sc[i]), kManyUnit, by, base);
+        const float top = r[i].template raise<kManySlack>(sc[i]);
+        // (asked at each step: kept over the steps, as in attn_few, it is slower here: 512 tokens over 8192 keys 201 -> 204 us)
+        r[i].template exponents<kManySlack>(sc[i], top, kManyUnit, __ballot(Rows<BITS, D>::is_far(top)) != 0, by, base);
         u4 h, l;
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
