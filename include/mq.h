@@ -427,8 +427,8 @@ int mq_kv_read(const mq_kv_cache* cache, const mq_kv_seqs* seqs, int64_t T, floa
  * j runs over the cached tokens of t's sequence, with causal != 0 up to t's own position, and with window > 0
  * (causal only) over the last `window` of these.  A row that sees no key gets zeros.  out must not overlap q.
  * max_q, max_kv: at least the largest number of rows and the largest kv_len of a sequence (they size the grid
- * and the scratch, so that the call reads nothing back): rows past max_q of a sequence are not computed, and
- * a kv_len above max_kv counts as max_kv.
+ * and the scratch, and choose the kernel, so that the call reads nothing back): rows past max_q of a sequence are not
+ * computed, and of a kv_len above max_kv the first max_kv tokens are used (rows keep the positions that kv_len gives them).
  * f32 accuracy: q is held to 21 bits or more, a weight times a value to 21 bits or to 2^-30 of the row's largest weight times the
  * largest value that it sees; sums and statistics are f32.  scale must be finite.  A row whose largest score
  * times log2 e passes f32's range, to either side, gets NaN (beside a larger one, a score below the range weighs nothing).  An
