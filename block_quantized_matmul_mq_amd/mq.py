@@ -701,8 +701,9 @@ def attn(cache, seqs, q, scale=None, causal=True, window=0, max_q=None, max_kv=N
          stream=None):
     """out f32 [T, q_heads, dim]: attention of q f32 [T, q_heads, dim] over the sequences' cached keys and values.
     scale: 1 / sqrt(dim) where None.  max_q, max_kv: at least the most rows and the largest kv_len of a sequence
-    (T and the table's width where None; tighter ones divide the work better).  scratch: attn_scratch_bytes(..) bytes,
-    its first 256 KiB zero before its first use, and for calls of attn only."""
+    (T and the table's width where None).  They choose the kernel and divide the work: give max_q for a batch of decoded
+    tokens, which is taken for one sequence's T rows otherwise, and max_kv where the table is wider than the contexts.
+    scratch: attn_scratch_bytes(..) bytes, its first 256 KiB zero before its first use, and for calls of attn only."""
     import torch
     fn = "attn"
     qs = _heads(q, fn, "q", None, None, cache.dim)
