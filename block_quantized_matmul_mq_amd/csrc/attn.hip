@@ -29,9 +29,12 @@
 // Both cut the keys of a tile into pieces over workgroups where there are few tiles, joined by the last one.
 //
 // Measured, 4 bits, heads of 128: one sequence of 32768 keys, 28 heads on 4, 24 us (0.8 TB/s; its pieces alone 15, the join of
-// 64 pieces the rest); 64 sequences of up to 8192 keys, 40 heads on 8, 109 us (2.8 TB/s; of 8192 each 3.9 TB/s, a copy here
-// reads and writes 4.7).  512 tokens over 8192 keys, 28 heads on 4: 201 us, 290 TF of the formula's operations, 2.5 times as many
-// on the matrix units for f32 accuracy; these are busy 27 % of the time, the vector ALU 30 %.
+// 64 pieces the rest); 64 sequences of up to 8192 keys, 40 heads on 8, 111 us (2.8 TB/s; of 8192 each 3.8 TB/s, a copy here
+// reads and writes 4.7).  512 tokens over 8192 keys, 28 heads on 4: 200 us, 291 TF of the formula's operations, 2.5 times as many
+// on the matrix units for f32 accuracy; these are busy 28 % of the time, the vector ALU 30 %.
+//
+// What is not finite: a NaN goes with the sum of weights, through pieces and their join; scores past f32's range, infinite scales of
+// keys and large ones of values have paths of their own (raise and exponents; attend; Piece).
 #include <algorithm>
 
 #include "kv_layout.h"
@@ -1115,16 +1118,16 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 2 : 1) void attn_many_kernel(A
 // How a call is cut: into tiles of 16 rows, or of 128 (64 in dimensions above 128) where a sequence has more than 256 and tiles of 16
 // would be more than kFewTiles; and the keys of a tile into pieces where there are few tiles.  Both sides, in us, 4-bit caches:
 //   rows x sequences and heads, keys, dimension    attn_few  attn_many
-//     84 x  4,  4096, 128                            17.5      52.5
-//    259 x 24,  4096, 128                            81        93
-//    511 x  4,  4096, 128                            33        66
-//   1029 x  4,  4096, 128                            63        72
-//    511 x 24,  4096, 128 (768 tiles of 16)         107       108
-//   1029 x 24,  4096, 128                           224       199
-//   2100 x 24,   600, 128                            80        59
-//    511 x 96,   600, 128                            84        66
-//    259 x 96,   600, 256                           136       123     (the rule's loss there)
-//   2100 x  4,  4096, 128                           103        93     (the same)
+//     84 x  4,  4096, 128                            17        51
+//    259 x 24,  4096, 128                            83        91
+//    511 x  4,  4096, 128                            31        63
+//   1029 x  4,  4096, 128                            61        69
+//    511 x 24,  4096, 128 (768 tiles of 16)         106       102     (the rule's loss: 4)
+//   1029 x 24,  4096, 128                           228       195
+//   2100 x 24,   600, 128                            80        58
+//    511 x 96,   600, 128                            85        65
+//    259 x 96,   600, 256                           150       121
+//   2100 x  4,  4096, 128 (528 tiles)               102        88     (the rule's loss: 14)
 struct Plan {
     int tile_rows, tiles, splits, chunk_steps;
     int64_t blocks;

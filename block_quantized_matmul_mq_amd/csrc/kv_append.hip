@@ -7,12 +7,13 @@
 //   code = clamp(rne(x / d) + 8, 0, 15); 8 bits: d = f16(amax / 127), code = clamp(rne(x / d), -127, 127) + 128
 //
 // Norm and rotation are formed in f64 and rounded once to f32: a key's code flips where its last f32 bit
-// does, and a cache should not depend on the order of a sum.
+// does, and so the cache is the formula's byte for byte (an f32 form in this order of sums would depend on
+// the batch as little, but flip single codes).
 //
 // A row (a head of a token) to a wave, the values in the lanes of the block that they belong to: a block's maximum and the
 // norm's sum are lane reductions, and a wave that takes several rows of a token forms its angles once.  Few tokens: 4 us, a
-// launch's latency.  Three prompts, 2980 tokens of 40 + 2 x 8 heads of 128, normed: 46.6 us, 3.2 TB/s (a copy here has 4.7), the vector ALU busy
-// for 64 % of it, mostly with f64; reading the 4-bit cache back as f32 11.7 us.
+// launch's latency.  Three prompts, 2980 tokens of 40 + 2 x 8 heads of 128, normed: 46.5 us, 3.2 TB/s (a copy here has 4.7), the vector ALU busy
+// for 58 to 63 % of it, mostly with f64; reading the 4-bit cache back as f32 11.5 us.
 #include "kv_layout.h"
 #include "mq_device.h"
 #include "mq_internal.h"

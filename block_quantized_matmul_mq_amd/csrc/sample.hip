@@ -19,7 +19,8 @@
 // A row of more than two blocks is divided over workgroups and the passes over launches (the last workgroup of a row does a
 // pass's single part, mmq_splitk.h's exchange); a shorter one is a workgroup's, which makes all passes by itself.
 // Measured: one row of 152064 25 us (launches of 3.6, 11.3 and 11.3: latency of their dependent rounds), nine of 32003 31 us,
-// 128 of 152064 98 us (0.8 TB/s; 16.5, 29.5 and 58: f64 exponentials of every token in the last two).
+// 128 of 152064 98 us (0.8 TB/s; 16.5, 28.8 and 54.5: vector ALU 51, 34 and 23 % of the time, LDS conflicts of the bins' atomics,
+// and a row's sort and choice, one workgroup's chain).
 // More collected tokens than fit (as where most logits are equal) are resolved by a radix selection over the row.
 #include <algorithm>
 
