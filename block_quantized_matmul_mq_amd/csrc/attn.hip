@@ -253,7 +253,7 @@ struct Rows {
     }
     // The score that weights are relative to follows these scores' maximum where that passes it by more than SLACK (a weight
     // may so be up to 2^SLACK, and the sums are rescaled in few steps only).  It is a rounded product, but the same in every
-    // weight's exponent, so that its rounding drops out as long as it is small beside the weights' range (see exponents).
+    // weight's exponent, so that its rounding drops out as long as f16 has room for it (see exponents).
     template <int SLACK>
     __device__ __forceinline__ float raise(const float (&sc)[8]) {
         float top = fmaxf(fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3])), fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7])));
@@ -270,10 +270,11 @@ struct Rows {
         }
         return m == kNone ? 0.0f : m;
     }
-    // Weight i is exp2(sc[i] by - base), 2^unit for a score of top (raise's).  Usually by = f, in one fma.  From 2^20 on, where the
-    // rounding of top would shift all weights by 2^(1/16) (from 2^27 on by 2^8 or more, out of f16's range), scores are rounded to
-    // f32 before top is taken off; they are not known to that anyway.  any_far: a row of the wave is there.
-    static __device__ __forceinline__ bool is_far(float top) { return fabsf(top) >= 0x1p20f; }
+    // Weight i is exp2(sc[i] by - base), 2^unit for a score of top (raise's).  Usually by = f, in one fma.  The roundings of top and
+    // base shift all weights of the row by up to 2^(1/2) below 2^23, which f16 has room for, but by 2^8 and more from 2^27 on: from
+    // 2^23 on scores are rounded to f32 (as they would be in a matrix of scores) before top is taken off.  any_far: a row of
+    // the wave is there.
+    static __device__ __forceinline__ bool is_far(float top) { return fabsf(top) >= 0x1p23f; }
     template <int SLACK>
     __device__ __forceinline__ void exponents(float (&sc)[8], float top, float unit, bool any_far, float& by, float& base) const {
 #pragma clang fp contract(off)
