@@ -379,7 +379,7 @@ int mq_moe_ffn(const void* Wg, const void* Wu, int gu_type, const void* Wd, int 
  * j % P.  Row i of n of sequence b so has the position kv_len[b] - n + i.  A sequence may have no row, or
  * no token.  A table entry outside [0, pages), and a position outside the table, is a page that is not there:
  * nothing is written to it and its keys are left out.  Rows behind the last sequence's are not touched.  The arrays are
- * not checked on the host: starts that fall, or lengths out of any order, give rows of no meaning, or none, and no access
+ * not checked on the host: starts that fall, or lengths below zero, give rows of no meaning, or none, and no access
  * outside the call's arrays and cache.
  */
 typedef struct mq_kv_cache {
